@@ -7,6 +7,7 @@ library, and raises BQError on a nonzero status. There is no CPU fallback: if
 libbq.so is missing or fails to load, every call raises.
 """
 import ctypes
+import dataclasses
 import os
 
 import torch
@@ -22,8 +23,18 @@ _LIB_NAME = "libbq.so"
 
 _STATUS = {0: "BQ_OK", -1: "BQ_ERR_INVALID_ARG", -2: "BQ_ERR_SHAPE", -3: "BQ_ERR_UNSUPPORTED",
            -4: "BQ_ERR_ALIGN", -5: "BQ_ERR_CUDA", -6: "BQ_ERR_TIMEOUT", -7: "BQ_ERR_WORKSPACE",
-           -8: "BQ_ERR_BASIS"}
+           -8: "BQ_ERR_BASIS", -9: "BQ_ERR_INDEX"}
 BASIS_PLAIN, BASIS_HADAMARD64 = 0, 1
+
+
+ELEM = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+class _CacheStruct(ctypes.Structure):
+    """bq_paged_cache of include/bq.h"""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
+                ("k_type", ctypes.c_int), ("v_type", ctypes.c_int), ("k_basis", ctypes.c_int)]
 
 
 class BQError(RuntimeError):
@@ -51,6 +62,7 @@ def lib():
                           "(the CUDA path has no fallback)")
     L = ctypes.CDLL(path)
     i, i64, vp, sz = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
+    cp = ctypes.POINTER(_CacheStruct)
     sig = {
         "bq_quantize_rows": ([i, vp, vp, i64, i64], i),
         "bq_dequantize_rows": ([i, vp, vp, i64, i64], i),
@@ -67,6 +79,13 @@ def lib():
         "bq_gemm": ([i, vp, vp, vp, i64, i64, i64], i),
         "bq_kv_quantize": ([i, vp, vp, vp, i64, i64, i64], i),
         "bq_kv_write": ([i, vp, vp, i, i, vp, i, vp, vp, i64, i64, i64], i),
+        "bq_paged_page_bytes": ([i, i64, i64, i64], sz),
+        "bq_paged_kv_write": ([cp, i, vp, i64, i64, vp, i64, i64, vp, i, vp, i64], i),
+        "bq_paged_kv_read": ([cp, i, vp, vp, vp, i, vp, i64], i),
+        "bq_paged_attn": ([cp, i, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64,
+                           ctypes.c_float, i, i64], i),
+        "bq_paged_attn_workspace_size": ([cp, i, i64, i64, i64, i64, i64, i, i64], sz),
+        "bq_paged_slot_check": ([cp, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)], i),
         "bq_block_dots": ([i, vp, vp, vp, i64, i64], i),
         "bq_set_stream": ([vp], i),
         "bq_get_stream": ([], vp),
@@ -322,6 +341,166 @@ def kv_bias(rows: torch.Tensor, basis: int = BASIS_PLAIN, out: torch.Tensor | No
         out = torch.empty((H, D), dtype=torch.float32, device=rows.device)
     L = _prep(rows.device)
     _check(L.bq_kv_bias(_ptr(rows), basis, _ptr(out), T, H, D), "bq_kv_bias")
+    return out
+
+
+# ---- paged KV cache ----
+
+
+@dataclasses.dataclass
+class PagedCache:
+    """One layer's paged KV cache: two pools of pages (layout in include/bq.h),
+    each uint8 (n_pages, n_kv_heads, page_size * head_dim / 32 * block bytes)."""
+    k_pages: torch.Tensor
+    v_pages: torch.Tensor
+    page_size: int
+    head_dim: int
+    k_type: int = Q4_0
+    v_type: int = Q4_0
+    k_basis: int = BASIS_PLAIN
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, k_type: int = Q4_0,
+              v_type: int = Q4_0, k_basis: int = BASIS_PLAIN, device="cuda") -> "PagedCache":
+        """A cache of n_pages pages of unwritten content."""
+        pools = []
+        for t in (k_type, v_type):
+            n = int(lib().bq_paged_page_bytes(t, page_size, n_kv_heads, head_dim))
+            if n == 0:
+                raise BQError(-2, f"no page of type {t} has page_size {page_size}, {n_kv_heads} heads, head_dim {head_dim}")
+            pools.append(torch.empty((n_pages, n_kv_heads, n // n_kv_heads), dtype=torch.uint8, device=device))
+        return cls(pools[0], pools[1], page_size, head_dim, k_type, v_type, k_basis)
+
+    def _struct(self):
+        k, v = self.k_pages, self.v_pages
+        for name, t, kind in (("k_pages", k, self.k_type), ("v_pages", v, self.v_type)):
+            _cuda(t, name)
+            _same_device(k, t, name)
+            if t.dtype != torch.uint8 or t.dim() != 3:
+                raise TypeError(f"{name} must be uint8 (n_pages, n_kv_heads, bytes)")
+            if t.shape[2] * QK != self.page_size * self.head_dim * block_bytes(kind):
+                raise ValueError(f"{name} has {t.shape[2]} bytes per head page, not page_size * head_dim / 32 blocks")
+        if k.shape[:2] != v.shape[:2]:
+            raise ValueError("k_pages and v_pages must have the same pages and heads")
+        return _CacheStruct(k.data_ptr(), v.data_ptr(), k.shape[0], self.page_size, k.shape[1], self.head_dim,
+                            self.k_type, self.v_type, self.k_basis)
+
+
+def _same_device(ref, t, name):
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {ref.device}")
+
+
+def _rows(cache, t, name, heads, dtype=None):
+    """A CUDA tensor (tokens, heads, head_dim) of an element type the paged
+    calls take, channels contiguous; other strides are free."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype not in ELEM or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}")
+    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be (tokens, {heads if heads is not None else 'heads'}, {cache.head_dim})")
+    if t.stride(2) != 1:
+        raise ValueError(f"the channels of {name} must be contiguous")
+    _same_device(cache.k_pages, t, name)
+    return t
+
+
+def _index(cache, t, name, dtype, shape):
+    _cuda(t, name)
+    _same_device(cache.k_pages, t, name)
+    if t.dtype != dtype or t.shape != shape:
+        raise TypeError(f"{name} must be {dtype} of shape {tuple(shape)}")
+    return t
+
+
+def _bias(cache, bias, heads):
+    return None if bias is None else _index(cache, bias, "bias", torch.float32, (heads, cache.head_dim))
+
+
+def paged_kv_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                   bias: torch.Tensor | None = None, bias_basis: int | None = None) -> None:
+    """Quantize the rows k and v (tokens, n_kv_heads, head_dim; fp32, fp16 or
+    bf16, any token and head strides) into the cache at slots (int64, page *
+    page_size + place; -1 skips a token). bias (n_kv_heads, head_dim) fp32:
+    subtracted from K, calibrated in bias_basis (default: the cache's)."""
+    s = cache._struct()
+    H = s.n_kv_heads
+    _rows(cache, k, "k", H)
+    _rows(cache, v, "v", H, k.dtype)
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    _index(cache, slots, "slots", torch.int64, k.shape[:1])
+    _bias(cache, bias, H)
+    with torch.cuda.device(k.device):
+        L = _prep(k.device)
+        _check(L.bq_paged_kv_write(s, ELEM[k.dtype], _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
+                                   v.stride(1), _ptr(bias), cache.k_basis if bias_basis is None else bias_basis,
+                                   _ptr(slots), k.shape[0]), "bq_paged_kv_write")
+
+
+def paged_kv_read(cache: PagedCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32,
+                  bias: torch.Tensor | None = None, bias_basis: int | None = None,
+                  out_k: torch.Tensor | None = None,
+                  out_v: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The rows at slots (int64; -1: zeros) as (K, V), each (tokens,
+    n_kv_heads, head_dim) of dtype; K out of the cache's basis, plus bias."""
+    s = cache._struct()
+    H, T = s.n_kv_heads, slots.numel()
+    _index(cache, slots, "slots", torch.int64, (T,))
+    _bias(cache, bias, H)
+    if dtype not in ELEM:
+        raise TypeError("dtype must be float32, float16 or bfloat16")
+    outs = []
+    for name, t in (("out_k", out_k), ("out_v", out_v)):
+        if t is None:
+            t = torch.empty((T, H, cache.head_dim), dtype=dtype, device=slots.device)
+        outs.append(_index(cache, t, name, dtype, (T, H, cache.head_dim)))
+    with torch.cuda.device(slots.device):
+        L = _prep(slots.device)
+        _check(L.bq_paged_kv_read(s, ELEM[dtype], _ptr(outs[0]), _ptr(outs[1]), _ptr(bias),
+                                  cache.k_basis if bias_basis is None else bias_basis, _ptr(slots), T),
+               "bq_paged_kv_read")
+    return outs[0], outs[1]
+
+
+def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
+               page_table: torch.Tensor, scale: float, *, max_q_len: int, max_kv_len: int, causal: bool = True,
+               window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of a batch of sequences over the cache (bq_paged_attn): q
+    (tokens, n_heads, head_dim), sequence b's tokens q_start[b] .. q_start[b +
+    1] - 1 being the last of its kv_len[b] cached ones; page_table (sequences,
+    max_pages). The index tensors are int32 on the device; max_q_len and
+    max_kv_len are their bounds on the host. window: tokens a causal query
+    sees (0: all). lse: optional fp32 (tokens, n_heads), written."""
+    s = cache._struct()
+    _rows(cache, q, "q", None)
+    n_q, H = q.shape[0], q.shape[1]
+    B = kv_len.numel()
+    _index(cache, kv_len, "kv_len", torch.int32, (B,))
+    _index(cache, q_start, "q_start", torch.int32, (B + 1,))
+    _index(cache, page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
+    if out is None:
+        out = torch.empty((n_q, H, cache.head_dim), dtype=q.dtype, device=q.device)
+    _rows(cache, out, "out", H, q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is not None:
+        _index(cache, lse, "lse", torch.float32, (n_q, H))
+    e, c = ELEM[q.dtype], 1 if causal else 0
+    with torch.cuda.device(q.device):
+        L = _prep(q.device)
+        need = int(L.bq_paged_attn_workspace_size(s, e, B, n_q, max_q_len, max_kv_len, H, c, window))
+        # a workspace of this call's own, from the current stream's pool: calls
+        # on other streams and captured launches never share it
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        _check(L.bq_set_workspace(_ptr(ws), ws.numel()), "bq_set_workspace")
+        try:
+            _check(L.bq_paged_attn(s, e, _ptr(q), q.stride(0), q.stride(1), _ptr(out), out.stride(0), out.stride(1),
+                                   _ptr(lse), _ptr(q_start), _ptr(kv_len), _ptr(page_table), page_table.shape[1], B,
+                                   n_q, max_q_len, max_kv_len, H, float(scale), c, window), "bq_paged_attn")
+        finally:
+            L.bq_set_workspace(None, 0)
     return out
 
 

@@ -136,6 +136,13 @@ int report_error(int status, const char *fmt, ...) {
 
 int report_ok() { return ok(); }
 
+cudaStream_t current_stream() { return t_stream; }
+
+void *current_workspace(size_t *bytes) {
+  *bytes = t_ws_bytes;
+  return t_ws;
+}
+
 namespace {
 struct SmemEntry {
   int device;
@@ -227,6 +234,8 @@ int bq_device_status(void) {
     e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof zero);
     if (e != cudaSuccess) return cuda_fail(e, "bq_device_status: clear error word");
     if (word & kErrTimeout) return fail(BQ_ERR_TIMEOUT, "a bounded in-kernel wait ran out (error word 0x%x)", word);
+    if (word & kErrIndex)
+      return fail(BQ_ERR_INDEX, "a slot, page or length of a paged cache was out of range (error word 0x%x)", word);
   }
   return ok();
 }

@@ -27,6 +27,7 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // error bits of the device error word
 constexpr unsigned kErrTimeout = 1u;
+constexpr unsigned kErrIndex = 2u;  // a slot, page or length of a paged cache out of range
 
 template <int TYPE> struct Fmt;
 template <> struct Fmt<kTypeQ4_0> {

@@ -10,6 +10,10 @@
 
 namespace bq {
 
+struct PagedPool;
+struct PagedShape;
+struct PagedAttnArgs;
+
 struct DeviceInfo {
   int device = -1;
   int sm_count = 0;
@@ -37,6 +41,10 @@ int tuning_value(const char *name);
 // `bytes` unless an earlier call already did (so that launches recorded in a
 // stream capture make no attribute calls after the first, uncaptured one).
 cudaError_t ensure_smem(const void *func, int bytes);
+
+// The calling thread's stream and workspace (bq_set_stream, bq_set_workspace).
+cudaStream_t current_stream();
+void *current_workspace(size_t *bytes);
 
 // Record a failure message for bq_last_error() on the calling thread and
 // return `status`; report_ok() records "no error" and returns BQ_OK.
@@ -107,6 +115,18 @@ enum class PrefillPath { kTc, kMmaSync };
 PrefillPath prefill_path(int64_t M, int64_t N, int64_t K, size_t ws_limit, size_t *ws_bytes);
 cudaError_t launch_prefill(PrefillPath path, const uint8_t *W, const float *X, float *Y, int64_t M, int64_t N,
                            int64_t K, void *ws, cudaStream_t stream);
+// Paged KV cache (paged_kv.cu, paged_attn.cu). Strides are in bytes; `rotate`:
+// K is kept in the Hadamard basis.
+cudaError_t launch_paged_write(const PagedPool &kp, const PagedPool &vp, const PagedShape &sh, int kt, int vt, int elem,
+                               bool rotate, const void *K, int64_t k_ts, int64_t k_hs, const void *V, int64_t v_ts,
+                               int64_t v_hs, const float *bias, const int64_t *slots, int64_t n_tokens,
+                               cudaStream_t stream);
+cudaError_t launch_paged_read(const PagedPool &kp, const PagedPool &vp, const PagedShape &sh, int kt, int vt, int elem,
+                              bool rotate, void *K, void *V, const float *bias, const int64_t *slots, int64_t n_tokens,
+                              cudaStream_t stream);
+bool paged_attn_dim(int64_t head_dim);
+size_t paged_attn_workspace_bytes(const PagedAttnArgs &a, int max_q);
+cudaError_t launch_paged_attn(PagedAttnArgs a, int max_q, void *ws, cudaStream_t stream);
 cudaError_t launch_block_dots(int type, const uint8_t *W, const uint8_t *xq, int32_t *out,
                               int64_t M, int64_t K, cudaStream_t stream);
 

@@ -1,0 +1,803 @@
+// paged_attn.cuh — attention of few query rows per kv head over a paged,
+// block-quantized KV cache (decode steps, drafted tokens): the streaming
+// kernel. A quantized V cache is read by flash attention ("05. llama.cpp：从
+// GGUF 文件到本地推理服务", §KV Cache 类型与 Flash Attention; the pages give no
+// formula): s_ij = scale q_i . k^_j over the tokens that row i sees, o_i =
+// sum_j softmax_j(s_i) v^_j, k^ and v^ being scale * code.
+//
+// Bound by reading the cache (0.56 or 1.06 bytes per value, each used once per
+// query row): at the measured copy rate an SM has ~6 cycles per 4-bit token
+// and kv head of 128 channels, so what counts is instructions per code.
+//   - Products run on m16n8k16 binary16 matrix instructions with the query
+//     rows as the 8 columns: K (tokens x channels) and V^T (channels x tokens)
+//     are the 16-row operand, and their fragments are cut straight out of the
+//     code words. A 4-bit code u in the low bits of a half-word IS the
+//     binary16 subnormal u * 2^-24, exactly, so a word of 8 codes becomes four
+//     operand registers with one mask each and one shift; codes in bits 4-7
+//     read as 16 u, and the matching half of q is divided by 16 (exactly).
+//   - The block scales stay out of the operands: a K block's two products
+//     leave sum(q u) 2^-24, the accumulators start at -8 sum(q) 2^-24, and
+//     d_k multiplies in fp32; d_v multiplies the weights in fp32, before their
+//     one rounding to binary16. So codes and scales enter exactly. q is
+//     brought to [2^10, 2^11) by a power of two per row (binary16 then holds
+//     bf16 and fp16 q exactly); fp32 q and weights are split in two binary16
+//     terms (22 bits), 2^-22 instead of 2^-11. A 16-bit output's weights take
+//     one term: 2^-11 each, an eighth of bf16's own rounding.
+//   - Weights d_v p are scaled by a power of two per warp that keeps them
+//     below 2^14 whatever the V scales are (d_v at most 2^6), and a row's
+//     maximum is only raised (and the accumulators rescaled) when a score
+//     passes it by 2^8: with fp32 accumulators any common factor serves.
+//     Weights below 2^-30 of the largest d_v round to nothing.
+//   - Softmax statistics and the accumulators are fp32; transposing the
+//     weights from "row = token" to "column = query row" is one movmatrix.
+//   - A warp streams its own tiles through a private ring of asynchronous
+//     16-byte copies; warps of a CTA meet only where a segment ends.
+// Work: the tiles of all (sequence, kv head, row group) segments form one
+// sequence that is cut into equal pieces, one per CTA, on the device (lengths
+// stay there), so ragged batches load every SM alike. A segment inside a piece
+// is finished there; one that is cut leaves partial results for the combine
+// launch, which merges them in a fixed order.
+#pragma once
+
+#include "bq_device.cuh"
+#include "bq_internal.h"
+#include "paged_attn.h"
+
+namespace bq {
+namespace paged {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr float kRaise = 8.0f;   // a maximum is raised when passed by this much (base-2 units)
+constexpr int kNoExp = 0x7fffffff;  // no V scale seen yet
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float2 half2_floats(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+// Token of fragment row slot r (0..7; slot r + 8 is 8 tokens on). Any
+// bijection serves (weights and V rows use the same one); this one lets the
+// eight lanes of a shared-memory phase read K rows of both parities, and a
+// V load's four lanes consecutive rows: no bank conflicts.
+__device__ __forceinline__ int slot_token(int r) { return (r & 1) ? 4 + ((r >> 1) ^ 1) : r >> 1; }
+
+// Shared-memory chunk (16 bytes) of chunk c of token t's codes, C chunks per row
+template <int C>
+__device__ __forceinline__ int swz_k(int t, int c) {
+  if constexpr (C == 8) return c ^ (t & 1);
+  if constexpr (C == 16) return c ^ (c >> 3) ^ ((t & 1) << 1);
+  return c;
+}
+template <int C>
+__device__ __forceinline__ int swz_v(int t, int c) {
+  if constexpr (C == 4) return c ^ (t & 2);
+  if constexpr (C == 8) return c ^ ((t & 3) << 1);
+  if constexpr (C == 16) return c ^ (((t & 1) << 2) | ((t & 2) >> 1));
+  return c;
+}
+
+// N bytes at byte `at` of token t's row, from a swizzled tile
+template <int N, int C, bool IS_V>
+__device__ __forceinline__ void lds_piece(const uint8_t *tile, int t, int at, uint32_t (&w)[(N + 3) / 4]) {
+  auto addr = [&](int o) {
+    const int c = o >> 4;
+    return tile + t * (C * 16) + ((IS_V ? swz_v<C>(t, c) : swz_k<C>(t, c)) << 4) + (o & 15);
+  };
+  if constexpr (N % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(addr(at + 16 * i));
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(addr(at + 8 * i));
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    }
+  } else if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = *reinterpret_cast<const uint32_t *>(addr(at + 4 * i));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const uint32_t h = *reinterpret_cast<const uint16_t *>(addr(at + 2 * i));
+      w[i / 2] = (i & 1) ? w[i / 2] | (h << 16) : h;
+    }
+  }
+}
+
+// The NB binary16 scales of token t (row of the tile)
+template <int NB>
+__device__ __forceinline__ void lds_scales(const uint8_t *tile, int t, uint32_t (&w)[(NB + 1) / 2]) {
+  const uint8_t *p = tile + t * NB * 2;
+  if constexpr (NB % 8 == 0) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(p);
+    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+  } else if constexpr (NB % 4 == 0) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    w[0] = v.x, w[1] = v.y;
+  } else if constexpr (NB % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < NB / 2; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      const uint32_t h = reinterpret_cast<const uint16_t *>(p)[i];
+      w[i / 2] = (i & 1) ? w[i / 2] | (h << 16) : h;
+    }
+  }
+}
+template <int N>
+__device__ __forceinline__ float scale_of(const uint32_t (&w)[N], int b) {
+  return half_bits_to_float((b & 1) ? w[b / 2] >> 16 : w[b / 2]);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// Sizes of one instantiation. R: groups of 8 query rows per pass.
+template <int NB, int KT, int VT, int R>
+struct Cfg {
+  static constexpr int D = NB * 32;
+  static constexpr int RBK = NB * Codes<KT>::kBytes, RBV = NB * Codes<VT>::kBytes;
+  static constexpr int SUB = 16 * (RBK + RBV) + 2 * 16 * NB * 2;   // bytes of 16 tokens
+  static constexpr int kHalf = 112 * 1024;                          // two CTAs per SM
+  static constexpr int TT = 2 * 2 * SUB * kWarps <= kHalf ? 2 : 1;  // 16-token tiles per stage
+  static constexpr int STAGE = TT * SUB;
+  static constexpr bool kTwo = 2 * STAGE * kWarps <= kHalf;
+  static constexpr int S = 3 * STAGE * kWarps <= kHalf ? 3 : kTwo ? 2 : 3;  // ring stages
+  static constexpr int TOK = 16 * TT;                               // tokens per stage
+  static constexpr int ROWS = 8 * R;
+  static constexpr int OP = D + 8;                                  // pitch of a merge row (floats)
+  static constexpr int kRing = kWarps * S * STAGE;
+  static constexpr int kMerge = kWarps * ROWS * OP * 4 + kWarps * ROWS * 8;
+  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
+  static constexpr int kCtas = kTwo && 2 * (kSmem + 1024) <= 227 * 1024 && NB * R <= 4 ? 2 : 1;
+};
+
+// Tiles of a sequence: [t_lo, t_lo + tiles) of `tok` tokens hold every token
+// that any of its rows sees; a sequence with rows has at least one tile, so
+// that its output is written even when no row sees a token.
+struct SeqTiles {
+  int t_lo, tiles, groups;  // per (kv head, row group)
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const PagedAttnArgs &a, const SeqSpan &s, int tok, int rows) {
+  SeqTiles t{0, 0, 0};
+  const int n_rows = s.q_len * a.group;
+  if (s.q_len == 0 || n_rows > a.tc_rows) return t;
+  int lo, hi, lo1, hi1;
+  seen_range(s, 0, a.causal, a.window, lo, hi1);
+  seen_range(s, s.q_len - 1, a.causal, a.window, lo1, hi);
+  t.t_lo = lo / tok;
+  const int t_hi = (hi + tok - 1) / tok;
+  t.tiles = t_hi > t.t_lo ? t_hi - t.t_lo : 1;
+  t.groups = (n_rows + rows - 1) / rows;
+  return t;
+}
+
+__device__ __forceinline__ SeqSpan load_span(const PagedAttnArgs &a, int b, bool report) {
+  bool bad;
+  const int64_t most = min(int64_t(a.max_kv), int64_t(a.max_pages) * a.sh.page_size);
+  const SeqSpan s = checked_span(__ldg(a.q_start + b), __ldg(a.q_start + b + 1), __ldg(a.kv_len + b), a.n_q, most, bad);
+  if (bad && report) atomicOr(a.err, kErrIndex);
+  return s;
+}
+
+template <int ELEM>
+__device__ __forceinline__ void store_out4(uint8_t *p, float4 v) {
+  if constexpr (ELEM == kElemF32)
+    *reinterpret_cast<float4 *>(p) = v;
+  else
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack_pair<ELEM>(v.x, v.y), pack_pair<ELEM>(v.z, v.w));
+}
+__device__ __forceinline__ void store_out4(int elem, uint8_t *row, int ch, float4 v) {
+  if (elem == kElemF32)
+    store_out4<kElemF32>(row + ch * 4, v);
+  else if (elem == kElemF16)
+    store_out4<kElemF16>(row + ch * 2, v);
+  else
+    store_out4<kElemBF16>(row + ch * 2, v);
+}
+
+// The 8 q values of lane c's unit of block b, as fp32
+template <int KT>
+__device__ __forceinline__ void load_q8(int elem, const uint8_t *row, int b, int c, float *x) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int ch = b * 32 + chan8<KT>(c, h);
+    if (elem == kElemF32) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(row + ch * 4));
+      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + ch * 2));
+      const float2 p = elem == kElemF16 ? unpack_pair<kElemF16>(v.x) : unpack_pair<kElemBF16>(v.x);
+      const float2 q = elem == kElemF16 ? unpack_pair<kElemF16>(v.y) : unpack_pair<kElemBF16>(v.y);
+      x[4 * h] = p.x, x[4 * h + 1] = p.y, x[4 * h + 2] = q.x, x[4 * h + 3] = q.y;
+    }
+  }
+}
+
+template <int NB, int KT, int VT, int R, int TERMS>
+__global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
+    k_paged_stream(const __grid_constant__ PagedAttnArgs a, int min_tiles) {
+  using C = Cfg<NB, KT, VT, R>;
+  constexpr int D = C::D, TT = C::TT, S = C::S, TOK = C::TOK, ROWS = C::ROWS, OP = C::OP;
+  constexpr int CK = C::RBK / 16, CV = C::RBV / 16;            // 16-byte chunks per row
+  constexpr int UK = C::RBK / kUnitsK, UV = C::RBV / kUnitsV;  // bytes of a lane's piece of a row
+  constexpr bool K4 = KT == kTypeQ4_0, V4 = VT == kTypeQ4_0;
+  // factor of the products' accumulators: 4-bit codes are read as u * 2^-24
+  constexpr float kKUnit = K4 ? 16777216.0f : 1.0f, kVUnit = V4 ? 16777216.0f : 1.0f;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t sh_scan[kWarps + 1];
+  __shared__ int64_t sh_find[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+  pdl_launch_dependents();  // the combine may become resident; it waits for this grid
+
+  // ---- this CTA's piece [t0, t1) of all tiles ----
+  const int per_thread = (a.n_seqs + kThreads - 1) / kThreads;
+  const int b_first = min(int(threadIdx.x) * per_thread, a.n_seqs), b_last = min(b_first + per_thread, a.n_seqs);
+  int64_t mine = 0;
+  for (int b = b_first; b < b_last; ++b) {
+    const SeqTiles t = seq_tiles(a, load_span(a, b, blockIdx.x == 0), TOK, ROWS);
+    mine += int64_t(t.tiles) * t.groups * a.sh.n_kv;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh_scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += sh_scan[w];
+    total += sh_scan[w];
+  }
+  const int64_t piece = max((total + gridDim.x - 1) / gridDim.x, int64_t(min_tiles));
+  const int64_t t0 = min(piece * blockIdx.x, total), t1 = min(t0 + piece, total);
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, -1);
+  if (t0 >= t1) return;
+  if (before <= t0 && t0 < before + mine) {
+    int64_t at = before;
+    for (int b = b_first; b < b_last; ++b) {
+      const SeqTiles t = seq_tiles(a, load_span(a, b, false), TOK, ROWS);
+      const int64_t n = int64_t(t.tiles) * t.groups * a.sh.n_kv;
+      if (t0 < at + n) {
+        sh_find[0] = b;
+        sh_find[1] = at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  int seq = int(sh_find[0]);
+  int64_t seq_at = sh_find[1];  // first tile of the sequence
+
+  uint8_t *ring = smem + warp * S * C::STAGE;
+  const uint32_t ring_u = smem_u32(ring);
+  float *merge_o = reinterpret_cast<float *>(smem);
+  float2 *merge_ml = reinterpret_cast<float2 *>(smem + kWarps * ROWS * OP * 4);
+
+  for (int64_t at = t0; at < t1;) {
+    // ---- the segment that holds tile `at` ----
+    SeqSpan span = load_span(a, seq, false);
+    SeqTiles st = seq_tiles(a, span, TOK, ROWS);
+    while (at >= seq_at + int64_t(st.tiles) * st.groups * a.sh.n_kv) {
+      seq_at += int64_t(st.tiles) * st.groups * a.sh.n_kv;
+      span = load_span(a, ++seq, false);
+      st = seq_tiles(a, span, TOK, ROWS);
+    }
+    const int64_t seg = (at - seq_at) / st.tiles, seg_at = seq_at + seg * st.tiles, seg_end = seg_at + st.tiles;
+    const int kvh = int(seg / st.groups), rg = int(seg - int64_t(kvh) * st.groups);
+    const int64_t stop = min(seg_end, t1);
+    const int n_rows = span.q_len * a.group, row0 = rg * ROWS, rows = min(ROWS, n_rows - row0);
+    // tokens that some row of the group sees, and tokens that all of them see
+    int lo_any, hi_any, lo_all, hi_all;
+    seen_range(span, row0 / a.group, a.causal, a.window, lo_any, hi_all);
+    seen_range(span, (row0 + rows - 1) / a.group, a.causal, a.window, lo_all, hi_any);
+    int tile = st.t_lo + int(at - seg_at), tile_end = st.t_lo + int(stop - seg_at);
+    tile = max(tile, lo_any / TOK);
+    tile_end = min(tile_end, (hi_any + TOK - 1) / TOK);
+
+    // ---- this lane's columns: rows 2c, 2c + 1 of each group of 8 ----
+    int lo[R][2], hi[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = min(row0 + 8 * r + 2 * c + e, n_rows - 1);
+        seen_range(span, row / a.group, a.causal, a.window, lo[r][e], hi[r][e]);
+      }
+    // q as operand columns: lane (g, c) holds row g's channels of unit c
+    uint32_t qf[R][TERMS][NB][4];
+    float init[R][NB][2];  // -8 sum(q) of the columns' blocks, in the products' unit
+    float qscale[R][2];    // score = qscale * sum_b d_k[b] * product[b]
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float x[NB][8];
+      const int row = row0 + 8 * r + g;
+      if (row < n_rows) {
+        const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+        const uint8_t *p = a.q + int64_t(span.q0 + tok) * a.q_token + int64_t(head) * a.q_head;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) load_q8<KT>(a.elem, p, b, c, x[b]);
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[b][i] = 0.0f;
+      }
+      if constexpr (NB % 2 == 0) {
+        if (a.rotate) {
+#pragma unroll
+          for (int b = 0; b < NB; b += 2) hadamard64_4lanes<KT>(reinterpret_cast<float(&)[2][8]>(x[b]));
+        }
+      }
+      float m = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[b][i]));
+      m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+      // 2^k brings the row's largest value to [2^10, 2^11)
+      const int k = m > 0.0f ? min(10 + 127 - int(__float_as_uint(m) >> 23), 110) : 0;
+      const float up = __int_as_float((127 + k) << 23);
+      const float fs = a.scale_log2 * kKUnit * __int_as_float((127 - k) << 23);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qscale[r][e] = __shfl_sync(kFull, fs, (2 * c + e) * 4);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float sum = 0.0f;
+        float y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = x[b][i] * up;
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          // fragment pairs: Q4_0 (i, i + 2) of the low channels then of the
+          // high ones (read as 16 u, so q / 16); Q8_0 consecutive channels
+          uint32_t h[4];
+          if constexpr (K4) {
+            h[0] = half2_bits(y[0], y[2]);
+            h[1] = half2_bits(y[4], y[6]);
+            h[2] = half2_bits(y[1], y[3]);
+            h[3] = half2_bits(y[5], y[7]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = half2_bits(y[2 * i], y[2 * i + 1]);
+          }
+          float z[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = half2_floats(h[i]);
+            const int i0 = K4 ? (i & 1) * 4 + (i >> 1) : 2 * i, i1 = K4 ? i0 + 2 : 2 * i + 1;
+            z[i0] = f.x;
+            z[i1] = f.y;
+            if (K4 && (i & 1)) h[i] = half2_bits(f.x * 0.0625f, f.y * 0.0625f);
+            qf[r][t][b][i] = h[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            sum += z[i];
+            y[i] -= z[i];
+          }
+        }
+        if constexpr (K4) {
+          sum += __shfl_xor_sync(kFull, sum, 1);
+          sum += __shfl_xor_sync(kFull, sum, 2);
+          sum *= -8.0f / kKUnit;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) init[r][b][e] = __shfl_sync(kFull, sum, (2 * c + e) * 4);
+        } else {
+          init[r][b][0] = init[r][b][1] = 0.0f;
+        }
+      }
+    }
+
+    float m[R][2], l[R][2], o[R][NB][2][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r][0] = m[r][1] = -INFINITY;
+      l[r][0] = l[r][1] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][b][i >> 2][i & 3] = 0.0f;
+    }
+    int vexp = kNoExp;  // weights are multiplied by 2^vexp
+
+    // ---- the tiles ----
+    const int64_t head_k = a.kp.head_bytes, head_v = a.vp.head_bytes;
+    const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
+    auto issue = [&](int ti, int stage) {
+      if (ti < tile_end) {
+#pragma unroll
+        for (int u = 0; u < TT; ++u) {
+          const int tok = ti * TOK + u * 16;
+          bool ok = tok < hi_any;
+          const int pi = a.sh.page_shift >= 0 ? tok >> a.sh.page_shift : tok / a.sh.page_size;
+          int page = ok ? __ldg(table + pi) : 0;
+          if (uint32_t(page) >= uint64_t(a.sh.n_pages)) {  // never read outside the pool
+            if (lane == 0) atomicOr(a.err, kErrIndex);
+            page = 0;
+            ok = false;
+          }
+          const int place = tok - pi * a.sh.page_size;
+          const uint8_t *hk = a.kp.base + (int64_t(page) * a.sh.n_kv + kvh) * head_k;
+          const uint8_t *hv = a.vp.base + (int64_t(page) * a.sh.n_kv + kvh) * head_v;
+          const uint32_t base = ring_u + stage * C::STAGE + u * C::SUB;
+          const uint8_t *sk = hk + (ok ? place * C::RBK : 0), *sv = hv + (ok ? place * C::RBV : 0);
+#pragma unroll
+          for (int i = 0; i < (16 * CK + 31) / 32; ++i) {
+            const int q = lane + 32 * i;
+            if (16 * CK % 32 == 0 || q < 16 * CK)
+              cp_async16(base + (q / CK) * C::RBK + (swz_k<CK>(q / CK, q % CK) << 4), ok ? sk + q * 16 : sk, ok);
+          }
+#pragma unroll
+          for (int i = 0; i < (16 * CV + 31) / 32; ++i) {
+            const int q = lane + 32 * i;
+            if (16 * CV % 32 == 0 || q < 16 * CV)
+              cp_async16(base + 16 * C::RBK + (q / CV) * C::RBV + (swz_v<CV>(q / CV, q % CV) << 4), ok ? sv + q * 16 : sv, ok);
+          }
+          // scales: 2 NB chunks of K's, then as many of V's
+          if (lane < 4 * NB) {
+            const bool is_v = lane >= 2 * NB;
+            const int q = is_v ? lane - 2 * NB : lane;
+            const uint8_t *ss = (is_v ? hv + a.vp.scale_off : hk + a.kp.scale_off) + (ok ? place * NB * 2 + q * 16 : 0);
+            cp_async16(base + 16 * (C::RBK + C::RBV) + lane * 16, ss, ok);
+          }
+        }
+      }
+      cp_commit();
+    };
+    int ti = tile + warp;
+#pragma unroll
+    for (int s = 0; s < S - 1; ++s) issue(ti + s * kWarps, s);
+    int stage = 0;
+    for (; ti < tile_end; ti += kWarps) {
+      issue(ti + (S - 1) * kWarps, stage == 0 ? S - 1 : stage - 1);
+      cp_wait<S - 1>();
+      __syncwarp();
+      const uint8_t *buf = ring + stage * C::STAGE;
+      const bool full = ti * TOK >= lo_all && (ti + 1) * TOK <= hi_all;
+
+      float s[TT][R][4];
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        const uint8_t *sub = buf + u * C::SUB;
+        uint32_t kw[2][UK / 4], ks[2][(NB + 1) / 2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = slot_token(g) + 8 * h;
+          lds_piece<UK, CK, false>(sub, t, c * UK, kw[h]);
+          lds_scales<NB>(sub + 16 * (C::RBK + C::RBV), t, ks[h]);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[u][r][0] = s[u][r][1] = s[u][r][2] = s[u][r][3] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t A[2][4];  // [token half][fragment pair], as qf
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (K4) {
+              const uint32_t w = kw[h][b], v = w >> 8;
+              A[h][0] = w & 0x000f000fu;
+              A[h][1] = w & 0x00f000f0u;
+              A[h][2] = v & 0x000f000fu;
+              A[h][3] = v & 0x00f000f0u;
+            } else {
+              const uint2 p = codes_to_f16x2(kw[h][2 * b]), q = codes_to_f16x2(kw[h][2 * b + 1]);
+              A[h][0] = p.x, A[h][1] = p.y, A[h][2] = q.x, A[h][3] = q.y;
+            }
+          }
+          const float d0 = scale_of(ks[0], b), d1 = scale_of(ks[1], b);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float acc[4] = {init[r][b][0], init[r][b][1], init[r][b][0], init[r][b][1]};
+#pragma unroll
+            for (int t = TERMS - 1; t >= 0; --t) {
+              mma16816(acc, A[0][0], A[1][0], A[0][1], A[1][1], qf[r][t][b][0], qf[r][t][b][1]);
+              mma16816(acc, A[0][2], A[1][2], A[0][3], A[1][3], qf[r][t][b][2], qf[r][t][b][3]);
+            }
+            s[u][r][0] = fmaf(d0, acc[0], s[u][r][0]);
+            s[u][r][1] = fmaf(d0, acc[1], s[u][r][1]);
+            s[u][r][2] = fmaf(d1, acc[2], s[u][r][2]);
+            s[u][r][3] = fmaf(d1, acc[3], s[u][r][3]);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[u][r][i] *= qscale[r][i & 1];
+      }
+      // V scales of the lane's two tokens per 16; outside what any row sees
+      // they count as zero, whatever the page holds there
+      uint32_t vs[TT][2][(NB + 1) / 2];
+      uint32_t vmax = 0;
+#pragma unroll
+      for (int u = 0; u < TT; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int t = slot_token(g) + 8 * h;
+          lds_scales<NB>(buf + u * C::SUB + 16 * (C::RBK + C::RBV) + 16 * NB * 2, t, vs[u][h]);
+          if (!full) {
+            const int tok = ti * TOK + u * 16 + t;
+            const bool live = tok >= lo_any && tok < hi_any;
+#pragma unroll
+            for (int i = 0; i < (NB + 1) / 2; ++i) vs[u][h][i] = live ? vs[u][h][i] : 0u;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (tok < lo[r][e] || tok >= hi[r][e]) s[u][r][2 * h + e] = -INFINITY;
+          }
+#pragma unroll
+          for (int i = 0; i < (NB + 1) / 2; ++i) vmax = __vmaxu2(vmax, vs[u][h][i] & 0x7fff7fffu);
+        }
+      // power of two that brings the largest V scale seen to [2^5, 2^6): the
+      // binary16 exponent (subnormals count as the smallest normal) decides
+      vmax = __reduce_max_sync(kFull, max(vmax & 0xffffu, vmax >> 16));
+      const int need = 20 - max(int(vmax >> 10), 1);  // 2^5 / 2^(e - 15)
+      if (need < vexp) {  // warp-uniform; rare after the first tile
+        if (vexp != kNoExp) {
+          const float f = __int_as_float((127 + need - vexp) << 23);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[r][b][i >> 2][i & 3] *= f;
+        }
+        vexp = need;
+      }
+      const float vup = __int_as_float((127 + vexp) << 23);
+
+      // ---- running maximum ----
+      bool raise = false;
+      float top[R][2];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = fmaxf(s[0][r][e], s[0][r][2 + e]);
+#pragma unroll
+          for (int u = 1; u < TT; ++u) t = fmaxf(t, fmaxf(s[u][r][e], s[u][r][2 + e]));
+          top[r][e] = t;
+          raise = raise || t > m[r][e] + kRaise;
+        }
+      if (__any_sync(kFull, raise)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = top[r][e];
+            t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
+            t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
+            t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
+            const float mn = fmaxf(m[r][e], t);
+            const float al = mn == -INFINITY ? 1.0f : ex2(m[r][e] - mn);
+            m[r][e] = mn;
+            l[r][e] *= al;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                o[r][b][mt][e] *= al;
+                o[r][b][mt][2 + e] *= al;
+              }
+          }
+      }
+#pragma unroll
+      for (int u = 0; u < TT; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            // a masked score weighs nothing, even where no score raised the maximum; NaN stays NaN
+            const float p = s[u][r][i] == -INFINITY ? 0.0f : ex2(s[u][r][i] - m[r][i & 1]);
+            l[r][i & 1] += p;
+            s[u][r][i] = p * vup;
+          }
+
+      // ---- weights times V ----
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        const uint8_t *sub = buf + u * C::SUB + 16 * C::RBK;
+        uint32_t vw[4][(UV + 3) / 4];  // fragment slots 2c, 2c + 1, 2c + 8, 2c + 9
+        lds_piece<UV, CV, true>(sub, c, g * UV, vw[0]);
+        lds_piece<UV, CV, true>(sub, 4 + (c ^ 1), g * UV, vw[1]);
+        lds_piece<UV, CV, true>(sub, 8 + c, g * UV, vw[2]);
+        lds_piece<UV, CV, true>(sub, 12 + (c ^ 1), g * UV, vw[3]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t A[2][4];  // two 16-channel tiles of the block
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if constexpr (V4) {
+              // half-word b of both tokens of the pair side by side
+              const uint32_t X = __byte_perm(vw[2 * k][b / 2], vw[2 * k + 1][b / 2], (b & 1) ? 0x7632 : 0x5410);
+              const uint32_t Y = X >> 8;
+              A[0][2 * k] = hsub2(X & 0x000f000fu, 0x00080008u);      // channels 2g
+              A[0][2 * k + 1] = hsub2(Y & 0x000f000fu, 0x00080008u);  // 2g + 1
+              A[1][2 * k] = hsub2(X & 0x00f000f0u, 0x00800080u);      // 16 + 2g, as 16 u
+              A[1][2 * k + 1] = hsub2(Y & 0x00f000f0u, 0x00800080u);
+            } else {
+              // bytes of both tokens interleaved, then the exact binary16 codes
+              const uint32_t w0 = vw[2 * k][b], w1 = vw[2 * k + 1][b];
+              const uint2 p = codes_to_f16x2(__byte_perm(w0, w1, 0x5140)), q = codes_to_f16x2(__byte_perm(w0, w1, 0x7362));
+              A[0][2 * k] = p.x, A[0][2 * k + 1] = p.y;  // channels 4g, 4g + 1
+              A[1][2 * k] = q.x, A[1][2 * k + 1] = q.y;  // 4g + 2, 4g + 3
+            }
+          }
+          const float d0 = scale_of(vs[u][0], b), d1 = scale_of(vs[u][1], b);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            float w0 = s[u][r][0] * d0, w1 = s[u][r][1] * d0, w2 = s[u][r][2] * d1, w3 = s[u][r][3] * d1;
+#pragma unroll
+            for (int t = 0; t < TERMS; ++t) {
+              const uint32_t h0 = half2_bits(w0, w1), h1 = half2_bits(w2, w3);
+              const uint32_t b0 = movmatrix_trans(h0), b1 = movmatrix_trans(h1);
+              mma16816(o[r][b][0], A[0][0], A[0][1], A[0][2], A[0][3], b0, b1);
+              mma16816(o[r][b][1], A[1][0], A[1][1], A[1][2], A[1][3], b0, b1);
+              if (t + 1 < TERMS) {
+                const float2 f0 = half2_floats(h0), f1 = half2_floats(h1);
+                w0 -= f0.x, w1 -= f0.y, w2 -= f1.x, w3 -= f1.y;
+              }
+            }
+          }
+        }
+      }
+      stage = stage + 1 == S ? 0 : stage + 1;
+      __syncwarp();  // every lane has read the stage before it is refilled
+    }
+    cp_wait<0>();
+    __syncthreads();  // the rings become the merge buffer
+
+    // ---- merge the warps ----
+    {
+      const float down = vexp == kNoExp ? 0.0f : __int_as_float((127 - vexp) << 23) * kVUnit;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[r][e] += __shfl_xor_sync(kFull, l[r][e], 4);
+          l[r][e] += __shfl_xor_sync(kFull, l[r][e], 8);
+          l[r][e] += __shfl_xor_sync(kFull, l[r][e], 16);
+          const int row = warp * ROWS + 8 * r + 2 * c + e;
+          if (g == 0) merge_ml[row] = make_float2(m[r][e], l[r][e]);
+          float *dst = merge_o + row * OP;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const float f = V4 && mt ? down * 0.0625f : down;
+              const int ch = b * 32 + (V4 ? 16 * mt + 2 * g : 4 * g + 2 * mt);
+              *reinterpret_cast<float2 *>(dst + ch) = make_float2(o[r][b][mt][e] * f, o[r][b][mt][2 + e] * f);
+            }
+        }
+      }
+    }
+    __syncthreads();
+    const bool whole = seg_at >= t0 && seg_end <= t1;
+    const int slot = seg_at >= t0 ? 1 : 0;  // partial results: 1 for a segment that starts in this piece
+    for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), ch = (i - r * (D / 4)) * 4;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, merge_ml[w * ROWS + r].x);
+      float sum = 0.0f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = merge_ml[w * ROWS + r];
+        if (ml.y == 0.0f) continue;  // the warp saw no token of this row
+        const float f = ex2(ml.x - top);
+        const float4 v = *reinterpret_cast<const float4 *>(merge_o + (w * ROWS + r) * OP + ch);
+        sum = fmaf(ml.y, f, sum);
+        acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+      }
+      if (whole) {
+        const int tok = (row0 + r) / a.group, head = kvh * a.group + (row0 + r - tok * a.group);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        uint8_t *row = a.o + int64_t(span.q0 + tok) * a.o_token + int64_t(head) * a.o_head;
+        store_out4(a.elem, row, ch, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (ch == 0 && a.lse)
+          a.lse[int64_t(span.q0 + tok) * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+      } else {
+        const int64_t p = (int64_t(blockIdx.x) * 2 + slot) * ROWS + r;
+        *reinterpret_cast<float4 *>(a.part_o + p * D + ch) = acc;
+        if (ch == 0) a.part_ml[p] = make_float2(top, sum);
+      }
+    }
+    if (!whole && slot == 1 && threadIdx.x == 0)
+      a.meta[blockIdx.x] = make_int4(seq, kvh, rg, int((seg_end - 1) / piece));
+    at = stop;
+    __syncthreads();  // the merge buffer becomes the rings again
+  }
+}
+
+// Each head dimension's instantiations are a translation unit of their own.
+template <int NB, int KT, int VT, int R, int TERMS>
+cudaError_t launch_stream_one(const PagedAttnArgs &a, int grid, int min_tiles, cudaStream_t stream) {
+  using C = Cfg<NB, KT, VT, R>;
+  cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_paged_stream<NB, KT, VT, R, TERMS>), C::kSmem);
+  if (e != cudaSuccess) return e;
+  k_paged_stream<NB, KT, VT, R, TERMS><<<grid, kThreads, C::kSmem, stream>>>(a, min_tiles);
+  return cudaGetLastError();
+}
+
+template <typename F>
+auto by_cache_types(int kt, int vt, F f) {
+  using Q4 = std::integral_constant<int, kTypeQ4_0>;
+  using Q8 = std::integral_constant<int, kTypeQ8_0>;
+  if (kt == kTypeQ4_0) return vt == kTypeQ4_0 ? f(Q4(), Q4()) : f(Q4(), Q8());
+  return vt == kTypeQ4_0 ? f(Q8(), Q4()) : f(Q8(), Q8());
+}
+
+// fp32 operands take two terms; more than 8 rows per pass only with one term
+// and up to 128 channels (accumulators and query fragments fill the registers)
+template <int NB>
+constexpr bool two_groups(int elem, int rows8) {
+  return NB <= 4 && elem != kElemF32 && rows8 > 1;
+}
+
+#define BQ_PAGED_STREAM_INSTANTIATE(NB)                                                                            \
+  template <>                                                                                                      \
+  StreamShape stream_shape<NB>(int kt, int vt, int elem, int rows8) {                                              \
+    return by_cache_types(kt, vt, [&](auto k, auto v) {                                                            \
+      using C1 = Cfg<NB, k.value, v.value, 1>;                                                                     \
+      using C2 = Cfg<NB, k.value, v.value, 2>;                                                                     \
+      if (two_groups<NB>(elem, rows8)) return StreamShape{C2::ROWS, C2::TOK, C2::kCtas};                           \
+      return StreamShape{C1::ROWS, C1::TOK, C1::kCtas};                                                            \
+    });                                                                                                            \
+  }                                                                                                                \
+  template <>                                                                                                      \
+  cudaError_t launch_stream<NB>(const PagedAttnArgs &a, int rows8, int grid, int min_tiles, cudaStream_t stream) { \
+    return by_cache_types(a.kt, a.vt, [&](auto k, auto v) {                                                        \
+      if (a.elem == kElemF32) return launch_stream_one<NB, k.value, v.value, 1, 2>(a, grid, min_tiles, stream);    \
+      if constexpr (NB <= 4) {                                                                                     \
+        if (rows8 > 1) return launch_stream_one<NB, k.value, v.value, 2, 1>(a, grid, min_tiles, stream);           \
+      }                                                                                                            \
+      return launch_stream_one<NB, k.value, v.value, 1, 1>(a, grid, min_tiles, stream);                            \
+    });                                                                                                            \
+  }
+
+}  // namespace paged
+}  // namespace bq

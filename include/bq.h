@@ -101,6 +101,7 @@ extern "C" {
 #define BQ_ERR_TIMEOUT (-6)     /* a bounded in-kernel wait ran out (see bq_device_status) */
 #define BQ_ERR_WORKSPACE (-7)   /* workspace missing or smaller than bq_workspace_size() */
 #define BQ_ERR_BASIS (-8)       /* a mean-centering bias calibrated in another basis than the K cache */
+#define BQ_ERR_INDEX (-9)       /* a slot, page or length of a paged cache out of range (see bq_device_status) */
 
 /* Largest K taken by bq_gemv (the quantized activation lives in shared memory). */
 #define BQ_GEMV_MAX_K 65536
@@ -278,6 +279,105 @@ int bq_kv_write(int k_type, const float *K_rows, const float *bias, int bias_bas
 int bq_kv_bias(const float *K_rows, int basis, float *bias, int64_t n_tokens, int64_t n_kv_heads,
                int64_t head_dim);
 
+/* ---- paged KV cache ----
+ * Sequences of a batch share one pool of pages per tensor; the pages describe
+ * one contiguous cache per sequence ("05. llama.cpp…", §KV Cache 类型与 Flash
+ * Attention), so the layout and the calls below are this library's own.
+ *
+ * A page holds page_size tokens of every kv head. Row `place` of page `p` is
+ * SLOT p * page_size + place. Pool layout: [page][kv head], each such head
+ * page being two planes: the codes of its tokens [place][row], then their
+ * binary16 scales [place][head_dim / 32]; bytes per value as in the blocks.
+ * A block's code bytes are those of the Q4_0 / Q8_0 block; they are cut into
+ * 4 units (K) or 8 units (V), and a row is unit 0 of every block of the head,
+ * then unit 1 of every block, and so on. Codes and scales are those of
+ * bq_kv_quantize_basis, bit for bit.
+ * Limits: page_size a multiple of 16 up to 2^20; head_dim a multiple of 32 (of
+ * 64 in the rotated basis); n_pages * page_size < 2^31 (pools may exceed 2^32
+ * bytes). Types Q4_0 or Q8_0 for each of K and V. Pools 16-byte aligned. */
+typedef struct bq_paged_cache {
+  void *k_pages, *v_pages; /* device, n_pages * bq_paged_page_bytes(type, ...) bytes each */
+  int64_t n_pages, page_size, n_kv_heads, head_dim;
+  int k_type, v_type, k_basis; /* BQ_TYPE_Q4_0 / BQ_TYPE_Q8_0; BQ_BASIS_* */
+} bq_paged_cache;
+
+/* Bytes of one page of one tensor (0 for sizes or types it cannot have). */
+size_t bq_paged_page_bytes(int type, int64_t page_size, int64_t n_kv_heads, int64_t head_dim);
+
+/* Element types of the rows a paged cache is written from and read into. */
+#define BQ_ELEM_F32 0
+#define BQ_ELEM_F16 1
+#define BQ_ELEM_BF16 2
+
+/* Write n_tokens token rows of K and V into the cache, token t at slots[t].
+ * K, V: [token][kv head][head_dim] of `elem`, token and head strides in
+ * elements (channels contiguous; rows 16-byte aligned). K rows are converted
+ * to fp32, rotated if the cache's basis is, minus `bias` (NULL or n_kv_heads x
+ * head_dim fp32, Q4_0 K only, calibrated in bias_basis == k_basis), then
+ * quantized; V rows are quantized. slots: n_tokens int64, DEVICE; -1 skips the
+ * token; no slot may occur twice. A slot outside the pool is skipped and
+ * reported by bq_device_status (BQ_ERR_INDEX). One launch.
+ * Errors: BQ_ERR_UNSUPPORTED (types, element type, basis, bias with a Q8_0 K),
+ * BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_BASIS, BQ_ERR_INVALID_ARG (null pointers,
+ * negative sizes, a pool overlapping an input). */
+int bq_paged_kv_write(const bq_paged_cache *cache, int elem, const void *K, int64_t k_token_stride,
+                      int64_t k_head_stride, const void *V, int64_t v_token_stride, int64_t v_head_stride,
+                      const float *bias, int bias_basis, const int64_t *slots, int64_t n_tokens);
+
+/* Read the token rows at slots[0 .. n_tokens) back: K and V, [token][kv
+ * head][head_dim] of `elem`, contiguous, 16-byte aligned. The values are scale
+ * * code in fp32; K's then plus `bias` (fp32) and out of the rotated basis
+ * (the same butterflies; H64 / 8 is its own inverse), and each is rounded once
+ * to `elem`. A slot of -1 gives rows of zeros, as does one outside the pool,
+ * which bq_device_status reports (BQ_ERR_INDEX). Errors as the write's. */
+int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, const float *bias, int bias_basis,
+                     const int64_t *slots, int64_t n_tokens);
+
+/* Attention of a batch of sequences over a paged cache that already holds
+ * their tokens. Sequence b has the query tokens q_start[b] .. q_start[b + 1] -
+ * 1 (q_len of them; none is allowed) and kv_len[b] cached tokens; its token j
+ * is row j % page_size of page page_table[b * max_pages + j / page_size].
+ * Query head h reads kv head h / (n_heads / n_kv_heads). With p_i = kv_len -
+ * q_len + i the place of query i,
+ *   s_ij = scale * q_i . k^_j   for the tokens it sees: j < kv_len; causal: j
+ *     <= p_i, and with window > 0 also j > p_i - window;
+ *   o_i = sum_j softmax_j(s_i) v^_j,   lse_i = log sum_j exp(s_ij).
+ * A query that sees no token (also kv_len 0, or p_i < 0) gets o = 0 and lse =
+ * -inf; rows of o and lse that belong to no sequence are not written. k^, v^:
+ * scale * code. In the rotated basis q is rotated in fp32. A mean-centred K
+ * needs nothing for o; its lse is that of the centred scores (lower by scale *
+ * q . bias).
+ * q, o: [token][head][head_dim] of `elem`, strides in elements as above; lse:
+ * NULL or n_q x n_heads fp32. q_start (n_seqs + 1), kv_len (n_seqs) and
+ * page_table (n_seqs x max_pages) are int32 on the DEVICE, so a captured
+ * launch follows them from step to step. max_q_len: the longest q_len (a
+ * longer one costs speed only); max_kv_len: an upper bound of kv_len.
+ * A kv_len above max_kv_len or max_pages * page_size is cut there, a page
+ * outside the pool counts as zero rows, and a q_start outside 0 .. n_q makes
+ * its sequence empty; bq_device_status reports each (BQ_ERR_INDEX).
+ * Accuracy: fp32 statistics and sums; q and weights in binary16 terms (fp32
+ * calls two each, 2^-22 together; 16-bit calls one: q exactly unless rotated,
+ * 2^-11 of a weight); weights below 2^-30 of the largest V scale vanish. The
+ * split of long sequences depends on the batch, and with it the order of sums:
+ * the same call gives the same bits, another batch may differ in the last.
+ * Limits: head_dim 64, 96, 128 or 256; n_heads a multiple of n_kv_heads. Needs
+ * a workspace of bq_paged_attn_workspace_size(...) bytes (bq_set_workspace).
+ * Errors: BQ_ERR_SHAPE, BQ_ERR_UNSUPPORTED (types, a window without causal),
+ * BQ_ERR_ALIGN, BQ_ERR_INVALID_ARG (null pointers, negative sizes, an output
+ * or the workspace overlapping another argument, rows of o overlapping),
+ * BQ_ERR_WORKSPACE. */
+int bq_paged_attn(const bq_paged_cache *cache, int elem, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                  void *o, int64_t o_token_stride, int64_t o_head_stride, float *lse, const int32_t *q_start,
+                  const int32_t *kv_len, const int32_t *page_table, int64_t max_pages, int64_t n_seqs, int64_t n_q,
+                  int64_t max_q_len, int64_t max_kv_len, int64_t n_heads, float scale, int causal, int64_t window);
+size_t bq_paged_attn_workspace_size(const bq_paged_cache *cache, int elem, int64_t n_seqs, int64_t n_q, int64_t max_q_len,
+                                    int64_t max_kv_len, int64_t n_heads, int causal, int64_t window);
+
+/* Page and place of a slot, by the code the kernels run (host only, nothing
+ * is launched): BQ_OK and (-1, -1) for the skipped slot -1, BQ_ERR_INDEX for a
+ * slot outside the pool. */
+int bq_paged_slot_check(const bq_paged_cache *cache, int64_t slot, int64_t *page, int64_t *place);
+
 /* Test export: out[m][b] = int32 dot of W block (m, b) (type Q4_0 or Q8_0)
  * with the Q8_0 block b of xq, computed by the same device code as bq_gemv's
  * inner loop. out: M x K/32 int32. */
@@ -353,8 +453,9 @@ int bq_block_bytes(int type);
 int bq_block_values(int type);
 
 /* Synchronize the calling thread's stream, then read and clear the device
- * error word: BQ_OK, BQ_ERR_TIMEOUT if a bounded wait ran out, BQ_ERR_CUDA if
- * the synchronization itself failed. */
+ * error word: BQ_OK, BQ_ERR_TIMEOUT if a bounded wait ran out, BQ_ERR_INDEX if
+ * a slot, page or length of a paged cache was out of range, BQ_ERR_CUDA if the
+ * synchronization itself failed. */
 int bq_device_status(void);
 
 /* Poll budget of the bounded waits inside kernels (each poll of an mbarrier
