@@ -345,6 +345,11 @@ def kv_bias(rows: torch.Tensor, basis: int = BASIS_PLAIN, out: torch.Tensor | No
 
 
 # ---- paged KV cache ----
+# A decode step makes these calls once per layer, so the host's share counts:
+# plain integers instead of ctypes objects, the device made current only where
+# it is not, checks on attributes that cost no call into the library.
+
+_BLOCK_BYTES = {Q4_0: 18, Q8_0: 34}
 
 
 @dataclasses.dataclass
@@ -373,49 +378,54 @@ class PagedCache:
 
     def _struct(self):
         k, v = self.k_pages, self.v_pages
-        for name, t, kind in (("k_pages", k, self.k_type), ("v_pages", v, self.v_type)):
+        ks, vs, n = k.shape, v.shape, self.page_size * self.head_dim
+        for name, t, shape, kind in (("k_pages", k, ks, self.k_type), ("v_pages", v, vs, self.v_type)):
             _cuda(t, name)
-            _same_device(k, t, name)
-            if t.dtype != torch.uint8 or t.dim() != 3:
+            if t.dtype is not torch.uint8 or len(shape) != 3:
                 raise TypeError(f"{name} must be uint8 (n_pages, n_kv_heads, bytes)")
-            if t.shape[2] * QK != self.page_size * self.head_dim * block_bytes(kind):
-                raise ValueError(f"{name} has {t.shape[2]} bytes per head page, not page_size * head_dim / 32 blocks")
-        if k.shape[:2] != v.shape[:2]:
-            raise ValueError("k_pages and v_pages must have the same pages and heads")
-        return _CacheStruct(k.data_ptr(), v.data_ptr(), k.shape[0], self.page_size, k.shape[1], self.head_dim,
-                            self.k_type, self.v_type, self.k_basis)
+            if kind in _BLOCK_BYTES and shape[2] * QK != n * _BLOCK_BYTES[kind]:
+                raise ValueError(f"{name} has {shape[2]} bytes per head page, not page_size * head_dim / 32 blocks")
+        if ks[:2] != vs[:2] or k.device != v.device:
+            raise ValueError("k_pages and v_pages must have the same pages, heads and device")
+        return _CacheStruct(k.data_ptr(), v.data_ptr(), ks[0], self.page_size, ks[1], self.head_dim, self.k_type,
+                            self.v_type, self.k_basis)
 
 
-def _same_device(ref, t, name):
-    if t.device != ref.device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {ref.device}")
-
-
-def _rows(cache, t, name, heads, dtype=None):
-    """A CUDA tensor (tokens, heads, head_dim) of an element type the paged
-    calls take, channels contiguous; other strides are free."""
+def _rows(t, name, device, heads, dim, dtype=None):
+    """A tensor (tokens, heads, head_dim) of an element type the paged calls
+    take, channels contiguous; other strides are free."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in ELEM or (dtype is not None and t.dtype != dtype):
+    if t.dtype not in ELEM or (dtype is not None and t.dtype is not dtype):
         raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}")
-    if t.dim() != 3 or t.shape[2] != cache.head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be (tokens, {heads if heads is not None else 'heads'}, {cache.head_dim})")
-    if t.stride(2) != 1:
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be (tokens, {heads if heads is not None else 'heads'}, {dim})")
+    strides = t.stride()
+    if strides[2] != 1:
         raise ValueError(f"the channels of {name} must be contiguous")
-    _same_device(cache.k_pages, t, name)
-    return t
+    return strides
 
 
-def _index(cache, t, name, dtype, shape):
+def _index(t, name, device, dtype, shape):
     _cuda(t, name)
-    _same_device(cache.k_pages, t, name)
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise TypeError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    return t
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+    return t.data_ptr()
 
 
-def _bias(cache, bias, heads):
-    return None if bias is None else _index(cache, bias, "bias", torch.float32, (heads, cache.head_dim))
+def _launch(device, call):
+    """call(library), with the device current and the library on its current torch stream."""
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _launch(device, call)
+    L = lib()
+    L.bq_set_stream(torch._C._cuda_getCurrentRawStream(device.index))
+    return call(L)
 
 
 def paged_kv_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
@@ -425,18 +435,17 @@ def paged_kv_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: t
     page_size + place; -1 skips a token). bias (n_kv_heads, head_dim) fp32:
     subtracted from K, calibrated in bias_basis (default: the cache's)."""
     s = cache._struct()
-    H = s.n_kv_heads
-    _rows(cache, k, "k", H)
-    _rows(cache, v, "v", H, k.dtype)
-    if v.shape != k.shape:
+    dev, H, D = cache.k_pages.device, s.n_kv_heads, cache.head_dim
+    ks = _rows(k, "k", dev, H, D)
+    vs = _rows(v, "v", dev, H, D, k.dtype)
+    T = k.shape[0]
+    if v.shape[0] != T:
         raise ValueError("k and v must have the same shape")
-    _index(cache, slots, "slots", torch.int64, k.shape[:1])
-    _bias(cache, bias, H)
-    with torch.cuda.device(k.device):
-        L = _prep(k.device)
-        _check(L.bq_paged_kv_write(s, ELEM[k.dtype], _ptr(k), k.stride(0), k.stride(1), _ptr(v), v.stride(0),
-                                   v.stride(1), _ptr(bias), cache.k_basis if bias_basis is None else bias_basis,
-                                   _ptr(slots), k.shape[0]), "bq_paged_kv_write")
+    at = _index(slots, "slots", dev, torch.int64, (T,))
+    b = None if bias is None else _index(bias, "bias", dev, torch.float32, (H, D))
+    _check(_launch(dev, lambda L: L.bq_paged_kv_write(
+        s, ELEM[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], b,
+        cache.k_basis if bias_basis is None else bias_basis, at, T)), "bq_paged_kv_write")
 
 
 def paged_kv_read(cache: PagedCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32,
@@ -446,22 +455,20 @@ def paged_kv_read(cache: PagedCache, slots: torch.Tensor, dtype: torch.dtype = t
     """The rows at slots (int64; -1: zeros) as (K, V), each (tokens,
     n_kv_heads, head_dim) of dtype; K out of the cache's basis, plus bias."""
     s = cache._struct()
-    H, T = s.n_kv_heads, slots.numel()
-    _index(cache, slots, "slots", torch.int64, (T,))
-    _bias(cache, bias, H)
+    dev, H, T = cache.k_pages.device, s.n_kv_heads, slots.numel()
+    shape = (T, H, cache.head_dim)
+    at = _index(slots, "slots", dev, torch.int64, (T,))
+    b = None if bias is None else _index(bias, "bias", dev, torch.float32, shape[1:])
     if dtype not in ELEM:
         raise TypeError("dtype must be float32, float16 or bfloat16")
-    outs = []
-    for name, t in (("out_k", out_k), ("out_v", out_v)):
-        if t is None:
-            t = torch.empty((T, H, cache.head_dim), dtype=dtype, device=slots.device)
-        outs.append(_index(cache, t, name, dtype, (T, H, cache.head_dim)))
-    with torch.cuda.device(slots.device):
-        L = _prep(slots.device)
-        _check(L.bq_paged_kv_read(s, ELEM[dtype], _ptr(outs[0]), _ptr(outs[1]), _ptr(bias),
-                                  cache.k_basis if bias_basis is None else bias_basis, _ptr(slots), T),
-               "bq_paged_kv_read")
-    return outs[0], outs[1]
+    if out_k is None:
+        out_k = torch.empty(shape, dtype=dtype, device=dev)
+    if out_v is None:
+        out_v = torch.empty(shape, dtype=dtype, device=dev)
+    kp, vp = _index(out_k, "out_k", dev, dtype, shape), _index(out_v, "out_v", dev, dtype, shape)
+    _check(_launch(dev, lambda L: L.bq_paged_kv_read(
+        s, ELEM[dtype], kp, vp, b, cache.k_basis if bias_basis is None else bias_basis, at, T)), "bq_paged_kv_read")
+    return out_k, out_v
 
 
 def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
@@ -474,33 +481,39 @@ def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len
     max_kv_len are their bounds on the host. window: tokens a causal query
     sees (0: all). lse: optional fp32 (tokens, n_heads), written."""
     s = cache._struct()
-    _rows(cache, q, "q", None)
-    n_q, H = q.shape[0], q.shape[1]
+    dev, D = cache.k_pages.device, cache.head_dim
+    qs = _rows(q, "q", dev, None, D)
+    n_q, H, _ = q.shape
     B = kv_len.numel()
-    _index(cache, kv_len, "kv_len", torch.int32, (B,))
-    _index(cache, q_start, "q_start", torch.int32, (B + 1,))
-    _index(cache, page_table, "page_table", torch.int32, (B, page_table.shape[-1]))
+    lens = _index(kv_len, "kv_len", dev, torch.int32, (B,))
+    starts = _index(q_start, "q_start", dev, torch.int32, (B + 1,))
+    pages = page_table.shape[-1]
+    table = _index(page_table, "page_table", dev, torch.int32, (B, pages))
     if out is None:
-        out = torch.empty((n_q, H, cache.head_dim), dtype=q.dtype, device=q.device)
-    _rows(cache, out, "out", H, q.dtype)
-    if out.shape != q.shape:
+        out = torch.empty((n_q, H, D), dtype=q.dtype, device=dev)
+    os = _rows(out, "out", dev, H, D, q.dtype)
+    if out.shape[0] != n_q:
         raise ValueError("out must have q's shape")
-    if lse is not None:
-        _index(cache, lse, "lse", torch.float32, (n_q, H))
+    lp = None if lse is None else _index(lse, "lse", dev, torch.float32, (n_q, H))
     e, c = ELEM[q.dtype], 1 if causal else 0
-    with torch.cuda.device(q.device):
-        L = _prep(q.device)
-        need = int(L.bq_paged_attn_workspace_size(s, e, B, n_q, max_q_len, max_kv_len, H, c, window))
+
+    def call(L):
+        need = L.bq_paged_attn_workspace_size(s, e, B, n_q, max_q_len, max_kv_len, H, c, window)
         # a workspace of this call's own, from the current stream's pool: calls
         # on other streams and captured launches never share it
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-        _check(L.bq_set_workspace(_ptr(ws), ws.numel()), "bq_set_workspace")
-        try:
-            _check(L.bq_paged_attn(s, e, _ptr(q), q.stride(0), q.stride(1), _ptr(out), out.stride(0), out.stride(1),
-                                   _ptr(lse), _ptr(q_start), _ptr(kv_len), _ptr(page_table), page_table.shape[1], B,
-                                   n_q, max_q_len, max_kv_len, H, float(scale), c, window), "bq_paged_attn")
-        finally:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        L.bq_set_workspace(ws.data_ptr(), ws.numel())
+        r = L.bq_paged_attn(s, e, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], lp, starts, lens, table,
+                            pages, B, n_q, max_q_len, max_kv_len, H, scale, c, window)
+        if r == 0:
             L.bq_set_workspace(None, 0)
+        return r
+
+    try:
+        _check(_launch(dev, call), "bq_paged_attn")
+    except Exception:
+        lib().bq_set_workspace(None, 0)
+        raise
     return out
 
 

@@ -47,6 +47,7 @@
 
 #include "bq_device.cuh"
 #include "bq_internal.h"
+#include "tcgen05.cuh"
 
 namespace bq {
 namespace {
@@ -73,7 +74,6 @@ constexpr int kEpiCols = kTN / (kEpiWarps / 4); // 32 columns per epilogue warp
 constexpr int kEpiChunks = kEpiCols / 32;       // 32-column tensor-memory loads per block
 constexpr int kConvWarps = 2;                   // 2 weight rows per thread
 constexpr int kTcThreads = (4 + kEpiWarps) * 32;
-constexpr uint32_t kDrainPolls = 1u << 22;
 
 constexpr int kOffA = 0;
 constexpr int kOffB = kOffA + kSubStages * kOpBytes;
@@ -97,71 +97,6 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 // bits 17-22, M >> 4 at bits 24-28.
 constexpr uint32_t kIdesc = (1u << 4) | (uint32_t(kTN >> 3) << 17) | (uint32_t(kTM >> 4) << 24);
 
-// Shared-memory matrix descriptor of a K-major operand in the 128-byte
-// swizzled layout: rows of 128 bytes, 8-row groups 1024 bytes apart (stride
-// byte offset), start address >> 4 in bits 0-13, descriptor version 1 at bit
-// 46, swizzle mode 2 (128 B) in bits 61-63. The leading byte offset is unused
-// by this layout and set to 1.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-         (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-
-// byte offset of 16-byte chunk c of row r in a 128-byte-swizzled operand tile
-__device__ __forceinline__ uint32_t sw128_off(int r, int c) {
-  return uint32_t((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-__device__ __forceinline__ void tc_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(kIdesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
-}
-
-// 32 consecutive columns of this warp's 32 lanes: thread i gets lane
-// (lane base + i), columns taddr.col .. + 31. The wait is in the same asm
-// statement so that no use of the registers can be scheduled before it.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
 // Shared-memory vector load kept in program order with the tensor-memory
 // loads around it (volatile), so that the compiler does not hoist a whole
 // block's worth of them and run out of registers.
@@ -180,39 +115,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, i
       "[%4];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
       : "memory");
-}
-
-// Bounded wait that also gives up once another thread of the CTA has given
-// up. Polls do not suspend in the barrier unit (whose wake-up came hundreds
-// of cycles after the phase completed); between polls the thread sleeps
-// briefly, so that waiting warps leave the issue slots to working ones. The
-// abort flag is read every 64 polls.
-__device__ __forceinline__ bool tc_wait(uint64_t *bar, uint32_t parity, uint32_t limit, volatile int *abort_flag,
-                                        unsigned *err) {
-  for (uint32_t i = 0; i < limit; ++i) {
-    if (mbar_test_wait(bar, parity)) return true;
-    __nanosleep(i < 64 ? 20 : 200);
-    if ((i & 63) == 63 && *abort_flag) return false;
-  }
-  *abort_flag = 1;
-  atomicOr(err, kErrTimeout);
-  return false;
-}
-// The same for a whole warp: lane 0 polls, the result is broadcast, and the
-// warp synchronizes (which orders the other lanes' later accesses after lane
-// 0's observation of the phase).
-__device__ __forceinline__ bool tc_wait_warp(uint64_t *bar, uint32_t parity, uint32_t limit, volatile int *abort_flag,
-                                             unsigned *err) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = tc_wait(bar, parity, limit, abort_flag, err);
-  ok = __shfl_sync(kFull, ok, 0);
-  __syncwarp();
-  return ok != 0;
-}
-// Wait for copies or MMAs already issued (they complete on their own).
-__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity) {
-  for (uint32_t i = 0; i < kDrainPolls; ++i)
-    if (mbar_try_wait(bar, parity)) return;
 }
 
 // One converter thread: rows r and r + 64 of operand stage k (0..3) of the
@@ -243,32 +145,6 @@ __device__ __forceinline__ void convert_stage(const uint8_t *raw, uint8_t *a, in
       *reinterpret_cast<uint4 *>(a + sw128_off(rr, cc)) = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
   }
-}
-
-// Issue a 32-column tensor-memory load without waiting for it.
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// Wait for this thread's tensor-memory loads; the registers of the last one
-// are operands so that no use of them can be scheduled before the wait.
-__device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
 }
 
 // part[2i], part[2i+1] += S[c] * (dw * dx[c]) for the 32 columns of one chunk
@@ -351,11 +227,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // slot (chunk last = the largest chunk < armed that used the slot)
     for (int i = 0; i < kRawStages && i < raw_armed; ++i) {
       const int last = raw_armed - 1 - ((raw_armed - 1 - i) % kRawStages);
-      drain(&bar[kRawFull + i], (last / kRawStages) & 1);
+      tc_drain(&bar[kRawFull + i], (last / kRawStages) & 1);
     }
     for (int i = 0; i < kScaleSlots && i < dx_armed; ++i) {
       const int last = dx_armed - 1 - ((dx_armed - 1 - i) % kScaleSlots);
-      drain(&bar[kDxFull + i], (last / kScaleSlots) & 1);
+      tc_drain(&bar[kDxFull + i], (last / kScaleSlots) & 1);
     }
   } else if (warp == 0 && lane == 1) {
     // ---- producer: activation operand tiles (1-D bulk, pre-swizzled) ----
@@ -369,7 +245,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < kSubStages && i < g; ++i) {
       const int last = g - 1 - ((g - 1 - i) % kSubStages);
-      drain(&bar[kBFull + i], (last / kSubStages) & 1);
+      tc_drain(&bar[kBFull + i], (last / kSubStages) & 1);
     }
   } else if (warp == 1 && lane == 0) {
     // ---- MMA issue (one lane) ----
@@ -385,13 +261,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint64_t ad = sw128_desc(a0 + as * kOpBytes) + uint64_t(j * 4);
       const uint64_t bd = sw128_desc(b0 + as * kOpBytes) + uint64_t(j * 4);
       const uint32_t d = tmem + uint32_t(sb * kTN);
-      tc_mma(d, ad, bd, 0);          // k 0..15 of the block
-      tc_mma(d, ad + 2, bd + 2, 1);  // k 16..31 (32 bytes further)
+      tc_mma(d, ad, bd, kIdesc, 0);          // k 0..15 of the block
+      tc_mma(d, ad + 2, bd + 2, kIdesc, 1);  // k 16..31 (32 bytes further)
       tc_commit(&bar[kTFull + sb]);
       if (j == 1) tc_commit(&bar[kSubEmpty + as]);
     }
     tc_commit(&bar[kDone]);
-    drain(&bar[kDone], 0);
+    tc_drain(&bar[kDone], 0);
   } else if (warp == 2 || warp == 3) {
     // ---- converters: raw Q8_0 blocks -> binary16 codes (swizzled) + fp32 scales ----
     const int r = (warp - 2) * 32 + lane;  // rows r and r + 64

@@ -13,23 +13,55 @@ constexpr int kMaxSms = 160;           // the workspace is sized without asking 
 constexpr int kMaxCtas = 2 * kMaxSms;  // pieces of the streaming kernel at most
 constexpr int kCombineThreads = 256;
 
-// Merges the partial results of one row of one split segment: block (i, r)
-// takes the segment that starts in piece i, if there is one, and its row r.
-// Bound by latency: at most a few megabytes of partials come out of L2. The
-// weights 2^(m_i - max) are made once per partial, then 256 threads read the
-// partials' rows as 16-byte vectors, D / 4 of them per row.
-__global__ void __launch_bounds__(kCombineThreads) k_paged_combine(const __grid_constant__ PagedAttnArgs a, int rows, int D) {
+// Merges partial results. Blocks below grid * rows take one row of one split
+// segment of the streaming kernel: block (i, r) the segment that starts in
+// piece i, if there is one, and its row r; 256 threads read several partials
+// at a time, D / 4 threads per row. The blocks after them take 1024 / D rows
+// each of the many-row kernel's items. Bound by latency: at most a few
+// megabytes come out of L2. The order of the sums is fixed.
+__global__ void __launch_bounds__(kCombineThreads)
+    k_paged_combine(const __grid_constant__ PagedAttnArgs a, int grid, int rows, int D, int n_split) {
   __shared__ float weight[kMaxCtas];
   __shared__ float red[kCombineThreads / 32][2];
   __shared__ float4 acc_s[kCombineThreads];
+  const int quads = D / 4, per = kCombineThreads / quads;
+  const int ch = int(threadIdx.x) % quads * 4, k = int(threadIdx.x) / quads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
-  const int4 mt = a.meta[blockIdx.x];
+  auto finish = [&](const SeqSpan &span, int kvh, int row, float4 acc, float top, float sum) {
+    const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint8_t *out = a.o + int64_t(span.q0 + tok) * a.o_token + int64_t(head) * a.o_head;
+    paged::store_out4(a.elem, out, ch, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (ch == 0 && a.lse)
+      a.lse[int64_t(span.q0 + tok) * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / paged::kLog2e;
+  };
+  if (int(blockIdx.x) >= grid * rows) {
+    const int blocks = (256 + per - 1) / per, i = int(blockIdx.x) - grid * rows, item = i / blocks, r = (i - item * blocks) * per + k;
+    const int4 mt = a.tc_meta[item];
+    if (mt.x < 0 || k >= per || r >= mt.w) return;
+    const int64_t p0 = int64_t(item) * n_split * 256 + r;
+    float top = -INFINITY, sum = 0.0f;
+    for (int s = 0; s < n_split; ++s) top = fmaxf(top, a.tc_part_ml[p0 + s * 256].x);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < n_split; ++s) {
+      const float2 ml = a.tc_part_ml[p0 + s * 256];
+      if (ml.y == 0.0f) continue;
+      const float w = paged::ex2(ml.x - top);
+      const float4 v = *reinterpret_cast<const float4 *>(a.tc_part_o + (p0 + s * 256) * D + ch);
+      sum = fmaf(ml.y, w, sum);
+      acc.x = fmaf(v.x, w, acc.x), acc.y = fmaf(v.y, w, acc.y), acc.z = fmaf(v.z, w, acc.z), acc.w = fmaf(v.w, w, acc.w);
+    }
+    finish(paged::load_span(a, mt.x, false), mt.y, mt.z + r, acc, top, sum);
+    return;
+  }
+  const int first = int(blockIdx.x) / rows, r = int(blockIdx.x) - first * rows;
+  const int4 mt = a.meta[first];
   if (mt.w < 0) return;
   const SeqSpan span = paged::load_span(a, mt.x, false);
-  const int row = mt.z * rows + int(blockIdx.y);
+  const int row = mt.z * rows + r;
   if (row >= span.q_len * a.group) return;
-  const int first = int(blockIdx.x), n = mt.w - first + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto part = [&](int i) { return (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * rows + int64_t(blockIdx.y); };
+  const int n = mt.w - first + 1;
+  auto part = [&](int i) { return (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * rows + r; };
   float top = -INFINITY;
   for (int i = threadIdx.x; i < n; i += kCombineThreads) top = fmaxf(top, a.part_ml[part(i)].x);
 #pragma unroll
@@ -52,9 +84,6 @@ __global__ void __launch_bounds__(kCombineThreads) k_paged_combine(const __grid_
   sum = 0.0f;
 #pragma unroll
   for (int w = 0; w < kCombineThreads / 32; ++w) sum += red[w][1];
-
-  const int quads = D / 4, per = kCombineThreads / quads;  // `per` partials at a time
-  const int ch = int(threadIdx.x) % quads * 4, k = int(threadIdx.x) / quads;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = k; i < n && k < per; i += per) {
     const float w = weight[i];
@@ -69,12 +98,7 @@ __global__ void __launch_bounds__(kCombineThreads) k_paged_combine(const __grid_
     const float4 v = acc_s[j * quads + threadIdx.x];
     acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
   }
-  const int tok = row / a.group, head = mt.y * a.group + (row - tok * a.group);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint8_t *out = a.o + int64_t(span.q0 + tok) * a.o_token + int64_t(head) * a.o_head;
-  paged::store_out4(a.elem, out, ch, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (threadIdx.x == 0 && a.lse)
-    a.lse[int64_t(span.q0 + tok) * a.n_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) / paged::kLog2e;
+  finish(span, mt.y, row, acc, top, sum);
 }
 
 StreamShape shape_of(int nb, int kt, int vt, int elem, int rows8) {
@@ -90,14 +114,30 @@ StreamShape shape_of(int nb, int kt, int vt, int elem, int rows8) {
 // CTA's start and the combine cost more than the tokens.
 constexpr int kMinTiles = 4;
 
-struct StreamPlan {
+// Sequences with more query rows per kv head than this go to the many-row
+// kernel (16-bit calls, head_dim 64 or 128): a pass of the streaming kernel
+// converts the cache for 16 rows, a step of the other for 256.
+constexpr int kTcRows = 64;
+constexpr int kFill = 152;           // CTAs (one per SM) that the many-row kernel's split aims at
+constexpr int kSplitTokens = 1024;   // tokens of a split at least
+
+struct Plan {
   StreamShape shape;
   int rows8, grid;
+  int64_t items;  // many-row kernel: (kv head, 256 rows) pairs at most; 0: not launched
+  int n_split;
+  size_t part_o, part_ml, meta, tc_o, tc_ml, tc_meta, bytes;  // workspace offsets
 };
 
-StreamPlan plan(const PagedAttnArgs &a, int max_q, int sm_count) {
-  StreamPlan p;
-  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(int64_t(a.group) * max_q, a.tc_rows));
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+Plan make_plan(PagedAttnArgs &a, int max_q, int sm_count) {
+  Plan p = {};
+  const int64_t most_rows = std::max<int64_t>(1, int64_t(a.group) * max_q), all_rows = int64_t(a.group) * a.n_q;
+  const int64_t items = (all_rows / 256 + std::min<int64_t>(a.n_seqs, all_rows / (kTcRows + 1))) * a.sh.n_kv;
+  const bool tc = a.elem != kElemF32 && (a.sh.nb == 2 || a.sh.nb == 4) && most_rows > kTcRows && items <= 0x7fffffff;
+  a.tc_rows = tc ? kTcRows : 0x7fffffff;
+  const int64_t rows = std::min<int64_t>(most_rows, a.tc_rows);
   p.rows8 = int(std::min<int64_t>((rows + 7) / 8, 1 << 20));
   p.shape = shape_of(a.sh.nb, a.kt, a.vt, a.elem, p.rows8);
   const int64_t seen = a.causal && a.window > 0 ? std::min<int64_t>(a.max_kv, int64_t(a.window) + max_q) : a.max_kv;
@@ -106,49 +146,69 @@ StreamPlan plan(const PagedAttnArgs &a, int max_q, int sm_count) {
   const double most = double(tiles) * double(groups) * a.sh.n_kv * a.n_seqs / kMinTiles;
   const int room = std::min(sm_count, kMaxSms) * p.shape.ctas_per_sm;
   p.grid = most >= room ? room : std::max(1, int(most) + 1);
+  p.n_split = 1;
+  if (tc) {
+    p.items = items;
+    if (p.items > 0 && p.items <= kFill / 2)
+      p.n_split = int(std::max<int64_t>(1, std::min<int64_t>(kFill / p.items, seen / kSplitTokens)));
+  }
+  const size_t D = size_t(a.sh.nb) * 32;
+  auto take = [&](size_t &at, size_t n) {
+    at = p.bytes;
+    p.bytes += up256(n);
+  };
+  // the streaming part is sized for the largest device, whatever this one is
+  const size_t srows = size_t(most >= kMaxSms * p.shape.ctas_per_sm ? kMaxSms * p.shape.ctas_per_sm : std::max(1, int(most) + 1)) * 2 * p.shape.rows;
+  take(p.part_o, srows * D * 4);
+  take(p.part_ml, srows * sizeof(float2));
+  take(p.meta, size_t(kMaxCtas) * sizeof(int4));
+  const size_t trows = p.n_split > 1 ? size_t(p.items) * size_t(p.n_split) * 256 : 0;
+  take(p.tc_o, trows * D * 4);
+  take(p.tc_ml, trows * sizeof(float2));
+  take(p.tc_meta, trows ? size_t(p.items) * sizeof(int4) : 0);
   return p;
 }
-
-size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 }  // namespace
 
 bool paged_attn_dim(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 256; }
 
-size_t paged_attn_workspace_bytes(const PagedAttnArgs &a, int max_q) {
-  const StreamPlan p = plan(a, max_q, kMaxSms);
-  const size_t rows = size_t(p.grid) * 2 * p.shape.rows;
-  return up256(rows * a.sh.nb * 32 * 4) + up256(rows * sizeof(float2)) + up256(size_t(p.grid) * sizeof(int4));
-}
+size_t paged_attn_workspace_bytes(PagedAttnArgs a, int max_q) { return make_plan(a, max_q, kMaxSms).bytes; }
 
 cudaError_t launch_paged_attn(PagedAttnArgs a, int max_q, void *ws, cudaStream_t stream) {
   cudaError_t err;
   const DeviceInfo *di = device_info(&err);
   if (!di) return err;
   a.err = di->err_word;
-  const StreamPlan p = plan(a, max_q, di->sm_count);
-  const size_t rows = size_t(p.grid) * 2 * p.shape.rows;
+  const Plan p = make_plan(a, max_q, di->sm_count);
   uint8_t *w = static_cast<uint8_t *>(ws);
-  a.part_o = reinterpret_cast<float *>(w);
-  a.part_ml = reinterpret_cast<float2 *>(w + up256(rows * a.sh.nb * 32 * 4));
-  a.meta = reinterpret_cast<int4 *>(w + up256(rows * a.sh.nb * 32 * 4) + up256(rows * sizeof(float2)));
+  a.part_o = reinterpret_cast<float *>(w + p.part_o);
+  a.part_ml = reinterpret_cast<float2 *>(w + p.part_ml);
+  a.meta = reinterpret_cast<int4 *>(w + p.meta);
+  a.tc_part_o = reinterpret_cast<float *>(w + p.tc_o);
+  a.tc_part_ml = reinterpret_cast<float2 *>(w + p.tc_ml);
+  a.tc_meta = reinterpret_cast<int4 *>(w + p.tc_meta);
+  const bool tc = p.items > 0;
+  if (tc && (err = paged::launch_tc(a, p.items, p.n_split, stream)) != cudaSuccess) return err;
   switch (a.sh.nb) {
-    case 2: err = paged::launch_stream<2>(a, p.rows8, p.grid, kMinTiles, stream); break;
-    case 3: err = paged::launch_stream<3>(a, p.rows8, p.grid, kMinTiles, stream); break;
-    case 4: err = paged::launch_stream<4>(a, p.rows8, p.grid, kMinTiles, stream); break;
-    default: err = paged::launch_stream<8>(a, p.rows8, p.grid, kMinTiles, stream); break;
+    case 2: err = paged::launch_stream<2>(a, p.rows8, p.grid, kMinTiles, tc, stream); break;
+    case 3: err = paged::launch_stream<3>(a, p.rows8, p.grid, kMinTiles, tc, stream); break;
+    case 4: err = paged::launch_stream<4>(a, p.rows8, p.grid, kMinTiles, tc, stream); break;
+    default: err = paged::launch_stream<8>(a, p.rows8, p.grid, kMinTiles, tc, stream); break;
   }
   if (err != cudaSuccess) return err;
+  const int D = a.sh.nb * 32, per = kCombineThreads / (D / 4);
+  const int64_t tc_blocks = p.n_split > 1 ? p.items * ((256 + per - 1) / per) : 0;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(p.grid), unsigned(std::min(p.shape.rows, p.rows8 * 8)));
+  cfg.gridDim = dim3(unsigned(p.grid * p.shape.rows + tc_blocks));
   cfg.blockDim = dim3(kCombineThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_paged_combine, a, p.shape.rows, a.sh.nb * 32);
+  return cudaLaunchKernelEx(&cfg, k_paged_combine, a, p.grid, p.shape.rows, D, p.n_split);
 }
 
 }  // namespace bq

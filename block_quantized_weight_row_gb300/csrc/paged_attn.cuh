@@ -292,7 +292,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
   const int64_t piece = max((total + gridDim.x - 1) / gridDim.x, int64_t(min_tiles));
   const int64_t t0 = min(piece * blockIdx.x, total), t1 = min(t0 + piece, total);
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, -1);
-  if (t0 >= t1) return;
+  if (t0 >= t1) {
+    pdl_wait();
+    return;
+  }
   if (before <= t0 && t0 < before + mine) {
     int64_t at = before;
     for (int b = b_first; b < b_last; ++b) {
@@ -751,16 +754,28 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
     at = stop;
     __syncthreads();  // the merge buffer becomes the rings again
   }
+  // launched beside the many-row kernel of the same call (they share no
+  // output): ends after it, so that what follows is ordered after both
+  pdl_wait();
 }
 
 // Each head dimension's instantiations are a translation unit of their own.
 template <int NB, int KT, int VT, int R, int TERMS>
-cudaError_t launch_stream_one(const PagedAttnArgs &a, int grid, int min_tiles, cudaStream_t stream) {
+cudaError_t launch_stream_one(const PagedAttnArgs &a, int grid, int min_tiles, bool beside, cudaStream_t stream) {
   using C = Cfg<NB, KT, VT, R>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_paged_stream<NB, KT, VT, R, TERMS>), C::kSmem);
   if (e != cudaSuccess) return e;
-  k_paged_stream<NB, KT, VT, R, TERMS><<<grid, kThreads, C::kSmem, stream>>>(a, min_tiles);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = beside ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_paged_stream<NB, KT, VT, R, TERMS>, a, min_tiles);
 }
 
 template <typename F>
@@ -789,13 +804,15 @@ constexpr bool two_groups(int elem, int rows8) {
     });                                                                                                            \
   }                                                                                                                \
   template <>                                                                                                      \
-  cudaError_t launch_stream<NB>(const PagedAttnArgs &a, int rows8, int grid, int min_tiles, cudaStream_t stream) { \
+  cudaError_t launch_stream<NB>(const PagedAttnArgs &a, int rows8, int grid, int min_tiles, bool beside,           \
+                                cudaStream_t stream) {                                                             \
     return by_cache_types(a.kt, a.vt, [&](auto k, auto v) {                                                        \
-      if (a.elem == kElemF32) return launch_stream_one<NB, k.value, v.value, 1, 2>(a, grid, min_tiles, stream);    \
+      if (a.elem == kElemF32)                                                                                      \
+        return launch_stream_one<NB, k.value, v.value, 1, 2>(a, grid, min_tiles, beside, stream);                  \
       if constexpr (NB <= 4) {                                                                                     \
-        if (rows8 > 1) return launch_stream_one<NB, k.value, v.value, 2, 1>(a, grid, min_tiles, stream);           \
+        if (rows8 > 1) return launch_stream_one<NB, k.value, v.value, 2, 1>(a, grid, min_tiles, beside, stream);   \
       }                                                                                                            \
-      return launch_stream_one<NB, k.value, v.value, 1, 1>(a, grid, min_tiles, stream);                            \
+      return launch_stream_one<NB, k.value, v.value, 1, 1>(a, grid, min_tiles, beside, stream);                    \
     });                                                                                                            \
   }
 

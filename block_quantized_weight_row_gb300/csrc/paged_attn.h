@@ -30,6 +30,10 @@ struct PagedAttnArgs {
   float *part_o;    // [cta][2][rows][D]
   float2 *part_ml;  // [cta][2][rows]: running maximum, sum of weights
   int4 *meta;       // [cta]: sequence, kv head, row group, last cta (or -1) of the split segment that starts there
+  // many-row kernel's partial results, when its rows' tokens are split
+  float *tc_part_o;    // [item][split][256][D]
+  float2 *tc_part_ml;  // [item][split][256]
+  int4 *tc_meta;       // [item]: sequence (or -1), kv head, first row, rows
 };
 
 // One sequence's lengths, checked: whatever the arrays hold, every row is in
@@ -67,8 +71,13 @@ struct StreamShape {
 };
 template <int NB>
 StreamShape stream_shape(int kt, int vt, int elem, int rows8);
+// beside: launched right after the many-row kernel of the same call
 template <int NB>
-cudaError_t launch_stream(const PagedAttnArgs &a, int rows8, int grid, int min_tiles, cudaStream_t stream);
+cudaError_t launch_stream(const PagedAttnArgs &a, int rows8, int grid, int min_tiles, bool beside, cudaStream_t stream);
+
+// The many-row kernel (paged_attn_tc.cu): `items` bounds the (kv head, 256
+// rows) pairs of the sequences with more than tc_rows rows.
+cudaError_t launch_tc(const PagedAttnArgs &a, int64_t items, int n_split, cudaStream_t stream);
 }  // namespace paged
 
 }  // namespace bq

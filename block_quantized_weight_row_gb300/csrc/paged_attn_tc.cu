@@ -1,0 +1,655 @@
+// paged_attn_tc.cu — attention of many query rows per kv head over a paged,
+// block-quantized KV cache (prompt chunks) on the fifth-generation tensor
+// cores: the many-row kernel, for bf16 and binary16 calls with 64 or 128
+// channels.
+//
+// Bound by the tensor pipe: 4 D flops per (row, token), one exponential and
+// ~3 further operations beside them; converting the cache's codes is shared by
+// the 256 rows of a CTA (about a fifth of the step's issue slots). A step is
+// 256 rows x 128 tokens:
+//   - S = Q K^T per 128-row tile (operands in shared memory, accumulator in
+//     tensor memory), softmax by one thread per row, P back into tensor memory
+//     over S as binary16, O += P V with P as the tensor-memory operand. The
+//     two row tiles alternate, so the tensor pipe works on one while the other
+//     is in its softmax.
+//   - K and V operands are made from the page bytes on the way into shared
+//     memory: k^ = d c as binary16, tokens x channels; V transposed, channels
+//     x tokens, so that both are plain K-major operands (128-byte swizzle).
+//     Channel orders inside the operands are those in which the code words
+//     fall apart (Q and the output rows use the same permutation). Rounding d
+//     c, q and the weights to binary16 costs 2^-11 each, an eighth of a bf16
+//     output's own rounding; scales enter relative to their tile's largest
+//     (brought to [2^5, 2^6) by a power of two, undone in fp32), so that
+//     neither large nor tiny scales leave binary16's range.
+//   - Maxima are raised only when passed by 2^8; weights are 2^(s - m + 6).
+// Warps: 0-3 and 4-7 softmax of row tiles A and B (and Q before, O after),
+// 8-11 K operand, 12-15 V operand, 16 tensor memory and MMA issue. Waits are
+// bounded as in the GEMM: one that runs out sets the error word, every role
+// leaves, MMAs in flight are waited for and the tensor memory is freed.
+// With few CTAs the tokens of a row tile are split over several, whose
+// partial results the combine merges.
+#include <cfloat>
+
+#include "paged_attn.cuh"
+#include "tcgen05.cuh"
+
+namespace bq {
+namespace paged {
+namespace {
+
+constexpr int kTcThreads = 17 * 32;
+constexpr int kTile = 128;  // tokens per step, rows per row tile
+constexpr int kHead = 6;    // weights carry 2^kHead
+constexpr int kSub = 128 * 128;  // bytes of an operand sub-tile: 128 rows x 64 binary16
+
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12, kQReady = 14, kKMax = 15, kVMax = 16, kAllDone = 17, kBars = 18 };
+
+template <int NB>
+struct TcCfg {
+  static constexpr int D = NB * 32, kSubs = D / 64;
+  static constexpr int kQBytes = kSubs * kSub;                // one row tile
+  static constexpr int kKBytes = kSubs * kSub;                // one K stage
+  static constexpr int kVSub = D * 128, kVBytes = 2 * kVSub;  // one V stage: two halves of 64 tokens
+  static constexpr int kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffBar = kOffV + 2 * kVBytes;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kSmem = kOffMisc + 256 + 1024;
+};
+
+struct Misc {
+  uint32_t tmem;
+  int abort_flag;
+  int kx[4], vx[4];  // exponents of the tiles' scale factors (tile & 3)
+  int kmax[2][4], vmax[2][4];
+  int64_t find[2];
+  int64_t scan[17];
+};
+static_assert(sizeof(Misc) <= 256 + 1024 - 1023, "shared layout");
+
+// D (tensor memory) (+)= A (tensor memory) * B (shared memory)
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// H64 x / 8 of 64 values of one thread, spans 1 .. 32 in order
+__device__ __forceinline__ void hadamard64_thread(float (&x)[64]) {
+#pragma unroll
+  for (int span = 1; span < 64; span <<= 1)
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if ((i & span) == 0) {
+        const float a = x[i], b = x[i + span];
+        x[i] = __fadd_rn(a, b);
+        x[i + span] = __fsub_rn(a, b);
+      }
+#pragma unroll
+  for (int i = 0; i < 64; ++i) x[i] *= 0.125f;
+}
+
+// 64 q values of a row from channel ch
+__device__ __forceinline__ void load_q64(int elem, const uint8_t *row, int ch, int rotate, float (&x)[64]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + ch * 2) + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = elem == kElemF16 ? unpack_pair<kElemF16>(w[k]) : unpack_pair<kElemBF16>(w[k]);
+      x[8 * i + 2 * k] = f.x;
+      x[8 * i + 2 * k + 1] = f.y;
+    }
+  }
+  if (rotate) hadamard64_thread(x);
+}
+
+// N bytes (a multiple of 4) from global memory
+template <int N>
+__device__ __forceinline__ void ldg_piece(const uint8_t *p, uint32_t (&w)[N / 4]) {
+  if constexpr (N % 16 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (N % 8 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 8; ++i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+      w[2 * i] = v.x, w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+  }
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Two 4-bit codes (bits 0-3 and 16-19 of w, or with `high` bits 4-7 and
+// 20-23) as binary16 u - 8, exactly: 1024 + u - 1032, (1024 + 16 u) / 16 - 72.
+__device__ __forceinline__ uint32_t codes4_lo(uint32_t w) { return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u); }
+__device__ __forceinline__ uint32_t codes4_hi(uint32_t w) { return hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u); }
+
+// binary16 exponent of the larger of two scales' magnitudes, at least 1
+__device__ __forceinline__ uint32_t max_exp(uint32_t m) { return max(max(m & 0x7fffu, (m >> 16) & 0x7fffu) >> 10, 1u); }
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
+
+template <int NB, int KT, int VT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    k_paged_tc(const __grid_constant__ PagedAttnArgs a, int n_split, uint32_t spin) {
+  using C = TcCfg<NB>;
+  constexpr int D = C::D;
+  constexpr bool K4 = KT == kTypeQ4_0, V4 = VT == kTypeQ4_0;
+  constexpr int RBK = NB * Codes<KT>::kBytes, RBV = NB * Codes<VT>::kBytes;
+  constexpr int UK = RBK / kUnitsK, UV = RBV / kUnitsV;
+  constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(kTile >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+  constexpr uint32_t kIdescO = (1u << 4) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+  extern __shared__ uint8_t smem_dyn[];
+  const uint32_t base = smem_u32(smem_dyn);
+  uint8_t *sm = smem_dyn + (((base + 1023u) & ~1023u) - base);
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::kOffBar);
+  Misc *mi = reinterpret_cast<Misc *>(sm + C::kOffMisc);
+  volatile int *abort_flag = &mi->abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch_dependents();  // the streaming kernel of the same call shares no output with this one
+
+  // ---- this CTA's item: sequence, kv head, 256 rows, share of the tokens ----
+  const int64_t item = blockIdx.x / n_split;
+  const int split = int(blockIdx.x - item * n_split);
+  const int per_thread = (a.n_seqs + kTcThreads - 1) / kTcThreads;
+  const int b_first = min(int(threadIdx.x) * per_thread, a.n_seqs), b_last = min(b_first + per_thread, a.n_seqs);
+  auto row_tiles = [&](const SeqSpan &s) {
+    const int n = s.q_len * a.group;
+    return n > a.tc_rows ? int64_t((n + 255) / 256) * a.sh.n_kv : int64_t(0);
+  };
+  int64_t mine = 0;
+  for (int b = b_first; b < b_last; ++b) mine += row_tiles(load_span(a, b, false));
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) mi->scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < 17; ++w) {
+    if (w < warp) before += mi->scan[w];
+    total += mi->scan[w];
+  }
+  if (item >= total) {
+    if (n_split > 1 && split == 0 && threadIdx.x == 0) a.tc_meta[item] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  if (before <= item && item < before + mine) {
+    int64_t at = before;
+    for (int b = b_first; b < b_last; ++b) {
+      const int64_t n = row_tiles(load_span(a, b, false));
+      if (item < at + n) {
+        mi->find[0] = b;
+        mi->find[1] = item - at;
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  const int seq = int(mi->find[0]);
+  const SeqSpan span = load_span(a, seq, false);
+  const int n_rows = span.q_len * a.group;
+  const int64_t in_seq = mi->find[1], tiles = (n_rows + 255) / 256;
+  const int kvh = int(in_seq % a.sh.n_kv);
+  const int row0 = int(tiles - 1 - in_seq / a.sh.n_kv) * 256;  // the longest rows first
+  const int rows = min(256, n_rows - row0), n_tiles_q = rows > 128 ? 2 : 1;
+  if (n_split > 1 && split == 0 && threadIdx.x == 0) a.tc_meta[item] = make_int4(seq, kvh, row0, rows);
+  int lo_any, hi_any, lo_all, hi_all;
+  seen_range(span, row0 / a.group, a.causal, a.window, lo_any, hi_all);
+  seen_range(span, (row0 + rows - 1) / a.group, a.causal, a.window, lo_all, hi_any);
+  const int first = lo_any / kTile, all = max(0, (hi_any + kTile - 1) / kTile - first);
+  const int j0 = first + int(int64_t(all) * split / n_split), n = first + int(int64_t(all) * (split + 1) / n_split) - j0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar[kKFull + i], 4);
+      mbar_init(&bar[kKEmpty + i], 1);
+      mbar_init(&bar[kVFull + i], 4);
+      mbar_init(&bar[kVEmpty + i], 1);
+      mbar_init(&bar[kSFull + i], 1);
+      mbar_init(&bar[kPReady + i], 4);
+      mbar_init(&bar[kODone + i], 1);
+    }
+    mbar_init(&bar[kQReady], 4 * n_tiles_q);
+    mbar_init(&bar[kKMax], 4);
+    mbar_init(&bar[kVMax], 4);
+    mbar_init(&bar[kAllDone], 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 16) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&mi->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = mi->tmem;
+  const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
+  // Page of 16 tokens from `tok`, -1 where nothing is to be read: past what
+  // any row sees, or a page outside the pool (reported)
+  auto page_of = [&](int tok) {
+    if (tok >= hi_any) return -1;
+    const int pi = a.sh.page_shift >= 0 ? tok >> a.sh.page_shift : tok / a.sh.page_size;
+    const int page = __ldg(table + pi);
+    if (uint32_t(page) < uint64_t(a.sh.n_pages)) return page;
+    atomicOr(a.err, kErrIndex);
+    return -1;
+  };
+  auto place_of = [&](int tok) {
+    return a.sh.page_shift >= 0 ? tok & (a.sh.page_size - 1) : tok % a.sh.page_size;
+  };
+
+  if (warp < 8) {
+    // ---- softmax: thread = row ----
+    const int t = warp >> 2, q4 = warp & 3, local = t * 128 + q4 * 32 + lane, row = row0 + local;
+    if (t < n_tiles_q) {
+      const bool live = local < rows;
+      const int tok = min(row, n_rows - 1) / a.group, head = kvh * a.group + (min(row, n_rows - 1) - tok * a.group);
+      int lo, hi;
+      seen_range(span, tok, a.causal, a.window, lo, hi);
+      float fq;  // score = fq * (kk's factor) * S
+      {
+        const uint8_t *p = a.q + int64_t(span.q0 + tok) * a.q_token + int64_t(head) * a.q_head;
+        float m = 0.0f, x[64];
+#pragma unroll 1
+        for (int h = 0; h < C::kSubs; ++h) {
+          load_q64(a.elem, p, 64 * h, a.rotate, x);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(x[i]));
+        }
+        // 2^k brings the row's largest value to [2^10, 2^11); the scale's sign goes into q
+        const int k = m > 0.0f ? min(10 + 127 - int(__float_as_uint(m) >> 23), 110) : 0;
+        const float up = live ? copysignf(pow2(k), a.scale_log2) : 0.0f;
+        fq = fabsf(a.scale_log2) * pow2(-k);
+        uint8_t *qs = sm + t * C::kQBytes;
+        const int r = q4 * 32 + lane;
+#pragma unroll 1
+        for (int h = 0; h < C::kSubs; ++h) {
+          load_q64(a.elem, p, 64 * h, a.rotate, x);
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] = live ? x[i] * up : 0.0f;
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {  // vector v: unit v & 3 of block v >> 2
+            const int b = (v >> 2) * 32, c = v & 3;
+            uint4 w;
+            if constexpr (K4) {
+              w.x = half2_bits(x[b + 4 * c], x[b + 4 * c + 2]);
+              w.y = half2_bits(x[b + 16 + 4 * c], x[b + 16 + 4 * c + 2]);
+              w.z = half2_bits(x[b + 4 * c + 1], x[b + 4 * c + 3]);
+              w.w = half2_bits(x[b + 16 + 4 * c + 1], x[b + 16 + 4 * c + 3]);
+            } else {
+              w.x = half2_bits(x[b + 8 * c], x[b + 8 * c + 1]);
+              w.y = half2_bits(x[b + 8 * c + 2], x[b + 8 * c + 3]);
+              w.z = half2_bits(x[b + 8 * c + 4], x[b + 8 * c + 5]);
+              w.w = half2_bits(x[b + 8 * c + 6], x[b + 8 * c + 7]);
+            }
+            *reinterpret_cast<uint4 *>(qs + h * kSub + sw128_off(r, v)) = w;
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kQReady]);
+      }
+      const uint32_t lanes = tmem + (uint32_t(q4 * 32) << 16);
+      const uint32_t s_col = lanes + uint32_t(t * 128), o_col = lanes + uint32_t(256 + t * 128);
+      float m = -FLT_MAX, l = 0.0f;
+      int k0 = 0;
+      bool ok = true;
+      for (int j = 0; j < n; ++j) {
+        if (!tc_wait_warp(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) ||
+            !tc_wait_warp(&bar[kSFull + t], j & 1, spin, abort_flag, a.err)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float f = fq * pow2(-mi->kx[j & 3]);
+        const int ve = mi->vx[j & 3];
+        if (j == 0) k0 = ve;
+        const int h = k0 - ve;  // this tile's V operand is 2^-h of the first one's unit
+        const int tile0 = (j0 + j) * kTile;
+        const bool full = tile0 >= lo_all && tile0 + kTile <= hi_all;
+        const int from = lo - tile0, to = hi - tile0;
+        uint32_t s[32];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(s_col + 32 * c, s);
+          if (full) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int col = 32 * c + i;
+              mx = fmaxf(mx, col >= from && col < to ? __uint_as_float(s[i]) : -INFINITY);
+            }
+          }
+        }
+        const float rm = mx * f + float(h);
+        const bool raise = rm > m + kRaise;
+        if (__any_sync(kFull, raise)) {
+          const float mn = raise ? rm : m, al = ex2(m - mn);
+          m = mn;
+          l *= al;
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < NB; ++c) {
+              uint32_t v[32];
+              tmem_ld32(o_col + 32 * c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * al);
+              tmem_st32(o_col + 32 * c, v);
+            }
+          }
+        }
+        const float c0 = float(kHead + h) - m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32(s_col + 32 * c, s);
+          uint32_t p[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float u = fmaf(__uint_as_float(s[2 * i]), f, c0), v = fmaf(__uint_as_float(s[2 * i + 1]), f, c0);
+            if (!full) {
+              const int col = 32 * c + 2 * i;
+              u = col >= from && col < to ? u : -INFINITY;
+              v = col + 1 >= from && col + 1 < to ? v : -INFINITY;
+            }
+            u = ex2(u);
+            v = ex2(v);
+            sum += u + v;
+            p[i] = half2_bits(u, v);
+          }
+          tmem_st16(s_col + 16 * c, p);
+        }
+        l = fmaf(sum, pow2(-h), l);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar[kPReady + t]);
+      }
+      // ---- output ----
+      if (ok && n > 0) ok = tc_wait_warp(&bar[kODone + t], 0, spin, abort_flag, a.err);
+      if (ok) {
+        tc_fence_after();
+        const bool part = n_split > 1;
+        const float scale = l == 0.0f ? 0.0f : part ? pow2(-k0 - kHead) : pow2(-k0) / l;
+        uint8_t *out = a.o + int64_t(span.q0 + tok) * a.o_token + int64_t(head) * a.o_head;
+        const int64_t pr = (item * n_split + split) * 256 + local;
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b) {
+          uint32_t v[32];
+          if (n > 0) {
+            tmem_ld32(o_col + 32 * b, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0;
+          }
+          float y[32];  // operand row 8 i + g of the block is channel i of unit g
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < 8; ++g)
+              y[V4 ? (i & 1) + 2 * g + 16 * (i >> 1) : 4 * g + i] = l == 0.0f ? 0.0f : __uint_as_float(v[8 * i + g]) * scale;
+          if (live) {
+            if (part) {
+              float *dst = a.tc_part_o + pr * D + b * 32;
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4 *>(dst)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                uint4 w;
+                if (a.elem == kElemF16) {
+                  w.x = pack_pair<kElemF16>(y[8 * i], y[8 * i + 1]), w.y = pack_pair<kElemF16>(y[8 * i + 2], y[8 * i + 3]);
+                  w.z = pack_pair<kElemF16>(y[8 * i + 4], y[8 * i + 5]), w.w = pack_pair<kElemF16>(y[8 * i + 6], y[8 * i + 7]);
+                } else {
+                  w.x = pack_pair<kElemBF16>(y[8 * i], y[8 * i + 1]), w.y = pack_pair<kElemBF16>(y[8 * i + 2], y[8 * i + 3]);
+                  w.z = pack_pair<kElemBF16>(y[8 * i + 4], y[8 * i + 5]), w.w = pack_pair<kElemBF16>(y[8 * i + 6], y[8 * i + 7]);
+                }
+                reinterpret_cast<uint4 *>(out + b * 64)[i] = w;
+              }
+            }
+          }
+        }
+        if (live) {
+          if (part)
+            a.tc_part_ml[pr] = make_float2(m, l * pow2(-kHead));
+          else if (a.lse)
+            a.lse[int64_t(span.q0 + tok) * a.n_heads + head] = l == 0.0f ? -INFINITY : (m - float(kHead) + log2f(l)) / kLog2e;
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp < 12) {
+    // ---- K operand: lane = (token of 8, unit), four groups of 8 tokens per thread ----
+    const int w = warp - 8, tk = lane & 7, c = lane >> 3;
+    uint32_t code[4][UK / 4], sc[4][NB / 2];
+    auto load = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
+        const int page = tok >= lo_any ? page_of(tok) : -1;
+#pragma unroll
+        for (int k = 0; k < UK / 4; ++k) code[i][k] = 0;
+#pragma unroll
+        for (int k = 0; k < NB / 2; ++k) sc[i][k] = 0;
+        if (page >= 0) {
+          const uint8_t *hp = a.kp.base + (int64_t(page) * a.sh.n_kv + kvh) * a.kp.head_bytes;
+          const int place = place_of(tok);
+          ldg_piece<UK>(hp + place * RBK + c * UK, code[i]);
+          ldg_piece<NB * 2>(hp + a.kp.scale_off + place * NB * 2, sc[i]);
+        }
+      }
+    };
+    if (n > 0) load(0);
+    for (int j = 0; j < n; ++j) {
+      uint32_t e = 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int k = 0; k < NB / 2; ++k) e = max(e, max_exp(sc[i][k]));
+      e = __reduce_max_sync(kFull, e);
+      if (lane == 0) {
+        mi->kmax[j & 1][w] = int(e);
+        mbar_arrive(&bar[kKMax]);
+      }
+      if (!tc_wait_warp(&bar[kKMax], j & 1, spin, abort_flag, a.err)) break;
+      const volatile int *km = mi->kmax[j & 1];
+      const int kk = 20 - max(max(km[0], km[1]), max(km[2], km[3]));
+      if (!tc_wait_warp(&bar[kKEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
+      if (w == 0 && lane == 0) mi->kx[j & 3] = kk;
+      const float up = pow2(kk);
+      uint8_t *ks = sm + C::kOffK + (j & 1) * C::kKBytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = w * 32 + i * 8 + tk;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float d = scale_of(sc[i], b) * up;
+          const uint32_t d2 = half2_bits(d, d);
+          uint4 v;
+          if constexpr (K4) {
+            const uint32_t x = code[i][b], y = x >> 8;
+            v = make_uint4(hmul2(codes4_lo(x), d2), hmul2(codes4_hi(x), d2), hmul2(codes4_lo(y), d2), hmul2(codes4_hi(y), d2));
+          } else {
+            const uint2 x = codes_to_f16x2(code[i][2 * b]), y = codes_to_f16x2(code[i][2 * b + 1]);
+            v = make_uint4(hmul2(x.x, d2), hmul2(x.y, d2), hmul2(y.x, d2), hmul2(y.y, d2));
+          }
+          *reinterpret_cast<uint4 *>(ks + (b >> 1) * kSub + sw128_off(r, (b & 1) * 4 + c)) = v;
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[kKFull + (j & 1)]);
+      if (j + 1 < n) load(j + 1);
+    }
+  } else if (warp < 16) {
+    // ---- V operand, transposed: thread = (8 tokens, unit g): 8 tokens of 4 channels per block ----
+    const int w = warp - 12, g = lane & 7, grp = w * 4 + (lane >> 3);
+    uint32_t code[8][(UV + 3) / 4], sc[8][NB / 2];
+    auto load = [&](int j) {
+      const int tok0 = (j0 + j) * kTile + grp * 8;
+      const int page = tok0 + 8 > lo_any ? page_of(tok0) : -1;
+      const uint8_t *hp = a.vp.base + (int64_t(max(page, 0)) * a.sh.n_kv + kvh) * a.vp.head_bytes;
+      const int place = place_of(tok0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int tok = tok0 + i;
+#pragma unroll
+        for (int k = 0; k < UV / 4; ++k) code[i][k] = 0;
+#pragma unroll
+        for (int k = 0; k < NB / 2; ++k) sc[i][k] = 0;
+        if (page >= 0 && tok >= lo_any && tok < hi_any) {
+          ldg_piece<UV>(hp + (place + i) * RBV + g * UV, code[i]);
+          ldg_piece<NB * 2>(hp + a.vp.scale_off + (place + i) * NB * 2, sc[i]);
+        }
+      }
+    };
+    if (n > 0) load(0);
+    for (int j = 0; j < n; ++j) {
+      uint32_t e = 1;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < NB / 2; ++k) e = max(e, max_exp(sc[i][k]));
+      e = __reduce_max_sync(kFull, e);
+      if (lane == 0) {
+        mi->vmax[j & 1][w] = int(e);
+        mbar_arrive(&bar[kVMax]);
+      }
+      if (!tc_wait_warp(&bar[kVMax], j & 1, spin, abort_flag, a.err)) break;
+      const volatile int *vm = mi->vmax[j & 1];
+      const int ve = 20 - max(max(vm[0], vm[1]), max(vm[2], vm[3]));
+      if (!tc_wait_warp(&bar[kVEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
+      if (w == 0 && lane == 0) mi->vx[j & 3] = ve;
+      const float up = pow2(ve);
+      uint8_t *vs = sm + C::kOffV + (j & 1) * C::kVBytes + (grp >> 3) * C::kVSub;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t o[4][4];  // [channel of the unit][token pair]
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t d2 = half2_bits(scale_of(sc[2 * k], b) * up, scale_of(sc[2 * k + 1], b) * up);
+          if constexpr (V4) {
+            const uint32_t x = __byte_perm(code[2 * k][b / 2], code[2 * k + 1][b / 2], (b & 1) ? 0x7632 : 0x5410), y = x >> 8;
+            o[0][k] = hmul2(codes4_lo(x), d2);  // channel 2g
+            o[1][k] = hmul2(codes4_lo(y), d2);  // 2g + 1
+            o[2][k] = hmul2(codes4_hi(x), d2);  // 16 + 2g
+            o[3][k] = hmul2(codes4_hi(y), d2);
+          } else {
+            const uint32_t w0 = code[2 * k][b], w1 = code[2 * k + 1][b];
+            const uint2 x = codes_to_f16x2(__byte_perm(w0, w1, 0x5140)), y = codes_to_f16x2(__byte_perm(w0, w1, 0x7362));
+            o[0][k] = hmul2(x.x, d2), o[1][k] = hmul2(x.y, d2), o[2][k] = hmul2(y.x, d2), o[3][k] = hmul2(y.y, d2);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4 *>(vs + sw128_off(b * 32 + 8 * i + g, grp & 7)) = make_uint4(o[i][0], o[i][1], o[i][2], o[i][3]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[kVFull + (j & 1)]);
+      if (j + 1 < n) load(j + 1);
+    }
+  } else if (lane == 0) {
+    // ---- MMA issue ----
+    const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + C::kOffK), va = smem_u32(sm + C::kOffV);
+    auto issue_s = [&](int t, int j) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t ad = sw128_desc(qa + t * C::kQBytes + (k >> 2) * kSub) + uint64_t((k & 3) * 2);
+        const uint64_t bd = sw128_desc(ka + (j & 1) * C::kKBytes + (k >> 2) * kSub) + uint64_t((k & 3) * 2);
+        tc_mma(tmem + uint32_t(t * 128), ad, bd, kIdescS, k > 0);
+      }
+      tc_commit(&bar[kSFull + t]);
+    };
+    bool ok = n > 0 && tc_wait(&bar[kQReady], 0, spin, abort_flag, a.err) && tc_wait(&bar[kKFull], 0, spin, abort_flag, a.err);
+    if (ok) {
+      tc_fence_after();
+      for (int t = 0; t < n_tiles_q; ++t) issue_s(t, 0);
+      tc_commit(&bar[kKEmpty]);
+    }
+    for (int j = 0; j < n && ok; ++j) {
+      const bool more = j + 1 < n;
+      ok = tc_wait(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) &&
+           (!more || tc_wait(&bar[kKFull + ((j + 1) & 1)], ((j + 1) >> 1) & 1, spin, abort_flag, a.err));
+      for (int t = 0; t < n_tiles_q && ok; ++t) {
+        if (!(ok = tc_wait(&bar[kPReady + t], j & 1, spin, abort_flag, a.err))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) {
+          const uint64_t bd = sw128_desc(va + (j & 1) * C::kVBytes + (k >> 2) * C::kVSub) + uint64_t((k & 3) * 2);
+          tc_mma_ts(tmem + uint32_t(256 + t * 128), tmem + uint32_t(t * 128 + k * 8), bd, kIdescO, j > 0 || k > 0);
+        }
+        if (t == n_tiles_q - 1) tc_commit(&bar[kVEmpty + (j & 1)]);
+        if (more) {
+          issue_s(t, j + 1);
+          if (t == n_tiles_q - 1) tc_commit(&bar[kKEmpty + ((j + 1) & 1)]);
+        } else {
+          tc_commit(&bar[kODone + t]);
+        }
+      }
+    }
+    tc_commit(&bar[kAllDone]);
+    tc_drain(&bar[kAllDone], 0);
+  }
+  __syncthreads();
+  if (warp == 16) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int NB, int KT, int VT>
+cudaError_t launch_one(const PagedAttnArgs &a, int64_t items, int n_split, cudaStream_t stream) {
+  cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_paged_tc<NB, KT, VT>), TcCfg<NB>::kSmem);
+  if (e != cudaSuccess) return e;
+  k_paged_tc<NB, KT, VT><<<unsigned(items * n_split), kTcThreads, TcCfg<NB>::kSmem, stream>>>(a, n_split, spin_limit());
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_tc(const PagedAttnArgs &a, int64_t items, int n_split, cudaStream_t stream) {
+  return by_cache_types(a.kt, a.vt, [&](auto k, auto v) {
+    return a.sh.nb == 4 ? launch_one<4, k.value, v.value>(a, items, n_split, stream)
+                        : launch_one<2, k.value, v.value>(a, items, n_split, stream);
+  });
+}
+
+}  // namespace paged
+}  // namespace bq

@@ -18,8 +18,11 @@ states. With u32 = 2^-24 and half a binary16 step u16 = 2^-11 (relative):
     min(w_j d_j, 2^-30 max d) |c_j| (binary32 weights vanish too, at 2^-149);
   sums: a warp's chain of products, then warps and pieces: (keys / 8 + 64) * 2 u32;
 so |o - o_ref| <= (2 ds + all of those) * sum_j w_j |v^_j| + the output type's
-half step of |o_ref|. The many-row kernel rounds k^, v^ and q to binary16 too:
-u16 * mag in the scores for each (|k^| for 16 d), u16 in the sum.
+half step of |o_ref|. The many-row kernel (16-bit calls with more than 64 query
+rows per kv head and 64 or 128 channels) rounds k^, v^ and q to binary16 too:
+u16 * mag in the scores for each (|k^| for 16 d), u16 in the sum, operands
+below 2^-25 of their unit 2^-30 max d; its products chain over all channels
+(D + 8 for 34 + blocks + 4) and its sums over all keys (keys for keys / 8).
 """
 import ctypes
 import itertools
@@ -452,8 +455,8 @@ class Batch:
                                window=window, lse=lse, **kw)
         return o, lse
 
-    def reference(self, causal=True, window=0, many_rows=()):
-        """o, lse and their tolerances, in 64 bits. many_rows: sequences that the many-row kernel takes."""
+    def reference(self, causal=True, window=0):
+        """o, lse and their tolerances, in 64 bits."""
         u16, u32 = 2.0**-11, 2.0**-24
         G, D = self.H // self.NKV, self.D
         n_q = self.q.shape[0]
@@ -468,7 +471,7 @@ class Batch:
             cv, sv = get_rows(self.pools[1], self.page, self.vt, D, 8, self.slots[b])
             dk = np.repeat(sk.astype(np.float64), 32, axis=-1)
             k, v = ck * dk, cv * np.repeat(sv.astype(np.float64), 32, axis=-1)
-            many = b in many_rows
+            many = self.elem != F32 and D in (64, 128) and n * G > 64
             wide = np.abs(k) if many or self.kt == Q8 else 16 * dk
             q = self.q[t0:t0 + n].double().numpy()
             if self.basis:
@@ -493,16 +496,20 @@ class Batch:
                 qerr = 3 * u16**2 * peak if two else u16 * mag if self.basis or many else 0.0 * mag
                 if self.basis:
                     qerr = qerr + 8 * u32 * peak  # the butterflies
-                ds = (34 + D // 32 + 4) * 2 * u32 * mag + qerr + (u16 * mag if many else 0.0) + 2 * u32 * np.abs(np.where(see, s, 0)).max(-1)
+                ds = (D + 8 if many else 34 + D // 32 + 4) * 2 * u32 * mag + qerr + 2 * u32 * np.abs(np.where(see, s, 0)).max(-1)
+                if many:
+                    ds = ds + u16 * mag + 2.0**-35 * peak + 2.0**-30 * dk[:, h // G].max() * np.abs(q[:, h]).sum(-1) * self.scale
                 top = np.where(any_, s.max(-1, initial=-np.inf), 0.0)
                 w = np.exp(s - top[:, None])
                 tot = w.sum(-1)
                 w = w / np.where(tot > 0, tot, 1)[:, None]
-                rel = 2 * ds + (u16**2 if two else u16) + (u16 if many else 0.0) + 6 * u32 + (kv / 8 + 64) * 2 * u32
+                rel = 2 * ds + (u16**2 if two else u16) + (u16 if many else 0.0) + 6 * u32 + ((kv if many else kv / 8) + 64) * 2 * u32
                 o[t0:t0 + n, h] = w @ vh
                 dv, cvh = sv[:, h // G].astype(np.float64), np.abs(cv[:, h // G]).astype(np.float64)
                 gone = np.concatenate([np.minimum(w * dv[None, :, x], 2.0**-30 * dv.max()) @ cvh[:, 32 * x:32 * x + 32]
                                        for x in range(D // 32)], axis=-1)
+                if many:
+                    gone = gone + 2.0**-30 * dv.max()
                 tol[t0:t0 + n, h] = rel[:, None] * (w @ np.abs(vh)) * 1.01 + half_step * np.abs(o[t0:t0 + n, h]) + gone
                 lse[t0:t0 + n, h] = np.where(any_, top + np.log(np.where(tot > 0, tot, 1)), -np.inf)
                 ltol[t0:t0 + n, h] = ds + (kv / 8 + 64) * 2 * u32 + 8 * u32 * (1 + np.abs(np.where(any_, lse[t0:t0 + n, h], 0)))
@@ -521,10 +528,10 @@ class Batch:
         assert (o[dead] == 0).all()
         assert (np.abs(lse[~dead] - rl[~dead]) <= lt[~dead]).all(), f"lse off by {np.max(np.abs(lse[~dead] - rl[~dead]) - lt[~dead])}"
 
-    def check(self, causal=True, window=0, many_rows=(), **kw):
+    def check(self, causal=True, window=0, **kw):
         o, lse = self.run(causal, window, **kw)
         assert self.bq.binding.device_status() == OK
-        self.compare(o, lse, self.reference(causal, window, many_rows))
+        self.compare(o, lse, self.reference(causal, window))
 
 
 DECODE = [
@@ -572,6 +579,35 @@ def test_attention_of_a_few_tokens(bq, case):
     Batch(bq, *args).check(causal, window)
 
 
+MANY = [
+    # q_len, kv_len, H, NKV, D, page, kt, vt, elem, basis, causal, window
+    ([65], [65], 1, 1, 128, 16, Q4, Q4, BF16, 0, True, 0),
+    ([200], [200], 4, 4, 64, 16, Q4, Q4, BF16, 0, True, 0),
+    ([70, 1, 0, 300], [500, 900, 10, 300], 8, 4, 128, 16, Q4, Q8, F16, 1, True, 0),
+    ([129, 40], [1000, 41], 6, 2, 128, 48, Q8, Q8, BF16, 0, False, 0),
+    ([513], [700], 4, 2, 64, 32, Q8, Q4, F16, 1, True, 0),
+    ([150, 90], [100, 0], 4, 2, 128, 16, Q4, Q4, BF16, 0, True, 0),     # rows before the first token, an empty cache
+    ([260], [2000], 3, 1, 128, 64, Q4, Q4, F16, 0, True, 130),           # a window that ends inside tiles
+    ([300], [5000], 4, 1, 64, 16, Q4, Q8, BF16, 0, True, 1),
+    ([100], [3500], 8, 8, 128, 128, Q4, Q4, BF16, 1, True, 0),           # tokens split over CTAs
+    ([700, 5, 333], [900, 800, 333], 16, 8, 128, 16, Q4, Q4, BF16, 0, True, 0),  # more CTAs than a split
+    ([96], [2300], 8, 1, 64, 32, Q8, Q8, F16, 0, False, 0),
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_attention_of_many_tokens(bq, case):
+    *args, causal, window = case
+    Batch(bq, *args).check(causal, window)
+
+
+@gpu
+@pytest.mark.parametrize("vscale,peaked", [(1e-4, 1.0), (3000.0, 1.0), (1.0, 30.0), (1.0, 1e-3)])
+def test_attention_of_many_tokens_scales(bq, vscale, peaked):
+    Batch(bq, [150], [400], 4, 2, 128, 16, Q4, Q4, F16, vscale=vscale, peaked=peaked).check()
+
+
 @gpu
 @pytest.mark.parametrize("elem", [F32, BF16])
 @pytest.mark.parametrize("vscale,peaked", [(1e-4, 1.0), (3000.0, 1.0), (1.0, 30.0), (1.0, 1e-3)])
@@ -581,10 +617,11 @@ def test_attention_scales_of_v_and_q(bq, elem, vscale, peaked):
 
 
 @gpu
-def test_attention_v_scales_that_grow_along_the_cache(bq):
+@pytest.mark.parametrize("n,elem", [(1, F32), (90, BF16)])
+def test_attention_v_scales_that_grow_along_the_cache(bq, n, elem):
     """The weights' common power of two has to follow: scales from 2^-14 to 2^12 in order, and back."""
     for flip in (False, True):
-        b = Batch(bq, [1], [1024], 8, 4, 128, 16, Q4, Q4, F32, seed=3)
+        b = Batch(bq, [n], [1024], 8, 4, 128, 16, Q4, Q4, elem, seed=3)
         nb, page = 4, 16
         d = np.exp2(np.linspace(-14, 12, 1024)).astype(np.float16)
         for j, slot in enumerate(b.slots[0]):
@@ -611,8 +648,9 @@ def test_attention_strides_and_given_outputs(bq):
 
 
 @gpu
-def test_attention_is_the_same_every_time_and_on_any_stream(bq):
-    b = Batch(bq, [1] * 9, [3000, 20, 1, 700, 2222, 64, 65, 1500, 4097], 16, 4, 128, 16, Q4, Q4, BF16)
+@pytest.mark.parametrize("many", [1, 80])
+def test_attention_is_the_same_every_time_and_on_any_stream(bq, many):
+    b = Batch(bq, [1] * 8 + [many], [3000, 20, 1, 700, 2222, 64, 65, 1500, 4097], 16, 4, 128, 16, Q4, Q4, BF16)
     first = b.run()
     q = b.q.cuda()
     torch.cuda.synchronize()
@@ -717,3 +755,18 @@ def test_nan_and_infinite_queries_stay_in_their_rows(bq):
     for t, h in itertools.product(range(3), range(4)):
         if (t, h) not in ((1, 2), (0, 1)):
             assert torch.equal(o[t, h], good[t, h])
+
+
+@gpu
+def test_many_row_timeout_path_returns_error(bq):
+    """A bounded wait that runs out ends the launch with a status, and the next call is right."""
+    b = Batch(bq, [150], [400], 4, 2, 128, 16, Q4, Q4, BF16)
+    L = bq.lib()
+    q = b.q.cuda()
+    try:
+        assert L.bq_set_spin_limit(0) == OK
+        b.run(q=q)
+        assert bq.binding.device_status() == -6
+    finally:
+        L.bq_set_spin_limit(-1)
+    b.check()
