@@ -18,12 +18,13 @@
 //     Channel orders inside the operands are those in which the code words
 //     fall apart (Q and the output rows use the same permutation). Rounding d
 //     c, q and the weights to binary16 costs 2^-11 each, an eighth of a bf16
-//     output's own rounding; scales enter relative to their tile's largest
-//     (brought to [2^5, 2^6) by a power of two, undone in fp32), so that
+//     output's own rounding; scales enter relative to the largest of 32
+//     tokens (brought to [2^5, 2^6) by a power of two, undone in fp32), so that
 //     neither large nor tiny scales leave binary16's range.
 //   - Maxima are raised only when passed by 2^8; weights are 2^(s - m + 6).
 // Warps: 0-3 and 4-7 softmax of row tiles A and B (and Q before, O after),
-// 8-11 K operand, 12-15 V operand, 16 tensor memory and MMA issue. Waits are
+// 8-11 K operand, 12-15 V operand, 16 tensor memory and MMA issue, 17-19 none
+// (they complete a warpgroup whose registers go to the softmax). Waits are
 // bounded as in the GEMM: one that runs out sets the error word, every role
 // leaves, MMAs in flight are waited for and the tensor memory is freed.
 // With few CTAs the tokens of a row tile are split over several, whose
@@ -37,12 +38,21 @@ namespace bq {
 namespace paged {
 namespace {
 
-constexpr int kTcThreads = 17 * 32;
+constexpr int kTcWarps = 20;
+constexpr int kTcThreads = kTcWarps * 32;
 constexpr int kTile = 128;  // tokens per step, rows per row tile
 constexpr int kHead = 6;    // weights carry 2^kHead
 constexpr int kSub = 128 * 128;  // bytes of an operand sub-tile: 128 rows x 64 binary16
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12, kQReady = 14, kKMax = 15, kVMax = 16, kAllDone = 17, kBars = 18 };
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12, kQReady = 14, kAllDone = 15, kVExp = 16, kBars = 20 };
+
+struct Misc {
+  uint32_t tmem;
+  int abort_flag;
+  int kx[4][4], vx[4][4];  // [tile & 3][32 tokens]: their operand holds d c 2^x
+  int64_t find[2];
+  int64_t scan[kTcWarps];
+};
 
 template <int NB>
 struct TcCfg {
@@ -52,18 +62,8 @@ struct TcCfg {
   static constexpr int kVSub = D * 128, kVBytes = 2 * kVSub;  // one V stage: two halves of 64 tokens
   static constexpr int kOffK = 2 * kQBytes, kOffV = kOffK + 2 * kKBytes, kOffBar = kOffV + 2 * kVBytes;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
-  static constexpr int kSmem = kOffMisc + 256 + 1024;
+  static constexpr int kSmem = kOffMisc + int(sizeof(Misc)) + 1024;  // + slack to align the base to 1024
 };
-
-struct Misc {
-  uint32_t tmem;
-  int abort_flag;
-  int kx[4], vx[4];  // exponents of the tiles' scale factors (tile & 3)
-  int kmax[2][4], vmax[2][4];
-  int64_t find[2];
-  int64_t scan[17];
-};
-static_assert(sizeof(Misc) <= 256 + 1024 - 1023, "shared layout");
 
 // D (tensor memory) (+)= A (tensor memory) * B (shared memory)
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -155,6 +155,17 @@ __device__ __forceinline__ uint32_t max_exp(uint32_t m) { return max(max(m & 0x7
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
+// Registers per thread: 96 at launch (20 warps); the shares add up to 20 * 96
+// or less: 8 * 128 + 8 * 88 + 4 * 40 = 1888 of 1920.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int NB, int KT, int VT>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_paged_tc(const __grid_constant__ PagedAttnArgs a, int n_split, uint32_t spin) {
@@ -194,7 +205,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (lane == 31) mi->scan[warp] = incl;
   __syncthreads();
   int64_t before = incl - mine, total = 0;
-  for (int w = 0; w < 17; ++w) {
+  for (int w = 0; w < kTcWarps; ++w) {
     if (w < warp) before += mi->scan[w];
     total += mi->scan[w];
   }
@@ -240,8 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&bar[kODone + i], 1);
     }
     mbar_init(&bar[kQReady], 4 * n_tiles_q);
-    mbar_init(&bar[kKMax], 4);
-    mbar_init(&bar[kVMax], 4);
+    for (int i = 0; i < 4; ++i) mbar_init(&bar[kVExp + i], 4);
     mbar_init(&bar[kAllDone], 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -255,15 +265,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
   const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
-  // Page of 16 tokens from `tok`, -1 where nothing is to be read: past what
-  // any row sees, or a page outside the pool (reported)
+  // Entry of the page table for token `tok`, 0 past what any row sees. It is
+  // looked at (and an entry outside the pool reported) a tile later, so that
+  // nothing waits for it here.
   auto page_of = [&](int tok) {
-    if (tok >= hi_any) return -1;
-    const int pi = a.sh.page_shift >= 0 ? tok >> a.sh.page_shift : tok / a.sh.page_size;
-    const int page = __ldg(table + pi);
-    if (uint32_t(page) < uint64_t(a.sh.n_pages)) return page;
+    return tok < hi_any ? __ldg(table + (a.sh.page_shift >= 0 ? tok >> a.sh.page_shift : tok / a.sh.page_size)) : 0;
+  };
+  auto page_ok = [&](int page) {
+    if (uint32_t(page) < uint64_t(a.sh.n_pages)) return true;
     atomicOr(a.err, kErrIndex);
-    return -1;
+    return false;
   };
   auto place_of = [&](int tok) {
     return a.sh.page_shift >= 0 ? tok & (a.sh.page_size - 1) : tok % a.sh.page_size;
@@ -271,6 +282,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 8) {
     // ---- softmax: thread = row ----
+    regs_up<128>();
     const int t = warp >> 2, q4 = warp & 3, local = t * 128 + q4 * 32 + lane, row = row0 + local;
     if (t < n_tiles_q) {
       const bool live = local < rows;
@@ -326,36 +338,44 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int k0 = 0;
       bool ok = true;
       for (int j = 0; j < n; ++j) {
-        if (!tc_wait_warp(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) ||
+        if (!tc_wait_warp(&bar[kVExp + (j & 3)], (j >> 2) & 1, spin, abort_flag, a.err) ||
             !tc_wait_warp(&bar[kSFull + t], j & 1, spin, abort_flag, a.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float f = fq * pow2(-mi->kx[j & 3]);
-        const int ve = mi->vx[j & 3];
-        if (j == 0) k0 = ve;
-        const int h = k0 - ve;  // this tile's V operand is 2^-h of the first one's unit
+        // per 32 tokens: score = f S, and the V operand is in 2^-h of the first one's unit
+        float f[4];
+        int h[4];
+        const volatile int *kx = mi->kx[j & 3], *vx = mi->vx[j & 3];
+        if (j == 0) k0 = vx[0];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f[c] = fq * pow2(-kx[c]);
+          h[c] = k0 - vx[c];
+        }
         const int tile0 = (j0 + j) * kTile;
         const bool full = tile0 >= lo_all && tile0 + kTile <= hi_all;
         const int from = lo - tile0, to = hi - tile0;
         uint32_t s[32];
-        float mx = -INFINITY;
+        float rm = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tmem_ld32(s_col + 32 * c, s);
-          if (full) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(s[i]));
-          } else {
+          if (!full) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
               const int col = 32 * c + i;
-              mx = fmaxf(mx, col >= from && col < to ? __uint_as_float(s[i]) : -INFINITY);
+              s[i] = col >= from && col < to ? s[i] : 0xff800000u;  // -infinity
             }
           }
+          float m4[4];  // four chains
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(s[i]);
+#pragma unroll
+          for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(s[i]));
+          rm = fmaxf(rm, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f[c], float(h[c])));
         }
-        const float rm = mx * f + float(h);
         const bool raise = rm > m + kRaise;
         if (__any_sync(kFull, raise)) {
           const float mn = raise ? rm : m, al = ex2(m - mn);
@@ -372,28 +392,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         }
-        const float c0 = float(kHead + h) - m;
-        float sum = 0.0f;
+        // straight-line code per 32 columns (a mask test per value would cut it
+        // into dependent pieces: 4600 cycles a tile instead of ~1000)
+        auto weigh = [&](auto masked) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(s_col + 32 * c, s);
-          uint32_t p[16];
+          for (int c = 0; c < 4; ++c) {
+            const float c0 = float(kHead + h[c]) - m;
+            const uint64_t f2 = pack2(__float_as_uint(f[c]), __float_as_uint(f[c])), c2 = pack2(__float_as_uint(c0), __float_as_uint(c0));
+            uint64_t sum2[2] = {0, 0};
+            tmem_ld32(s_col + 32 * c, s);
+            uint32_t p[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float u = fmaf(__uint_as_float(s[2 * i]), f, c0), v = fmaf(__uint_as_float(s[2 * i + 1]), f, c0);
-            if (!full) {
-              const int col = 32 * c + 2 * i;
-              u = col >= from && col < to ? u : -INFINITY;
-              v = col + 1 >= from && col + 1 < to ? v : -INFINITY;
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t x = ffma2(pack2(s[2 * i], s[2 * i + 1]), f2, c2);
+              float u = __uint_as_float(uint32_t(x)), v = __uint_as_float(uint32_t(x >> 32));
+              if constexpr (decltype(masked)::value) {
+                const int col = 32 * c + 2 * i;
+                u = col >= from && col < to ? u : -INFINITY;
+                v = col + 1 >= from && col + 1 < to ? v : -INFINITY;
+              }
+              u = ex2(u);
+              v = ex2(v);
+              sum2[i & 1] = fadd2(sum2[i & 1], pack2(__float_as_uint(u), __float_as_uint(v)));
+              p[i] = half2_bits(u, v);
             }
-            u = ex2(u);
-            v = ex2(v);
-            sum += u + v;
-            p[i] = half2_bits(u, v);
+            tmem_st16(s_col + 16 * c, p);
+            const uint64_t both = fadd2(sum2[0], sum2[1]);
+            l = fmaf(__uint_as_float(uint32_t(both)) + __uint_as_float(uint32_t(both >> 32)), pow2(-h[c]), l);
           }
-          tmem_st16(s_col + 16 * c, p);
-        }
-        l = fmaf(sum, pow2(-h), l);
+        };
+        if (full)
+          weigh(std::false_type());
+        else
+          weigh(std::true_type());
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -454,26 +485,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc_fence_before();
     }
   } else if (warp < 12) {
+    regs_down<88>();
     // ---- K operand: lane = (token of 8, unit), four groups of 8 tokens per thread ----
     const int w = warp - 8, tk = lane & 7, c = lane >> 3;
     uint32_t code[4][UK / 4], sc[4][NB / 2];
+    int next[4];  // pages of the next tile to load, asked for a tile ahead
+    auto pages = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
+        next[i] = j < n ? page_of(tok) : 0;
+      }
+    };
     auto load = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
-        const int page = tok >= lo_any ? page_of(tok) : -1;
+        const int page = next[i];
 #pragma unroll
         for (int k = 0; k < UK / 4; ++k) code[i][k] = 0;
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) sc[i][k] = 0;
-        if (page >= 0) {
+        if (tok >= lo_any && tok < hi_any && page_ok(page)) {
           const uint8_t *hp = a.kp.base + (int64_t(page) * a.sh.n_kv + kvh) * a.kp.head_bytes;
           const int place = place_of(tok);
           ldg_piece<UK>(hp + place * RBK + c * UK, code[i]);
           ldg_piece<NB * 2>(hp + a.kp.scale_off + place * NB * 2, sc[i]);
         }
       }
+      pages(j + 1);
     };
+    pages(0);
     if (n > 0) load(0);
     for (int j = 0; j < n; ++j) {
       uint32_t e = 1;
@@ -481,16 +523,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) e = max(e, max_exp(sc[i][k]));
-      e = __reduce_max_sync(kFull, e);
-      if (lane == 0) {
-        mi->kmax[j & 1][w] = int(e);
-        mbar_arrive(&bar[kKMax]);
-      }
-      if (!tc_wait_warp(&bar[kKMax], j & 1, spin, abort_flag, a.err)) break;
-      const volatile int *km = mi->kmax[j & 1];
-      const int kk = 20 - max(max(km[0], km[1]), max(km[2], km[3]));
+      const int kk = 20 - int(__reduce_max_sync(kFull, e));
       if (!tc_wait_warp(&bar[kKEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
-      if (w == 0 && lane == 0) mi->kx[j & 3] = kk;
+      if (lane == 0) mi->kx[j & 3][w] = kk;
       const float up = pow2(kk);
       uint8_t *ks = sm + C::kOffK + (j & 1) * C::kKBytes;
 #pragma unroll
@@ -517,13 +552,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (j + 1 < n) load(j + 1);
     }
   } else if (warp < 16) {
+    regs_down<88>();
     // ---- V operand, transposed: thread = (8 tokens, unit g): 8 tokens of 4 channels per block ----
     const int w = warp - 12, g = lane & 7, grp = w * 4 + (lane >> 3);
     uint32_t code[8][(UV + 3) / 4], sc[8][NB / 2];
+    int next = 0;  // page of the next tile to load
+    auto pages = [&](int j) {
+      const int tok0 = (j0 + j) * kTile + grp * 8;
+      next = j < n ? page_of(tok0) : 0;
+    };
     auto load = [&](int j) {
       const int tok0 = (j0 + j) * kTile + grp * 8;
-      const int page = tok0 + 8 > lo_any ? page_of(tok0) : -1;
-      const uint8_t *hp = a.vp.base + (int64_t(max(page, 0)) * a.sh.n_kv + kvh) * a.vp.head_bytes;
+      const bool some = tok0 < hi_any && tok0 + 8 > lo_any && page_ok(next);
+      const uint8_t *hp = a.vp.base + (int64_t(some ? next : 0) * a.sh.n_kv + kvh) * a.vp.head_bytes;
       const int place = place_of(tok0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -532,12 +573,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int k = 0; k < UV / 4; ++k) code[i][k] = 0;
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) sc[i][k] = 0;
-        if (page >= 0 && tok >= lo_any && tok < hi_any) {
+        if (some && tok >= lo_any && tok < hi_any) {
           ldg_piece<UV>(hp + (place + i) * RBV + g * UV, code[i]);
           ldg_piece<NB * 2>(hp + a.vp.scale_off + (place + i) * NB * 2, sc[i]);
         }
       }
+      pages(j + 1);
     };
+    pages(0);
     if (n > 0) load(0);
     for (int j = 0; j < n; ++j) {
       uint32_t e = 1;
@@ -545,16 +588,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) e = max(e, max_exp(sc[i][k]));
-      e = __reduce_max_sync(kFull, e);
+      const int ve = 20 - int(__reduce_max_sync(kFull, e));
       if (lane == 0) {
-        mi->vmax[j & 1][w] = int(e);
-        mbar_arrive(&bar[kVMax]);
+        mi->vx[j & 3][w] = ve;
+        mbar_arrive(&bar[kVExp + (j & 3)]);
       }
-      if (!tc_wait_warp(&bar[kVMax], j & 1, spin, abort_flag, a.err)) break;
-      const volatile int *vm = mi->vmax[j & 1];
-      const int ve = 20 - max(max(vm[0], vm[1]), max(vm[2], vm[3]));
       if (!tc_wait_warp(&bar[kVEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
-      if (w == 0 && lane == 0) mi->vx[j & 3] = ve;
       const float up = pow2(ve);
       uint8_t *vs = sm + C::kOffV + (j & 1) * C::kVBytes + (grp >> 3) * C::kVSub;
 #pragma unroll
@@ -584,7 +623,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (lane == 0) mbar_arrive(&bar[kVFull + (j & 1)]);
       if (j + 1 < n) load(j + 1);
     }
-  } else if (lane == 0) {
+  } else {
+    regs_down<40>();
+    if (warp == 16 && lane == 0) {
     // ---- MMA issue ----
     const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + C::kOffK), va = smem_u32(sm + C::kOffV);
     auto issue_s = [&](int t, int j) {
@@ -625,6 +666,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc_commit(&bar[kAllDone]);
     tc_drain(&bar[kAllDone], 0);
+    }
   }
   __syncthreads();
   if (warp == 16) {
