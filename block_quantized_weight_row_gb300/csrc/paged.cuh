@@ -41,12 +41,22 @@ struct PagedPool {
 struct PagedShape {
   int64_t n_pages;
   int page_size, page_shift;  // shift: log2(page_size), or -1
+  uint64_t page_magic;        // ceil(2^64 / (page_size / 16)), for page sizes that are no power of two
   int n_kv, nb;               // kv heads, blocks of 32 channels per head
 };
 
 __host__ __device__ __forceinline__ void split_slot(const PagedShape &s, uint32_t slot, uint32_t &page, uint32_t &place) {
   page = s.page_shift >= 0 ? slot >> s.page_shift : slot / uint32_t(s.page_size);
   place = slot - page * uint32_t(s.page_size);
+}
+
+// Page number of a sequence's token, without a branch (one would make loads
+// in flight wait where it ends). token < 2^31: token / 16 < 2^27 and
+// page_size / 16 <= 2^16, so the product with the rounded-up reciprocal errs
+// by less than 2^43 / 2^64 and the quotient is exact.
+__device__ __forceinline__ int token_page(const PagedShape &s, int token) {
+  const int by_shift = token >> (s.page_shift & 31), by_magic = int(__umul64hi(uint64_t(token >> 4), s.page_magic));
+  return s.page_shift >= 0 ? by_shift : by_magic;
 }
 
 // A slot of the caller: a row of the pool, skipped (-1), or neither. Slots

@@ -61,7 +61,8 @@ int check_cache(const bq_paged_cache *c, const char *who, Cache &out) {
   int shift = -1;
   if ((c->page_size & (c->page_size - 1)) == 0)
     for (shift = 0; (int64_t(1) << shift) < c->page_size;) ++shift;
-  out.sh = PagedShape{c->n_pages, int(c->page_size), shift, int(c->n_kv_heads), nb};
+  const uint64_t p16 = uint64_t(c->page_size / kPagedTile);
+  out.sh = PagedShape{c->n_pages, int(c->page_size), shift, ~uint64_t(0) / p16 + 1, int(c->n_kv_heads), nb};
   auto pool = [&](void *base, int type) {
     PagedPool p;
     p.base = static_cast<uint8_t *>(base);

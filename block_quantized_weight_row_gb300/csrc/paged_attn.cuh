@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
         for (int u = 0; u < TT; ++u) {
           const int tok = ti * TOK + u * 16;
           bool ok = tok < hi_any;
-          const int pi = a.sh.page_shift >= 0 ? tok >> a.sh.page_shift : tok / a.sh.page_size;
+          const int pi = token_page(a.sh, tok);
           int page = ok ? __ldg(table + pi) : 0;
           if (uint32_t(page) >= uint64_t(a.sh.n_pages)) {  // never read outside the pool
             if (lane == 0) atomicOr(a.err, kErrIndex);

@@ -7,11 +7,16 @@
 // ~3 further operations beside them; converting the cache's codes is shared by
 // the 256 rows of a CTA (about a fifth of the step's issue slots). A step is
 // 256 rows x 128 tokens:
-//   - S = Q K^T per 128-row tile (operands in shared memory, accumulator in
-//     tensor memory), softmax by one thread per row, P back into tensor memory
-//     over S as binary16, O += P V with P as the tensor-memory operand. The
-//     two row tiles alternate, so the tensor pipe works on one while the other
-//     is in its softmax.
+//   - S = Q K^T per 128-row tile and 64 tokens (operands in shared memory,
+//     accumulator in tensor memory), softmax by one thread per row, P back
+//     into tensor memory over S as binary16, O += P V with P as the
+//     tensor-memory operand. Two row tiles and two halves of the tokens are in
+//     flight: while a warp works on one half, the tensor pipe finishes P V and
+//     the next S of the other (one 128-token S per row tile leaves each softmax
+//     warp waiting for its own products: 8300 cycles a step).
+//   - A thread reads its row of S once: weights are made with the maximum as it
+//     was and kept in registers; only if a score passed it by 2^8 are they made
+//     again, with the row read again, before they are written over S.
 //   - K and V operands are made from the page bytes on the way into shared
 //     memory: k^ = d c as binary16, tokens x channels; V transposed, channels
 //     x tokens, so that both are plain K-major operands (128-byte swizzle).
@@ -44,7 +49,8 @@ constexpr int kTile = 128;  // tokens per step, rows per row tile
 constexpr int kHead = 6;    // weights carry 2^kHead
 constexpr int kSub = 128 * 128;  // bytes of an operand sub-tile: 128 rows x 64 binary16
 
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 10, kODone = 12, kQReady = 14, kAllDone = 15, kVExp = 16, kBars = 20 };
+// kSFull, kPReady: [row tile][half]
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 12, kODone = 16, kQReady = 18, kAllDone = 19, kVExp = 20, kBars = 24 };
 
 struct Misc {
   uint32_t tmem;
@@ -73,15 +79,6 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // H64 x / 8 of 64 values of one thread, spans 1 .. 32 in order
 __device__ __forceinline__ void hadamard64_thread(float (&x)[64]) {
@@ -114,24 +111,29 @@ __device__ __forceinline__ void load_q64(int elem, const uint8_t *row, int ch, i
   if (rotate) hadamard64_thread(x);
 }
 
-// N bytes (a multiple of 4) from global memory
+// Global loads that stay where they are written: a plain load may be moved
+// down to its first use, which here is a tile later, behind the waits.
+__device__ __forceinline__ int ldg_now(const int32_t *p) {
+  int v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+// N bytes (a multiple of 4)
 template <int N>
 __device__ __forceinline__ void ldg_piece(const uint8_t *p, uint32_t (&w)[N / 4]) {
   if constexpr (N % 16 == 0) {
 #pragma unroll
-    for (int i = 0; i < N / 16; ++i) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
-      w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-    }
+    for (int i = 0; i < N / 16; ++i)
+      asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                   : "l"(p + 16 * i));
   } else if constexpr (N % 8 == 0) {
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
-      w[2 * i] = v.x, w[2 * i + 1] = v.y;
-    }
+    for (int i = 0; i < N / 8; ++i)
+      asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(w[2 * i]), "=r"(w[2 * i + 1]) : "l"(p + 8 * i));
   } else {
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+    for (int i = 0; i < N / 4; ++i) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(w[i]) : "l"(p + 4 * i));
   }
 }
 
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr bool K4 = KT == kTypeQ4_0, V4 = VT == kTypeQ4_0;
   constexpr int RBK = NB * Codes<KT>::kBytes, RBV = NB * Codes<VT>::kBytes;
   constexpr int UK = RBK / kUnitsK, UV = RBV / kUnitsV;
-  constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(kTile >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+  constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(64 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
   constexpr uint32_t kIdescO = (1u << 4) | (uint32_t(D >> 3) << 17) | (uint32_t(128 >> 4) << 24);
   extern __shared__ uint8_t smem_dyn[];
   const uint32_t base = smem_u32(smem_dyn);
@@ -246,9 +248,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&bar[kKEmpty + i], 1);
       mbar_init(&bar[kVFull + i], 4);
       mbar_init(&bar[kVEmpty + i], 1);
+      mbar_init(&bar[kODone + i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
       mbar_init(&bar[kSFull + i], 1);
       mbar_init(&bar[kPReady + i], 4);
-      mbar_init(&bar[kODone + i], 1);
     }
     mbar_init(&bar[kQReady], 4 * n_tiles_q);
     for (int i = 0; i < 4; ++i) mbar_init(&bar[kVExp + i], 4);
@@ -265,20 +269,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
   const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
-  // Entry of the page table for token `tok`, 0 past what any row sees. It is
-  // looked at (and an entry outside the pool reported) a tile later, so that
-  // nothing waits for it here.
-  auto page_of = [&](int tok) {
-    return tok < hi_any ? __ldg(table + (a.sh.page_shift >= 0 ? tok >> a.sh.page_shift : tok / a.sh.page_size)) : 0;
-  };
-  auto page_ok = [&](int page) {
-    if (uint32_t(page) < uint64_t(a.sh.n_pages)) return true;
-    atomicOr(a.err, kErrIndex);
-    return false;
-  };
-  auto place_of = [&](int tok) {
-    return a.sh.page_shift >= 0 ? tok & (a.sh.page_size - 1) : tok % a.sh.page_size;
-  };
+  // Entry of the page table for token `tok` (for its last seen token past it).
+  // It is looked at a tile later, so that nothing waits for it here. n > 0.
+  auto page_of = [&](int tok) { return ldg_now(table + token_page(a.sh, min(tok, hi_any - 1))); };
+  auto place_of = [&](int tok) { return tok - token_page(a.sh, tok) * a.sh.page_size; };
 
   if (warp < 8) {
     // ---- softmax: thread = row ----
@@ -337,98 +331,100 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       float m = -FLT_MAX, l = 0.0f;
       int k0 = 0;
       bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        if (!tc_wait_warp(&bar[kVExp + (j & 3)], (j >> 2) & 1, spin, abort_flag, a.err) ||
-            !tc_wait_warp(&bar[kSFull + t], j & 1, spin, abort_flag, a.err)) {
+      for (int i = 0; i < 2 * n; ++i) {  // half tiles of 64 tokens
+        const int j = i >> 1, half = i & 1;
+        if (!tc_wait_warp(&bar[kSFull + 2 * t + half], j & 1, spin, abort_flag, a.err)) {
           ok = false;
           break;
         }
         tc_fence_after();
+        const uint32_t col0 = s_col + 64 * half;
+        uint32_t s[2][32];
+        tmem_ld32_issue(col0, s[0]);
+        tmem_ld32_issue(col0 + 32, s[1]);
         // per 32 tokens: score = f S, and the V operand is in 2^-h of the first one's unit
-        float f[4];
-        int h[4];
-        const volatile int *kx = mi->kx[j & 3], *vx = mi->vx[j & 3];
-        if (j == 0) k0 = vx[0];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          f[c] = fq * pow2(-kx[c]);
-          h[c] = k0 - vx[c];
-        }
-        const int tile0 = (j0 + j) * kTile;
-        const bool full = tile0 >= lo_all && tile0 + kTile <= hi_all;
-        const int from = lo - tile0, to = hi - tile0;
-        uint32_t s[32];
-        float rm = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32(s_col + 32 * c, s);
-          if (!full) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int col = 32 * c + i;
-              s[i] = col >= from && col < to ? s[i] : 0xff800000u;  // -infinity
-            }
-          }
-          float m4[4];  // four chains
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(s[i]);
-#pragma unroll
-          for (int i = 4; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], __uint_as_float(s[i]));
-          rm = fmaxf(rm, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f[c], float(h[c])));
-        }
-        const bool raise = rm > m + kRaise;
-        if (__any_sync(kFull, raise)) {
-          const float mn = raise ? rm : m, al = ex2(m - mn);
-          m = mn;
-          l *= al;
-          if (j > 0) {
-#pragma unroll 1
-            for (int c = 0; c < NB; ++c) {
-              uint32_t v[32];
-              tmem_ld32(o_col + 32 * c, v);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * al);
-              tmem_st32(o_col + 32 * c, v);
-            }
-          }
-        }
-        // straight-line code per 32 columns (a mask test per value would cut it
-        // into dependent pieces: 4600 cycles a tile instead of ~1000)
+        const volatile int *kx = mi->kx[j & 3] + 2 * half, *vx = mi->vx[j & 3] + 2 * half;
+        if (i == 0) k0 = vx[0];
+        const float f[2] = {fq * pow2(-kx[0]), fq * pow2(-kx[1])};
+        const int h[2] = {k0 - vx[0], k0 - vx[1]};
+        const int tok0 = (j0 + j) * kTile + 64 * half;
+        const bool full = tok0 >= lo_all && tok0 + 64 <= hi_all;
+        uint32_t p[32];
+        float rm, part;
+        // Weights and their sum with the maximum as it is, and the scores'
+        // maximum. Straight-line code (a mask test per value would cut it into
+        // dependent pieces).
         auto weigh = [&](auto masked) {
+          rm = -INFINITY;
+          part = 0.0f;
+          tmem_ld_wait(s[0]);
+          tmem_ld_wait(s[1]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < 2; ++c) {
             const float c0 = float(kHead + h[c]) - m;
             const uint64_t f2 = pack2(__float_as_uint(f[c]), __float_as_uint(f[c])), c2 = pack2(__float_as_uint(c0), __float_as_uint(c0));
             uint64_t sum2[2] = {0, 0};
-            tmem_ld32(s_col + 32 * c, s);
-            uint32_t p[16];
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t x = ffma2(pack2(s[2 * i], s[2 * i + 1]), f2, c2);
-              float u = __uint_as_float(uint32_t(x)), v = __uint_as_float(uint32_t(x >> 32));
+            for (int k = 0; k < 16; ++k) {
+              uint32_t a0 = s[c][2 * k], a1 = s[c][2 * k + 1];
               if constexpr (decltype(masked)::value) {
-                const int col = 32 * c + 2 * i;
-                u = col >= from && col < to ? u : -INFINITY;
-                v = col + 1 >= from && col + 1 < to ? v : -INFINITY;
+                const int tk = tok0 + 32 * c + 2 * k;
+                a0 = tk >= lo && tk < hi ? a0 : 0xff800000u;  // -infinity
+                a1 = tk + 1 >= lo && tk + 1 < hi ? a1 : 0xff800000u;
+              }
+              m4[(2 * k) & 3] = fmaxf(m4[(2 * k) & 3], __uint_as_float(a0));
+              m4[(2 * k + 1) & 3] = fmaxf(m4[(2 * k + 1) & 3], __uint_as_float(a1));
+              const uint64_t x = ffma2(pack2(a0, a1), f2, c2);
+              float u = __uint_as_float(uint32_t(x)), v = __uint_as_float(uint32_t(x >> 32));
+              if constexpr (decltype(masked)::value) {  // where f is 0 the product of a masked score is NaN
+                u = a0 == 0xff800000u ? -INFINITY : u;
+                v = a1 == 0xff800000u ? -INFINITY : v;
               }
               u = ex2(u);
               v = ex2(v);
-              sum2[i & 1] = fadd2(sum2[i & 1], pack2(__float_as_uint(u), __float_as_uint(v)));
-              p[i] = half2_bits(u, v);
+              sum2[k & 1] = fadd2(sum2[k & 1], pack2(__float_as_uint(u), __float_as_uint(v)));
+              p[16 * c + k] = half2_bits(u, v);
             }
-            tmem_st16(s_col + 16 * c, p);
+            rm = fmaxf(rm, fmaf(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])), f[c], float(h[c])));
             const uint64_t both = fadd2(sum2[0], sum2[1]);
-            l = fmaf(__uint_as_float(uint32_t(both)) + __uint_as_float(uint32_t(both >> 32)), pow2(-h[c]), l);
+            part = fmaf(__uint_as_float(uint32_t(both)) + __uint_as_float(uint32_t(both >> 32)), pow2(-h[c]), part);
           }
         };
         if (full)
           weigh(std::false_type());
         else
           weigh(std::true_type());
-        tmem_st_wait();
+        const bool raise = rm > m + kRaise;
+        if (__any_sync(kFull, raise)) {
+          const float mn = raise ? rm : m, al = ex2(m - mn);
+          m = mn;
+          l *= al;
+          if (i > 0) {
+            // O is only touched once the product of the half before is done:
+            // the other half's next S comes after it
+            if (!tc_wait_warp(&bar[kSFull + 2 * t + (half ^ 1)], (j + half) & 1, spin, abort_flag, a.err)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NB; ++c) {
+              tmem_ld32(o_col + 32 * c, s[0]);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) s[0][k] = __float_as_uint(__uint_as_float(s[0][k]) * al);
+              tmem_st32(o_col + 32 * c, s[0]);
+            }
+          }
+          tmem_ld32_issue(col0, s[0]);
+          tmem_ld32_issue(col0 + 32, s[1]);
+          weigh(std::true_type());
+        }
+        l += part;
+        tmem_st32(col0, p);
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar[kPReady + t]);
+        if (lane == 0) mbar_arrive(&bar[kPReady + 2 * t + half]);
       }
       // ---- output ----
       if (ok && n > 0) ok = tc_wait_warp(&bar[kODone + t], 0, spin, abort_flag, a.err);
@@ -494,35 +490,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
-        next[i] = j < n ? page_of(tok) : 0;
+        next[i] = page_of(tok);
       }
     };
+    // Loads have no branch around them (at its end they would be waited for):
+    // where there is nothing to read, q's first bytes stand in and the scale
+    // is cleared when it is used.
+    uint32_t live = 0;
     auto load = [&](int j) {
+      live = 0;
+      bool wrong = false;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
-        const int page = next[i];
+        const bool want = tok >= lo_any && tok < hi_any, ok = uint32_t(next[i]) < uint64_t(a.sh.n_pages);
+        live |= uint32_t(want && ok) << i;
+        wrong = wrong || (want && !ok);
+      }
+      if (wrong) atomicOr(a.err, kErrIndex);
 #pragma unroll
-        for (int k = 0; k < UK / 4; ++k) code[i][k] = 0;
-#pragma unroll
-        for (int k = 0; k < NB / 2; ++k) sc[i][k] = 0;
-        if (tok >= lo_any && tok < hi_any && page_ok(page)) {
-          const uint8_t *hp = a.kp.base + (int64_t(page) * a.sh.n_kv + kvh) * a.kp.head_bytes;
-          const int place = place_of(tok);
-          ldg_piece<UK>(hp + place * RBK + c * UK, code[i]);
-          ldg_piece<NB * 2>(hp + a.kp.scale_off + place * NB * 2, sc[i]);
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk, place = place_of(tok);
+        const bool ok = live >> i & 1;
+        const uint8_t *hp = a.kp.base + (int64_t(next[i]) * a.sh.n_kv + kvh) * a.kp.head_bytes;
+        ldg_piece<UK>(ok ? hp + place * RBK + c * UK : a.q, code[i]);
+        ldg_piece<NB * 2>(ok ? hp + a.kp.scale_off + place * NB * 2 : a.q, sc[i]);
       }
       pages(j + 1);
     };
-    pages(0);
-    if (n > 0) load(0);
+    if (n > 0) {
+      pages(0);
+      load(0);
+    }
     for (int j = 0; j < n; ++j) {
       uint32_t e = 1;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int k = 0; k < NB / 2; ++k) e = max(e, max_exp(sc[i][k]));
+        for (int k = 0; k < NB / 2; ++k) {
+          sc[i][k] = live >> i & 1 ? sc[i][k] : 0;
+          e = max(e, max_exp(sc[i][k]));
+        }
       const int kk = 20 - int(__reduce_max_sync(kFull, e));
       if (!tc_wait_warp(&bar[kKEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
       if (lane == 0) mi->kx[j & 3][w] = kk;
@@ -559,35 +567,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     int next = 0;  // page of the next tile to load
     auto pages = [&](int j) {
       const int tok0 = (j0 + j) * kTile + grp * 8;
-      next = j < n ? page_of(tok0) : 0;
+      next = page_of(tok0);
     };
-    auto load = [&](int j) {
-      const int tok0 = (j0 + j) * kTile + grp * 8;
-      const bool some = tok0 < hi_any && tok0 + 8 > lo_any && page_ok(next);
-      const uint8_t *hp = a.vp.base + (int64_t(some ? next : 0) * a.sh.n_kv + kvh) * a.vp.head_bytes;
-      const int place = place_of(tok0);
+    uint32_t live = 0;
+    auto load = [&](int j) {  // no branch around the loads, as for K
+      const int tok0 = (j0 + j) * kTile + grp * 8, place = place_of(tok0);
+      const bool want = tok0 < hi_any && tok0 + 8 > lo_any, ok = want && uint32_t(next) < uint64_t(a.sh.n_pages);
+      if (want && !ok) atomicOr(a.err, kErrIndex);
+      const uint8_t *hp = a.vp.base + (int64_t(next) * a.sh.n_kv + kvh) * a.vp.head_bytes;
+      const uint8_t *pc = ok ? hp + place * RBV + g * UV : a.q, *ps = ok ? hp + a.vp.scale_off + place * NB * 2 : a.q;
+      const int sc_step = ok ? NB * 2 : 0, code_step = ok ? RBV : 0;
+      live = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int tok = tok0 + i;
-#pragma unroll
-        for (int k = 0; k < UV / 4; ++k) code[i][k] = 0;
-#pragma unroll
-        for (int k = 0; k < NB / 2; ++k) sc[i][k] = 0;
-        if (some && tok >= lo_any && tok < hi_any) {
-          ldg_piece<UV>(hp + (place + i) * RBV + g * UV, code[i]);
-          ldg_piece<NB * 2>(hp + a.vp.scale_off + (place + i) * NB * 2, sc[i]);
-        }
+        live |= uint32_t(ok && tok0 + i >= lo_any && tok0 + i < hi_any) << i;
+        ldg_piece<UV>(pc + i * code_step, code[i]);
+        ldg_piece<NB * 2>(ps + i * sc_step, sc[i]);
       }
       pages(j + 1);
     };
-    pages(0);
-    if (n > 0) load(0);
+    if (n > 0) {
+      pages(0);
+      load(0);
+    }
     for (int j = 0; j < n; ++j) {
       uint32_t e = 1;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int k = 0; k < NB / 2; ++k) e = max(e, max_exp(sc[i][k]));
+        for (int k = 0; k < NB / 2; ++k) {
+          sc[i][k] = live >> i & 1 ? sc[i][k] : 0;
+          e = max(e, max_exp(sc[i][k]));
+        }
       const int ve = 20 - int(__reduce_max_sync(kFull, e));
       if (lane == 0) {
         mi->vx[j & 3][w] = ve;
@@ -627,42 +638,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     regs_down<40>();
     if (warp == 16 && lane == 0) {
     // ---- MMA issue ----
-    const uint32_t qa = smem_u32(sm), ka = smem_u32(sm + C::kOffK), va = smem_u32(sm + C::kOffV);
-    auto issue_s = [&](int t, int j) {
+    // Operand descriptors differ in their low words' address field only (in
+    // 16 bytes, below 2^14): one 32-bit addition per product.
+    const uint64_t d0 = sw128_desc(smem_u32(sm));
+    const uint32_t lo0 = uint32_t(d0), hi0 = uint32_t(d0 >> 32);
+    auto desc = [&](uint32_t offset) { return pack2(lo0 + (offset >> 4), hi0); };
+    // S of row tile t and half h of tile j
+    auto issue_s = [&](int t, int h, int j) {
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint64_t ad = sw128_desc(qa + t * C::kQBytes + (k >> 2) * kSub) + uint64_t((k & 3) * 2);
-        const uint64_t bd = sw128_desc(ka + (j & 1) * C::kKBytes + (k >> 2) * kSub) + uint64_t((k & 3) * 2);
-        tc_mma(tmem + uint32_t(t * 128), ad, bd, kIdescS, k > 0);
+        const uint32_t at = (k >> 2) * kSub + (k & 3) * 32;
+        tc_mma(tmem + uint32_t(t * 128 + h * 64), desc(t * C::kQBytes + at),
+               desc(C::kOffK + (j & 1) * C::kKBytes + h * (kSub / 2) + at), kIdescS, k > 0);
       }
-      tc_commit(&bar[kSFull + t]);
+      tc_commit(&bar[kSFull + 2 * t + h]);
     };
-    bool ok = n > 0 && tc_wait(&bar[kQReady], 0, spin, abort_flag, a.err) && tc_wait(&bar[kKFull], 0, spin, abort_flag, a.err);
+    // K operand and V exponents of tile j are there
+    auto tile_there = [&](int j) {
+      return tc_wait(&bar[kKFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) &&
+             tc_wait(&bar[kVExp + (j & 3)], (j >> 2) & 1, spin, abort_flag, a.err);
+    };
+    bool ok = n > 0 && tc_wait(&bar[kQReady], 0, spin, abort_flag, a.err) && tile_there(0);
     if (ok) {
       tc_fence_after();
-      for (int t = 0; t < n_tiles_q; ++t) issue_s(t, 0);
+      for (int h = 0; h < 2; ++h)
+        for (int t = 0; t < n_tiles_q; ++t) issue_s(t, h, 0);
       tc_commit(&bar[kKEmpty]);
     }
     for (int j = 0; j < n && ok; ++j) {
       const bool more = j + 1 < n;
-      ok = tc_wait(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) &&
-           (!more || tc_wait(&bar[kKFull + ((j + 1) & 1)], ((j + 1) >> 1) & 1, spin, abort_flag, a.err));
-      for (int t = 0; t < n_tiles_q && ok; ++t) {
-        if (!(ok = tc_wait(&bar[kPReady + t], j & 1, spin, abort_flag, a.err))) break;
-        tc_fence_after();
+      ok = tc_wait(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) && (!more || tile_there(j + 1));
+      for (int h = 0; h < 2 && ok; ++h)
+        for (int t = 0; t < n_tiles_q && ok; ++t) {
+          const bool last = h == 1 && t == n_tiles_q - 1;
+          if (!(ok = tc_wait(&bar[kPReady + 2 * t + h], j & 1, spin, abort_flag, a.err))) break;
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          const uint64_t bd = sw128_desc(va + (j & 1) * C::kVBytes + (k >> 2) * C::kVSub) + uint64_t((k & 3) * 2);
-          tc_mma_ts(tmem + uint32_t(256 + t * 128), tmem + uint32_t(t * 128 + k * 8), bd, kIdescO, j > 0 || k > 0);
+          for (int k = 0; k < 4; ++k) {
+            tc_mma_ts(tmem + uint32_t(256 + t * 128), tmem + uint32_t(t * 128 + h * 64 + k * 8),
+                      desc(C::kOffV + (j & 1) * C::kVBytes + h * C::kVSub + k * 32), kIdescO, j > 0 || h > 0 || k > 0);
+          }
+          if (last) tc_commit(&bar[kVEmpty + (j & 1)]);
+          if (more) {
+            issue_s(t, h, j + 1);
+            if (last) tc_commit(&bar[kKEmpty + ((j + 1) & 1)]);
+          } else if (h == 0) {
+            tc_commit(&bar[kSFull + 2 * t]);  // no S: the product is done
+          } else {
+            tc_commit(&bar[kODone + t]);
+          }
         }
-        if (t == n_tiles_q - 1) tc_commit(&bar[kVEmpty + (j & 1)]);
-        if (more) {
-          issue_s(t, j + 1);
-          if (t == n_tiles_q - 1) tc_commit(&bar[kKEmpty + ((j + 1) & 1)]);
-        } else {
-          tc_commit(&bar[kODone + t]);
-        }
-      }
     }
     tc_commit(&bar[kAllDone]);
     tc_drain(&bar[kAllDone], 0);
