@@ -28,8 +28,8 @@
 //     neither large nor tiny scales leave binary16's range.
 //   - Maxima are raised only when passed by 2^8; weights are 2^(s - m + 6).
 // Warps: 0-3 and 4-7 softmax of row tiles A and B (and Q before, O after),
-// 8-11 K operand, 12-15 V operand, 16 tensor memory and MMA issue, 17-19 none
-// (they complete a warpgroup whose registers go to the softmax). Waits are
+// 8-11 K operand, 12-15 V operand, 16 and 17 MMA issue for A and B, 18 and 19
+// none (they complete a warpgroup whose registers go to the softmax). Waits are
 // bounded as in the GEMM: one that runs out sets the error word, every role
 // leaves, MMAs in flight are waited for and the tensor memory is freed.
 // With few CTAs the tokens of a row tile are split over several, whose
@@ -50,7 +50,7 @@ constexpr int kHead = 6;    // weights carry 2^kHead
 constexpr int kSub = 128 * 128;  // bytes of an operand sub-tile: 128 rows x 64 binary16
 
 // kSFull, kPReady: [row tile][half]
-enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 12, kODone = 16, kQReady = 18, kAllDone = 19, kVExp = 20, kBars = 24 };
+enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 12, kODone = 16, kAllDone = 18, kQReady = 20, kBars = 21 };
 
 struct Misc {
   uint32_t tmem;
@@ -78,6 +78,24 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc
       " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
       "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// Bounded wait that gives up once another thread has: a test, then waits that
+// suspend the thread in the barrier unit. (Polling between naps, as the GEMM
+// does, took a third of this kernel's issue slots.)
+__device__ __forceinline__ bool pa_wait(uint64_t *bar, uint32_t parity, uint32_t limit, volatile int *abort_flag, unsigned *err) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 15) == 15 && *abort_flag) return false;
+  }
+  *abort_flag = 1;
+  atomicOr(err, kErrTimeout);
+  return false;
+}
+// The same for a whole warp, every lane waiting for itself.
+__device__ __forceinline__ bool pa_wait_warp(uint64_t *bar, uint32_t parity, uint32_t limit, volatile int *abort_flag, unsigned *err) {
+  const bool ok = pa_wait(bar, parity, limit, abort_flag, err);
+  return __all_sync(kFull, ok);
 }
 
 // H64 x / 8 of 64 values of one thread, spans 1 .. 32 in order
@@ -244,10 +262,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar[kKFull + i], 4);
-      mbar_init(&bar[kKEmpty + i], 1);
+      mbar_init(&bar[kKFull + i], 8);  // the K operand and the V exponents of the tile
+      mbar_init(&bar[kKEmpty + i], n_tiles_q);
       mbar_init(&bar[kVFull + i], 4);
-      mbar_init(&bar[kVEmpty + i], 1);
+      mbar_init(&bar[kVEmpty + i], n_tiles_q);
+      mbar_init(&bar[kAllDone + i], 1);
       mbar_init(&bar[kODone + i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -255,8 +274,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&bar[kPReady + i], 4);
     }
     mbar_init(&bar[kQReady], 4 * n_tiles_q);
-    for (int i = 0; i < 4; ++i) mbar_init(&bar[kVExp + i], 4);
-    mbar_init(&bar[kAllDone], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -333,7 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool ok = true;
       for (int i = 0; i < 2 * n; ++i) {  // half tiles of 64 tokens
         const int j = i >> 1, half = i & 1;
-        if (!tc_wait_warp(&bar[kSFull + 2 * t + half], j & 1, spin, abort_flag, a.err)) {
+        if (!pa_wait_warp(&bar[kSFull + 2 * t + half], j & 1, spin, abort_flag, a.err)) {
           ok = false;
           break;
         }
@@ -391,22 +408,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             part = fmaf(__uint_as_float(uint32_t(both)) + __uint_as_float(uint32_t(both >> 32)), pow2(-h[c]), part);
           }
         };
-        if (full)
-          weigh(std::false_type());
-        else
-          weigh(std::true_type());
-        const bool raise = rm > m + kRaise;
-        if (__any_sync(kFull, raise)) {
+        for (int pass = 0; pass < 2; ++pass) {
+          if (full)
+            weigh(std::false_type());
+          else
+            weigh(std::true_type());
+          const bool raise = rm > m + kRaise;
+          if (!__any_sync(kFull, raise)) break;
           const float mn = raise ? rm : m, al = ex2(m - mn);
           m = mn;
           l *= al;
           if (i > 0) {
             // O is only touched once the product of the half before is done:
             // the other half's next S comes after it
-            if (!tc_wait_warp(&bar[kSFull + 2 * t + (half ^ 1)], (j + half) & 1, spin, abort_flag, a.err)) {
-              ok = false;
-              break;
-            }
+            ok = pa_wait_warp(&bar[kSFull + 2 * t + (half ^ 1)], (j + half) & 1, spin, abort_flag, a.err);
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < NB; ++c) {
@@ -418,8 +434,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           tmem_ld32_issue(col0, s[0]);
           tmem_ld32_issue(col0 + 32, s[1]);
-          weigh(std::true_type());
         }
+        if (!ok) break;
         l += part;
         tmem_st32(col0, p);
         tc_fence_before();
@@ -427,7 +443,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) mbar_arrive(&bar[kPReady + 2 * t + half]);
       }
       // ---- output ----
-      if (ok && n > 0) ok = tc_wait_warp(&bar[kODone + t], 0, spin, abort_flag, a.err);
+      if (ok && n > 0) ok = pa_wait_warp(&bar[kODone + t], 0, spin, abort_flag, a.err);
       if (ok) {
         tc_fence_after();
         const bool part = n_split > 1;
@@ -532,7 +548,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           e = max(e, max_exp(sc[i][k]));
         }
       const int kk = 20 - int(__reduce_max_sync(kFull, e));
-      if (!tc_wait_warp(&bar[kKEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
+      if (!pa_wait_warp(&bar[kKEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
       if (lane == 0) mi->kx[j & 3][w] = kk;
       const float up = pow2(kk);
       uint8_t *ks = sm + C::kOffK + (j & 1) * C::kKBytes;
@@ -602,9 +618,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int ve = 20 - int(__reduce_max_sync(kFull, e));
       if (lane == 0) {
         mi->vx[j & 3][w] = ve;
-        mbar_arrive(&bar[kVExp + (j & 3)]);
+        mbar_arrive(&bar[kKFull + (j & 1)]);
       }
-      if (!tc_wait_warp(&bar[kVEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
+      if (!pa_wait_warp(&bar[kVEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
       const float up = pow2(ve);
       uint8_t *vs = sm + C::kOffV + (j & 1) * C::kVBytes + (grp >> 3) * C::kVSub;
 #pragma unroll
@@ -636,61 +652,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     regs_down<40>();
-    if (warp == 16 && lane == 0) {
-    // ---- MMA issue ----
-    // Operand descriptors differ in their low words' address field only (in
-    // 16 bytes, below 2^14): one 32-bit addition per product.
-    const uint64_t d0 = sw128_desc(smem_u32(sm));
-    const uint32_t lo0 = uint32_t(d0), hi0 = uint32_t(d0 >> 32);
-    auto desc = [&](uint32_t offset) { return pack2(lo0 + (offset >> 4), hi0); };
-    // S of row tile t and half h of tile j
-    auto issue_s = [&](int t, int h, int j) {
+    const int t = warp - 16;
+    if (t < n_tiles_q && lane == 0) {
+      // ---- MMA issue, a warp per row tile ----
+      // Operand descriptors differ in their low words' address field only (in
+      // 16 bytes, below 2^14): one 32-bit addition per product.
+      const uint64_t d0 = sw128_desc(smem_u32(sm));
+      const uint32_t lo0 = uint32_t(d0), hi0 = uint32_t(d0 >> 32);
+      auto desc = [&](uint32_t offset) { return pack2(lo0 + (offset >> 4), hi0); };
+      // S of half h of tile j
+      auto issue_s = [&](int h, int j) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint32_t at = (k >> 2) * kSub + (k & 3) * 32;
-        tc_mma(tmem + uint32_t(t * 128 + h * 64), desc(t * C::kQBytes + at),
-               desc(C::kOffK + (j & 1) * C::kKBytes + h * (kSub / 2) + at), kIdescS, k > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t at = (k >> 2) * kSub + (k & 3) * 32;
+          tc_mma(tmem + uint32_t(t * 128 + h * 64), desc(t * C::kQBytes + at),
+                 desc(C::kOffK + (j & 1) * C::kKBytes + h * (kSub / 2) + at), kIdescS, k > 0);
+        }
+        tc_commit(&bar[kSFull + 2 * t + h]);
+      };
+      bool ok = n > 0 && pa_wait(&bar[kQReady], 0, spin, abort_flag, a.err) && pa_wait(&bar[kKFull], 0, spin, abort_flag, a.err);
+      if (ok) {
+        tc_fence_after();
+        issue_s(0, 0);
+        issue_s(1, 0);
+        tc_commit(&bar[kKEmpty]);
       }
-      tc_commit(&bar[kSFull + 2 * t + h]);
-    };
-    // K operand and V exponents of tile j are there
-    auto tile_there = [&](int j) {
-      return tc_wait(&bar[kKFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) &&
-             tc_wait(&bar[kVExp + (j & 3)], (j >> 2) & 1, spin, abort_flag, a.err);
-    };
-    bool ok = n > 0 && tc_wait(&bar[kQReady], 0, spin, abort_flag, a.err) && tile_there(0);
-    if (ok) {
-      tc_fence_after();
-      for (int h = 0; h < 2; ++h)
-        for (int t = 0; t < n_tiles_q; ++t) issue_s(t, h, 0);
-      tc_commit(&bar[kKEmpty]);
-    }
-    for (int j = 0; j < n && ok; ++j) {
-      const bool more = j + 1 < n;
-      ok = tc_wait(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) && (!more || tile_there(j + 1));
-      for (int h = 0; h < 2 && ok; ++h)
-        for (int t = 0; t < n_tiles_q && ok; ++t) {
-          const bool last = h == 1 && t == n_tiles_q - 1;
-          if (!(ok = tc_wait(&bar[kPReady + 2 * t + h], j & 1, spin, abort_flag, a.err))) break;
+      for (int j = 0; j < n && ok; ++j) {
+        const bool more = j + 1 < n;
+        ok = pa_wait(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) &&
+             (!more || pa_wait(&bar[kKFull + ((j + 1) & 1)], ((j + 1) >> 1) & 1, spin, abort_flag, a.err));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!ok || !(ok = pa_wait(&bar[kPReady + 2 * t + h], j & 1, spin, abort_flag, a.err))) break;
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4; ++k)
             tc_mma_ts(tmem + uint32_t(256 + t * 128), tmem + uint32_t(t * 128 + h * 64 + k * 8),
                       desc(C::kOffV + (j & 1) * C::kVBytes + h * C::kVSub + k * 32), kIdescO, j > 0 || h > 0 || k > 0);
-          }
-          if (last) tc_commit(&bar[kVEmpty + (j & 1)]);
+          if (h == 1) tc_commit(&bar[kVEmpty + (j & 1)]);
           if (more) {
-            issue_s(t, h, j + 1);
-            if (last) tc_commit(&bar[kKEmpty + ((j + 1) & 1)]);
+            issue_s(h, j + 1);
+            if (h == 1) tc_commit(&bar[kKEmpty + ((j + 1) & 1)]);
           } else if (h == 0) {
             tc_commit(&bar[kSFull + 2 * t]);  // no S: the product is done
           } else {
             tc_commit(&bar[kODone + t]);
           }
         }
-    }
-    tc_commit(&bar[kAllDone]);
-    tc_drain(&bar[kAllDone], 0);
+      }
+      tc_commit(&bar[kAllDone + t]);
+      tc_drain(&bar[kAllDone + t], 0);
     }
   }
   __syncthreads();
