@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   if (row >= span.q_len * a.group) return;
   const int n = mt.w - first + 1;
   auto part = [&](int i) { return (int64_t(first + i) * 2 + (i == 0 ? 1 : 0)) * rows + r; };
-  float top = -INFINITY;
+  float top = paged::kNoMax;
   for (int i = threadIdx.x; i < n; i += kCombineThreads) top = fmaxf(top, a.part_ml[part(i)].x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
@@ -112,7 +112,7 @@ StreamShape shape_of(int nb, int kt, int vt, int elem, int rows8) {
 
 // A piece has at least this many tiles (of 16 or 32 tokens): below that a
 // CTA's start and the combine cost more than the tokens.
-constexpr int kMinTiles = 4;
+constexpr int kMinTiles = 2;
 
 // Sequences with more query rows per kv head than this go to the many-row
 // kernel (16-bit calls, head_dim 64 or 128): a pass of the streaming kernel

@@ -14,7 +14,11 @@
 //     code words. A 4-bit code u in the low bits of a half-word IS the
 //     binary16 subnormal u * 2^-24, exactly, so a word of 8 codes becomes four
 //     operand registers with one mask each and one shift; codes in bits 4-7
-//     read as 16 u, and the matching half of q is divided by 16 (exactly).
+//     read as 16 u, and the matching half of q is divided by 16 (exactly). The
+//     products' adder aligns a subnormal by its nominal exponent, which costs
+//     their sum up to 2^-17 (measured: 6e-6 of the output): nothing beside a
+//     16-bit output's rounding, but fp32 calls turn the codes into u - 8 as
+//     normal numbers (one more instruction per pair; 3e-7).
 //   - The block scales stay out of the operands: a K block's two products
 //     leave sum(q u) 2^-24, the accumulators start at -8 sum(q) 2^-24, and
 //     d_k multiplies in fp32; d_v multiplies the weights in fp32, before their
@@ -49,6 +53,7 @@ namespace paged {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr float kRaise = 8.0f;   // a maximum is raised when passed by this much (base-2 units)
+constexpr float kNoMax = -3.402823466e38f;  // no score seen yet
 constexpr int kNoExp = 0x7fffffff;  // no V scale seen yet
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -83,6 +88,16 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ float2 half2_floats(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+// Two 4-bit codes (bits 0-3 and 16-19 of w, or with _hi bits 4-7 and 20-23)
+// as binary16 u - 8, exactly: 1024 + u - 1032, (1024 + 16 u) / 16 - 72.
+__device__ __forceinline__ uint32_t codes4_lo(uint32_t w) { return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u); }
+__device__ __forceinline__ uint32_t codes4_hi(uint32_t w) { return hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u); }
 
 // Token of fragment row slot r (0..7; slot r + 8 is 8 tokens on). Any
 // bijection serves (weights and V rows use the same one); this one lets the
@@ -169,8 +184,9 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// Sizes of one instantiation. R: groups of 8 query rows per pass.
-template <int NB, int KT, int VT, int R>
+// Sizes of one instantiation. R: groups of 8 query rows per pass; TERMS:
+// binary16 terms of q and the weights.
+template <int NB, int KT, int VT, int R, int TERMS>
 struct Cfg {
   static constexpr int D = NB * 32;
   static constexpr int RBK = NB * Codes<KT>::kBytes, RBV = NB * Codes<VT>::kBytes;
@@ -185,18 +201,26 @@ struct Cfg {
   static constexpr int OP = D + 8;                                  // pitch of a merge row (floats)
   static constexpr int kRing = kWarps * S * STAGE;
   static constexpr int kMerge = kWarps * ROWS * OP * 4 + kWarps * ROWS * 8;
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 128;
+  static constexpr int QV = NB == 3 ? 4 : NB;                       // channels per lane while q is prepared
+  static constexpr int QP = TERMS * D * 2 + 64;                     // pitch of a prepared q row (bytes)
+  static constexpr int kOffQ = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kOffScale = kOffQ + ROWS * QP;               // [row]: score factor
+  static constexpr int kOffInit = kOffScale + ROWS * 4;             // [row][block]: what the products start at
+  static constexpr int kSmem = kOffInit + ROWS * NB * 4;
   static constexpr int kCtas = kTwo && 2 * (kSmem + 1024) <= 227 * 1024 && NB * R <= 4 ? 2 : 1;
 };
 
 // Tiles of a sequence: [t_lo, t_lo + tiles) of `tok` tokens hold every token
 // that any of its rows sees; a sequence with rows has at least one tile, so
 // that its output is written even when no row sees a token.
+// `cost` counts a segment's start and merge too, in tiles: a batch's short
+// sequences would otherwise leave their CTAs far behind the others.
+constexpr int kSegTokens = 512;
 struct SeqTiles {
-  int t_lo, tiles, groups;  // per (kv head, row group)
+  int t_lo, tiles, cost, groups;  // per (kv head, row group)
 };
 __device__ __forceinline__ SeqTiles seq_tiles(const PagedAttnArgs &a, const SeqSpan &s, int tok, int rows) {
-  SeqTiles t{0, 0, 0};
+  SeqTiles t{0, 0, 0, 0};
   const int n_rows = s.q_len * a.group;
   if (s.q_len == 0 || n_rows > a.tc_rows) return t;
   int lo, hi, lo1, hi1;
@@ -205,6 +229,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const PagedAttnArgs &a, const SeqS
   t.t_lo = lo / tok;
   const int t_hi = (hi + tok - 1) / tok;
   t.tiles = t_hi > t.t_lo ? t_hi - t.t_lo : 1;
+  t.cost = t.tiles + kSegTokens / tok;
   t.groups = (n_rows + rows - 1) / rows;
   return t;
 }
@@ -233,34 +258,37 @@ __device__ __forceinline__ void store_out4(int elem, uint8_t *row, int ch, float
     store_out4<kElemBF16>(row + ch * 2, v);
 }
 
-// The 8 q values of lane c's unit of block b, as fp32
-template <int KT>
-__device__ __forceinline__ void load_q8(int elem, const uint8_t *row, int b, int c, float *x) {
+// V consecutive q values from channel ch, as fp32
+template <int V>
+__device__ __forceinline__ void load_q(int elem, const uint8_t *row, int ch, float (&x)[V]) {
+  if (elem == kElemF32) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int ch = b * 32 + chan8<KT>(c, h);
-    if (elem == kElemF32) {
-      const float4 v = __ldg(reinterpret_cast<const float4 *>(row + ch * 4));
-      x[4 * h] = v.x, x[4 * h + 1] = v.y, x[4 * h + 2] = v.z, x[4 * h + 3] = v.w;
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + ch * 2));
-      const float2 p = elem == kElemF16 ? unpack_pair<kElemF16>(v.x) : unpack_pair<kElemBF16>(v.x);
-      const float2 q = elem == kElemF16 ? unpack_pair<kElemF16>(v.y) : unpack_pair<kElemBF16>(v.y);
-      x[4 * h] = p.x, x[4 * h + 1] = p.y, x[4 * h + 2] = q.x, x[4 * h + 3] = q.y;
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = __ldg(reinterpret_cast<const float2 *>(row + (ch + i) * 4));
+      x[i] = v.x, x[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t *>(row + (ch + i) * 2));
+      const float2 v = elem == kElemF16 ? unpack_pair<kElemF16>(w) : unpack_pair<kElemBF16>(w);
+      x[i] = v.x, x[i + 1] = v.y;
     }
   }
 }
 
 template <int NB, int KT, int VT, int R, int TERMS>
-__global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
+__global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
     k_paged_stream(const __grid_constant__ PagedAttnArgs a, int min_tiles) {
-  using C = Cfg<NB, KT, VT, R>;
+  using C = Cfg<NB, KT, VT, R, TERMS>;
   constexpr int D = C::D, TT = C::TT, S = C::S, TOK = C::TOK, ROWS = C::ROWS, OP = C::OP;
   constexpr int CK = C::RBK / 16, CV = C::RBV / 16;            // 16-byte chunks per row
   constexpr int UK = C::RBK / kUnitsK, UV = C::RBV / kUnitsV;  // bytes of a lane's piece of a row
   constexpr bool K4 = KT == kTypeQ4_0, V4 = VT == kTypeQ4_0;
-  // factor of the products' accumulators: 4-bit codes are read as u * 2^-24
-  constexpr float kKUnit = K4 ? 16777216.0f : 1.0f, kVUnit = V4 ? 16777216.0f : 1.0f;
+  // 4-bit codes as subnormals u * 2^-24 (16-bit calls), and then the factor
+  // of the products' accumulators
+  constexpr bool KSUB = K4 && TERMS == 1, VSUB = V4 && TERMS == 1;
+  constexpr float kKUnit = KSUB ? 16777216.0f : 1.0f, kVUnit = VSUB ? 16777216.0f : 1.0f;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sh_scan[kWarps + 1];
   __shared__ int64_t sh_find[2];
@@ -273,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
   int64_t mine = 0;
   for (int b = b_first; b < b_last; ++b) {
     const SeqTiles t = seq_tiles(a, load_span(a, b, blockIdx.x == 0), TOK, ROWS);
-    mine += int64_t(t.tiles) * t.groups * a.sh.n_kv;
+    mine += int64_t(t.cost) * t.groups * a.sh.n_kv;
   }
   int64_t incl = mine;
 #pragma unroll
@@ -300,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
     int64_t at = before;
     for (int b = b_first; b < b_last; ++b) {
       const SeqTiles t = seq_tiles(a, load_span(a, b, false), TOK, ROWS);
-      const int64_t n = int64_t(t.tiles) * t.groups * a.sh.n_kv;
+      const int64_t n = int64_t(t.cost) * t.groups * a.sh.n_kv;
       if (t0 < at + n) {
         sh_find[0] = b;
         sh_find[1] = at;
@@ -317,17 +345,19 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
   const uint32_t ring_u = smem_u32(ring);
   float *merge_o = reinterpret_cast<float *>(smem);
   float2 *merge_ml = reinterpret_cast<float2 *>(smem + kWarps * ROWS * OP * 4);
+  uint8_t *q_rows = smem + C::kOffQ;
+  float *q_scale = reinterpret_cast<float *>(smem + C::kOffScale), *q_init = reinterpret_cast<float *>(smem + C::kOffInit);
 
   for (int64_t at = t0; at < t1;) {
     // ---- the segment that holds tile `at` ----
     SeqSpan span = load_span(a, seq, false);
     SeqTiles st = seq_tiles(a, span, TOK, ROWS);
-    while (at >= seq_at + int64_t(st.tiles) * st.groups * a.sh.n_kv) {
-      seq_at += int64_t(st.tiles) * st.groups * a.sh.n_kv;
+    while (at >= seq_at + int64_t(st.cost) * st.groups * a.sh.n_kv) {
+      seq_at += int64_t(st.cost) * st.groups * a.sh.n_kv;
       span = load_span(a, ++seq, false);
       st = seq_tiles(a, span, TOK, ROWS);
     }
-    const int64_t seg = (at - seq_at) / st.tiles, seg_at = seq_at + seg * st.tiles, seg_end = seg_at + st.tiles;
+    const int64_t seg = (at - seq_at) / st.cost, seg_at = seq_at + seg * st.cost, seg_end = seg_at + st.cost;
     const int kvh = int(seg / st.groups), rg = int(seg - int64_t(kvh) * st.groups);
     const int64_t stop = min(seg_end, t1);
     const int n_rows = span.q_len * a.group, row0 = rg * ROWS, rows = min(ROWS, n_rows - row0);
@@ -335,118 +365,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
     int lo_any, hi_any, lo_all, hi_all;
     seen_range(span, row0 / a.group, a.causal, a.window, lo_any, hi_all);
     seen_range(span, (row0 + rows - 1) / a.group, a.causal, a.window, lo_all, hi_any);
-    int tile = st.t_lo + int(at - seg_at), tile_end = st.t_lo + int(stop - seg_at);
+    // the segment's fixed cost comes before its tiles
+    const int fixed = st.cost - st.tiles;
+    int tile = st.t_lo + max(int(at - seg_at) - fixed, 0), tile_end = st.t_lo + max(int(stop - seg_at) - fixed, 0);
     tile = max(tile, lo_any / TOK);
     tile_end = min(tile_end, (hi_any + TOK - 1) / TOK);
 
-    // ---- this lane's columns: rows 2c, 2c + 1 of each group of 8 ----
-    int lo[R][2], hi[R][2];
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int row = min(row0 + 8 * r + 2 * c + e, n_rows - 1);
-        seen_range(span, row / a.group, a.causal, a.window, lo[r][e], hi[r][e]);
-      }
-    // q as operand columns: lane (g, c) holds row g's channels of unit c
-    uint32_t qf[R][TERMS][NB][4];
-    float init[R][NB][2];  // -8 sum(q) of the columns' blocks, in the products' unit
-    float qscale[R][2];    // score = qscale * sum_b d_k[b] * product[b]
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float x[NB][8];
-      const int row = row0 + 8 * r + g;
-      if (row < n_rows) {
-        const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
-        const uint8_t *p = a.q + int64_t(span.q0 + tok) * a.q_token + int64_t(head) * a.q_head;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) load_q8<KT>(a.elem, p, b, c, x[b]);
-      } else {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[b][i] = 0.0f;
-      }
-      if constexpr (NB % 2 == 0) {
-        if (a.rotate) {
-#pragma unroll
-          for (int b = 0; b < NB; b += 2) hadamard64_4lanes<KT>(reinterpret_cast<float(&)[2][8]>(x[b]));
-        }
-      }
-      float m = 0.0f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[b][i]));
-      m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-      // 2^k brings the row's largest value to [2^10, 2^11)
-      const int k = m > 0.0f ? min(10 + 127 - int(__float_as_uint(m) >> 23), 110) : 0;
-      const float up = __int_as_float((127 + k) << 23);
-      const float fs = a.scale_log2 * kKUnit * __int_as_float((127 - k) << 23);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) qscale[r][e] = __shfl_sync(kFull, fs, (2 * c + e) * 4);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float sum = 0.0f;
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[b][i] * up;
-#pragma unroll
-        for (int t = 0; t < TERMS; ++t) {
-          // fragment pairs: Q4_0 (i, i + 2) of the low channels then of the
-          // high ones (read as 16 u, so q / 16); Q8_0 consecutive channels
-          uint32_t h[4];
-          if constexpr (K4) {
-            h[0] = half2_bits(y[0], y[2]);
-            h[1] = half2_bits(y[4], y[6]);
-            h[2] = half2_bits(y[1], y[3]);
-            h[3] = half2_bits(y[5], y[7]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = half2_bits(y[2 * i], y[2 * i + 1]);
-          }
-          float z[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 f = half2_floats(h[i]);
-            const int i0 = K4 ? (i & 1) * 4 + (i >> 1) : 2 * i, i1 = K4 ? i0 + 2 : 2 * i + 1;
-            z[i0] = f.x;
-            z[i1] = f.y;
-            if (K4 && (i & 1)) h[i] = half2_bits(f.x * 0.0625f, f.y * 0.0625f);
-            qf[r][t][b][i] = h[i];
-          }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            sum += z[i];
-            y[i] -= z[i];
-          }
-        }
-        if constexpr (K4) {
-          sum += __shfl_xor_sync(kFull, sum, 1);
-          sum += __shfl_xor_sync(kFull, sum, 2);
-          sum *= -8.0f / kKUnit;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) init[r][b][e] = __shfl_sync(kFull, sum, (2 * c + e) * 4);
-        } else {
-          init[r][b][0] = init[r][b][1] = 0.0f;
-        }
-      }
-    }
-
-    float m[R][2], l[R][2], o[R][NB][2][4];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      m[r][0] = m[r][1] = -INFINITY;
-      l[r][0] = l[r][1] = 0.0f;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[r][b][i >> 2][i & 3] = 0.0f;
-    }
-    int vexp = kNoExp;  // weights are multiplied by 2^vexp
-
-    // ---- the tiles ----
+    // ---- the warp's first tiles are on their way while q is prepared ----
     const int64_t head_k = a.kp.head_bytes, head_v = a.vp.head_bytes;
     const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
     auto issue = [&](int ti, int stage) {
@@ -493,6 +418,121 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
     int ti = tile + warp;
 #pragma unroll
     for (int s = 0; s < S - 1; ++s) issue(ti + s * kWarps, s);
+
+    // ---- this lane's columns: rows 2c, 2c + 1 of each group of 8 ----
+    int lo[R][2], hi[R][2];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = min(row0 + 8 * r + 2 * c + e, n_rows - 1);
+        seen_range(span, row / a.group, a.causal, a.window, lo[r][e], hi[r][e]);
+      }
+    // q as operand columns, a warp per row (every warp for itself would cost a
+    // segment as much as 400 of its tokens): scaled, split, and stored as
+    // [block][unit][fragment pair] so that a lane (row, unit) reads 16 bytes
+    // per block
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      constexpr int V = C::QV;
+      const int local = 8 * r + warp, row = row0 + local, ch = lane * V;
+      float x[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[i] = 0.0f;
+      if (row < n_rows && ch < D) {
+        const int tok = row / a.group, head = kvh * a.group + (row - tok * a.group);
+        load_q<V>(a.elem, a.q + int64_t(span.q0 + tok) * a.q_token + int64_t(head) * a.q_head, ch, x);
+      }
+      if constexpr (NB != 3) {
+        if (a.rotate) {  // spans 1, 2, ..., 32 in order: below V in the lane, then across
+#pragma unroll
+          for (int w = 1; w < V; w <<= 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+              if ((i & w) == 0) {
+                const float p = x[i], q = x[i + w];
+                x[i] = __fadd_rn(p, q);
+                x[i + w] = __fsub_rn(p, q);
+              }
+#pragma unroll
+          for (int w = 1; w < 64 / V; w <<= 1)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              const float q = __shfl_xor_sync(kFull, x[i], w);
+              x[i] = (lane & w) ? __fsub_rn(q, x[i]) : __fadd_rn(x[i], q);
+            }
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[i] = __fmul_rn(x[i], 0.125f);
+        }
+      }
+      float top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+      for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
+      // 2^k brings the row's largest value to [2^10, 2^11)
+      const int k = top > 0.0f ? min(10 + 127 - int(__float_as_uint(top) >> 23), 110) : 0;
+      const float up = __int_as_float((127 + k) << 23);
+      if (lane == 0) q_scale[local] = a.scale_log2 * kKUnit * __int_as_float((127 - k) << 23);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        // position of the channel: 4-bit codes (c, c + 2) of a unit's low
+        // channels, of its high ones (read as 16 u: q / 16), then (c + 1, c + 3)
+        const int e = (ch + i) & 31;
+        const int unit = K4 ? (e & 15) >> 2 : e >> 3, high = K4 ? e >> 4 : 0;
+        const int half = K4 ? (e & 1) * 4 + high * 2 + ((e >> 1) & 1) : e & 7;
+        float y = x[i] * up;
+#pragma unroll
+        for (int t = 0; t < TERMS; ++t) {
+          const __half z = __float2half_rn(y);
+          const float f = __half2float(z);
+          if (ch < D)
+            *reinterpret_cast<__half *>(q_rows + local * C::QP + t * D * 2 + ((ch + i) >> 5) * 64 + unit * 16 + half * 2) =
+                KSUB && high ? __float2half_rn(f * 0.0625f) : z;
+          sum += f;
+          y -= f;
+        }
+      }
+      if constexpr (KSUB) {  // the products start at -8 sum(q) of the block
+#pragma unroll
+        for (int w = 1; w < 32 / V; w <<= 1) sum += __shfl_xor_sync(kFull, sum, w);
+        if (lane % (32 / V) == 0 && ch < D) q_init[local * NB + (ch >> 5)] = sum * (-8.0f / kKUnit);
+      }
+    }
+    __syncthreads();
+    uint32_t qf[R][TERMS][NB][4];
+    float init[R][NB][2], qscale[R][2];  // score = qscale * sum_b d_k[b] * product[b]
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(q_rows + (8 * r + g) * C::QP + t * D * 2 + b * 64 + c * 16);
+          qf[r][t][b][0] = v.x, qf[r][t][b][1] = v.y, qf[r][t][b][2] = v.z, qf[r][t][b][3] = v.w;
+        }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        qscale[r][e] = q_scale[8 * r + 2 * c + e];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) init[r][b][e] = KSUB ? q_init[(8 * r + 2 * c + e) * NB + b] : 0.0f;
+      }
+    }
+
+    float m[R][2], l[R][2], o[R][NB][2][4];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r][0] = m[r][1] = kNoMax;
+      l[r][0] = l[r][1] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[r][b][i >> 2][i & 3] = 0.0f;
+    }
+    int vexp = kNoExp;  // weights are multiplied by 2^vexp
+
+    // ---- the tiles ----
     int stage = 0;
     for (; ti < tile_end; ti += kWarps) {
       issue(ti + (S - 1) * kWarps, stage == 0 ? S - 1 : stage - 1);
@@ -521,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
           for (int h = 0; h < 2; ++h) {
             if constexpr (K4) {
               const uint32_t w = kw[h][b], v = w >> 8;
-              A[h][0] = w & 0x000f000fu;
-              A[h][1] = w & 0x00f000f0u;
-              A[h][2] = v & 0x000f000fu;
-              A[h][3] = v & 0x00f000f0u;
+              A[h][0] = KSUB ? w & 0x000f000fu : codes4_lo(w);
+              A[h][1] = KSUB ? w & 0x00f000f0u : codes4_hi(w);
+              A[h][2] = KSUB ? v & 0x000f000fu : codes4_lo(v);
+              A[h][3] = KSUB ? v & 0x00f000f0u : codes4_hi(v);
             } else {
               const uint2 p = codes_to_f16x2(kw[h][2 * b]), q = codes_to_f16x2(kw[h][2 * b + 1]);
               A[h][0] = p.x, A[h][1] = p.y, A[h][2] = q.x, A[h][3] = q.y;
@@ -615,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
             t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
             t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
             const float mn = fmaxf(m[r][e], t);
-            const float al = mn == -INFINITY ? 1.0f : ex2(m[r][e] - mn);
+            const float al = ex2(m[r][e] - mn);
             m[r][e] = mn;
             l[r][e] *= al;
 #pragma unroll
@@ -633,8 +673,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
         for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            // a masked score weighs nothing, even where no score raised the maximum; NaN stays NaN
-            const float p = s[u][r][i] == -INFINITY ? 0.0f : ex2(s[u][r][i] - m[r][i & 1]);
+            const float p = ex2(s[u][r][i] - m[r][i & 1]);  // 0 for a masked score: the maximum is finite
             l[r][i & 1] += p;
             s[u][r][i] = p * vup;
           }
@@ -657,10 +696,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
               // half-word b of both tokens of the pair side by side
               const uint32_t X = __byte_perm(vw[2 * k][b / 2], vw[2 * k + 1][b / 2], (b & 1) ? 0x7632 : 0x5410);
               const uint32_t Y = X >> 8;
-              A[0][2 * k] = hsub2(X & 0x000f000fu, 0x00080008u);      // channels 2g
-              A[0][2 * k + 1] = hsub2(Y & 0x000f000fu, 0x00080008u);  // 2g + 1
-              A[1][2 * k] = hsub2(X & 0x00f000f0u, 0x00800080u);      // 16 + 2g, as 16 u
-              A[1][2 * k + 1] = hsub2(Y & 0x00f000f0u, 0x00800080u);
+              A[0][2 * k] = VSUB ? hsub2(X & 0x000f000fu, 0x00080008u) : codes4_lo(X);      // channels 2g
+              A[0][2 * k + 1] = VSUB ? hsub2(Y & 0x000f000fu, 0x00080008u) : codes4_lo(Y);  // 2g + 1
+              A[1][2 * k] = VSUB ? hsub2(X & 0x00f000f0u, 0x00800080u) : codes4_hi(X);      // 16 + 2g (subnormal: 16 u)
+              A[1][2 * k + 1] = VSUB ? hsub2(Y & 0x00f000f0u, 0x00800080u) : codes4_hi(Y);
             } else {
               // bytes of both tokens interleaved, then the exact binary16 codes
               const uint32_t w0 = vw[2 * k][b], w1 = vw[2 * k + 1][b];
@@ -673,16 +712,29 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
 #pragma unroll
           for (int r = 0; r < R; ++r) {
             float w0 = s[u][r][0] * d0, w1 = s[u][r][1] * d0, w2 = s[u][r][2] * d1, w3 = s[u][r][3] * d1;
+            // The matrix instruction's adder truncates. One term: along the
+            // cache that adds up to some 1e-5 of the output, nothing beside
+            // 16 bits. Two: 16 tokens at a time, then a rounded addition.
+            float fresh[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int t = 0; t < TERMS; ++t) {
               const uint32_t h0 = half2_bits(w0, w1), h1 = half2_bits(w2, w3);
               const uint32_t b0 = movmatrix_trans(h0), b1 = movmatrix_trans(h1);
-              mma16816(o[r][b][0], A[0][0], A[0][1], A[0][2], A[0][3], b0, b1);
-              mma16816(o[r][b][1], A[1][0], A[1][1], A[1][2], A[1][3], b0, b1);
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt) {
+                float(&acc)[4] = TERMS == 1 ? o[r][b][mt] : fresh[mt];
+                mma16816(acc, A[mt][0], A[mt][1], A[mt][2], A[mt][3], b0, b1);
+              }
               if (t + 1 < TERMS) {
                 const float2 f0 = half2_floats(h0), f1 = half2_floats(h1);
                 w0 -= f0.x, w1 -= f0.y, w2 -= f1.x, w3 -= f1.y;
               }
+            }
+            if constexpr (TERMS > 1) {
+#pragma unroll
+              for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[r][b][mt][i] += fresh[mt][i];
             }
           }
         }
@@ -710,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
-              const float f = V4 && mt ? down * 0.0625f : down;
+              const float f = VSUB && mt ? down * 0.0625f : down;
               const int ch = b * 32 + (V4 ? 16 * mt + 2 * g : 4 * g + 2 * mt);
               *reinterpret_cast<float2 *>(dst + ch) = make_float2(o[r][b][mt][e] * f, o[r][b][mt][2 + e] * f);
             }
@@ -722,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
     const int slot = seg_at >= t0 ? 1 : 0;  // partial results: 1 for a segment that starts in this piece
     for (int i = threadIdx.x; i < rows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), ch = (i - r * (D / 4)) * 4;
-      float top = -INFINITY;
+      float top = kNoMax;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, merge_ml[w * ROWS + r].x);
       float sum = 0.0f;
@@ -762,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R>::kCtas))
 // Each head dimension's instantiations are a translation unit of their own.
 template <int NB, int KT, int VT, int R, int TERMS>
 cudaError_t launch_stream_one(const PagedAttnArgs &a, int grid, int min_tiles, bool beside, cudaStream_t stream) {
-  using C = Cfg<NB, KT, VT, R>;
+  using C = Cfg<NB, KT, VT, R, TERMS>;
   cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_paged_stream<NB, KT, VT, R, TERMS>), C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -797,8 +849,10 @@ constexpr bool two_groups(int elem, int rows8) {
   template <>                                                                                                      \
   StreamShape stream_shape<NB>(int kt, int vt, int elem, int rows8) {                                              \
     return by_cache_types(kt, vt, [&](auto k, auto v) {                                                            \
-      using C1 = Cfg<NB, k.value, v.value, 1>;                                                                     \
-      using C2 = Cfg<NB, k.value, v.value, 2>;                                                                     \
+      using C1 = Cfg<NB, k.value, v.value, 1, 1>;                                                                  \
+      using C2 = Cfg<NB, k.value, v.value, 2, 1>;                                                                  \
+      using C1F = Cfg<NB, k.value, v.value, 1, 2>;                                                                 \
+      if (elem == kElemF32) return StreamShape{C1F::ROWS, C1F::TOK, C1F::kCtas};                                   \
       if (two_groups<NB>(elem, rows8)) return StreamShape{C2::ROWS, C2::TOK, C2::kCtas};                           \
       return StreamShape{C1::ROWS, C1::TOK, C1::kCtas};                                                            \
     });                                                                                                            \

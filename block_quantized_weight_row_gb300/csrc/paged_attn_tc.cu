@@ -160,16 +160,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-// Two 4-bit codes (bits 0-3 and 16-19 of w, or with `high` bits 4-7 and
-// 20-23) as binary16 u - 8, exactly: 1024 + u - 1032, (1024 + 16 u) / 16 - 72.
-__device__ __forceinline__ uint32_t codes4_lo(uint32_t w) { return hsub2((w & 0x000f000fu) | 0x64006400u, 0x64086408u); }
-__device__ __forceinline__ uint32_t codes4_hi(uint32_t w) { return hfma2((w & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd480d480u); }
-
 // binary16 exponent of the larger of two scales' magnitudes, at least 1
 __device__ __forceinline__ uint32_t max_exp(uint32_t m) { return max(max(m & 0x7fffu, (m >> 16) & 0x7fffu) >> 10, 1u); }
 
