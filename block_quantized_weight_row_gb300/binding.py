@@ -345,11 +345,23 @@ def kv_bias(rows: torch.Tensor, basis: int = BASIS_PLAIN, out: torch.Tensor | No
 
 
 # ---- paged KV cache ----
-# A decode step makes these calls once per layer, so the host's share counts:
-# plain integers instead of ctypes objects, the device made current only where
-# it is not, checks on attributes that cost no call into the library.
+# The tensors are checked and the library called in _paged.so (csrc/paged_binding.cpp).
 
-_BLOCK_BYTES = {Q4_0: 18, Q8_0: 34}
+_ext = None
+
+
+def _paged():
+    """Load _paged.so (built in-tree by build.py); raise if it is missing."""
+    global _ext
+    if _ext is None:
+        lib()
+        try:
+            from . import _paged as ext
+        except ImportError as e:
+            raise ImportError(f"the paged calls' _paged.so is not built or does not load ({e}); run "
+                              "__graft_entry__.build() (the CUDA path has no fallback)") from e
+        _ext = ext
+    return _ext
 
 
 @dataclasses.dataclass
@@ -376,57 +388,6 @@ class PagedCache:
             pools.append(torch.empty((n_pages, n_kv_heads, n // n_kv_heads), dtype=torch.uint8, device=device))
         return cls(pools[0], pools[1], page_size, head_dim, k_type, v_type, k_basis)
 
-    def _struct(self):
-        k, v = self.k_pages, self.v_pages
-        ks, vs, n = k.shape, v.shape, self.page_size * self.head_dim
-        for name, t, shape, kind in (("k_pages", k, ks, self.k_type), ("v_pages", v, vs, self.v_type)):
-            _cuda(t, name)
-            if t.dtype is not torch.uint8 or len(shape) != 3:
-                raise TypeError(f"{name} must be uint8 (n_pages, n_kv_heads, bytes)")
-            if kind in _BLOCK_BYTES and shape[2] * QK != n * _BLOCK_BYTES[kind]:
-                raise ValueError(f"{name} has {shape[2]} bytes per head page, not page_size * head_dim / 32 blocks")
-        if ks[:2] != vs[:2] or k.device != v.device:
-            raise ValueError("k_pages and v_pages must have the same pages, heads and device")
-        return _CacheStruct(k.data_ptr(), v.data_ptr(), ks[0], self.page_size, ks[1], self.head_dim, self.k_type,
-                            self.v_type, self.k_basis)
-
-
-def _rows(t, name, device, heads, dim, dtype=None):
-    """A tensor (tokens, heads, head_dim) of an element type the paged calls
-    take, channels contiguous; other strides are free."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in ELEM or (dtype is not None and t.dtype is not dtype):
-        raise TypeError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    shape = t.shape
-    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be (tokens, {heads if heads is not None else 'heads'}, {dim})")
-    strides = t.stride()
-    if strides[2] != 1:
-        raise ValueError(f"the channels of {name} must be contiguous")
-    return strides
-
-
-def _index(t, name, device, dtype, shape):
-    _cuda(t, name)
-    if t.dtype is not dtype or t.shape != shape:
-        raise TypeError(f"{name} must be {dtype} of shape {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-    return t.data_ptr()
-
-
-def _launch(device, call):
-    """call(library), with the device current and the library on its current torch stream."""
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _launch(device, call)
-    L = lib()
-    L.bq_set_stream(torch._C._cuda_getCurrentRawStream(device.index))
-    return call(L)
-
 
 def paged_kv_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
                    bias: torch.Tensor | None = None, bias_basis: int | None = None) -> None:
@@ -434,18 +395,10 @@ def paged_kv_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: t
     bf16, any token and head strides) into the cache at slots (int64, page *
     page_size + place; -1 skips a token). bias (n_kv_heads, head_dim) fp32:
     subtracted from K, calibrated in bias_basis (default: the cache's)."""
-    s = cache._struct()
-    dev, H, D = cache.k_pages.device, s.n_kv_heads, cache.head_dim
-    ks = _rows(k, "k", dev, H, D)
-    vs = _rows(v, "v", dev, H, D, k.dtype)
-    T = k.shape[0]
-    if v.shape[0] != T:
-        raise ValueError("k and v must have the same shape")
-    at = _index(slots, "slots", dev, torch.int64, (T,))
-    b = None if bias is None else _index(bias, "bias", dev, torch.float32, (H, D))
-    _check(_launch(dev, lambda L: L.bq_paged_kv_write(
-        s, ELEM[k.dtype], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], b,
-        cache.k_basis if bias_basis is None else bias_basis, at, T)), "bq_paged_kv_write")
+    r = (_ext or _paged()).kv_write(cache.k_pages, cache.v_pages, cache.page_size, cache.head_dim, cache.k_type,
+                                    cache.v_type, cache.k_basis, k, v, slots, bias, -1 if bias_basis is None else bias_basis)
+    if r is not None:
+        _check(r, "bq_paged_kv_write")
 
 
 def paged_kv_read(cache: PagedCache, slots: torch.Tensor, dtype: torch.dtype = torch.float32,
@@ -454,21 +407,12 @@ def paged_kv_read(cache: PagedCache, slots: torch.Tensor, dtype: torch.dtype = t
                   out_v: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """The rows at slots (int64; -1: zeros) as (K, V), each (tokens,
     n_kv_heads, head_dim) of dtype; K out of the cache's basis, plus bias."""
-    s = cache._struct()
-    dev, H, T = cache.k_pages.device, s.n_kv_heads, slots.numel()
-    shape = (T, H, cache.head_dim)
-    at = _index(slots, "slots", dev, torch.int64, (T,))
-    b = None if bias is None else _index(bias, "bias", dev, torch.float32, shape[1:])
-    if dtype not in ELEM:
-        raise TypeError("dtype must be float32, float16 or bfloat16")
-    if out_k is None:
-        out_k = torch.empty(shape, dtype=dtype, device=dev)
-    if out_v is None:
-        out_v = torch.empty(shape, dtype=dtype, device=dev)
-    kp, vp = _index(out_k, "out_k", dev, dtype, shape), _index(out_v, "out_v", dev, dtype, shape)
-    _check(_launch(dev, lambda L: L.bq_paged_kv_read(
-        s, ELEM[dtype], kp, vp, b, cache.k_basis if bias_basis is None else bias_basis, at, T)), "bq_paged_kv_read")
-    return out_k, out_v
+    r = (_ext or _paged()).kv_read(cache.k_pages, cache.v_pages, cache.page_size, cache.head_dim, cache.k_type,
+                                   cache.v_type, cache.k_basis, slots, ELEM.get(dtype, -1), bias,
+                                   -1 if bias_basis is None else bias_basis, out_k, out_v)
+    if type(r) is int:
+        _check(r, "bq_paged_kv_read")
+    return r
 
 
 def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len: torch.Tensor,
@@ -480,41 +424,12 @@ def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len
     max_pages). The index tensors are int32 on the device; max_q_len and
     max_kv_len are their bounds on the host. window: tokens a causal query
     sees (0: all). lse: optional fp32 (tokens, n_heads), written."""
-    s = cache._struct()
-    dev, D = cache.k_pages.device, cache.head_dim
-    qs = _rows(q, "q", dev, None, D)
-    n_q, H, _ = q.shape
-    B = kv_len.numel()
-    lens = _index(kv_len, "kv_len", dev, torch.int32, (B,))
-    starts = _index(q_start, "q_start", dev, torch.int32, (B + 1,))
-    pages = page_table.shape[-1]
-    table = _index(page_table, "page_table", dev, torch.int32, (B, pages))
-    if out is None:
-        out = torch.empty((n_q, H, D), dtype=q.dtype, device=dev)
-    os = _rows(out, "out", dev, H, D, q.dtype)
-    if out.shape[0] != n_q:
-        raise ValueError("out must have q's shape")
-    lp = None if lse is None else _index(lse, "lse", dev, torch.float32, (n_q, H))
-    e, c = ELEM[q.dtype], 1 if causal else 0
-
-    def call(L):
-        need = L.bq_paged_attn_workspace_size(s, e, B, n_q, max_q_len, max_kv_len, H, c, window)
-        # a workspace of this call's own, from the current stream's pool: calls
-        # on other streams and captured launches never share it
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
-        L.bq_set_workspace(ws.data_ptr(), ws.numel())
-        r = L.bq_paged_attn(s, e, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os[0], os[1], lp, starts, lens, table,
-                            pages, B, n_q, max_q_len, max_kv_len, H, scale, c, window)
-        if r == 0:
-            L.bq_set_workspace(None, 0)
-        return r
-
-    try:
-        _check(_launch(dev, call), "bq_paged_attn")
-    except Exception:
-        lib().bq_set_workspace(None, 0)
-        raise
-    return out
+    r = (_ext or _paged()).attn(cache.k_pages, cache.v_pages, cache.page_size, cache.head_dim, cache.k_type,
+                                cache.v_type, cache.k_basis, q, q_start, kv_len, page_table, scale, max_q_len,
+                                max_kv_len, causal, window, out, lse)
+    if type(r) is tuple:
+        raise BQError(r[0], f"bq_paged_attn: {r[1]}")
+    return r
 
 
 def block_dots(t: int, w_blocks: torch.Tensor, xq_blocks: torch.Tensor, M: int, K: int) -> torch.Tensor:

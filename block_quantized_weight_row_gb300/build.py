@@ -18,6 +18,9 @@ LIB = os.path.join(HERE, "libbq.so")
 # measurement probe (tensor-op rates for the roofline denominators); not part of the libbq ABI
 PROBE_SRC = "probe_mma.cu"
 PROBE_LIB = os.path.join(HERE, "libbq_probe.so")
+# the paged calls' host side (CPython + torch headers, no device code)
+EXT_SRC = "paged_binding.cpp"
+EXT_LIB = os.path.join(HERE, "_paged.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["bq_api.cu", "quantize.cu", "gemv.cu", "gemv_seq.cu", "gemm.cu", "gemm_tc.cu", "gemm_noalloc.cu", "attn.cu",
@@ -33,6 +36,25 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+def ext_commands(tmp):
+    """Compile and link lines of the paged calls' host side."""
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    abi = int(torch.compiled_with_cxx11_abi())
+    obj = os.path.join(OBJ_DIR, EXT_SRC.replace(".cpp", ".o"))
+    compile_ = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={abi}", *[x for i in inc for x in ("-isystem", i)],
+                "-c", os.path.join(CSRC, EXT_SRC), "-o", obj]
+    libs = os.path.join(t, "lib")
+    link = ["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libbq.so", f"-L{libs}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    return obj, compile_, link
 
 
 def _deps():
@@ -63,7 +85,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"compiler failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stderr
 
     probe_src = os.path.join(CSRC, PROBE_SRC)
@@ -71,16 +93,24 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     build_probe = force or _stale(PROBE_LIB, [probe_src, __file__] + deps)
     if build_probe:
         jobs.append([cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-shared", probe_src, "-o", probe_tmp])
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+    ext_tmp = EXT_LIB + f".tmp{os.getpid()}"
+    ext_obj, ext_compile, ext_link = ext_commands(ext_tmp)
+    build_ext = force or _stale(ext_obj, [os.path.join(CSRC, EXT_SRC), __file__, os.path.join(INCLUDE, "bq.h")])
+    if build_ext:
+        jobs.append(ext_compile)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 2) as ex:
         for out in ex.map(run, jobs):
             if verbose and out:
                 print(out, file=sys.stderr)
     if build_probe:
         os.replace(probe_tmp, PROBE_LIB)
-    if force or any("-c" in j for j in jobs) or _stale(LIB, objs):
+    if force or any(j[0] == cc and "-c" in j for j in jobs) or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
+    if build_ext or _stale(EXT_LIB, [ext_obj]):
+        run(ext_link)
+        os.replace(ext_tmp, EXT_LIB)
     return LIB
 
 
