@@ -104,47 +104,70 @@ __device__ __forceinline__ int chan8(int c, int half) {
   return TYPE == kTypeQ4_0 ? 4 * c + 16 * half : 8 * c + 4 * half;
 }
 
+// Butterflies on fp32 pairs. In the lane: (P[i], P[i + h]) -> sum, difference
+// for h = 1, 2, .. N / 2 pairs; across lanes: lanes m apart.
+template <int N>
+__device__ __forceinline__ void hadamard_pairs(uint64_t (&P)[N]) {
+  const uint64_t m1 = pack2(__float_as_uint(-1.0f), __float_as_uint(-1.0f));
+#pragma unroll
+  for (int h = 1; h < N; h <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & h) == 0) {
+        const uint64_t t = P[i];
+        P[i] = fadd2(t, P[i + h]);
+        P[i + h] = ffma2(m1, P[i + h], t);
+      }
+}
+template <int N>
+__device__ __forceinline__ void hadamard_cross(uint64_t (&P)[N], int m, int lane) {
+  const float s = (lane & m) ? -1.0f : 1.0f;
+  const uint64_t s2 = pack2(__float_as_uint(s), __float_as_uint(s));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t lo = __shfl_xor_sync(kFull, uint32_t(P[i]), m), hi = __shfl_xor_sync(kFull, uint32_t(P[i] >> 32), m);
+    P[i] = ffma2(s2, P[i], pack2(lo, hi));
+  }
+}
+
 // The butterflies of a 64-channel group held by 4 lanes (two blocks x 8
 // values each), spans in order 1, 2, ..., 32, then 1/8.
 template <int TYPE>
 __device__ __forceinline__ void hadamard64_4lanes(float (&x)[2][8]) {
   const int lane = threadIdx.x & 31;
-  auto inner = [&](int bit) {  // span within the lane: bit of the value index
+  uint64_t P[2][4];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < 2; ++b) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if ((i & bit) == 0) {
-          const float p = x[b][i], q = x[b][i + bit];
-          x[b][i] = __fadd_rn(p, q);
-          x[b][i + bit] = __fsub_rn(p, q);
+    for (int i = 0; i < 4; ++i)  // span 1
+      P[b][i] = pack2(__float_as_uint(__fadd_rn(x[b][2 * i], x[b][2 * i + 1])), __float_as_uint(__fsub_rn(x[b][2 * i], x[b][2 * i + 1])));
+    const uint64_t m1 = pack2(__float_as_uint(-1.0f), __float_as_uint(-1.0f));
+    auto inner = [&](int h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((i & h) == 0) {
+          const uint64_t t = P[b][i];
+          P[b][i] = fadd2(t, P[b][i + h]);
+          P[b][i + h] = ffma2(m1, P[b][i + h], t);
         }
-  };
-  auto cross = [&](int m) {
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_xor_sync(kFull, x[b][i], m);
-        x[b][i] = (lane & m) ? __fsub_rn(o, x[b][i]) : __fadd_rn(x[b][i], o);
-      }
-  };
-  inner(1);
-  inner(2);
-  if constexpr (TYPE == kTypeQ4_0) {  // channel bits 2, 3 are the lane's, bit 4 the value's
-    cross(1);
-    cross(2);
-    inner(4);
-  } else {  // channel bit 2 is the value's, bits 3, 4 the lane's
-    inner(4);
-    cross(1);
-    cross(2);
+    };
+    inner(1);  // span 2
+    if constexpr (TYPE == kTypeQ4_0) {  // channel bits 2, 3 are the lane's, bit 4 the value's
+      hadamard_cross<4>(P[b], 1, lane);
+      hadamard_cross<4>(P[b], 2, lane);
+      inner(2);
+    } else {  // channel bit 2 is the value's, bits 3, 4 the lane's
+      inner(2);
+      hadamard_cross<4>(P[b], 1, lane);
+      hadamard_cross<4>(P[b], 2, lane);
+    }
   }
+  const uint64_t e2 = pack2(__float_as_uint(0.125f), __float_as_uint(0.125f)), m1 = pack2(__float_as_uint(-1.0f), __float_as_uint(-1.0f));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float p = x[0][i], q = x[1][i];
-    x[0][i] = __fmul_rn(__fadd_rn(p, q), 0.125f);
-    x[1][i] = __fmul_rn(__fsub_rn(p, q), 0.125f);
+  for (int i = 0; i < 4; ++i) {  // span 32
+    const uint64_t p = fmul2(fadd2(P[0][i], P[1][i]), e2), q = fmul2(ffma2(m1, P[1][i], P[0][i]), e2);
+    x[0][2 * i] = __uint_as_float(uint32_t(p)), x[0][2 * i + 1] = __uint_as_float(uint32_t(p >> 32));
+    x[1][2 * i] = __uint_as_float(uint32_t(q)), x[1][2 * i + 1] = __uint_as_float(uint32_t(q >> 32));
   }
 }
 

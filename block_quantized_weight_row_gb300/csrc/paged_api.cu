@@ -210,6 +210,7 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
   if (!K || !V || !slots) return report_error(BQ_ERR_INVALID_ARG, "%s: null pointer", who);
   if (!aligned(K, 16) || !aligned(V, 16) || !aligned(slots, 8))
     return report_error(BQ_ERR_ALIGN, "%s: K and V must be 16-byte, slots 8-byte aligned", who);
+  if (cache->n_pages == 0) return report_error(BQ_ERR_INVALID_ARG, "%s: the cache has no pages", who);
   const uint64_t out = uint64_t(n_tokens) * uint64_t(H * D) * uint64_t(es);
   const Range ins[4] = {{cache->k_pages, c.k_bytes}, {cache->v_pages, c.v_bytes}, {bias, uint64_t(H * D) * 4}, {slots, uint64_t(n_tokens) * 8}};
   for (const Range &p : ins)
