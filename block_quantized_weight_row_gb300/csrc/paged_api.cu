@@ -242,6 +242,7 @@ int bq_paged_attn(const bq_paged_cache *cache, int elem, const void *q, int64_t 
   if (st != BQ_OK) return st;
   if (!std::isfinite(scale)) return report_error(BQ_ERR_INVALID_ARG, "%s: scale is not finite", who);
   if (n_seqs == 0 || n_q == 0) return report_ok();
+  if (cache->n_pages == 0) return report_error(BQ_ERR_INVALID_ARG, "%s: the cache has no pages", who);
   const int64_t D = cache->head_dim;
   const int es = elem_bytes(elem);
   uint64_t qb, ob;

@@ -59,10 +59,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// d = a b + (c0, c1, c0, c1)
+__device__ __forceinline__ void mma16816_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1, float c0, float c1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -74,6 +83,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -174,11 +189,13 @@ __device__ __forceinline__ void lds_scales(const uint8_t *tile, int t, uint32_t 
 }
 template <int N>
 __device__ __forceinline__ float scale_of(const uint32_t (&w)[N], int b) {
-  return half_bits_to_float((b & 1) ? w[b / 2] >> 16 : w[b / 2]);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[b / 2]));
+  return (b & 1) ? f.y : f.x;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// bytes: 16, or 0 to fill with zeros
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -343,6 +360,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
 
   uint8_t *ring = smem + warp * S * C::STAGE;
   const uint32_t ring_u = smem_u32(ring);
+  // where this lane's 16-byte chunks of a 16-token tile go
+  uint32_t dst_k[(16 * CK + 31) / 32], dst_v[(16 * CV + 31) / 32];
+#pragma unroll
+  for (int i = 0; i < (16 * CK + 31) / 32; ++i) {
+    const int q = lane + 32 * i;
+    dst_k[i] = uint32_t(q / CK * C::RBK + (swz_k<CK>(q / CK, q % CK) << 4));
+  }
+#pragma unroll
+  for (int i = 0; i < (16 * CV + 31) / 32; ++i) {
+    const int q = lane + 32 * i;
+    dst_v[i] = uint32_t(16 * C::RBK + q / CV * C::RBV + (swz_v<CV>(q / CV, q % CV) << 4));
+  }
+  const bool scales_v = lane >= 2 * NB;
+  const uint32_t dst_s = 16 * (C::RBK + C::RBV) + lane * 16;
+  const int64_t scale_at = (scales_v ? a.vp.scale_off : a.kp.scale_off) + (scales_v ? lane - 2 * NB : lane) * 16;
   float *merge_o = reinterpret_cast<float *>(smem);
   float2 *merge_ml = reinterpret_cast<float2 *>(smem + kWarps * ROWS * OP * 4);
   uint8_t *q_rows = smem + C::kOffQ;
@@ -374,43 +406,35 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
     // ---- the warp's first tiles are on their way while q is prepared ----
     const int64_t head_k = a.kp.head_bytes, head_v = a.vp.head_bytes;
     const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
+    const uint8_t *kh = a.kp.base + int64_t(kvh) * head_k, *vh = a.vp.base + int64_t(kvh) * head_v;
+    const int64_t page_k = head_k * a.sh.n_kv, page_v = head_v * a.sh.n_kv;
+    // A stage: 16-token tiles, each within one page. A tile past what any row
+    // sees, or on a page outside the pool (never read: reported), is zero-filled
+    // with the pool's first tile as the address.
     auto issue = [&](int ti, int stage) {
       if (ti < tile_end) {
 #pragma unroll
         for (int u = 0; u < TT; ++u) {
           const int tok = ti * TOK + u * 16;
-          bool ok = tok < hi_any;
+          const bool seen = tok < hi_any;
           const int pi = token_page(a.sh, tok);
-          int page = ok ? __ldg(table + pi) : 0;
-          if (uint32_t(page) >= uint64_t(a.sh.n_pages)) {  // never read outside the pool
+          uint32_t page = seen ? uint32_t(__ldg(table + pi)) : 0u;
+          uint32_t place = uint32_t(tok - pi * a.sh.page_size), bytes = seen ? 16u : 0u;
+          if (page >= uint64_t(a.sh.n_pages)) {
             if (lane == 0) atomicOr(a.err, kErrIndex);
-            page = 0;
-            ok = false;
+            page = place = bytes = 0u;
           }
-          const int place = tok - pi * a.sh.page_size;
-          const uint8_t *hk = a.kp.base + (int64_t(page) * a.sh.n_kv + kvh) * head_k;
-          const uint8_t *hv = a.vp.base + (int64_t(page) * a.sh.n_kv + kvh) * head_v;
+          const uint8_t *tk = kh + int64_t(page) * page_k, *tv = vh + int64_t(page) * page_v;
           const uint32_t base = ring_u + stage * C::STAGE + u * C::SUB;
-          const uint8_t *sk = hk + (ok ? place * C::RBK : 0), *sv = hv + (ok ? place * C::RBV : 0);
+          const uint8_t *sk = tk + place * C::RBK + lane * 16, *sv = tv + place * C::RBV + lane * 16;
 #pragma unroll
-          for (int i = 0; i < (16 * CK + 31) / 32; ++i) {
-            const int q = lane + 32 * i;
-            if (16 * CK % 32 == 0 || q < 16 * CK)
-              cp_async16(base + (q / CK) * C::RBK + (swz_k<CK>(q / CK, q % CK) << 4), ok ? sk + q * 16 : sk, ok);
-          }
+          for (int i = 0; i < (16 * CK + 31) / 32; ++i)
+            if (16 * CK % 32 == 0 || lane + 32 * i < 16 * CK) cp_async16(base + dst_k[i], sk + i * 512, bytes);
 #pragma unroll
-          for (int i = 0; i < (16 * CV + 31) / 32; ++i) {
-            const int q = lane + 32 * i;
-            if (16 * CV % 32 == 0 || q < 16 * CV)
-              cp_async16(base + 16 * C::RBK + (q / CV) * C::RBV + (swz_v<CV>(q / CV, q % CV) << 4), ok ? sv + q * 16 : sv, ok);
-          }
+          for (int i = 0; i < (16 * CV + 31) / 32; ++i)
+            if (16 * CV % 32 == 0 || lane + 32 * i < 16 * CV) cp_async16(base + dst_v[i], sv + i * 512, bytes);
           // scales: 2 NB chunks of K's, then as many of V's
-          if (lane < 4 * NB) {
-            const bool is_v = lane >= 2 * NB;
-            const int q = is_v ? lane - 2 * NB : lane;
-            const uint8_t *ss = (is_v ? hv + a.vp.scale_off : hk + a.kp.scale_off) + (ok ? place * NB * 2 + q * 16 : 0);
-            cp_async16(base + 16 * (C::RBK + C::RBV) + lane * 16, ss, ok);
-          }
+          if (lane < 4 * NB) cp_async16(base + dst_s, (scales_v ? tv : tk) + (place * NB * 2 + scale_at), bytes);
         }
       }
       cp_commit();
@@ -472,8 +496,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
       for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
       // 2^k brings the row's largest value to [2^10, 2^11)
       const int k = top > 0.0f ? min(10 + 127 - int(__float_as_uint(top) >> 23), 110) : 0;
-      const float up = __int_as_float((127 + k) << 23);
-      if (lane == 0) q_scale[local] = a.scale_log2 * kKUnit * __int_as_float((127 - k) << 23);
+      // (the scale's sign goes into q, and a scale of 0 leaves scores of ~0)
+      const float up = copysignf(__int_as_float((127 + k) << 23), a.scale_log2);
+      if (lane == 0) q_scale[local] = fmaxf(fabsf(a.scale_log2), 1e-30f) * kKUnit * __int_as_float((127 - k) << 23);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -520,10 +545,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
       }
     }
 
-    float m[R][2], l[R][2], o[R][NB][2][4];
+    float m[R][2], l[R][2], limit[R][2], o[R][NB][2][4];  // limit: the unscaled score that raises m
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       m[r][0] = m[r][1] = kNoMax;
+      limit[r][0] = limit[r][1] = kNoMax;
       l[r][0] = l[r][1] = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -573,10 +599,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
           const float d0 = scale_of(ks[0], b), d1 = scale_of(ks[1], b);
 #pragma unroll
           for (int r = 0; r < R; ++r) {
-            float acc[4] = {init[r][b][0], init[r][b][1], init[r][b][0], init[r][b][1]};
+            float acc[4];
 #pragma unroll
             for (int t = TERMS - 1; t >= 0; --t) {
-              mma16816(acc, A[0][0], A[1][0], A[0][1], A[1][1], qf[r][t][b][0], qf[r][t][b][1]);
+              if (t == TERMS - 1)
+                mma16816_from(acc, A[0][0], A[1][0], A[0][1], A[1][1], qf[r][t][b][0], qf[r][t][b][1], init[r][b][0], init[r][b][1]);
+              else
+                mma16816(acc, A[0][0], A[1][0], A[0][1], A[1][1], qf[r][t][b][0], qf[r][t][b][1]);
               mma16816(acc, A[0][2], A[1][2], A[0][3], A[1][3], qf[r][t][b][2], qf[r][t][b][3]);
             }
             s[u][r][0] = fmaf(d0, acc[0], s[u][r][0]);
@@ -585,10 +614,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
             s[u][r][3] = fmaf(d1, acc[3], s[u][r][3]);
           }
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[u][r][i] *= qscale[r][i & 1];
       }
       // V scales of the lane's two tokens per 16; outside what any row sees
       // they count as zero, whatever the page holds there
@@ -612,25 +637,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
                 if (tok < lo[r][e] || tok >= hi[r][e]) s[u][r][2 * h + e] = -INFINITY;
           }
 #pragma unroll
-          for (int i = 0; i < (NB + 1) / 2; ++i) vmax = __vmaxu2(vmax, vs[u][h][i] & 0x7fff7fffu);
+          for (int i = 0; i < (NB + 1) / 2; ++i) vmax = max_u16x2(vmax, vs[u][h][i]);  // scales are not negative
         }
       // power of two that brings the largest V scale seen to [2^5, 2^6): the
       // binary16 exponent (subnormals count as the smallest normal) decides
-      vmax = __reduce_max_sync(kFull, max(vmax & 0xffffu, vmax >> 16));
+      vmax = __reduce_max_sync(kFull, max(vmax & 0x7fffu, (vmax >> 16) & 0x7fffu));
       const int need = 20 - max(int(vmax >> 10), 1);  // 2^5 / 2^(e - 15)
       if (need < vexp) {  // warp-uniform; rare after the first tile
         if (vexp != kNoExp) {
           const float f = __int_as_float((127 + need - vexp) << 23);
 #pragma unroll
-          for (int r = 0; r < R; ++r)
+          for (int r = 0; r < R; ++r) {
+            l[r][0] *= f;
+            l[r][1] *= f;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
               for (int i = 0; i < 8; ++i) o[r][b][i >> 2][i & 3] *= f;
+          }
         }
         vexp = need;
       }
-      const float vup = __int_as_float((127 + vexp) << 23);
 
       // ---- running maximum ----
       bool raise = false;
@@ -643,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
 #pragma unroll
           for (int u = 1; u < TT; ++u) t = fmaxf(t, fmaxf(s[u][r][e], s[u][r][2 + e]));
           top[r][e] = t;
-          raise = raise || t > m[r][e] + kRaise;
+          raise = raise || t > limit[r][e];
         }
       if (__any_sync(kFull, raise)) {
 #pragma unroll
@@ -654,9 +681,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
             t = fmaxf(t, __shfl_xor_sync(kFull, t, 4));
             t = fmaxf(t, __shfl_xor_sync(kFull, t, 8));
             t = fmaxf(t, __shfl_xor_sync(kFull, t, 16));
-            const float mn = fmaxf(m[r][e], t);
+            // a whole number, so that the weights' power of two joins it exactly
+            const float mn = fmaxf(m[r][e], ceilf(t * qscale[r][e]));
             const float al = ex2(m[r][e] - mn);
             m[r][e] = mn;
+            limit[r][e] = (mn + kRaise) / qscale[r][e];
             l[r][e] *= al;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
@@ -668,15 +697,17 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
           }
       }
 #pragma unroll
-      for (int u = 0; u < TT; ++u)
+      for (int r = 0; r < R; ++r) {
+        const float off[2] = {float(vexp) - m[r][0], float(vexp) - m[r][1]};
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int u = 0; u < TT; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float p = ex2(s[u][r][i] - m[r][i & 1]);  // 0 for a masked score: the maximum is finite
+            const float p = ex2(fmaf(s[u][r][i], qscale[r][i & 1], off[i & 1]));  // 0 for a masked score: the maximum is finite
             l[r][i & 1] += p;
-            s[u][r][i] = p * vup;
+            s[u][r][i] = p;
           }
+      }
 
       // ---- weights times V ----
 #pragma unroll
@@ -756,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
           l[r][e] += __shfl_xor_sync(kFull, l[r][e], 8);
           l[r][e] += __shfl_xor_sync(kFull, l[r][e], 16);
           const int row = warp * ROWS + 8 * r + 2 * c + e;
-          if (g == 0) merge_ml[row] = make_float2(m[r][e], l[r][e]);
+          if (g == 0) merge_ml[row] = make_float2(m[r][e], l[r][e] * (vexp == kNoExp ? 0.0f : __int_as_float((127 - vexp) << 23)));
           float *dst = merge_o + row * OP;
 #pragma unroll
           for (int b = 0; b < NB; ++b)
