@@ -770,3 +770,12 @@ def test_many_row_timeout_path_returns_error(bq):
     finally:
         L.bq_set_spin_limit(-1)
     b.check()
+
+
+@gpu
+@pytest.mark.parametrize("seed", [1, 2])
+def test_serving_example(bq, seed):
+    from examples import paged_serving
+    lines = []
+    assert paged_serving.main(seed, lines.append) <= paged_serving.TOLERANCE
+    assert "2: 130" in lines[5]
