@@ -160,8 +160,15 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// binary16 exponent of the larger of two scales' magnitudes, at least 1
-__device__ __forceinline__ uint32_t max_exp(uint32_t m) { return max(max(m & 0x7fffu, (m >> 16) & 0x7fffu) >> 10, 1u); }
+// Exponent k of the power of two that brings the largest of a warp's scales
+// (pairs of binary16, not negative) to [2^5, 2^6); at most 2^15, which
+// binary16 holds (scales below 2^-10 then stay below 2^5, all the same exact).
+__device__ __forceinline__ int scale_up(uint32_t m) {
+  const uint32_t e = __reduce_max_sync(kFull, max(m & 0x7fffu, (m >> 16) & 0x7fffu)) >> 10;
+  return min(20 - int(e), 15);
+}
+// 2^k twice, -14 <= k <= 15
+__device__ __forceinline__ uint32_t half2_pow2(int k) { return uint32_t(15 + k) * 0x04000400u; }
 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
@@ -276,10 +283,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = mi->tmem;
   const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
-  // Entry of the page table for token `tok` (for its last seen token past it).
-  // It is looked at a tile later, so that nothing waits for it here. n > 0.
-  auto page_of = [&](int tok) { return ldg_now(table + token_page(a.sh, min(tok, hi_any - 1))); };
-  auto place_of = [&](int tok) { return tok - token_page(a.sh, tok) * a.sh.page_size; };
+  // Page-table entry and place of the 8 or 16 tokens from `tok` (page sizes are
+  // multiples of 16); past the last seen token only the entry's address has to
+  // be valid. The entry is looked at a tile later, so that nothing waits for it
+  // here. n > 0.
+  auto find_page = [&](int tok, int &entry, int &place) {
+    const int p = token_page(a.sh, min(tok, hi_any - 1));
+    entry = ldg_now(table + p);
+    place = tok - p * a.sh.page_size;
+  };
 
   if (warp < 8) {
     // ---- softmax: thread = row ----
@@ -491,13 +503,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- K operand: lane = (token of 8, unit), four groups of 8 tokens per thread ----
     const int w = warp - 8, tk = lane & 7, c = lane >> 3;
     uint32_t code[4][UK / 4], sc[4][NB / 2];
-    int next[4];  // pages of the next tile to load, asked for a tile ahead
+    int next[2], place[2];  // of the next tile to load (16 tokens each), asked for a tile ahead
     auto pages = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
-        next[i] = page_of(tok);
-      }
+      for (int h = 0; h < 2; ++h) find_page((j0 + j) * kTile + w * 32 + 16 * h, next[h], place[h]);
     };
     // Loads have no branch around them (at its end they would be waited for):
     // where there is nothing to read, q's first bytes stand in and the scale
@@ -507,21 +516,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       live = 0;
       bool wrong = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk;
-        const bool want = tok >= lo_any && tok < hi_any, ok = uint32_t(next[i]) < uint64_t(a.sh.n_pages);
-        live |= uint32_t(want && ok) << i;
+      for (int h = 0; h < 2; ++h) {
+        const int tok0 = (j0 + j) * kTile + w * 32 + 16 * h;
+        const bool want = tok0 < hi_any && tok0 + 16 > lo_any, ok = want && uint32_t(next[h]) < uint64_t(a.sh.n_pages);
         wrong = wrong || (want && !ok);
+        const uint8_t *hp = a.kp.base + (int64_t(next[h]) * a.sh.n_kv + kvh) * a.kp.head_bytes;
+        const uint8_t *pc = ok ? hp + ((place[h] + tk) * RBK + c * UK) : a.q;
+        const uint8_t *ps = ok ? hp + a.kp.scale_off + (place[h] + tk) * (NB * 2) : a.q;
+        const int code_step = ok ? 8 * RBK : 0, scale_step = ok ? 8 * NB * 2 : 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int tok = tok0 + 8 * k + tk;
+          live |= uint32_t(ok && tok >= lo_any && tok < hi_any) << (2 * h + k);
+          ldg_piece<UK>(pc + k * code_step, code[2 * h + k]);
+          ldg_piece<NB * 2>(ps + k * scale_step, sc[2 * h + k]);
+        }
       }
       if (wrong) atomicOr(a.err, kErrIndex);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int tok = (j0 + j) * kTile + w * 32 + i * 8 + tk, place = place_of(tok);
-        const bool ok = live >> i & 1;
-        const uint8_t *hp = a.kp.base + (int64_t(next[i]) * a.sh.n_kv + kvh) * a.kp.head_bytes;
-        ldg_piece<UK>(ok ? hp + place * RBK + c * UK : a.q, code[i]);
-        ldg_piece<NB * 2>(ok ? hp + a.kp.scale_off + place * NB * 2 : a.q, sc[i]);
-      }
       pages(j + 1);
     };
     if (n > 0) {
@@ -529,26 +540,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       load(0);
     }
     for (int j = 0; j < n; ++j) {
-      uint32_t e = 1;
+      uint32_t e = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) {
           sc[i][k] = live >> i & 1 ? sc[i][k] : 0;
-          e = max(e, max_exp(sc[i][k]));
+          e = max_u16x2(e, sc[i][k]);
         }
-      const int kk = 20 - int(__reduce_max_sync(kFull, e));
+      const int kk = scale_up(e);
       if (!pa_wait_warp(&bar[kKEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
       if (lane == 0) mi->kx[j & 3][w] = kk;
-      const float up = pow2(kk);
+      const uint32_t up = half2_pow2(kk);
       uint8_t *ks = sm + C::kOffK + (j & 1) * C::kKBytes;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int r = w * 32 + i * 8 + tk;
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const float d = scale_of(sc[i], b) * up;
-          const uint32_t d2 = half2_bits(d, d);
+          const uint32_t d = hmul2(sc[i][b / 2], up), d2 = __byte_perm(d, d, (b & 1) ? 0x3232 : 0x1010);
           uint4 v;
           if constexpr (K4) {
             const uint32_t x = code[i][b], y = x >> 8;
@@ -570,14 +580,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- V operand, transposed: thread = (8 tokens, unit g): 8 tokens of 4 channels per block ----
     const int w = warp - 12, g = lane & 7, grp = w * 4 + (lane >> 3);
     uint32_t code[8][(UV + 3) / 4], sc[8][NB / 2];
-    int next = 0;  // page of the next tile to load
-    auto pages = [&](int j) {
-      const int tok0 = (j0 + j) * kTile + grp * 8;
-      next = page_of(tok0);
-    };
+    int next = 0, place = 0;  // of the next tile to load
+    auto pages = [&](int j) { find_page((j0 + j) * kTile + grp * 8, next, place); };
     uint32_t live = 0;
     auto load = [&](int j) {  // no branch around the loads, as for K
-      const int tok0 = (j0 + j) * kTile + grp * 8, place = place_of(tok0);
+      const int tok0 = (j0 + j) * kTile + grp * 8;
       const bool want = tok0 < hi_any && tok0 + 8 > lo_any, ok = want && uint32_t(next) < uint64_t(a.sh.n_pages);
       if (want && !ok) atomicOr(a.err, kErrIndex);
       const uint8_t *hp = a.vp.base + (int64_t(next) * a.sh.n_kv + kvh) * a.vp.head_bytes;
@@ -597,28 +604,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       load(0);
     }
     for (int j = 0; j < n; ++j) {
-      uint32_t e = 1;
+      uint32_t e = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int k = 0; k < NB / 2; ++k) {
           sc[i][k] = live >> i & 1 ? sc[i][k] : 0;
-          e = max(e, max_exp(sc[i][k]));
+          e = max_u16x2(e, sc[i][k]);
         }
-      const int ve = 20 - int(__reduce_max_sync(kFull, e));
+      const int ve = scale_up(e);
       if (lane == 0) {
         mi->vx[j & 3][w] = ve;
         mbar_arrive(&bar[kKFull + (j & 1)]);
       }
       if (!pa_wait_warp(&bar[kVEmpty + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
-      const float up = pow2(ve);
+      const uint32_t up = half2_pow2(ve);
       uint8_t *vs = sm + C::kOffV + (j & 1) * C::kVBytes + (grp >> 3) * C::kVSub;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t o[4][4];  // [channel of the unit][token pair]
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t d2 = half2_bits(scale_of(sc[2 * k], b) * up, scale_of(sc[2 * k + 1], b) * up);
+          const uint32_t d2 = hmul2(__byte_perm(sc[2 * k][b / 2], sc[2 * k + 1][b / 2], (b & 1) ? 0x7632 : 0x5410), up);
           if constexpr (V4) {
             const uint32_t x = __byte_perm(code[2 * k][b / 2], code[2 * k + 1][b / 2], (b & 1) ? 0x7632 : 0x5410), y = x >> 8;
             o[0][k] = hmul2(codes4_lo(x), d2);  // channel 2g
@@ -667,10 +674,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         issue_s(1, 0);
         tc_commit(&bar[kKEmpty]);
       }
+      // A wait holds up the products behind it even where its phase is long
+      // complete, so a step's operands are tested for while the products of
+      // the step before are queued.
+      auto operands = [&](auto look, int j) {
+        return look(&bar[kVFull + (j & 1)], (j >> 1) & 1) && (j + 1 >= n || look(&bar[kKFull + ((j + 1) & 1)], ((j + 1) >> 1) & 1));
+      };
+      bool seen = false;
       for (int j = 0; j < n && ok; ++j) {
         const bool more = j + 1 < n;
-        ok = pa_wait(&bar[kVFull + (j & 1)], (j >> 1) & 1, spin, abort_flag, a.err) &&
-             (!more || pa_wait(&bar[kKFull + ((j + 1) & 1)], ((j + 1) >> 1) & 1, spin, abort_flag, a.err));
+        if (!seen)
+          ok = operands([&](uint64_t *b, uint32_t parity) { return pa_wait(b, parity, spin, abort_flag, a.err); }, j);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!ok || !(ok = pa_wait(&bar[kPReady + 2 * t + h], j & 1, spin, abort_flag, a.err))) break;
@@ -680,6 +694,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_mma_ts(tmem + uint32_t(256 + t * 128), tmem + uint32_t(t * 128 + h * 64 + k * 8),
                       desc(C::kOffV + (j & 1) * C::kVBytes + h * C::kVSub + k * 32), kIdescO, j > 0 || h > 0 || k > 0);
           if (h == 1) tc_commit(&bar[kVEmpty + (j & 1)]);
+          if (h == 1 && more) seen = operands([](uint64_t *b, uint32_t parity) { return mbar_test_wait(b, parity); }, j + 1);
           if (more) {
             issue_s(h, j + 1);
             if (h == 1) tc_commit(&bar[kKEmpty + ((j + 1) & 1)]);
