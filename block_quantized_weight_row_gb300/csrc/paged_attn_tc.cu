@@ -113,11 +113,12 @@ __device__ __forceinline__ void hadamard64_thread(float (&x)[64]) {
   for (int i = 0; i < 64; ++i) x[i] *= 0.125f;
 }
 
-// 64 q values of a row from channel ch
-__device__ __forceinline__ void load_q64(int elem, const uint8_t *row, int ch, int rotate, float (&x)[64]) {
+// Row r's 64 q values at its swizzled place in an operand sub-tile, as they
+// were copied there
+__device__ __forceinline__ void load_q64(int elem, const uint8_t *sub, int r, int rotate, float (&x)[64]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row + ch * 2) + i);
+    const uint4 v = *reinterpret_cast<const uint4 *>(sub + sw128_off(r, i));
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -173,7 +174,13 @@ __device__ __forceinline__ uint32_t half2_pow2(int k) { return uint32_t(15 + k) 
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
 // Registers per thread: 96 at launch (20 warps); the shares add up to 20 * 96
-// or less: 8 * 128 + 8 * 88 + 4 * 40 = 1888 of 1920.
+// or less: 8 * 136 + 8 * 72 + 4 * 56 = 1888 or 8 * 136 + 8 * 80 + 4 * 48 =
+// 1920 of 1920. Each is the split that leaves nothing in local memory.
+template <int VT>
+struct Regs {
+  static constexpr bool kV4 = VT == kTypeQ4_0;
+  static constexpr int kSoftmax = 136, kOperand = kV4 ? 72 : 80, kIssue = kV4 ? 56 : 48;
+};
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -257,6 +264,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int first = lo_any / kTile, all = max(0, (hi_any + kTile - 1) / kTile - first);
   const int j0 = first + int(int64_t(all) * split / n_split), n = first + int(int64_t(all) * (split + 1) / n_split) - j0;
 
+  // q's rows are copied to where their operand rows will be, whole rows by
+  // consecutive lanes (a thread reading its own row from global memory touches
+  // 32 lines per load: 6.5 us for the operand of 256 rows, this 3).
+  for (int i = threadIdx.x; i < n_tiles_q * 128 * (D / 8); i += kTcThreads) {
+    const int r = i / (D / 8), piece = i % (D / 8), row = min(row0 + r, n_rows - 1), tok = row / a.group;
+    cp_async16(smem_u32(sm + (r >> 7) * C::kQBytes + (piece >> 3) * kSub + sw128_off(r & 127, piece & 7)),
+               a.q + int64_t(span.q0 + tok) * a.q_token + int64_t(kvh * a.group + row - tok * a.group) * a.q_head + piece * 16, 16);
+  }
+  cp_commit();
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar[kKFull + i], 8);  // the K operand and the V exponents of the tile
@@ -278,6 +295,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&mi->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  cp_wait<0>();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -295,7 +313,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 8) {
     // ---- softmax: thread = row ----
-    regs_up<128>();
+    regs_up<Regs<VT>::kSoftmax>();
     const int t = warp >> 2, q4 = warp & 3, local = t * 128 + q4 * 32 + lane, row = row0 + local;
     if (t < n_tiles_q) {
       const bool live = local < rows;
@@ -304,11 +322,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       seen_range(span, tok, a.causal, a.window, lo, hi);
       float fq;  // score = fq * (kk's factor) * S
       {
-        const uint8_t *p = a.q + int64_t(span.q0 + tok) * a.q_token + int64_t(head) * a.q_head;
+        uint8_t *qs = sm + t * C::kQBytes;
+        const int r = q4 * 32 + lane;
         float m = 0.0f, x[64];
 #pragma unroll 1
         for (int h = 0; h < C::kSubs; ++h) {
-          load_q64(a.elem, p, 64 * h, a.rotate, x);
+          load_q64(a.elem, qs + h * kSub, r, a.rotate, x);
 #pragma unroll
           for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(x[i]));
         }
@@ -316,11 +335,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const int k = m > 0.0f ? min(10 + 127 - int(__float_as_uint(m) >> 23), 110) : 0;
         const float up = live ? copysignf(pow2(k), a.scale_log2) : 0.0f;
         fq = fabsf(a.scale_log2) * pow2(-k);
-        uint8_t *qs = sm + t * C::kQBytes;
-        const int r = q4 * 32 + lane;
 #pragma unroll 1
         for (int h = 0; h < C::kSubs; ++h) {
-          load_q64(a.elem, p, 64 * h, a.rotate, x);
+          load_q64(a.elem, qs + h * kSub, r, a.rotate, x);
 #pragma unroll
           for (int i = 0; i < 64; ++i) x[i] = live ? x[i] * up : 0.0f;
 #pragma unroll
@@ -499,7 +516,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc_fence_before();
     }
   } else if (warp < 12) {
-    regs_down<88>();
+    regs_down<Regs<VT>::kOperand>();
     // ---- K operand: lane = (token of 8, unit), four groups of 8 tokens per thread ----
     const int w = warp - 8, tk = lane & 7, c = lane >> 3;
     uint32_t code[4][UK / 4], sc[4][NB / 2];
@@ -576,7 +593,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (j + 1 < n) load(j + 1);
     }
   } else if (warp < 16) {
-    regs_down<88>();
+    regs_down<Regs<VT>::kOperand>();
     // ---- V operand, transposed: thread = (8 tokens, unit g): 8 tokens of 4 channels per block ----
     const int w = warp - 12, g = lane & 7, grp = w * 4 + (lane >> 3);
     uint32_t code[8][(UV + 3) / 4], sc[8][NB / 2];
@@ -648,7 +665,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (j + 1 < n) load(j + 1);
     }
   } else {
-    regs_down<40>();
+    regs_down<Regs<VT>::kIssue>();
     const int t = warp - 16;
     if (t < n_tiles_q && lane == 0) {
       // ---- MMA issue, a warp per row tile ----
