@@ -111,15 +111,25 @@ StreamShape shape_of(int nb, int kt, int vt, int elem, int rows8) {
 }
 
 // A piece has at least this many tiles (of 16 or 32 tokens): below that a
-// CTA's start and the combine cost more than the tokens.
+// CTA's start and the combine cost more than the tokens (one sequence of 777
+// tokens, 16 query over 8 kv heads of 128: 11.3 us with 2, 12.3 with 4, 13.3
+// with 8).
 constexpr int kMinTiles = 2;
 
 // Sequences with more query rows per kv head than this go to the many-row
-// kernel (16-bit calls, head_dim 64 or 128): a pass of the streaming kernel
-// converts the cache for 16 rows, a step of the other for 256.
-constexpr int kTcRows = 64;
+// kernel (16-bit calls, head_dim 64 or 128). A pass of the streaming kernel
+// reads and converts the cache for 16 rows, a step of the other for 256, but
+// the other's CTAs start slower and are fewer. Measured (8 kv heads of 128,
+// 4 bits; streaming / many-row kernel): 16 sequences of 4096 tokens 69 / 70 us
+// at 32 rows, 96 / 70 at 48, 122 / 70 at 64; one sequence of 8192 tokens 23.4 /
+// 28.2 us at 48 rows, 26.2 / 28.4 at 64, 28.4 / 29.0 at 80, 39.6 / 30.0 at 128.
+// So a batch that fills a quarter of the SMs by itself turns at 32, others at
+// 64.
 constexpr int kFill = 152;           // CTAs (one per SM) that the many-row kernel's split aims at
-constexpr int kSplitTokens = 1024;   // tokens of a split at least
+int tc_rows_of(int64_t n_seqs, int64_t n_kv) { return n_seqs * n_kv > kFill / 4 ? 32 : 64; }
+// Tokens of a split at least (that one sequence at 64 rows: 256 tokens 29.9
+// us, 512 28.4, 1024 31.5).
+constexpr int kSplitTokens = 512;
 
 struct Plan {
   StreamShape shape;
@@ -134,9 +144,10 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Plan make_plan(PagedAttnArgs &a, int max_q, int sm_count) {
   Plan p = {};
   const int64_t most_rows = std::max<int64_t>(1, int64_t(a.group) * max_q), all_rows = int64_t(a.group) * a.n_q;
-  const int64_t items = (all_rows / 256 + std::min<int64_t>(a.n_seqs, all_rows / (kTcRows + 1))) * a.sh.n_kv;
-  const bool tc = a.elem != kElemF32 && (a.sh.nb == 2 || a.sh.nb == 4) && most_rows > kTcRows && items <= 0x7fffffff;
-  a.tc_rows = tc ? kTcRows : 0x7fffffff;
+  const int tc_rows = tc_rows_of(a.n_seqs, a.sh.n_kv);
+  const int64_t items = (all_rows / 256 + std::min<int64_t>(a.n_seqs, all_rows / (tc_rows + 1))) * a.sh.n_kv;
+  const bool tc = a.elem != kElemF32 && (a.sh.nb == 2 || a.sh.nb == 4) && most_rows > tc_rows && items <= 0x7fffffff;
+  a.tc_rows = tc ? tc_rows : 0x7fffffff;
   const int64_t rows = std::min<int64_t>(most_rows, a.tc_rows);
   p.rows8 = int(std::min<int64_t>((rows + 7) / 8, 1 << 20));
   p.shape = shape_of(a.sh.nb, a.kt, a.vt, a.elem, p.rows8);

@@ -358,12 +358,13 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
  * Accuracy: fp32 statistics and sums; q and weights in binary16 terms (fp32
  * calls two each, 2^-22 together; 16-bit calls one: q exactly unless rotated,
  * 2^-11 of a weight); weights below 2^-30 of the largest V scale vanish. In
- * 16-bit calls with head_dim 64 or 128, sequences of more than 64 query rows
- * per kv head (q_len * n_heads / n_kv_heads) run on the tensor-memory kernel,
- * where k^, v^ and a rotated q are binary16 too (2^-11 each). Scales are taken
- * as the write makes them: finite and not negative. The
- * split of long sequences depends on the batch, and with it the order of sums:
- * the same call gives the same bits, another batch may differ in the last.
+ * 16-bit calls with head_dim 64 or 128, sequences of many query rows per kv
+ * head (q_len * n_heads / n_kv_heads above 64, or above 32 where n_seqs *
+ * n_kv_heads is above 38) run on the tensor-memory kernel, where k^, v^ and a
+ * rotated q are binary16 too (2^-11 each). Scales are taken as the write makes
+ * them: finite and not negative. The split of long sequences depends on the
+ * batch, and with it the order of sums: the same call gives the same bits,
+ * another batch may differ in the last.
  * Limits: head_dim 64, 96, 128 or 256; n_heads a multiple of n_kv_heads. Needs
  * a workspace of bq_paged_attn_workspace_size(...) bytes (bq_set_workspace).
  * Errors: BQ_ERR_SHAPE, BQ_ERR_UNSUPPORTED (types, a window without causal),

@@ -19,7 +19,8 @@ states. With u32 = 2^-24 and half a binary16 step u16 = 2^-11 (relative):
   sums: a warp's chain of products, then warps and pieces: (keys / 8 + 64) * 2 u32;
 so |o - o_ref| <= (2 ds + all of those) * sum_j w_j |v^_j| + the output type's
 half step of |o_ref|. The many-row kernel (16-bit calls with more than 64 query
-rows per kv head and 64 or 128 channels) rounds k^, v^ and q to binary16 too:
+rows per kv head, or 32 where sequences times kv heads pass 38, and 64 or 128
+channels) rounds k^, v^ and q to binary16 too:
 u16 * mag in the scores for each (|k^| for 16 d), u16 in the sum, operands
 below 2^-25 of their unit 2^-30 max d; its products chain over all channels
 (D + 8 for 34 + blocks + 4) and its sums over all keys (keys for keys / 8).
@@ -471,7 +472,7 @@ class Batch:
             cv, sv = get_rows(self.pools[1], self.page, self.vt, D, 8, self.slots[b])
             dk = np.repeat(sk.astype(np.float64), 32, axis=-1)
             k, v = ck * dk, cv * np.repeat(sv.astype(np.float64), 32, axis=-1)
-            many = self.elem != F32 and D in (64, 128) and n * G > 64
+            many = self.elem != F32 and D in (64, 128) and n * G > (32 if len(self.q_len) * self.NKV > 38 else 64)
             wide = np.abs(k) if many or self.kt == Q8 else 16 * dk
             q = self.q[t0:t0 + n].double().numpy()
             if self.basis:
@@ -592,6 +593,10 @@ MANY = [
     ([100], [3500], 8, 8, 128, 128, Q4, Q4, BF16, 1, True, 0),           # tokens split over CTAs
     ([700, 5, 333], [900, 800, 333], 16, 8, 128, 16, Q4, Q4, BF16, 0, True, 0),  # more CTAs than a split
     ([96], [2300], 8, 1, 64, 32, Q8, Q8, F16, 0, False, 0),
+    # 33 to 64 rows per kv head, with sequences enough to fill SMs, beside shorter ones
+    ([12, 9, 8, 1] * 3, [(61 * i) % 700 + 12 for i in range(12)], 16, 4, 128, 16, Q4, Q8, BF16, 1, True, 0),
+    ([33, 64, 32] * 13, [(83 * i) % 900 for i in range(39)], 1, 1, 64, 16, Q4, Q4, F16, 0, True, 200),
+    ([5, 4] * 4, [300 + 150 * i for i in range(8)], 40, 5, 128, 48, Q8, Q4, F16, 0, False, 0),
 ]
 
 
