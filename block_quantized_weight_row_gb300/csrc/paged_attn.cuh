@@ -41,6 +41,13 @@
 // stay there), so ragged batches load every SM alike. A segment inside a piece
 // is finished there; one that is cut leaves partial results for the combine
 // launch, which merges them in a fixed order.
+// Measured (8 kv heads of 128 channels, bf16): 64 ragged sequences of up to
+// 8192 tokens, 32 query heads, 4 bits, 99.7 us, 3.1 TB/s of cache; 4 sequences
+// of up to 131071 tokens, 16 query heads, 8-bit V, 101 us, 4.9 TB/s (0.72 of
+// the copy rate); one of 777 tokens in fp32 12.3 us. With the products and the softmax
+// taken out (copies, segment starts and combine left) the first takes 63 us,
+// the second 81: what is above that is instruction issue (452 per 16 tokens
+// and warp, ALU pipe 48% busy), and the pieces' unequal ends (67 to 95 us).
 #pragma once
 
 #include "bq_device.cuh"
@@ -231,7 +238,9 @@ struct Cfg {
 // that any of its rows sees; a sequence with rows has at least one tile, so
 // that its output is written even when no row sees a token.
 // `cost` counts a segment's start and merge too, in tiles: a batch's short
-// sequences would otherwise leave their CTAs far behind the others.
+// sequences would otherwise leave their CTAs far behind the others (512
+// tokens' worth: a ragged decode batch of 64 sequences took 114 us without,
+// 107 with 256, 101 with 512, 102 with 768).
 constexpr int kSegTokens = 512;
 struct SeqTiles {
   int t_lo, tiles, cost, groups;  // per (kv head, row group)
