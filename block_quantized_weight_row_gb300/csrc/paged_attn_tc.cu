@@ -332,19 +332,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       {
         uint8_t *qs = sm + t * C::kQBytes;
         const int r = q4 * 32 + lane;
-        float m = 0.0f, x[64];
-#pragma unroll 1
-        for (int h = 0; h < C::kSubs; ++h) {
-          load_q64(a.elem, qs + h * kSub, r, a.rotate, x);
+        // the row's largest magnitude, from the bits as they are
+        uint32_t most = 0;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) m = fmaxf(m, fabsf(x[i]));
+        for (int v = 0; v < D / 8; ++v) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(qs + (v >> 3) * kSub + sw128_off(r, v & 7));
+          most = max_u16x2(max_u16x2(max_u16x2(max_u16x2(most, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu), w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
         }
-        // 2^k brings the row's largest value to [2^10, 2^11); the scale's sign goes into q
+        most = max(most & 0xffffu, most >> 16);
+        float m = a.elem == kElemF16 ? __half2float(__ushort_as_half(uint16_t(most))) : __uint_as_float(most << 16);
+        if (a.rotate) m *= 8.0f;  // H64 / 8 can make a value 8 times as large
+        // 2^k brings that to [2^10, 2^11); the scale's sign goes into q
         const int k = m > 0.0f ? min(10 + 127 - int(__float_as_uint(m) >> 23), 110) : 0;
         const float up = live ? copysignf(pow2(k), a.scale_log2) : 0.0f;
         fq = fabsf(a.scale_log2) * pow2(-k);
 #pragma unroll 1
         for (int h = 0; h < C::kSubs; ++h) {
+          float x[64];
           load_q64(a.elem, qs + h * kSub, r, a.rotate, x);
 #pragma unroll
           for (int i = 0; i < 64; ++i) x[i] = live ? x[i] * up : 0.0f;
