@@ -183,9 +183,11 @@ constexpr int kMinTiles = 2;
 // at 32 rows, 96 / 70 at 48, 122 / 70 at 64; one sequence of 8192 tokens 23.4 /
 // 28.2 us at 48 rows, 26.2 / 28.4 at 64, 28.4 / 29.0 at 80, 39.6 / 30.0 at 128.
 // So a batch that fills a quarter of the SMs by itself turns at 32, others at
-// 64.
+// 64; a binary16 call at 64 always, as the many-row kernel's binary16 operands
+// show in its output (4.5e-4 of its norm; streaming 2.9e-4, rounding alone
+// 2.1e-4; a bf16 output's rounding hides them: 1.7e-3 in all).
 constexpr int kFill = 152;           // CTAs (one per SM) that the many-row kernel's split aims at
-int tc_rows_of(int64_t n_seqs, int64_t n_kv) { return n_seqs * n_kv > kFill / 4 ? 32 : 64; }
+int tc_rows_of(int elem, int64_t n_seqs, int64_t n_kv) { return elem == kElemBF16 && n_seqs * n_kv > kFill / 4 ? 32 : 64; }
 // Tokens of a split at least (that one sequence at 64 rows: 256 tokens 29.9
 // us, 512 28.4, 1024 31.5).
 constexpr int kSplitTokens = 512;
@@ -203,7 +205,7 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Plan make_plan(PagedAttnArgs &a, int max_q, int sm_count) {
   Plan p = {};
   const int64_t most_rows = std::max<int64_t>(1, int64_t(a.group) * max_q), all_rows = int64_t(a.group) * a.n_q;
-  const int tc_rows = tc_rows_of(a.n_seqs, a.sh.n_kv);
+  const int tc_rows = tc_rows_of(a.elem, a.n_seqs, a.sh.n_kv);
   const int64_t items = (all_rows / 256 + std::min<int64_t>(a.n_seqs, all_rows / (tc_rows + 1))) * a.sh.n_kv;
   const bool tc = a.elem != kElemF32 && (a.sh.nb == 2 || a.sh.nb == 4) && most_rows > tc_rows && items <= 0x7fffffff;
   a.tc_rows = tc ? tc_rows : 0x7fffffff;

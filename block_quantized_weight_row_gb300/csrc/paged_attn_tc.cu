@@ -10,7 +10,7 @@
 // TFLOP/s (0.46 of the measured bf16 rate). A step takes 4300 cycles; its
 // products alone, issued without a wait, 2520 (2048 where S is 128 tokens wide:
 // 64 tokens' operands are fetched at 49 cycles per product, not 33), its 11600
-// instructions 2900 issue slots of each scheduler. 9 us of an item are its
+// instructions 2900 issue slots of each scheduler. 11 us of an item are its
 // start and its output, and 256 items on 152 SMs leave a sixth of them idle in
 // the second wave. A step is 256 rows x 128 tokens:
 //   - S = Q K^T per 128-row tile and 64 tokens (operands in shared memory,

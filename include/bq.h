@@ -329,7 +329,8 @@ int bq_paged_kv_write(const bq_paged_cache *cache, int elem, const void *K, int6
  * * code in fp32; K's then plus `bias` (fp32) and out of the rotated basis
  * (the same butterflies; H64 / 8 is its own inverse), and each is rounded once
  * to `elem`. A slot of -1 gives rows of zeros, as does one outside the pool,
- * which bq_device_status reports (BQ_ERR_INDEX). Errors as the write's. */
+ * which bq_device_status reports (BQ_ERR_INDEX). Errors as the write's; a cache
+ * without pages is BQ_ERR_INVALID_ARG. */
 int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, const float *bias, int bias_basis,
                      const int64_t *slots, int64_t n_tokens);
 
@@ -359,7 +360,7 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
  * calls two each, 2^-22 together; 16-bit calls one: q exactly unless rotated,
  * 2^-11 of a weight); weights below 2^-30 of the largest V scale vanish. In
  * 16-bit calls with head_dim 64 or 128, sequences of many query rows per kv
- * head (q_len * n_heads / n_kv_heads above 64, or above 32 where n_seqs *
+ * head (q_len * n_heads / n_kv_heads above 64; in bf16 above 32 where n_seqs *
  * n_kv_heads is above 38) run on the tensor-memory kernel, where k^, v^ and a
  * rotated q are binary16 too (2^-11 each). Scales are taken as the write makes
  * them: finite and not negative. The split of long sequences depends on the
@@ -369,7 +370,8 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
  * a workspace of bq_paged_attn_workspace_size(...) bytes (bq_set_workspace).
  * Errors: BQ_ERR_SHAPE, BQ_ERR_UNSUPPORTED (types, a window without causal),
  * BQ_ERR_ALIGN, BQ_ERR_INVALID_ARG (null pointers, negative sizes, an output
- * or the workspace overlapping another argument, rows of o overlapping),
+ * or the workspace overlapping another argument, rows of o overlapping, a
+ * cache without pages),
  * BQ_ERR_WORKSPACE. */
 int bq_paged_attn(const bq_paged_cache *cache, int elem, const void *q, int64_t q_token_stride, int64_t q_head_stride,
                   void *o, int64_t o_token_stride, int64_t o_head_stride, float *lse, const int32_t *q_start,

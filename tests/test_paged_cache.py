@@ -19,8 +19,8 @@ states. With u32 = 2^-24 and half a binary16 step u16 = 2^-11 (relative):
   sums: a warp's chain of products, then warps and pieces: (keys / 8 + 64) * 2 u32;
 so |o - o_ref| <= (2 ds + all of those) * sum_j w_j |v^_j| + the output type's
 half step of |o_ref|. The many-row kernel (16-bit calls with more than 64 query
-rows per kv head, or 32 where sequences times kv heads pass 38, and 64 or 128
-channels) rounds k^, v^ and q to binary16 too:
+rows per kv head, in bf16 32 where sequences times kv heads pass 38, and 64 or
+128 channels) rounds k^, v^ and q to binary16 too:
 u16 * mag in the scores for each (|k^| for 16 d), u16 in the sum, operands
 below 2^-25 of their unit 2^-30 max d; its products chain over all channels
 (D + 8 for 34 + blocks + 4) and its sums over all keys (keys for keys / 8).
@@ -194,6 +194,7 @@ def test_read_refusals(bq):
         assert _read(bq, s, **kw) == INVALID, kw
     for kw in (dict(K=OUT1 + 8), dict(V=OUT2 + 4), dict(slots=IDX + 2)):
         assert _read(bq, s, **kw) == ALIGN, kw
+    assert _read(bq, _struct(bq, n_pages=0)) == INVALID
     assert _read(bq, s, bias=FAKE + (40 << 33), basis=1) == BASIS
     assert _read(bq, _struct(bq, k_type=Q8), bias=FAKE + (40 << 33)) == UNSUPPORTED
 
@@ -211,6 +212,7 @@ def test_attention_refusals(bq):
         assert _attn(bq, s, **kw) == INVALID, kw
     for kw in (dict(H=5), dict(H=0), dict(B=1 << 21), dict(max_kv=2**31 - 1)):
         assert _attn(bq, s, **kw) == SHAPE, kw
+    assert _attn(bq, _struct(bq, n_pages=0)) == INVALID
     assert _attn(bq, _struct(bq, head_dim=32)) == SHAPE and _attn(bq, _struct(bq, head_dim=160)) == SHAPE
     assert _attn(bq, s, elem=7) == UNSUPPORTED and _attn(bq, s, causal=0, window=3) == UNSUPPORTED
     for kw in (dict(q=IN1 + 8), dict(qs=(258, 64)), dict(os=(256, 66)), dict(o=OUT1 + 4), dict(qst=IDX + 2), dict(lse=OUT2 + 2)):
@@ -472,7 +474,7 @@ class Batch:
             cv, sv = get_rows(self.pools[1], self.page, self.vt, D, 8, self.slots[b])
             dk = np.repeat(sk.astype(np.float64), 32, axis=-1)
             k, v = ck * dk, cv * np.repeat(sv.astype(np.float64), 32, axis=-1)
-            many = self.elem != F32 and D in (64, 128) and n * G > (32 if len(self.q_len) * self.NKV > 38 else 64)
+            many = self.elem != F32 and D in (64, 128) and n * G > (32 if self.elem == BF16 and len(self.q_len) * self.NKV > 38 else 64)
             wide = np.abs(k) if many or self.kt == Q8 else 16 * dk
             q = self.q[t0:t0 + n].double().numpy()
             if self.basis:
@@ -595,7 +597,7 @@ MANY = [
     ([96], [2300], 8, 1, 64, 32, Q8, Q8, F16, 0, False, 0),
     # 33 to 64 rows per kv head, with sequences enough to fill SMs, beside shorter ones
     ([12, 9, 8, 1] * 3, [(61 * i) % 700 + 12 for i in range(12)], 16, 4, 128, 16, Q4, Q8, BF16, 1, True, 0),
-    ([33, 64, 32] * 13, [(83 * i) % 900 for i in range(39)], 1, 1, 64, 16, Q4, Q4, F16, 0, True, 200),
+    ([33, 64, 32] * 13, [(83 * i) % 900 for i in range(39)], 1, 1, 64, 16, Q4, Q4, BF16, 0, True, 200),
     ([5, 4] * 4, [300 + 150 * i for i in range(8)], 40, 5, 128, 48, Q8, Q4, F16, 0, False, 0),
 ]
 
@@ -635,6 +637,21 @@ def test_attention_v_scales_that_grow_along_the_cache(bq, n, elem):
             b.pools[1][p, :, at:at + nb * 2] = np.repeat(d[-1 - j if flip else j], nb).view(np.uint8)
         b.cache.v_pages.copy_(torch.from_numpy(b.pools[1]))
         b.check()
+
+
+@gpu
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("n,elem", [(1, F32), (3, F16), (90, BF16)])
+def test_attention_of_zero_scales(bq, n, elem, which):
+    """Blocks of zeros: every weight alike (K), or outputs of exactly zero (V)."""
+    b = Batch(bq, [n], [n + 300], 4, 2, 128, 16, Q4, Q4, elem)
+    i = "kv".index(which)
+    b.pools[i][:, :, 16 * 4 * 16:] = 0
+    pools = [torch.from_numpy(p).cuda() for p in b.pools]
+    b.cache = bq.PagedCache(*pools, 16, 128, Q4, Q4, 0)
+    b.check()
+    if which == "v":
+        assert (b.run()[0] == 0).all()
 
 
 @gpu
