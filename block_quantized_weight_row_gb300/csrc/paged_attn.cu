@@ -175,19 +175,26 @@ StreamShape shape_of(int nb, int kt, int vt, int elem, int rows8) {
 // with 8).
 constexpr int kMinTiles = 2;
 
-// Sequences with more query rows per kv head than this go to the many-row
-// kernel (16-bit calls, head_dim 64 or 128). A pass of the streaming kernel
-// reads and converts the cache for 16 rows, a step of the other for 256, but
-// the other's CTAs start slower and are fewer. Measured (8 kv heads of 128,
-// 4 bits; streaming / many-row kernel): 16 sequences of 4096 tokens 69 / 70 us
-// at 32 rows, 96 / 70 at 48, 122 / 70 at 64; one sequence of 8192 tokens 23.4 /
-// 28.2 us at 48 rows, 26.2 / 28.4 at 64, 28.4 / 29.0 at 80, 39.6 / 30.0 at 128.
-// So a batch that fills a quarter of the SMs by itself turns at 32, others at
-// 64; a binary16 call at 64 always, as the many-row kernel's binary16 operands
-// show in its output (4.5e-4 of its norm; streaming 2.9e-4, rounding alone
-// 2.1e-4; a bf16 output's rounding hides them: 1.7e-3 in all).
+// Sequences with more query rows per kv head than tc_rows_of go to the
+// many-row kernel (16-bit calls, head_dim 64 or 128), if the call has work for
+// it: kTcWork or more of passes x sequences x kv heads x (tokens + the 512 that
+// a segment's start costs), by the host's bounds. A pass of the streaming
+// kernel reads and converts the cache for 16 rows, a step of the other for
+// 256, but the other's CTAs start slower (14 us an item) and are fewer.
+// Measured (8 kv heads of 128, 4 bits; streaming / many-row kernel, us):
+// sequences x tokens   rows 36    64         80         128        256        512
+//  1 x 1024          11 / 20   15 / 21    16 / 21    17 / 22    21 / 27    31 / 29
+//  1 x 8192                    26 / 24    28 / 24    40 / 25    66 / 40
+//  4 x 256           15 / 16   16 / 15    17 / 16    21 / 16    32 / 19    49 / 20
+// 16 x 512           31 / 20   38 / 20    45 / 21    62 / 20   111 / 23   214 / 43
+// 16 x 4096 (48 rows 96 / 70) 122 / 71   149 / 71   227 / 71   440 / 85
+// (16 x 4096 at 32 rows: 69 / 70.) A binary16 call turns at 64 rows at the
+// earliest, as the many-row kernel's binary16 operands show in its output
+// (4.5e-4 of its norm; streaming 2.9e-4, rounding alone 2.1e-4; a bf16
+// output's rounding hides them: 1.7e-3 in all).
 constexpr int kFill = 152;           // CTAs (one per SM) that the many-row kernel's split aims at
-int tc_rows_of(int elem, int64_t n_seqs, int64_t n_kv) { return elem == kElemBF16 && n_seqs * n_kv > kFill / 4 ? 32 : 64; }
+constexpr double kTcWork = 250000;
+int tc_rows_of(int elem) { return elem == kElemBF16 ? 32 : 64; }
 // Tokens of a split at least (that one sequence at 64 rows: 256 tokens 29.9
 // us, 512 28.4, 1024 31.5).
 constexpr int kSplitTokens = 512;
@@ -205,14 +212,15 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 Plan make_plan(PagedAttnArgs &a, int max_q, int sm_count) {
   Plan p = {};
   const int64_t most_rows = std::max<int64_t>(1, int64_t(a.group) * max_q), all_rows = int64_t(a.group) * a.n_q;
-  const int tc_rows = tc_rows_of(a.elem, a.n_seqs, a.sh.n_kv);
+  const int64_t seen = a.causal && a.window > 0 ? std::min<int64_t>(a.max_kv, int64_t(a.window) + max_q) : a.max_kv;
+  const int tc_rows = tc_rows_of(a.elem);
+  const bool work = double((most_rows + 15) / 16) * double(a.n_seqs) * a.sh.n_kv * double(seen + 512) >= kTcWork;
   const int64_t items = (all_rows / 256 + std::min<int64_t>(a.n_seqs, all_rows / (tc_rows + 1))) * a.sh.n_kv;
-  const bool tc = a.elem != kElemF32 && (a.sh.nb == 2 || a.sh.nb == 4) && most_rows > tc_rows && items <= 0x7fffffff;
+  const bool tc = a.elem != kElemF32 && (a.sh.nb == 2 || a.sh.nb == 4) && work && most_rows > tc_rows && items <= 0x7fffffff;
   a.tc_rows = tc ? tc_rows : 0x7fffffff;
   const int64_t rows = std::min<int64_t>(most_rows, a.tc_rows);
   p.rows8 = int(std::min<int64_t>((rows + 7) / 8, 1 << 20));
   p.shape = shape_of(a.sh.nb, a.kt, a.vt, a.elem, p.rows8);
-  const int64_t seen = a.causal && a.window > 0 ? std::min<int64_t>(a.max_kv, int64_t(a.window) + max_q) : a.max_kv;
   const int64_t tiles = seen / p.shape.tokens + 2, groups = (rows + p.shape.rows - 1) / p.shape.rows;
   // saturating: only the smaller of this and the device's room matters
   const double most = double(tiles) * double(groups) * a.sh.n_kv * a.n_seqs / kMinTiles;

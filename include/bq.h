@@ -359,9 +359,10 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
  * Accuracy: fp32 statistics and sums; q and weights in binary16 terms (fp32
  * calls two each, 2^-22 together; 16-bit calls one: q exactly unless rotated,
  * 2^-11 of a weight); weights below 2^-30 of the largest V scale vanish. In
- * 16-bit calls with head_dim 64 or 128, sequences of many query rows per kv
- * head (q_len * n_heads / n_kv_heads above 64; in bf16 above 32 where n_seqs *
- * n_kv_heads is above 38) run on the tensor-memory kernel, where k^, v^ and a
+ * 16-bit calls with head_dim 64 or 128 and work enough by the bounds given
+ * (query rows / 16 x n_seqs x n_kv_heads x (max_kv_len + 512) from 250000),
+ * sequences of many query rows per kv head (q_len * n_heads / n_kv_heads above
+ * 64, in bf16 above 32) run on the tensor-memory kernel, where k^, v^ and a
  * rotated q are binary16 too (2^-11 each). Scales are taken as the write makes
  * them: finite and not negative. The split of long sequences depends on the
  * batch, and with it the order of sums: the same call gives the same bits,

@@ -18,9 +18,8 @@ states. With u32 = 2^-24 and half a binary16 step u16 = 2^-11 (relative):
     min(w_j d_j, 2^-30 max d) |c_j| (binary32 weights vanish too, at 2^-149);
   sums: a warp's chain of products, then warps and pieces: (keys / 8 + 64) * 2 u32;
 so |o - o_ref| <= (2 ds + all of those) * sum_j w_j |v^_j| + the output type's
-half step of |o_ref|. The many-row kernel (16-bit calls with more than 64 query
-rows per kv head, in bf16 32 where sequences times kv heads pass 38, and 64 or
-128 channels) rounds k^, v^ and q to binary16 too:
+half step of |o_ref|. The many-row kernel (16-bit calls with 64 or 128 channels,
+sequences of more than 64 query rows per kv head, in bf16 32, and work enough) rounds k^, v^ and q to binary16 too:
 u16 * mag in the scores for each (|k^| for 16 d), u16 in the sum, operands
 below 2^-25 of their unit 2^-30 max d; its products chain over all channels
 (D + 8 for 34 + blocks + 4) and its sums over all keys (keys for keys / 8).
@@ -415,7 +414,7 @@ def test_pool_beyond_32_bit_offsets(bq):
 class Batch:
     """A batch over a cache of random codes, with everything unused set to garbage (NaN scales)."""
 
-    def __init__(self, bq, q_len, kv_len, H, NKV, D, page, kt, vt, elem, basis=0, seed=0, peaked=1.0, vscale=1.0):
+    def __init__(self, bq, q_len, kv_len, H, NKV, D, page, kt, vt, elem, basis=0, seed=0, peaked=1.0, vscale=1.0, wide=True):
         rng = np.random.default_rng(seed)
         self.bq, self.q_len, self.kv_len, self.H, self.NKV, self.D, self.page = bq, q_len, kv_len, H, NKV, D, page
         self.kt, self.vt, self.elem, self.basis = kt, vt, elem, basis
@@ -449,12 +448,17 @@ class Batch:
         self.kvl = torch.tensor(kv_len, dtype=torch.int32, device="cuda")
         self.pt = torch.from_numpy(self.table).cuda()
         self.scale = 1.0 / math.sqrt(D)
+        # wide: a bound of kv_len that gives a call of many rows the work by which the many-row kernel is taken
+        self.bound = max(list(kv_len) + [0])
+        rows = max(list(q_len) + [0]) * H // NKV
+        if wide and rows > 32:
+            self.bound = max(self.bound, 250000 // (-(-rows // 16) * len(q_len) * NKV))
 
     def run(self, causal=True, window=0, **kw):
         q = kw.pop("q", None)
         lse = torch.full((self.q.shape[0], self.H), 7.0, device="cuda")
         o = self.bq.paged_attn(self.cache, self.q.cuda() if q is None else q, self.q_start, self.kvl, self.pt, self.scale,
-                               max_q_len=max(self.q_len + [0]), max_kv_len=max(self.kv_len + [0]), causal=causal,
+                               max_q_len=max(self.q_len + [0]), max_kv_len=self.bound, causal=causal,
                                window=window, lse=lse, **kw)
         return o, lse
 
@@ -474,7 +478,7 @@ class Batch:
             cv, sv = get_rows(self.pools[1], self.page, self.vt, D, 8, self.slots[b])
             dk = np.repeat(sk.astype(np.float64), 32, axis=-1)
             k, v = ck * dk, cv * np.repeat(sv.astype(np.float64), 32, axis=-1)
-            many = self.elem != F32 and D in (64, 128) and n * G > (32 if self.elem == BF16 and len(self.q_len) * self.NKV > 38 else 64)
+            many = self.elem != F32 and D in (64, 128) and n * G > (32 if self.elem == BF16 else 64)
             wide = np.abs(k) if many or self.kt == Q8 else 16 * dk
             q = self.q[t0:t0 + n].double().numpy()
             if self.basis:
@@ -599,14 +603,18 @@ MANY = [
     ([12, 9, 8, 1] * 3, [(61 * i) % 700 + 12 for i in range(12)], 16, 4, 128, 16, Q4, Q8, BF16, 1, True, 0),
     ([33, 64, 32] * 13, [(83 * i) % 900 for i in range(39)], 1, 1, 64, 16, Q4, Q4, BF16, 0, True, 200),
     ([5, 4] * 4, [300 + 150 * i for i in range(8)], 40, 5, 128, 48, Q8, Q4, F16, 0, False, 0),
+    # row tiles enough that no tokens are split
+    ([640, 700], [640, 900], 16, 8, 128, 16, Q4, Q4, F16, 0, True, 0),
+    ([500], [520], 40, 20, 64, 32, Q8, Q8, BF16, 1, True, 0),
 ]
 
 
 @gpu
+@pytest.mark.parametrize("wide", [True, False])
 @pytest.mark.parametrize("case", MANY, ids=str)
-def test_attention_of_many_tokens(bq, case):
+def test_attention_of_many_tokens(bq, case, wide):
     *args, causal, window = case
-    Batch(bq, *args).check(causal, window)
+    Batch(bq, *args, wide=wide).check(causal, window)
 
 
 @gpu
