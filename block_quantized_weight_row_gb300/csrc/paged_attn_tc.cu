@@ -55,7 +55,11 @@ constexpr int kTile = 128;  // tokens per step, rows per row tile
 constexpr int kHead = 6;    // weights carry 2^kHead
 constexpr int kSub = 128 * 128;  // bytes of an operand sub-tile: 128 rows x 64 binary16
 
-// kSFull, kPReady: [row tile][half]
+// kSFull, kPReady: [row tile][half]. A phase of a barrier counts each of its
+// arrivals once: no thread may arrive for a later phase while the one before is
+// open. The empty barriers see to it for all but one, the V warps' arrival
+// on kKFull (their exponents), which comes before their wait for kVEmpty: it
+// waits for the phase of two tiles before itself.
 enum Bar { kKFull = 0, kKEmpty = 2, kVFull = 4, kVEmpty = 6, kSFull = 8, kPReady = 12, kODone = 16, kAllDone = 18, kQReady = 20, kBars = 21 };
 
 struct Misc {
@@ -655,6 +659,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           e = max_u16x2(e, sc[i][k]);
         }
       const int ve = scale_up(e);
+      // kVEmpty of the first two tiles lets this warp get to tile 2 before a K
+      // warp has arrived for tile 0: without the wait it would count in its
+      // place, and S of tile 0 be taken from rows not written yet. Nearly
+      // always complete.
+      if (!pa_wait_warp(&bar[kKFull + (j & 1)], ((j >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
       if (lane == 0) {
         mi->vx[j & 3][w] = ve;
         mbar_arrive(&bar[kKFull + (j & 1)]);

@@ -1,0 +1,28 @@
+"""Paged KV cache: calls at the edges of what is promised, each against the plain
+64-bit implementation of test_paged_cache.py or the documented status."""
+import torch
+
+from test_paged_cache import BF16, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
+
+
+@gpu
+def test_many_rows_from_cold_pages_every_time(bq):  # noqa: F811
+    """Operand warps that arrive late (pages out of L2 and of the address caches, scattered over gigabytes): the same bits each time."""
+    kv = [900, 64, 700, 385, 513, 800, 260, 129]
+    b = Batch(bq, [64] * 8, kv, 48, 12, 128, 16, Q4, Q8, BF16, seed=5)  # row tiles enough that no tokens are split
+    n_pages = (1 << 32) // (12 * b.pools[0].shape[2])
+    pools = [torch.empty(n_pages, 12, p.shape[2], dtype=torch.uint8, device="cuda") for p in b.pools]
+    far = torch.arange(b.pools[0].shape[0]) * ((n_pages - 1) // b.pools[0].shape[0])
+    for pool, page in zip(pools, b.pools):
+        pool[far.cuda()] = torch.from_numpy(page).cuda()
+    b.cache = bq.PagedCache(*pools, 16, 128, Q4, Q8, 0)
+    table = b.pt.long().cpu()
+    used = table < len(far)  # the rest is never to be read
+    b.pt = torch.where(used, far[torch.where(used, table, 0)], table).int().cuda()
+    b.check()
+    first = b.run()
+    q, flush = b.q.cuda(), torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for _ in range(50):
+        flush.fill_(1)
+        for x, y in zip(b.run(q=q), first):
+            assert torch.equal(x, y)
