@@ -505,9 +505,11 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
       for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, w));
       // 2^k brings the row's largest value to [2^10, 2^11)
       const int k = top > 0.0f ? min(10 + 127 - int(__float_as_uint(top) >> 23), 110) : 0;
-      // (the scale's sign goes into q, and a scale of 0 leaves scores of ~0)
+      // (the scale's sign goes into q). The factor stays positive, also for a
+      // scale of 0 or a product below binary32's range: it multiplies the -infinity
+      // of masked scores and divides; any score is below 2^42 times it, ~0.
       const float up = copysignf(__int_as_float((127 + k) << 23), a.scale_log2);
-      if (lane == 0) q_scale[local] = fmaxf(fabsf(a.scale_log2), 1e-30f) * kKUnit * __int_as_float((127 - k) << 23);
+      if (lane == 0) q_scale[local] = fmaxf(fabsf(a.scale_log2) * kKUnit * __int_as_float((127 - k) << 23), 1e-37f);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {

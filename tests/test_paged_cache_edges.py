@@ -1,8 +1,9 @@
 """Paged KV cache: calls at the edges of what is promised, each against the plain
 64-bit implementation of test_paged_cache.py or the documented status."""
+import pytest
 import torch
 
-from test_paged_cache import BF16, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
+from test_paged_cache import BF16, F32, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
 
 
 @gpu
@@ -26,3 +27,13 @@ def test_many_rows_from_cold_pages_every_time(bq):  # noqa: F811
         flush.fill_(1)
         for x, y in zip(b.run(q=q), first):
             assert torch.equal(x, y)
+
+
+@gpu
+@pytest.mark.parametrize("scale,peaked", [(0.0, 1.0), (0.0, 1e-13), (-0.0, 1e-25), (1e-30, 1e-10)])
+@pytest.mark.parametrize("n,elem,kt", [(1, F32, Q4), (3, F32, Q8), (1, BF16, Q4), (5, BF16, Q8), (90, BF16, Q4)])
+def test_scores_of_zero_give_the_mean(bq, n, elem, kt, scale, peaked):  # noqa: F811
+    """A scale of 0, and products of scale and q below binary32's range: every token seen weighs the same, masked ones nothing."""
+    b = Batch(bq, [n, n], [n + 300, n + 13], 8, 4, 128, 16, kt, Q4, elem, peaked=peaked)
+    b.scale = scale
+    b.check()
