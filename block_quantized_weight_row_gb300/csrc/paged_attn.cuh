@@ -417,15 +417,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
     const int32_t *table = a.page_table + int64_t(seq) * a.table_stride;
     const uint8_t *kh = a.kp.base + int64_t(kvh) * head_k, *vh = a.vp.base + int64_t(kvh) * head_v;
     const int64_t page_k = head_k * a.sh.n_kv, page_v = head_v * a.sh.n_kv;
-    // A stage: 16-token tiles, each within one page. A tile past what any row
-    // sees, or on a page outside the pool (never read: reported), is zero-filled
-    // with the pool's first tile as the address.
+    // A stage: 16-token tiles, each within one page. A tile outside what any row
+    // sees (its table entry may be stale: before a window too), or on a page
+    // outside the pool (never read: reported), is zero-filled with the pool's
+    // first tile as the address.
     auto issue = [&](int ti, int stage) {
       if (ti < tile_end) {
 #pragma unroll
         for (int u = 0; u < TT; ++u) {
           const int tok = ti * TOK + u * 16;
-          const bool seen = tok < hi_any;
+          const bool seen = tok < hi_any && tok + 16 > lo_any;
           const int pi = token_page(a.sh, tok);
           uint32_t page = seen ? uint32_t(__ldg(table + pi)) : 0u;
           uint32_t place = uint32_t(tok - pi * a.sh.page_size), bytes = seen ? 16u : 0u;

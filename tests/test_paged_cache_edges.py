@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from test_paged_cache import BF16, F32, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
+from test_paged_cache import BF16, F16, F32, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
 
 
 @gpu
@@ -37,3 +37,15 @@ def test_scores_of_zero_give_the_mean(bq, n, elem, kt, scale, peaked):  # noqa: 
     b = Batch(bq, [n, n], [n + 300, n + 13], 8, 4, 128, 16, kt, Q4, elem, peaked=peaked)
     b.scale = scale
     b.check()
+
+
+@gpu
+@pytest.mark.parametrize("n,D,elem,kt", [(1, 128, BF16, Q4), (3, 64, F32, Q4), (2, 96, F16, Q8), (1, 256, BF16, Q4), (130, 128, BF16, Q4)])
+@pytest.mark.parametrize("window", [1, 85, 102])
+def test_pages_before_the_window_are_not_needed(bq, n, D, elem, kt, window):  # noqa: F811
+    """Pages that lie wholly before what a sequence's first query sees have been given back: entries of no page are no error."""
+    kv = [777, 300, 1000, n, 4099, 110]
+    b = Batch(bq, [n] * 6, kv, 8, 4, D, 16, kt, Q4, elem)
+    for s, length in enumerate(kv):
+        b.pt[s, :max(0, length - n - window + 1) // 16] = -1 if s % 2 else 12345678
+    b.check(window=window)
