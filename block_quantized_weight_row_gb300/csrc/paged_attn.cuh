@@ -28,10 +28,14 @@
 //     terms (22 bits), 2^-22 instead of 2^-11. A 16-bit output's weights take
 //     one term: 2^-11 each, an eighth of bf16's own rounding.
 //   - Weights d_v p are scaled by a power of two per warp that keeps them
-//     below 2^14 whatever the V scales are (d_v at most 2^6), and a row's
-//     maximum is only raised (and the accumulators rescaled) when a score
-//     passes it by 2^8: with fp32 accumulators any common factor serves.
-//     Weights below 2^-30 of the largest d_v round to nothing.
+//     in binary16 whatever the V scales are, and a row's maximum is only raised
+//     (and the accumulators rescaled) when a score passes it by 2^8 (16-bit
+//     calls; d_v below 2^6) or 2 (fp32 calls; d_v in [2^13, 2^14)): with fp32
+//     accumulators any common factor serves. The terms end at binary16's
+//     smallest subnormal: d_v p is off by up to 2^-25, that is 2^-29 (16-bit) or
+//     2^-37 (fp32) of the warp's largest d_v and the row's largest p there. The
+//     headroom of the 16-bit calls would cost an fp32 call with 131071 tokens
+//     beside dominant ones up to 2^-12 of its output; so 2^-20.
 //   - Softmax statistics and the accumulators are fp32; transposing the
 //     weights from "row = token" to "column = query row" is one movmatrix.
 //   - A warp streams its own tiles through a private ring of asynchronous
@@ -59,7 +63,7 @@ namespace paged {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr float kRaise = 8.0f;   // a maximum is raised when passed by this much (base-2 units)
+constexpr float kRaise = 8.0f;   // a maximum is raised when passed by this much (base-2 units; fp32 calls: below)
 constexpr float kNoMax = -3.402823466e38f;  // no score seen yet
 constexpr int kNoExp = 0x7fffffff;  // no V scale seen yet
 constexpr float kLog2e = 1.4426950408889634f;
@@ -315,6 +319,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
   // of the products' accumulators
   constexpr bool KSUB = K4 && TERMS == 1, VSUB = V4 && TERMS == 1;
   constexpr float kKUnit = KSUB ? 16777216.0f : 1.0f, kVUnit = VSUB ? 16777216.0f : 1.0f;
+  // A maximum is raised when passed by kPass, the largest V scale brought to
+  // [2^kHeadV, 2^(kHeadV + 1)): weights stay below 2^14 or 2^15. (64 ragged
+  // sequences of up to 8192 tokens in fp32: 132 us; 137 raised by anything, 136
+  // with the 16-bit calls' 2^8.)
+  constexpr float kPass = TERMS == 1 ? kRaise : 1.0f;
+  constexpr int kHeadV = TERMS == 1 ? 5 : 13;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sh_scan[kWarps + 1];
   __shared__ int64_t sh_find[2];
@@ -651,10 +661,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
 #pragma unroll
           for (int i = 0; i < (NB + 1) / 2; ++i) vmax = max_u16x2(vmax, vs[u][h][i]);  // scales are not negative
         }
-      // power of two that brings the largest V scale seen to [2^5, 2^6): the
-      // binary16 exponent (subnormals count as the smallest normal) decides
+      // power of two that brings the largest V scale seen there: the binary16
+      // exponent (subnormals count as the smallest normal) decides
       vmax = __reduce_max_sync(kFull, max(vmax & 0x7fffu, (vmax >> 16) & 0x7fffu));
-      const int need = 20 - max(int(vmax >> 10), 1);  // 2^5 / 2^(e - 15)
+      const int need = 15 + kHeadV - max(int(vmax >> 10), 1);  // 2^kHeadV / 2^(e - 15)
       if (need < vexp) {  // warp-uniform; rare after the first tile
         if (vexp != kNoExp) {
           const float f = __int_as_float((127 + need - vexp) << 23);
@@ -697,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<NB, KT, VT, R, TERMS>::kCtas))
             const float mn = fmaxf(m[r][e], ceilf(t * qscale[r][e]));
             const float al = ex2(m[r][e] - mn);
             m[r][e] = mn;
-            limit[r][e] = (mn + kRaise) / qscale[r][e];
+            limit[r][e] = (mn + kPass) / qscale[r][e];
             l[r][e] *= al;
 #pragma unroll
             for (int b = 0; b < NB; ++b)

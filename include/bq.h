@@ -358,8 +358,12 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
  * its sequence empty; bq_device_status reports each (BQ_ERR_INDEX).
  * Accuracy: fp32 statistics and sums; q and weights in binary16 terms (fp32
  * calls two each, 2^-22 together; 16-bit calls one: q exactly unless rotated,
- * 2^-11 of a weight); weights below 2^-30 of the largest V scale vanish. In
- * 16-bit calls with head_dim 64 or 128 and work enough by the bounds given
+ * 2^-11 of a weight). The terms end where binary16 does: beside a token of
+ * weight w and the largest V scale d, another's weight times its V scale is off
+ * by up to 2^-37 w d (fp32 calls) or 2^-29 w d (16-bit calls), and n tokens
+ * together by at most n times that (131071 of them: 2^-20, 2^-12). Scores are
+ * taken to stay below 2^20 in magnitude.
+ * In 16-bit calls with head_dim 64 or 128 and work enough by the bounds given
  * (query rows / 16 x n_seqs x n_kv_heads x (max_kv_len + 512) from 250000),
  * sequences of many query rows per kv head (q_len * n_heads / n_kv_heads above
  * 64, in bf16 above 32) run on the tensor-memory kernel, where k^, v^ and a

@@ -1,5 +1,8 @@
 """Paged KV cache: calls at the edges of what is promised, each against the plain
 64-bit implementation of test_paged_cache.py or the documented status."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
@@ -49,3 +52,36 @@ def test_pages_before_the_window_are_not_needed(bq, n, D, elem, kt, window):  # 
     for s, length in enumerate(kv):
         b.pt[s, :max(0, length - n - window + 1) // 16] = -1 if s % 2 else 12345678
     b.check(window=window)
+
+
+@gpu
+@pytest.mark.parametrize("bits", [18.0, 26.3, 30.0, 34.0])
+def test_fp32_small_weights_beside_dominant_ones(bq, bits):  # noqa: F811
+    """Many tokens whose weights are 2^-bits of the largest, in every warp beside one of those, are not lost from an fp32 call.
+
+    16 tokens of V = 0 hold almost all weight; the others have V = 7, so that the output is their share. Each other
+    token's weight is off by half a step of binary16's subnormals where the largest V scale (1 here) times the
+    row's largest weight is at least 2^12: 2^-37 of that largest weight; by 2^-22 of itself; and by the scores' and sums'
+    roundings as derived in test_paged_cache.py.
+    """
+    n, D, page, B = 2048, 64, 64, 304
+    k = np.zeros((n // page, 1, page * 2 * 34), np.uint8)
+    v = np.full((n // page, 1, page * 2 * 18), 0xFF, np.uint8)  # codes of 7
+    for pool, codes in ((k, 64), (v, 32)):
+        pool[:, :, page * codes::2], pool[:, :, page * codes + 1::2] = 0x00, 0x3C  # scales of 1
+    for t in range(0, 256, 16):  # in each of the 16-token tiles that the warps start with
+        p, i = divmod(t, page)
+        k[p, :, i * 64:(i + 1) * 64] = 1
+        v[p, :, i * 32:(i + 1) * 32] = 0x88  # codes of 0
+    cache = bq.PagedCache(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), page, D, Q8, Q4)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    scale = float(np.float32(bits * math.log(2) / D))
+    o = bq.paged_attn(cache, torch.ones(B, 1, D, device="cuda"), torch.arange(B + 1, dtype=torch.int32, device="cuda"), i32([n] * B),
+                      i32([list(range(n // page))] * B), scale, max_q_len=1, max_kv_len=n).double().cpu().numpy()
+    u16, u32, mag = 2.0**-11, 2.0**-24, scale * D
+    w = (n - 16) * math.exp(-mag)
+    want = 7 * w / (16 + w)
+    ds = (34 + 2 + 4) * 2 * u32 * mag + 3 * u16**2 * mag + 2 * u32 * mag
+    rel = 2 * ds + u16**2 + 6 * u32 + (n / 8 + 64) * 2 * u32
+    tol = rel * want * 1.01 + 7 * (n - 16) * 2.0**-37 / 16 + u32 * want
+    assert np.isfinite(o).all() and np.abs(o - want).max() <= tol, f"{np.abs(o - want).max() / want:.3g} of the output, {tol / want:.3g} allowed"
