@@ -396,7 +396,7 @@ def paged_kv_write(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, slots: t
     page_size + place; -1 skips a token). bias (n_kv_heads, head_dim) fp32:
     subtracted from K, calibrated in bias_basis (default: the cache's)."""
     r = (_ext or _paged()).kv_write(cache.k_pages, cache.v_pages, cache.page_size, cache.head_dim, cache.k_type,
-                                    cache.v_type, cache.k_basis, k, v, slots, bias, -1 if bias_basis is None else bias_basis)
+                                    cache.v_type, cache.k_basis, k, v, slots, bias, bias_basis)
     if r is not None:
         _check(r, "bq_paged_kv_write")
 
@@ -408,8 +408,8 @@ def paged_kv_read(cache: PagedCache, slots: torch.Tensor, dtype: torch.dtype = t
     """The rows at slots (int64; -1: zeros) as (K, V), each (tokens,
     n_kv_heads, head_dim) of dtype; K out of the cache's basis, plus bias."""
     r = (_ext or _paged()).kv_read(cache.k_pages, cache.v_pages, cache.page_size, cache.head_dim, cache.k_type,
-                                   cache.v_type, cache.k_basis, slots, ELEM.get(dtype, -1), bias,
-                                   -1 if bias_basis is None else bias_basis, out_k, out_v)
+                                   cache.v_type, cache.k_basis, slots, ELEM.get(dtype, -1), bias, bias_basis,
+                                   out_k, out_v)
     if type(r) is int:
         _check(r, "bq_paged_kv_read")
     return r

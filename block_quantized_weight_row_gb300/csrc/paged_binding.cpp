@@ -16,6 +16,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdarg>
 
 #include "bq.h"
@@ -48,6 +49,13 @@ int64_t to_int(PyObject *o, const char *name) {
   return v;
 }
 
+// A type, basis or other code that the library takes as an int.
+int to_code(PyObject *o, const char *name) {
+  const int64_t v = to_int(o, name);
+  if (v < INT_MIN || v > INT_MAX) wrong(PyExc_ValueError, "%s must fit 32 bits", name);
+  return int(v);
+}
+
 int elem_of(at::ScalarType t) {
   switch (t) {
     case at::kFloat: return BQ_ELEM_F32;
@@ -57,7 +65,7 @@ int elem_of(at::ScalarType t) {
   }
 }
 
-int block_bytes(int64_t type) { return type == BQ_TYPE_Q4_0 ? 18 : type == BQ_TYPE_Q8_0 ? 34 : 0; }
+int block_bytes(int type) { return type == BQ_TYPE_Q4_0 ? 18 : type == BQ_TYPE_Q8_0 ? 34 : 0; }
 
 // args[0..6]: k_pages, v_pages, page_size, head_dim, k_type, v_type, k_basis
 struct Cache {
@@ -67,9 +75,9 @@ struct Cache {
 constexpr int kCacheArgs = 7;
 
 Cache cache_of(PyObject *const *args) {
-  const at::Tensor &k = cuda_tensor(args[0], "k_pages"), &v = cuda_tensor(args[1], "v_pages");
   const int64_t page = to_int(args[2], "page_size"), dim = to_int(args[3], "head_dim");
-  const int64_t types[2] = {to_int(args[4], "k_type"), to_int(args[5], "v_type")};
+  const int types[2] = {to_code(args[4], "k_type"), to_code(args[5], "v_type")}, basis = to_code(args[6], "k_basis");
+  const at::Tensor &k = cuda_tensor(args[0], "k_pages"), &v = cuda_tensor(args[1], "v_pages");
   const at::Tensor *pools[2] = {&k, &v};
   const char *names[2] = {"k_pages", "v_pages"};
   for (int i = 0; i < 2; ++i) {
@@ -84,9 +92,7 @@ Cache cache_of(PyObject *const *args) {
   }
   if (k.size(0) != v.size(0) || k.size(1) != v.size(1) || k.device() != v.device())
     wrong(PyExc_ValueError, "k_pages and v_pages must have the same pages, heads and device");
-  return Cache{bq_paged_cache{k.data_ptr(), v.data_ptr(), k.size(0), page, k.size(1), dim, int(types[0]), int(types[1]),
-                              int(to_int(args[6], "k_basis"))},
-               k.device()};
+  return Cache{bq_paged_cache{k.data_ptr(), v.data_ptr(), k.size(0), page, k.size(1), dim, types[0], types[1], basis}, k.device()};
 }
 
 void same_device(const at::Tensor &t, const at::Device &d, const char *name) {
@@ -118,11 +124,8 @@ const float *bias_of(PyObject *o, const Cache &c) {
   return o == Py_None ? nullptr : exact(o, "bias", c, at::kFloat, {c.c.n_kv_heads, c.c.head_dim}).data_ptr<float>();
 }
 
-// -1 as the bias's basis: the cache's
-int basis_of(PyObject *o, const Cache &c) {
-  const int64_t b = to_int(o, "bias_basis");
-  return b < 0 ? c.c.k_basis : int(b);
-}
+// None as the bias's basis: the cache's
+int basis_of(PyObject *o, const Cache &c) { return o == Py_None ? c.c.k_basis : to_code(o, "bias_basis"); }
 
 void use_stream() { bq_set_stream(c10::cuda::getCurrentCUDAStream().stream()); }
 

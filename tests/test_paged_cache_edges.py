@@ -85,3 +85,30 @@ def test_fp32_small_weights_beside_dominant_ones(bq, bits):  # noqa: F811
     rel = 2 * ds + u16**2 + 6 * u32 + (n / 8 + 64) * 2 * u32
     tol = rel * want * 1.01 + 7 * (n - 16) * 2.0**-37 / 16 + u32 * want
     assert np.isfinite(o).all() and np.abs(o - want).max() <= tol, f"{np.abs(o - want).max() / want:.3g} of the output, {tol / want:.3g} allowed"
+
+
+@pytest.mark.parametrize("name", ["k_type", "v_type", "k_basis"])
+@pytest.mark.parametrize("value", [Q4 + (1 << 32), Q8 - (1 << 32), 1 << 31, 1 << 62])
+def test_codes_beyond_32_bits_are_refused(bq, name, value):  # noqa: F811
+    """No type or basis reaches the library cut to 32 bits, past the check of the pools' sizes (looked at before any tensor)."""
+    pool = torch.zeros(2, 1, 16 * 36, dtype=torch.uint8)
+    c = bq.PagedCache(pool, pool.clone(), 16, 64, **{name: value})
+    x, i = torch.zeros(1, 1, 64), torch.zeros(1, dtype=torch.int32)
+    for call in (lambda: bq.paged_kv_write(c, x, x, i.long()), lambda: bq.paged_kv_read(c, i.long()),
+                 lambda: bq.paged_attn(c, x, i, i, i[None], 0.1, max_q_len=1, max_kv_len=1)):
+        with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+            call()
+
+
+@gpu
+def test_a_biass_basis_is_taken_as_given(bq):  # noqa: F811
+    """Only no basis at all means the cache's: -1 and a code beyond 32 bits are refused."""
+    c = bq.PagedCache.empty(2, 16, 1, 64)
+    x, slots, bias = torch.zeros(1, 1, 64, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda"), torch.zeros(1, 64, device="cuda")
+    bq.paged_kv_write(c, x, x, slots, bias)
+    bq.paged_kv_read(c, slots, bias=bias, bias_basis=0)
+    for basis, error in ((-1, bq.BQError), (1, bq.BQError), (1 << 32, ValueError)):
+        with pytest.raises(error):
+            bq.paged_kv_write(c, x, x, slots, bias, basis)
+        with pytest.raises(error):
+            bq.paged_kv_read(c, slots, bias=bias, bias_basis=basis)
