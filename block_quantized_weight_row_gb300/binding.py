@@ -90,6 +90,7 @@ def lib():
         "bq_set_stream": ([vp], i),
         "bq_get_stream": ([], vp),
         "bq_set_workspace": ([vp, sz], i),
+        "bq_get_workspace": ([ctypes.POINTER(sz)], vp),
         "bq_workspace_size": ([i, i64, i64, i64], sz),
         "bq_gemv_workspace_size": ([i, i64], sz),
         "bq_last_error": ([], ctypes.c_char_p),

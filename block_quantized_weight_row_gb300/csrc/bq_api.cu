@@ -205,6 +205,11 @@ int bq_set_workspace(void *dev_ptr, size_t bytes) {
   return ok();
 }
 
+void *bq_get_workspace(size_t *bytes) {
+  if (bytes) *bytes = t_ws_bytes;
+  return t_ws;
+}
+
 size_t bq_workspace_size(int type, int64_t M, int64_t N, int64_t K) {
   if (type != BQ_TYPE_Q8_0 || M <= 0 || N <= 0 || K <= 0 || K % kQK) return 0;
   if (!sizes_ok(N, K) || M > 0x7fffffffll || N > 0x7fffffffll) return 0;

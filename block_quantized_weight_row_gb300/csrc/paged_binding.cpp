@@ -221,20 +221,23 @@ PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
     }
     float *lse = args[10] == Py_None ? nullptr : exact(args[10], "lse", c, at::kFloat, {n_q, H}).data_ptr<float>();
     // a workspace of this call's own, from the current stream's pool: calls on
-    // other streams and captured launches never share it
+    // other streams and captured launches never share it; the one that the
+    // thread had set for other calls is set again after it
     const size_t need = bq_paged_attn_workspace_size(&c.c, elem, B, n_q, max_q, max_kv, H, causal, window);
     const at::Tensor ws = at::empty({int64_t(std::max<size_t>(need, 256))}, q.options().dtype(at::kByte));
     use_stream();
+    size_t before_bytes;
+    void *const before = bq_get_workspace(&before_bytes);
     bq_set_workspace(ws.data_ptr(), size_t(ws.numel()));
     const int r = bq_paged_attn(&c.c, elem, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1), lse,
                                 start.data_ptr<int>(), lens.data_ptr<int>(), table.data_ptr<int>(), pages, B, n_q, max_q, max_kv, H,
                                 float(scale), causal, window);
     if (r) {  // the message of the call stays the last one
       const std::string message = bq_last_error();
-      bq_set_workspace(nullptr, 0);
+      bq_set_workspace(before, before_bytes);
       return Py_BuildValue("(is)", r, message.c_str());
     }
-    bq_set_workspace(nullptr, 0);
+    bq_set_workspace(before, before_bytes);
     return THPVariable_Wrap(out);
   } catch (const Wrong &) {
     return nullptr;

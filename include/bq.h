@@ -438,6 +438,8 @@ int bq_set_weight_prefetch(int enable);
 
 /* Caller-owned device workspace for the calling thread (NULL, 0 clears it). */
 int bq_set_workspace(void *dev_ptr, size_t bytes);
+/* The one set (NULL if none); *bytes, where bytes is not NULL: its size. */
+void *bq_get_workspace(size_t *bytes);
 /* Bytes of workspace an entry point needs for these sizes (0 if none). */
 size_t bq_workspace_size(int type, int64_t M, int64_t N, int64_t K);
 

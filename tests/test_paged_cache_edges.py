@@ -1,5 +1,6 @@
 """Paged KV cache: calls at the edges of what is promised, each against the plain
 64-bit implementation of test_paged_cache.py or the documented status."""
+import ctypes
 import math
 
 import numpy as np
@@ -112,3 +113,36 @@ def test_a_biass_basis_is_taken_as_given(bq):  # noqa: F811
             bq.paged_kv_write(c, x, x, slots, bias, basis)
         with pytest.raises(error):
             bq.paged_kv_read(c, slots, bias=bias, bias_basis=basis)
+
+
+@gpu
+def test_attention_leaves_the_callers_workspace_set(bq):  # noqa: F811
+    """paged_attn takes a workspace of its own: one that the thread had set for C calls is still set after it, a failed call too."""
+    b = Batch(bq, [1], [100], 4, 2, 64, 16, Q4, Q4, F32)
+    L = bq.lib()
+    mine, size = torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), ctypes.c_size_t()
+    try:
+        assert L.bq_set_workspace(mine.data_ptr(), 1 << 20) == 0
+        b.run()
+        assert (L.bq_get_workspace(size), size.value) == (mine.data_ptr(), 1 << 20)
+        with pytest.raises(bq.BQError):
+            b.run(causal=False, window=3)
+        assert (L.bq_get_workspace(None), size.value) == (mine.data_ptr(), 1 << 20)
+        L.bq_set_workspace(None, 0)
+        b.run()
+        assert (L.bq_get_workspace(size), size.value) == (None, 0)
+    finally:
+        L.bq_set_workspace(None, 0)
+
+
+def test_workspace_is_read_as_it_was_set(bq):  # noqa: F811
+    L, size = bq.lib(), ctypes.c_size_t(7)
+    L.bq_set_workspace(None, 0)
+    assert (L.bq_get_workspace(size), size.value) == (None, 0)
+    try:
+        assert L.bq_set_workspace(1 << 40, 4096) == 0
+        assert (L.bq_get_workspace(size), size.value) == (1 << 40, 4096) and L.bq_get_workspace(None) == 1 << 40
+        assert L.bq_set_workspace((1 << 40) + 8, 4096) != 0  # refused: the one before stays
+        assert L.bq_get_workspace(None) == 1 << 40
+    finally:
+        L.bq_set_workspace(None, 0)
