@@ -235,8 +235,9 @@ int bq_device_status(void) {
   e = cudaMemcpyFromSymbol(&word, g_error_word, sizeof word);
   if (e != cudaSuccess) return cuda_fail(e, "bq_device_status: read error word");
   if (word) {
-    const unsigned int zero = 0;
-    e = cudaMemcpyToSymbol(g_error_word, &zero, sizeof zero);
+    // one kind per call: another that is set stays for the next
+    const unsigned int rest = word & kErrTimeout ? word & ~kErrTimeout : word & ~kErrIndex;
+    e = cudaMemcpyToSymbol(g_error_word, &rest, sizeof rest);
     if (e != cudaSuccess) return cuda_fail(e, "bq_device_status: clear error word");
     if (word & kErrTimeout) return fail(BQ_ERR_TIMEOUT, "a bounded in-kernel wait ran out (error word 0x%x)", word);
     if (word & kErrIndex)

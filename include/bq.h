@@ -466,9 +466,10 @@ int bq_block_bytes(int type);
  * unknown type. */
 int bq_block_values(int type);
 
-/* Synchronize the calling thread's stream, then read and clear the device
- * error word: BQ_OK, BQ_ERR_TIMEOUT if a bounded wait ran out, BQ_ERR_INDEX if
- * a slot, page or length of a paged cache was out of range, BQ_ERR_CUDA if the
+/* Synchronize the calling thread's stream, then report and clear one kind of
+ * error from the device error word: BQ_ERR_TIMEOUT if a bounded wait ran out,
+ * else BQ_ERR_INDEX if a slot, page or length of a paged cache was out of range,
+ * else BQ_OK (where both happened, two calls report them). BQ_ERR_CUDA if the
  * synchronization itself failed. */
 int bq_device_status(void);
 

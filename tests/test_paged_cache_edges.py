@@ -146,3 +146,17 @@ def test_workspace_is_read_as_it_was_set(bq):  # noqa: F811
         assert L.bq_get_workspace(None) == 1 << 40
     finally:
         L.bq_set_workspace(None, 0)
+
+
+@gpu
+def test_device_status_reports_every_kind_of_error(bq):  # noqa: F811
+    """A wait that ran out and a wrong page in one batch: both are reported, one call each."""
+    b = Batch(bq, [150, 1], [400, 100], 4, 2, 128, 16, Q4, Q4, BF16)
+    b.pt[1, 0] = -1
+    L = bq.lib()
+    try:
+        assert L.bq_set_spin_limit(0) == 0
+        b.run()
+    finally:
+        L.bq_set_spin_limit(-1)
+    assert [bq.binding.device_status() for _ in range(3)] == [-6, -9, 0]
