@@ -1,7 +1,9 @@
 """Build libbq.so in-tree with nvcc for sm_103a (GB300).
 
 Each CUDA translation unit compiles in parallel to an object file under
-csrc/_build/, and the objects link into block_quantized_weight_row_gb300/libbq.so.
+csrc/_build/, and the objects link into block_quantized_weight_row_gb300/libbq.so. The paged
+calls' host side (_paged.so, against torch's headers) comes after it: where that
+cannot be built, the library is there all the same and build() raises.
 No CPU fallback is built: the library is CUDA-only.
 """
 import concurrent.futures as cf
@@ -93,24 +95,30 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     build_probe = force or _stale(PROBE_LIB, [probe_src, __file__] + deps)
     if build_probe:
         jobs.append([cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-shared", probe_src, "-o", probe_tmp])
-    ext_tmp = EXT_LIB + f".tmp{os.getpid()}"
-    ext_obj, ext_compile, ext_link = ext_commands(ext_tmp)
-    build_ext = force or _stale(ext_obj, [os.path.join(CSRC, EXT_SRC), __file__, os.path.join(INCLUDE, "bq.h")])
-    if build_ext:
-        jobs.append(ext_compile)
+
+    def compile_ext():
+        """The extension's object: its link line, and whether to link it."""
+        obj, compile_, link = ext_commands(EXT_LIB + f".tmp{os.getpid()}")
+        new = force or _stale(obj, [os.path.join(CSRC, EXT_SRC), __file__, os.path.join(INCLUDE, "bq.h")])
+        if new:
+            run(compile_)
+        return link, new or _stale(EXT_LIB, [obj])
+
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 2) as ex:
+        ext = ex.submit(compile_ext)
         for out in ex.map(run, jobs):
             if verbose and out:
                 print(out, file=sys.stderr)
     if build_probe:
         os.replace(probe_tmp, PROBE_LIB)
-    if force or any(j[0] == cc and "-c" in j for j in jobs) or _stale(LIB, objs):
+    if force or any("-c" in j for j in jobs) or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         run([cc, *ARCH, "-shared", "-o", tmp, *objs])
         os.replace(tmp, LIB)
-    if build_ext or _stale(EXT_LIB, [ext_obj]):
-        run(ext_link)
-        os.replace(ext_tmp, EXT_LIB)
+    link, relink = ext.result()  # raises here what it raised
+    if relink:
+        run(link)
+        os.replace(link[link.index("-o") + 1], EXT_LIB)
     return LIB
 
 
