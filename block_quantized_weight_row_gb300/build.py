@@ -59,6 +59,12 @@ def ext_commands(tmp):
     return obj, compile_, link
 
 
+def ext_versions() -> str:
+    """What the extension's object depends on besides its sources."""
+    import torch
+    return f"torch {torch.__version__} {torch.version.git_version} {os.path.dirname(torch.__file__)}, python {sys.version}"
+
+
 def _deps():
     hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     return hdrs + [os.path.join(INCLUDE, "bq.h"), __file__]
@@ -97,11 +103,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         jobs.append([cc, *ARCH, *NVCC_FLAGS, *extra_flags, "-shared", probe_src, "-o", probe_tmp])
 
     def compile_ext():
-        """The extension's object: its link line, and whether to link it."""
+        """The extension's object: its link line, and whether to link it.
+
+        An object is as good as the headers it was made with: another torch or
+        Python than the one noted beside it makes it stale.
+        """
         obj, compile_, link = ext_commands(EXT_LIB + f".tmp{os.getpid()}")
+        made_with, note = ext_versions(), obj + ".with"
         new = force or _stale(obj, [os.path.join(CSRC, EXT_SRC), __file__, os.path.join(INCLUDE, "bq.h")])
+        if not new:
+            new = not os.path.exists(note) or open(note, encoding="utf-8").read() != made_with
         if new:
             run(compile_)
+            with open(note, "w", encoding="utf-8") as f:
+                f.write(made_with)
         return link, new or _stale(EXT_LIB, [obj])
 
     with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 2) as ex:

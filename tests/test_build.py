@@ -69,3 +69,15 @@ def test_the_library_is_linked_where_the_extension_cannot_be_built(tree, monkeyp
     monkeypatch.setattr(bq_build, "ext_commands", commands)  # mended: the rest follows
     bq_build.build()
     assert (path / "ext.so").exists() and "lib.so" not in built()
+
+
+def test_the_extension_follows_torch(tree, monkeypatch):
+    """Another torch (or Python): only the extension is compiled and linked again, once."""
+    path, built = tree
+    bq_build.build()
+    built()
+    monkeypatch.setattr("torch.__version__", "2.999.0")
+    bq_build.build()
+    assert built() == ["e.o", "ext.so"]
+    bq_build.build()
+    assert built() == []
