@@ -85,6 +85,7 @@ def lib():
         "bq_paged_attn": ([cp, i, vp, i64, i64, vp, i64, i64, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64,
                            ctypes.c_float, i, i64], i),
         "bq_paged_attn_workspace_size": ([cp, i, i64, i64, i64, i64, i64, i, i64], sz),
+        "bq_paged_attn_many_rows": ([cp, i, i64, i64, i64, i64, i64, i, i64], i64),
         "bq_paged_slot_check": ([cp, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)], i),
         "bq_block_dots": ([i, vp, vp, vp, i64, i64], i),
         "bq_set_stream": ([vp], i),

@@ -126,6 +126,7 @@ cudaError_t launch_paged_read(const PagedPool &kp, const PagedPool &vp, const Pa
                               cudaStream_t stream);
 bool paged_attn_dim(int64_t head_dim);
 size_t paged_attn_workspace_bytes(PagedAttnArgs a, int max_q);
+int64_t paged_attn_many_rows(PagedAttnArgs a, int max_q);  // rows of a sequence above which the many-row kernel has it; 0: never
 cudaError_t launch_paged_attn(PagedAttnArgs a, int max_q, void *ws, cudaStream_t stream);
 cudaError_t launch_block_dots(int type, const uint8_t *W, const uint8_t *xq, int32_t *out,
                               int64_t M, int64_t K, cudaStream_t stream);

@@ -231,6 +231,15 @@ size_t bq_paged_attn_workspace_size(const bq_paged_cache *cache, int elem, int64
   return paged_attn_workspace_bytes(a, int(std::min(max_q_len, n_q)));
 }
 
+int64_t bq_paged_attn_many_rows(const bq_paged_cache *cache, int elem, int64_t n_seqs, int64_t n_q, int64_t max_q_len,
+                                int64_t max_kv_len, int64_t n_heads, int causal, int64_t window) {
+  Cache c;
+  PagedAttnArgs a;
+  if (check_attn(cache, elem, n_seqs, n_q, max_q_len, max_kv_len, 0, n_heads, causal, window, "bq_paged_attn_many_rows", c, a) != BQ_OK)
+    return 0;
+  return paged_attn_many_rows(a, int(std::min(max_q_len, n_q)));
+}
+
 int bq_paged_attn(const bq_paged_cache *cache, int elem, const void *q, int64_t q_token_stride, int64_t q_head_stride,
                   void *o, int64_t o_token_stride, int64_t o_head_stride, float *lse, const int32_t *q_start,
                   const int32_t *kv_len, const int32_t *page_table, int64_t max_pages, int64_t n_seqs, int64_t n_q,

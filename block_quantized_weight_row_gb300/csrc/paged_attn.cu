@@ -255,6 +255,8 @@ bool paged_attn_dim(int64_t D) { return D == 64 || D == 96 || D == 128 || D == 2
 
 size_t paged_attn_workspace_bytes(PagedAttnArgs a, int max_q) { return make_plan(a, max_q, kMaxSms).bytes; }
 
+int64_t paged_attn_many_rows(PagedAttnArgs a, int max_q) { return make_plan(a, max_q, kMaxSms).items > 0 ? a.tc_rows : 0; }
+
 cudaError_t launch_paged_attn(PagedAttnArgs a, int max_q, void *ws, cudaStream_t stream) {
   cudaError_t err;
   const DeviceInfo *di = device_info(&err);

@@ -384,6 +384,12 @@ int bq_paged_attn(const bq_paged_cache *cache, int elem, const void *q, int64_t 
                   int64_t max_q_len, int64_t max_kv_len, int64_t n_heads, float scale, int causal, int64_t window);
 size_t bq_paged_attn_workspace_size(const bq_paged_cache *cache, int elem, int64_t n_seqs, int64_t n_q, int64_t max_q_len,
                                     int64_t max_kv_len, int64_t n_heads, int causal, int64_t window);
+/* Which sequences of a call with these arguments run on the tensor-memory
+ * kernel, by the code that the call runs (host only, nothing is launched): those
+ * with more query rows per kv head than this; 0 if none do (or for arguments
+ * that the call refuses). */
+int64_t bq_paged_attn_many_rows(const bq_paged_cache *cache, int elem, int64_t n_seqs, int64_t n_q, int64_t max_q_len,
+                                int64_t max_kv_len, int64_t n_heads, int causal, int64_t window);
 
 /* Page and place of a slot, by the code the kernels run (host only, nothing
  * is launched): BQ_OK and (-1, -1) for the skipped slot -1, BQ_ERR_INDEX for a

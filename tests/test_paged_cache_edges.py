@@ -7,7 +7,15 @@ import numpy as np
 import pytest
 import torch
 
+from block_quantized_weight_row_gb300.binding import _CacheStruct
 from test_paged_cache import BF16, F16, F32, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
+
+
+def many_rows(bq, cache, elem, n_seqs, n_q, max_q, max_kv, heads, causal=True, window=0):  # noqa: F811
+    """bq_paged_attn_many_rows of a call's arguments."""
+    c = _CacheStruct(cache.k_pages.data_ptr(), cache.v_pages.data_ptr(), cache.k_pages.shape[0], cache.page_size,
+                     cache.k_pages.shape[1], cache.head_dim, cache.k_type, cache.v_type, cache.k_basis)
+    return bq.lib().bq_paged_attn_many_rows(c, elem, n_seqs, n_q, max_q, max_kv, heads, causal, window)
 
 
 @gpu
@@ -160,3 +168,64 @@ def test_device_status_reports_every_kind_of_error(bq):  # noqa: F811
     finally:
         L.bq_set_spin_limit(-1)
     assert [bq.binding.device_status() for _ in range(3)] == [-6, -9, 0]
+
+
+@gpu
+def test_serving_example_runs_both_attention_kernels(bq, monkeypatch):  # noqa: F811
+    """Its tolerance and smoke() count on it: some step has a sequence on the many-row kernel beside single tokens."""
+    from examples import paged_serving
+    attn, steps = paged_serving.bq.paged_attn, []
+
+    def noted(cache, q, q_start, kv_len, page_table, scale, *, max_q_len, max_kv_len):
+        many = many_rows(bq, cache, 2, kv_len.numel(), q.shape[0], max_q_len, max_kv_len, q.shape[1])
+        rows = q_start.diff().cpu() * (q.shape[1] // cache.k_pages.shape[1])
+        steps.append([many > 0 and int(r) > many for r in rows])
+        return attn(cache, q, q_start, kv_len, page_table, scale, max_q_len=max_q_len, max_kv_len=max_kv_len)
+
+    monkeypatch.setattr(paged_serving.bq, "paged_attn", noted)
+    paged_serving.main(report=lambda line: None)
+    assert [False, True] in steps and [False, False] in steps
+
+
+@gpu
+@pytest.mark.parametrize("elem,D,q_len,kv_len,H,NKV,bound,window", [
+    (BF16, 128, [33, 8, 1], [200, 900, 777], 8, 8, 4096 * 8, 0),      # 33 rows, one above the limit of bf16
+    (BF16, 128, [32, 8, 1], [200, 900, 777], 8, 8, 4096 * 8, 0),      # 32 rows
+    (F16, 64, [65, 1], [300, 40], 4, 4, 1 << 15, 0),
+    (F16, 64, [64, 1], [300, 40], 4, 4, 1 << 15, 0),
+    (BF16, 128, [100], [100], 8, 2, 100, 0),                           # too little work
+    (BF16, 128, [300, 260], [900, 300], 32, 8, 900, 130),
+    (BF16, 64, [300, 260], [900, 300], 32, 8, 900, 130),
+    (F16, 96, [300, 260], [900, 300], 32, 8, 900, 0),                  # no such kernel for 96 and 256 channels, or fp32
+    (BF16, 256, [300, 260], [900, 300], 32, 8, 900, 0),
+    (F32, 128, [300, 260], [900, 300], 32, 8, 900, 0),
+])
+def test_calls_take_the_kernel_they_are_said_to(bq, elem, D, q_len, kv_len, H, NKV, bound, window):  # noqa: F811
+    """The rule of include/bq.h, what the query says, and what runs: with no polls left the many-row kernel alone reports a wait that ran out."""
+    b = Batch(bq, q_len, kv_len, H, NKV, D, 16, Q4, Q4, elem, wide=False)
+    b.bound = bound
+    limit, seen = 32 if elem == BF16 else 64, min(bound, window + max(q_len)) if window else bound
+    work = -(-max(q_len) * (H // NKV) // 16) * len(q_len) * NKV * (seen + 512)
+    many = elem != F32 and D in (64, 128) and max(q_len) * (H // NKV) > limit and work >= 250000
+    assert many_rows(bq, b.cache, elem, len(q_len), sum(q_len), max(q_len), bound, H, True, window) == (limit if many else 0)
+    L = bq.lib()
+    try:
+        assert L.bq_set_spin_limit(0) == 0
+        b.run(window=window)
+        assert bq.binding.device_status() == (-6 if many else 0)
+    finally:
+        L.bq_set_spin_limit(-1)
+    b.check(window=window)
+
+
+def test_the_route_of_a_call_on_the_host(bq):  # noqa: F811
+    """The query beside the refusals of the call itself: no kernel for those."""
+    ask = bq.lib().bq_paged_attn_many_rows
+    c = _CacheStruct(1 << 40, 2 << 40, 100, 16, 8, 128, Q4, Q4, 0)
+    assert ask(c, BF16, 1, 2048, 2048, 8192, 32, 1, 0) == 32 and ask(c, F16, 1, 2048, 2048, 8192, 32, 1, 0) == 64
+    assert ask(c, F32, 1, 2048, 2048, 8192, 32, 1, 0) == 0
+    assert ask(c, BF16, 64, 64, 1, 8192, 32, 1, 0) == 0  # 4 rows each
+    assert ask(c, BF16, 1, 2048, 9, 100, 32, 1, 0) == 0  # little work by the bounds
+    for bad in ((c, 5, 1, 2048, 2048, 8192, 32, 1, 0), (c, BF16, 1, 2048, 2048, 8192, 33, 1, 0), (c, BF16, 1, -1, 2048, 8192, 32, 1, 0),
+                (c, BF16, 1, 2048, 2048, 8192, 32, 0, 5), (None, BF16, 1, 2048, 2048, 8192, 32, 1, 0)):
+        assert ask(*bad) == 0
