@@ -1,5 +1,6 @@
 """Paged KV cache: calls at the edges of what is promised, each against the plain
 64-bit implementation of test_paged_cache.py or the documented status."""
+import copy
 import ctypes
 import math
 
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 from block_quantized_weight_row_gb300.binding import _CacheStruct
-from test_paged_cache import BF16, F16, F32, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
+from test_paged_cache import BF16, F16, F32, MANY, Q4, Q8, Batch, bq, gpu  # noqa: F401  (bq: a fixture)
 
 
 def many_rows(bq, cache, elem, n_seqs, n_q, max_q, max_kv, heads, causal=True, window=0):  # noqa: F811
@@ -229,3 +230,31 @@ def test_the_route_of_a_call_on_the_host(bq):  # noqa: F811
     for bad in ((c, 5, 1, 2048, 2048, 8192, 32, 1, 0), (c, BF16, 1, 2048, 2048, 8192, 33, 1, 0), (c, BF16, 1, -1, 2048, 8192, 32, 1, 0),
                 (c, BF16, 1, 2048, 2048, 8192, 32, 0, 5), (None, BF16, 1, 2048, 2048, 8192, 32, 1, 0)):
         assert ask(*bad) == 0
+
+
+def streaming_reference(b, causal, window):
+    """Batch.reference with the streaming kernel's tolerances for any number of rows: a sequence's rows a few at a time, each time over
+    the tokens up to the last of them, which leaves what every row sees as it is."""
+    c, most = copy.copy(b), max(1, (32 if b.elem == BF16 else 64) * b.NKV // b.H)
+    c.q_len, c.kv_len, c.slots = [], [], []
+    for n, kv, slots in zip(b.q_len, b.kv_len, b.slots):
+        for i in range(0, n, most):
+            m = min(most, n - i)
+            c.q_len.append(m)
+            c.kv_len.append(max(0, kv - n + i + m) if causal else kv)
+            c.slots.append(slots[:c.kv_len[-1]])
+    return c.reference(causal, window)
+
+
+@gpu
+@pytest.mark.parametrize("case", MANY, ids=str)
+def test_many_rows_with_little_work_keep_the_streaming_kernels_accuracy(bq, case):  # noqa: F811
+    """k^ and q exact, fp32 sums: calls below the many-row kernel's work are not held to that one's roundings only."""
+    *args, causal, window = case
+    b = Batch(bq, *args, wide=False)
+    if many_rows(bq, b.cache, b.elem, len(b.q_len), b.q.shape[0], max(b.q_len), b.bound, b.H, causal, window):
+        b.check(causal, window)  # enough work even so
+        return
+    o, lse = b.run(causal, window)
+    assert bq.binding.device_status() == 0
+    b.compare(o, lse, streaming_reference(b, causal, window))
