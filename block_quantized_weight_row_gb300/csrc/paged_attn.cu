@@ -171,7 +171,7 @@ StreamShape shape_of(int nb, int kt, int vt, int elem, int rows8) {
 
 // A piece has at least this many tiles (of 16 or 32 tokens): below that a
 // CTA's start and the combine cost more than the tokens (one sequence of 777
-// tokens, 16 query over 8 kv heads of 128: 11.3 us with 2, 12.3 with 4, 13.3
+// tokens, 16 query over 8 kv heads of 128: 12.3 us with 2, 11.9 with 4, 13.3
 // with 8).
 constexpr int kMinTiles = 2;
 
@@ -188,7 +188,10 @@ constexpr int kMinTiles = 2;
 //  4 x 256           15 / 16   16 / 15    17 / 16    21 / 16    32 / 19    49 / 20
 // 16 x 512           31 / 20   38 / 20    45 / 21    62 / 20   111 / 23   214 / 43
 // 16 x 4096 (48 rows 96 / 70) 122 / 71   149 / 71   227 / 71   440 / 85
-// (16 x 4096 at 32 rows: 69 / 70.) A binary16 call turns at 64 rows at the
+// (16 x 4096 at 32 rows: 69 / 70.) All with 128 channels; the rule serves 64 as
+// well. Work alone does not separate the entries: 4 x 256 at 128 rows and 1 x
+// 1024 at 256 rows have the same, 196608, and with four times the items the
+// first would be a quarter faster on the other kernel. A binary16 call turns at 64 rows at the
 // earliest, as the many-row kernel's binary16 operands show in its output
 // (4.5e-4 of its norm; streaming 2.9e-4, rounding alone 2.1e-4; a bf16
 // output's rounding hides them: 1.7e-3 in all).

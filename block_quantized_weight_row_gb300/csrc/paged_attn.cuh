@@ -46,9 +46,9 @@
 // is finished there; one that is cut leaves partial results for the combine
 // launch, which merges them in a fixed order.
 // Measured (8 kv heads of 128 channels, bf16): 64 ragged sequences of up to
-// 8192 tokens, 32 query heads, 4 bits, 99.7 us, 3.1 TB/s of cache; 4 sequences
-// of up to 131071 tokens, 16 query heads, 8-bit V, 101 us, 4.9 TB/s (0.72 of
-// the copy rate); one of 777 tokens in fp32 12.3 us. With the products and the softmax
+// 8192 tokens, 32 query heads, 4 bits, 100.5 us, 3.1 TB/s of cache (132 us in
+// fp32); 4 sequences of up to 131071 tokens, 16 query heads, 8-bit V, 101 us, 4.9
+// TB/s (0.73 of the copy rate); one of 777 tokens in fp32 12.3 us. With the products and the softmax
 // taken out (copies, segment starts and combine left) the first takes 63 us,
 // the second 81: what is above that is instruction issue (452 per 16 tokens
 // and warp, ALU pipe 48% busy), and the pieces' unequal ends (67 to 95 us).

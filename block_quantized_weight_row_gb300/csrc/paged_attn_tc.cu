@@ -6,8 +6,8 @@
 // Bound by the tensor pipe and the issue slots together: 4 D flops per (row,
 // token), one exponential and ~3 further operations beside them; converting
 // the cache's codes is shared by the 256 rows of a CTA. Measured, a chunk of
-// 2048 tokens at 8192, 32 query over 8 kv heads of 128, 4 bits: 268 us, 897
-// TFLOP/s (0.46 of the measured bf16 rate). A step takes 4300 cycles; its
+// 2048 tokens at 8192, 32 query over 8 kv heads of 128, 4 bits: 268 us, 898
+// TFLOP/s (0.47 of the measured bf16 rate). A step takes 4300 cycles; its
 // products alone, issued without a wait, 2520 (2048 where S is 128 tokens wide:
 // 64 tokens' operands are fetched at 49 cycles per product, not 33), its 11600
 // instructions 2900 issue slots of each scheduler. 11 us of an item are its
@@ -185,7 +185,7 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) <
 
 // Registers per thread: 96 at launch (20 warps); the shares add up to 20 * 96
 // or less: 8 * 136 + 8 * 72 + 4 * 56 = 1888 or 8 * 136 + 8 * 80 + 4 * 48 =
-// 1920 of 1920. Each is the split that leaves nothing in local memory (4 bytes
+// 1920 of 1920. Each is the split that leaves nothing in local memory (8 bytes
 // with 8-bit K and 4-bit V); 128 / 88 / 40 took 284 us where 136 / 72 / 56
 // takes 270.
 template <int VT>

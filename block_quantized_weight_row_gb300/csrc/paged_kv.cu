@@ -10,17 +10,21 @@
 // d * c in fp32, plus the bias, out of the basis (H64 / 8 is its own inverse),
 // rounded once to the output type.
 //
-// Both are bound by HBM: 2 or 4 bytes per value on one side and 0.56 or 1.06
-// on the other, against ~10 instructions per value to quantize. Write: 2 lanes
-// per block (below), the next block's loads in flight. Read: 4 lanes per row,
-// the next row's loads in flight. K and V are the two halves of one grid (a
-// decode step's write is one launch).
-// Measured, a layer of 32768 rows of 8 x 128 fp32 values, K in 4 and V in 8
-// bits: write 58 us (5.6 TB/s of its 323 MB, 0.82 of the copy rate), read 61 us
-// (5.3 TB/s; 4/5 of its bytes are writes, and a kernel that only writes reaches
-// 3.85 TB/s here). 65536 rows in 4 bits to bf16: 84 us, 4.1 TB/s. Before, with
-// a block per thread in a grid as large as the rows, the write took 95 us, and
-// the read 65 and 94.
+// The floor is HBM: 2 or 4 bytes per value on one side and 0.56 or 1.06 on the
+// other, against ~10 instructions per value to quantize. Write: 2 lanes per
+// block (below), the next block's loads in flight. Read: 4 lanes per row, the
+// next row's loads in flight. K and V are the two halves of one grid (a decode
+// step's write is one launch); each half alone is as many CTAs as fit at once,
+// so that V's start where K's leave.
+// Measured, a layer of 32768 rows of 8 x 128 fp32 values, K in 4 (mean-centred)
+// and V in 8 bits: write 58 us (5.6 TB/s of its 323 MB, 0.83 of the copy rate),
+// read 61 us (5.3 TB/s): HBM and the latency of loads, 47 and 36 % of the SMs'
+// warp slots in use. 65536 rows of 16-bit values in 4 bits, as many bytes but
+// twice the values: write from bf16 104 us plain, 117 rotated and centred, read
+// to bf16 67 and 84 us (4.1 TB/s). Instructions bind there: that read issues 2.9
+// times the fp32 one's, its issue slots are 60 % used and its DRAM 43 %. Before,
+// with a block per thread in a grid as large as the rows, the write took 95 us,
+// and the read 65 and 94.
 #include <algorithm>
 
 #include "bq_internal.h"
@@ -30,9 +34,12 @@ namespace bq {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kWriteCtas = 4;  // per SM, for K and as many for V: 64 registers; at 5 they spill (113 us per layer, not 58)
-constexpr int kReadCtas = 3;  // per SM, for K and as many for V: the layer and the 65536 rows above took 63 / 90 us at 2,
-                              // 62 / 86 at 3, 70 / 92 at 4, 78 / 120 at 5
+// CTAs per SM, for K and as many for V. Write: 4 fit with fp32 rows (64 registers), 5 with 16-bit ones (48); the layer and
+// the 65536 rotated rows above took 61 / 118 us at 2, 69 / 124 at 3, 60 / 117 at 4, 63 / 117 at 5, 61 / 116 at 8. Read: also
+// the launch bounds' minimum (80 registers at 3, fewer and spilled above); 60 / 99 us at 1, 63 / 90 at 2, 61 / 86 at 3, 69 / 92
+// at 4, 78 / 122 at 5.
+constexpr int kWriteCtas = 4;
+constexpr int kReadCtas = 3;
 
 // n / d for n < 2^29 by a multiplication: m = ceil(2^(32 + s) / d) with 2^s <=
 // d < 2^(s + 1) errs by less than d <= 2^(s + 1) in 2^(32 + s), so n m errs by
@@ -570,7 +577,7 @@ cudaError_t launch_paged_write(const PagedPool &kp, const PagedPool &vp, const P
     const uint32_t n_blocks = uint32_t(std::min(chunk, n_tokens - t) * sh.n_kv * sh.nb);
     const WriteSide k{static_cast<const uint8_t *>(K) + t * k_ts, k_ts, k_hs, bias, kp};
     const WriteSide v{static_cast<const uint8_t *>(V) + t * v_ts, v_ts, v_hs, nullptr, vp};
-    // as many CTAs as are resident, each with several blocks per thread
+    // a half as large as what is resident, with several blocks per thread
     const uint32_t ctas = (n_blocks + kThreads / 2 - 1) / (kThreads / 2);
     const dim3 grid(std::min<uint32_t>(ctas, uint32_t(di->sm_count) * kWriteCtas), 2);
     err = by_types(kt, vt, elem, [&](auto k_, auto v_, auto e_) {

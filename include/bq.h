@@ -317,6 +317,12 @@ size_t bq_paged_page_bytes(int type, int64_t page_size, int64_t n_kv_heads, int6
  * quantized; V rows are quantized. slots: n_tokens int64, DEVICE; -1 skips the
  * token; no slot may occur twice. A slot outside the pool is skipped and
  * reported by bq_device_status (BQ_ERR_INDEX). One launch.
+ * Values are taken to be finite and below 65504 times 7 (Q4_0) or 127 (Q8_0) in
+ * magnitude, as by every quantizer here; 16-bit rows are not checked for
+ * overflow. Others spoil their own blocks (of a rotated K their 64 channels): an
+ * infinity leaves an infinite scale, from which attention over the token is NaN;
+ * a NaN takes no part in the scale, and where nothing else is left, as in a
+ * rotated K, the channels are read back as zeros.
  * Errors: BQ_ERR_UNSUPPORTED (types, element type, basis, bias with a Q8_0 K),
  * BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_BASIS, BQ_ERR_INVALID_ARG (null pointers,
  * negative sizes, a pool overlapping an input). */
@@ -355,7 +361,9 @@ int bq_paged_kv_read(const bq_paged_cache *cache, int elem, void *K, void *V, co
  * longer one costs speed only); max_kv_len: an upper bound of kv_len.
  * A kv_len above max_kv_len or max_pages * page_size is cut there, a page
  * outside the pool counts as zero rows, and a q_start outside 0 .. n_q makes
- * its sequence empty; bq_device_status reports each (BQ_ERR_INDEX).
+ * its sequence empty; bq_device_status reports each (BQ_ERR_INDEX). Table
+ * entries of pages of which no query sees a token (past kv_len, wholly before a
+ * window) may hold anything.
  * Accuracy: fp32 statistics and sums; q and weights in binary16 terms (fp32
  * calls two each, 2^-22 together; 16-bit calls one: q exactly unless rotated,
  * 2^-11 of a weight). The terms end where binary16 does: beside a token of
