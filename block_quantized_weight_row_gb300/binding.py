@@ -9,6 +9,7 @@ libbq.so is missing or fails to load, every call raises.
 import ctypes
 import dataclasses
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -87,6 +88,14 @@ def lib():
         "bq_paged_attn_workspace_size": ([cp, i, i64, i64, i64, i64, i64, i, i64], sz),
         "bq_paged_attn_many_rows": ([cp, i, i64, i64, i64, i64, i64, i, i64], i64),
         "bq_paged_slot_check": ([cp, i64, ctypes.POINTER(i64), ctypes.POINTER(i64)], i),
+        "bq_paged_extend": ([i64, i64, vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp], i),
+        "bq_add_rms_norm": ([i, vp, i64, vp, i64, vp, ctypes.c_double, vp, i64, vp, i64, vp, i64, i64], i),
+        "bq_gemv_q8": ([i, vp, vp, vp, i64, i64], i),
+        "bq_gemm_q8": ([i, vp, vp, vp, i64, i64, i64], i),
+        "bq_rotary": ([i, vp, i64, i64, i64, vp, i64, i64, i64, i, vp, i64, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64,
+                       i64, i, i], i),
+        "bq_lora": ([i, vp, i64, i, vp, vp, vp, i64, i64, vp, i, vp, i64, vp, i64, i64, i64, i64], i),
+        "bq_lora_workspace_size": ([i64, i64, i64, i64, i64], sz),
         "bq_block_dots": ([i, vp, vp, vp, i64, i64], i),
         "bq_set_stream": ([vp], i),
         "bq_get_stream": ([], vp),
@@ -151,6 +160,12 @@ def _cuda(t, name):
     return t
 
 
+def _q8_rows(x, rows, K):
+    """Activations given as Q8_0 blocks: the bytes of whole rows."""
+    if x.dtype == torch.uint8 and x.numel() != rows * (K // QK) * 34:
+        raise ValueError(f"activations of {rows} x {K} values in Q8_0 are {rows * (K // QK) * 34} bytes, not {x.numel()}")
+
+
 def block_bytes(t: int) -> int:
     return int(lib().bq_block_bytes(t))
 
@@ -187,13 +202,18 @@ def dequantize_rows(t: int, blocks: torch.Tensor, cols: int, out: torch.Tensor |
 
 def gemv(t: int, w_blocks: torch.Tensor, x: torch.Tensor, M: int, K: int,
          out: torch.Tensor | None = None) -> torch.Tensor:
-    """y[M] = W (M x K, blocks of type t) . x[K] (fp32, quantized to Q8_0 in-kernel)."""
+    """y[M] = W (M x K, blocks of type t) . x[K] (fp32, quantized to Q8_0 in-kernel;
+    or uint8: its Q8_0 blocks, as add_rms_norm and quantize_rows give them)."""
     _cuda(w_blocks, "w_blocks")
     _cuda(x, "x")
+    _q8_rows(x, 1, K)
     if out is None:
         out = torch.empty(M, dtype=torch.float32, device=x.device)
     L = _prep(x.device)
     _workspace(x.device, int(L.bq_gemv_workspace_size(t, K)))
+    if x.dtype == torch.uint8:
+        _check(L.bq_gemv_q8(t, _ptr(w_blocks), _ptr(x), _ptr(out), M, K), "bq_gemv_q8")
+        return out
     _check(L.bq_gemv(t, _ptr(w_blocks), _ptr(x), _ptr(out), M, K), "bq_gemv")
     return out
 
@@ -282,13 +302,18 @@ def attn_decode(k_type: int, v_type: int, q: torch.Tensor, K_cache: torch.Tensor
 
 def gemm(t: int, w_blocks: torch.Tensor, X: torch.Tensor, M: int, N: int, K: int,
          out: torch.Tensor | None = None) -> torch.Tensor:
-    """Y (N x M) = X (N x K fp32, quantized to Q8_0) . W^T (W: M x K blocks)."""
+    """Y (N x M) = X (N x K fp32, quantized to Q8_0; or uint8: its Q8_0 blocks) . W^T
+    (W: M x K blocks)."""
     _cuda(w_blocks, "w_blocks")
     _cuda(X, "X")
+    _q8_rows(X, N, K)
     if out is None:
         out = torch.empty((N, M), dtype=torch.float32, device=X.device)
     L = _prep(X.device)
     _workspace(X.device, int(L.bq_workspace_size(t, M, N, K)))
+    if X.dtype == torch.uint8:
+        _check(L.bq_gemm_q8(t, _ptr(w_blocks), _ptr(X), _ptr(out), M, N, K), "bq_gemm_q8")
+        return out
     _check(L.bq_gemm(t, _ptr(w_blocks), _ptr(X), _ptr(out), M, N, K), "bq_gemm")
     return out
 
@@ -431,6 +456,90 @@ def paged_attn(cache: PagedCache, q: torch.Tensor, q_start: torch.Tensor, kv_len
                                 max_kv_len, causal, window, out, lse)
     if type(r) is tuple:
         raise BQError(r[0], f"bq_paged_attn: {r[1]}")
+    return r
+
+
+# ---- around the projections and the paged cache of a served layer ----
+
+
+def _raise(r, what):
+    raise BQError(r[0], f"{what}: {r[1]}")
+
+
+class PagedStep(NamedTuple):
+    """What paged_extend makes of a batch's lengths (all on the device)."""
+    q_start: torch.Tensor    # int32 (sequences + 1): rows of each sequence in the batch
+    kv_len: torch.Tensor     # int32 (sequences): tokens cached once the step's rows are written
+    slots: torch.Tensor      # int64 (n_slots): where each row goes, -1 behind the last
+    positions: torch.Tensor  # int32 (n_slots): each row's place in its sequence, 0 behind the last
+    taken: torch.Tensor      # int32 (2): pages taken off the front of free_pages; pages needed
+
+
+def paged_extend(page_size: int, n_pages: int, kv_len: torch.Tensor, n_new: torch.Tensor, page_table: torch.Tensor,
+                 free_pages: torch.Tensor, n_slots: int) -> PagedStep:
+    """The next tokens of a batch of sequences in paged caches of n_pages pages
+    (bq_paged_extend): kv_len and n_new (sequences) int32, the cached and the coming
+    tokens; page_table (sequences, max_pages) int32, to which new pages are added in
+    place, from the front of free_pages (int32); n_slots: room for the batch's
+    tokens. A sequence that cannot grow gets slots of -1 and keeps its kv_len, which
+    device_status reports; taken[1] > taken[0] tells so too where pages ran out."""
+    r = (_ext or _paged()).paged_extend(page_size, n_pages, kv_len, n_new, page_table, free_pages, n_slots)
+    if type(r[0]) is int:
+        _raise(r, "bq_paged_extend")
+    return PagedStep(*r)
+
+
+class NormRows(NamedTuple):
+    """Outputs of add_rms_norm; None where not wanted."""
+    out: torch.Tensor | None  # the norm's rows, in x's type
+    sum: torch.Tensor | None  # x + residual, in x's type
+    q8: torch.Tensor | None   # the norm's rows in Q8_0: uint8 (rows, cols / 32 * 34)
+
+
+def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: torch.Tensor | None = None, *,
+                 out: bool | torch.Tensor = True, q8: bool | torch.Tensor = False,
+                 sum: torch.Tensor | None = None) -> NormRows:
+    """Root-mean-square norm of the rows x + residual (bq_add_rms_norm): x and
+    residual (rows, cols) fp32, fp16 or bf16, any row stride; weight (cols) fp32. out
+    and q8: which of the two outputs to make, or a tensor for it; sum: a tensor for
+    x + residual (x or residual themselves: in place), else a new one is made."""
+    r = (_ext or _paged()).add_rms_norm(x, weight, eps, residual, out, q8, sum)
+    if type(r[0]) is int:
+        _raise(r, "bq_add_rms_norm")
+    return NormRows(*r)
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor,
+           axis: torch.Tensor | None = None, *, interleaved: bool = False, inverse: bool = False,
+           dtype: torch.dtype | None = None, out_q: torch.Tensor | None = None,
+           out_k: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """Rotary positions (bq_rotary): q and k (tokens, heads, head_dim), any token and
+    head strides, turned in their first 2 * len(inv_freq) channels by positions (int32,
+    (axes, tokens) or (tokens)) of the axis of each pair (axis: int32, None: the first)
+    times inv_freq (fp64). interleaved: pairs of adjacent channels, else of the two
+    halves. inverse: the opposite turn. dtype: of the outputs (from fp32 any; else q's).
+    out_q, out_k may be q and k themselves."""
+    code = -1 if dtype is None else ELEM.get(dtype, 3)
+    if dtype is None and out_q is not None:
+        code = ELEM.get(out_q.dtype, 3)
+    r = (_ext or _paged()).rotary(q, k, positions, inv_freq, axis, interleaved, inverse, code, out_q, out_k)
+    if type(r[0]) is int:
+        _raise(r, "bq_rotary")
+    return r
+
+
+def lora(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, adapter: torch.Tensor, y: torch.Tensor | None = None,
+         scale: torch.Tensor | None = None, *, out: torch.Tensor | None = None,
+         dtype: torch.dtype | None = None) -> torch.Tensor:
+    """y + scale[adapter] * (x a[adapter]^T) b[adapter]^T per row (bq_lora): x (tokens,
+    K) and y (tokens, M) fp32 or in the adapters' type; a (adapters, rank, K) and b
+    (adapters, M, rank) fp16 or bf16; adapter (tokens) int32, -1 for none; scale
+    (adapters) fp32, None for 1. out may be y itself. Without y, nothing is added to,
+    and dtype is out's (default: x's)."""
+    code = -1 if dtype is None else ELEM.get(dtype, 3)
+    r = (_ext or _paged()).lora(x, a, b, adapter, y, scale, out, code)
+    if type(r) is tuple:
+        _raise(r, "bq_lora")
     return r
 
 

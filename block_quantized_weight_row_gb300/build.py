@@ -20,14 +20,15 @@ LIB = os.path.join(HERE, "libbq.so")
 # measurement probe (tensor-op rates for the roofline denominators); not part of the libbq ABI
 PROBE_SRC = "probe_mma.cu"
 PROBE_LIB = os.path.join(HERE, "libbq_probe.so")
-# the paged calls' host side (CPython + torch headers, no device code)
+# the host side of the paged calls and those around them (CPython + torch headers, no device code)
 EXT_SRC = "paged_binding.cpp"
 EXT_LIB = os.path.join(HERE, "_paged.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["bq_api.cu", "quantize.cu", "gemv.cu", "gemv_seq.cu", "gemm.cu", "gemm_tc.cu", "gemm_noalloc.cu", "attn.cu",
            "attn_fixed_q4k.cu", "attn_fixed_q8k.cu", "paged_api.cu", "paged_kv.cu", "paged_attn.cu", "paged_attn_tc.cu",
-           "paged_attn_d64.cu", "paged_attn_d96.cu", "paged_attn_d128.cu", "paged_attn_d256.cu"]
+           "paged_attn_d64.cu", "paged_attn_d96.cu", "paged_attn_d128.cu", "paged_attn_d256.cu", "layer_api.cu",
+           "paged_extend.cu", "norm.cu", "rotary.cu", "lora.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]
@@ -65,8 +66,13 @@ def ext_versions() -> str:
     return f"torch {torch.__version__} {torch.version.git_version} {os.path.dirname(torch.__file__)}, python {sys.version}"
 
 
+def _is_binding(f):
+    """Whether a header is of the extension's host side alone."""
+    return f in ("binding_common.h", "layer_binding.h")
+
+
 def _deps():
-    hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    hdrs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h")) and not _is_binding(f)]
     return hdrs + [os.path.join(INCLUDE, "bq.h"), __file__]
 
 
@@ -110,7 +116,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         """
         obj, compile_, link = ext_commands(EXT_LIB + f".tmp{os.getpid()}")
         made_with, note = ext_versions(), obj + ".with"
-        new = force or _stale(obj, [os.path.join(CSRC, EXT_SRC), __file__, os.path.join(INCLUDE, "bq.h")])
+        parts = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if _is_binding(f)]
+        new = force or _stale(obj, [os.path.join(CSRC, EXT_SRC), __file__, os.path.join(INCLUDE, "bq.h"), *parts])
         if not new:
             new = not os.path.exists(note) or open(note, encoding="utf-8").read() != made_with
         if new:

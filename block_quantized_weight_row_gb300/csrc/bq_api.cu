@@ -241,7 +241,7 @@ int bq_device_status(void) {
     if (e != cudaSuccess) return cuda_fail(e, "bq_device_status: clear error word");
     if (word & kErrTimeout) return fail(BQ_ERR_TIMEOUT, "a bounded in-kernel wait ran out (error word 0x%x)", word);
     if (word & kErrIndex)
-      return fail(BQ_ERR_INDEX, "a slot, page or length of a paged cache was out of range (error word 0x%x)", word);
+      return fail(BQ_ERR_INDEX, "a slot, page or length of a paged cache, an adapter or an axis was out of range (error word 0x%x)", word);
   }
   return ok();
 }
@@ -507,6 +507,67 @@ int bq_gemm(int type, const void *W, const float *X, float *Y, int64_t M, int64_
     return fail(BQ_ERR_INVALID_ARG, "bq_gemm: workspace overlaps an argument");
   cudaError_t e = launch_prefill(path, static_cast<const uint8_t *>(W), X, Y, M, N, K, t_ws, t_stream);
   return e == cudaSuccess ? ok() : cuda_fail(e, "bq_gemm launch");
+}
+
+int bq_gemv_q8(int type, const void *W, const void *xq, float *y, int64_t M, int64_t K) {
+  const int bb = block_bytes(type);
+  if (!bb) return fail(BQ_ERR_UNSUPPORTED, "bq_gemv_q8: unknown type %d", type);
+  if (K < 0 || M < 0) return fail(BQ_ERR_INVALID_ARG, "bq_gemv_q8: a size is negative");
+  const int bv = block_values(type);
+  if (K % bv) return fail(BQ_ERR_SHAPE, "bq_gemv_q8: K %lld is not a multiple of %d", (long long)K, bv);
+  if (K > BQ_GEMV_MAX_K) return fail(BQ_ERR_SHAPE, "bq_gemv_q8: K %lld exceeds %d", (long long)K, BQ_GEMV_MAX_K);
+  if (M > 0x7fffffffll) return fail(BQ_ERR_SHAPE, "bq_gemv_q8: rows exceed 2^31-1");
+  if (M == 0) return ok();
+  if (!y || (K > 0 && (!W || !xq))) return fail(BQ_ERR_INVALID_ARG, "bq_gemv_q8: null pointer");
+  if (!aligned(y, 4) || (K > 0 && (!aligned(W, 16) || !aligned(xq, 16))))
+    return fail(BQ_ERR_ALIGN, "bq_gemv_q8: W and x_blocks must be 16-byte aligned, y 4-byte aligned");
+  const size_t ybytes = size_t(M) * 4, xbytes = size_t(K / kQK) * Fmt<kTypeQ8_0>::kBytes, wbytes = size_t(M) * size_t(K / bv) * bb;
+  if (overlap(y, ybytes, xq, xbytes) || overlap(y, ybytes, W, wbytes)) return fail(BQ_ERR_INVALID_ARG, "bq_gemv_q8: y overlaps an input");
+  if (K == 0) {
+    cudaError_t e = cudaMemsetAsync(y, 0, ybytes, t_stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "bq_gemv_q8 memset");
+  }
+  const size_t need = gemv_workspace_bytes(K);
+  if (!t_ws || t_ws_bytes < need)
+    return fail(BQ_ERR_WORKSPACE, "bq_gemv_q8: needs %zu workspace bytes, %zu set", need, t_ws_bytes);
+  if (overlap(t_ws, need, xq, xbytes) || overlap(t_ws, need, y, ybytes) || overlap(t_ws, need, W, wbytes))
+    return fail(BQ_ERR_INVALID_ARG, "bq_gemv_q8: workspace overlaps an argument");
+  const uint8_t *w = static_cast<const uint8_t *>(W);
+  cudaError_t e = launch_gemv(type, 1, &w, &y, &M, nullptr, K, static_cast<uint32_t *>(t_ws), t_stream, static_cast<const uint8_t *>(xq));
+  return e == cudaSuccess ? ok() : cuda_fail(e, "bq_gemv_q8 launch");
+}
+
+int bq_gemm_q8(int type, const void *W, const void *Xq, float *Y, int64_t M, int64_t N, int64_t K) {
+  const int bb = block_bytes(type);
+  if (!bb) return fail(BQ_ERR_UNSUPPORTED, "bq_gemm_q8: unknown type %d", type);
+  if (type != BQ_TYPE_Q8_0) return fail(BQ_ERR_UNSUPPORTED, "bq_gemm_q8: only Q8_0 weights are supported");
+  if (!sizes_ok(M, K) || !sizes_ok(N, K) || !sizes_ok(M, N)) return fail(BQ_ERR_INVALID_ARG, "bq_gemm_q8: bad sizes");
+  if (K % kQK) return fail(BQ_ERR_SHAPE, "bq_gemm_q8: K %lld is not a multiple of 32", (long long)K);
+  if (M > 0x7fffffffll || N > 0x7fffffffll) return fail(BQ_ERR_SHAPE, "bq_gemm_q8: M and N must be below 2^31");
+  if (M == 0 || N == 0) return ok();
+  if (!Y || (K > 0 && (!W || !Xq))) return fail(BQ_ERR_INVALID_ARG, "bq_gemm_q8: null pointer");
+  if (!aligned(Y, 4) || (K > 0 && (!aligned(W, 16) || !aligned(Xq, 16))))
+    return fail(BQ_ERR_ALIGN, "bq_gemm_q8: W and X_blocks must be 16-byte aligned, Y 4-byte aligned");
+  const size_t ybytes = size_t(M) * size_t(N) * 4, wbytes = size_t(M) * size_t(K / kQK) * bb;
+  const size_t xbytes = size_t(N) * size_t(K / kQK) * Fmt<kTypeQ8_0>::kBytes;
+  if (overlap(Y, ybytes, W, wbytes) || overlap(Y, ybytes, Xq, xbytes)) return fail(BQ_ERR_INVALID_ARG, "bq_gemm_q8: Y overlaps an input");
+  if (K == 0) {
+    cudaError_t e = cudaMemsetAsync(Y, 0, ybytes, t_stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "bq_gemm_q8 memset");
+  }
+  size_t need = 0;
+  const PrefillPath path = prefill_path(M, N, K, SIZE_MAX, &need);
+  const uint8_t *w = static_cast<const uint8_t *>(W), *x = static_cast<const uint8_t *>(Xq);
+  if (path == PrefillPath::kMmaSync) {  // takes the blocks as they are
+    cudaError_t e = launch_gemm(type, w, x, Y, M, N, K, t_stream);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "bq_gemm_q8 launch");
+  }
+  if (!t_ws || t_ws_bytes < need)
+    return fail(BQ_ERR_WORKSPACE, "bq_gemm_q8: needs %zu workspace bytes, %zu set", need, t_ws_bytes);
+  if (overlap(t_ws, need, Y, ybytes) || overlap(t_ws, need, Xq, xbytes) || overlap(t_ws, need, W, wbytes))
+    return fail(BQ_ERR_INVALID_ARG, "bq_gemm_q8: workspace overlaps an argument");
+  cudaError_t e = launch_gemm_tc(w, nullptr, Y, M, N, K, t_ws, t_stream, x);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "bq_gemm_q8 launch");
 }
 
 int bq_kv_quantize(int type, const float *rows, const float *bias, void *dst, int64_t n_tokens,

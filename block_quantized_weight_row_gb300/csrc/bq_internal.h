@@ -73,9 +73,11 @@ cudaError_t launch_dequantize_rows(int type, const uint8_t *blocks, float *dst, 
 // n matrices (n <= BQ_GEMV_MAX_MATS) sharing one input x; matrix i has M[i] rows.
 // rec_ws: optional workspace of gemv_workspace_bytes(K) for x's quantized
 // records (then a prep kernel quantizes x once and prefetches the weights
-// into L2); null: every GEMV CTA quantizes x itself.
+// into L2); null: every GEMV CTA quantizes x itself. xq: x's Q8_0 blocks instead
+// of x (with a workspace only; the prep kernel takes the codes from them).
 cudaError_t launch_gemv(int type, int n, const uint8_t *const *W, float *const *y, const int64_t *M,
-                        const float *x, int64_t K, uint32_t *rec_ws, cudaStream_t stream);
+                        const float *x, int64_t K, uint32_t *rec_ws, cudaStream_t stream,
+                        const uint8_t *xq = nullptr);
 size_t gemv_workspace_bytes(int64_t K);
 // A sequence of GEMV batches in one launch per at most 256 batches: batch g
 // (n_mats[g] matrices from the flattened W / y / M arrays, input x[g], K[g] a
@@ -102,11 +104,12 @@ cudaError_t launch_attn_decode(int kt, int vt, const float *q, const uint8_t *K,
 cudaError_t launch_gemm(int type, const uint8_t *W, const uint8_t *Xq, float *Y, int64_t M,
                         int64_t N, int64_t K, cudaStream_t stream);
 // Prefill GEMM on the tcgen05 tensor cores (K a multiple of 256): quantizes X
-// into `ws` (gemm_tc_workspace_bytes(N, K) bytes) and runs the GEMM.
+// into `ws` (gemm_tc_workspace_bytes(N, K) bytes) and runs the GEMM. Xq: its
+// Q8_0 blocks instead of X.
 bool gemm_tc_supported(int64_t M, int64_t N, int64_t K);
 size_t gemm_tc_workspace_bytes(int64_t N, int64_t K);
 cudaError_t launch_gemm_tc(const uint8_t *W, const float *X, float *Y, int64_t M, int64_t N, int64_t K, void *ws,
-                           cudaStream_t stream);
+                           cudaStream_t stream, const uint8_t *Xq = nullptr);
 // The prefill path bq_gemm and bq_gemm_noalloc take for these sizes, given
 // `ws_limit` bytes of scratch (SIZE_MAX: any): the tcgen05 kernel where it
 // applies and its workspace fits, else the mma.sync kernel over Q8_0

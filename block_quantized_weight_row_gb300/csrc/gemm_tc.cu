@@ -400,6 +400,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
+// Four codes of token n, block b (words j of its 8) and the block's scale, where
+// the kernel above reads them.
+__device__ __forceinline__ void store_x_operand(int64_t n, int b, int j, int nb, uint16_t scale, uint32_t word, uint8_t *xp, float *dxs) {
+  const int64_t t = n >> 7;
+  const int r = int(n & 127);
+  uint8_t *tile = xp + (t * (nb / 2) + (b >> 1)) * int64_t(kOpBytes);
+  const int chunk = (b & 1) * 4 + (j >> 1);
+  *reinterpret_cast<uint2 *>(tile + sw128_off(r, chunk) + (j & 1) * 8) = codes_to_f16x2(word);
+  if (j == 0) dxs[(t * nb + b) * 128 + r] = half_bits_to_float(scale);
+}
+
 // Activations for the kernel above: X (N x K fp32) quantized to Q8_0 codes
 // (the same rule as the row quantizer), written as binary16 codes in the
 // operand layout — per 128-token tile t and 2-block group a, one 16 KB
@@ -423,12 +434,27 @@ __global__ void __launch_bounds__(256)
     uint32_t word;
     int sum;
     quantize_block_8lanes(v, scale, word, sum);
-    const int64_t t = n >> 7;
-    const int r = int(n & 127);
-    uint8_t *tile = xp + (t * (nb / 2) + (b >> 1)) * int64_t(kOpBytes);
-    const int chunk = (b & 1) * 4 + (j >> 1);
-    *reinterpret_cast<uint2 *>(tile + sw128_off(r, chunk) + (j & 1) * 8) = codes_to_f16x2(word);
-    if (j == 0) dxs[(t * nb + b) * 128 + r] = half_bits_to_float(scale);
+    store_x_operand(n, b, j, nb, scale, word, xp, dxs);
+  }
+}
+
+// The same operand from rows that are in Q8_0 blocks already.
+__global__ void __launch_bounds__(256)
+    k_pack_x_tc(const uint8_t *__restrict__ Xq, int N, int nb, int n_pad, uint8_t *__restrict__ xp, float *__restrict__ dxs) {
+  const int j = threadIdx.x & 7;
+  const int64_t total = int64_t(n_pad) * nb;
+  const int64_t step = int64_t(gridDim.x) * (blockDim.x >> 3);
+  for (int64_t item = int64_t(blockIdx.x) * (blockDim.x >> 3) + (threadIdx.x >> 3); item < total; item += step) {
+    const int64_t n = item / nb;
+    const int b = int(item % nb);
+    uint16_t scale = 0;
+    uint32_t word = 0;
+    if (n < N) {
+      const uint16_t *block = reinterpret_cast<const uint16_t *>(Xq + (n * nb + b) * Fmt<kTypeQ8_0>::kBytes);
+      scale = block[0];
+      word = uint32_t(block[1 + 2 * j]) | uint32_t(block[2 + 2 * j]) << 16;
+    }
+    store_x_operand(n, b, j, nb, scale, word, xp, dxs);
   }
 }
 
@@ -459,7 +485,7 @@ size_t gemm_tc_workspace_bytes(int64_t N, int64_t K) {
 }
 
 cudaError_t launch_gemm_tc(const uint8_t *W, const float *X, float *Y, int64_t M, int64_t N, int64_t K, void *ws,
-                           cudaStream_t stream) {
+                           cudaStream_t stream, const uint8_t *Xq) {
   if (M == 0 || N == 0) return cudaSuccess;
   cudaError_t err;
   const DeviceInfo *di = device_info(&err);
@@ -471,7 +497,10 @@ cudaError_t launch_gemm_tc(const uint8_t *W, const float *X, float *Y, int64_t M
   {
     const int64_t items = n_tiles * kTN * nb;
     const int64_t grid = std::min<int64_t>((items + 31) / 32, int64_t(di->sm_count) * 16);
-    k_quantize_x_tc<<<unsigned(grid), 256, 0, stream>>>(X, int(N), nb, int(n_tiles * kTN), xp, dxs);
+    if (Xq)
+      k_pack_x_tc<<<unsigned(grid), 256, 0, stream>>>(Xq, int(N), nb, int(n_tiles * kTN), xp, dxs);
+    else
+      k_quantize_x_tc<<<unsigned(grid), 256, 0, stream>>>(X, int(N), nb, int(n_tiles * kTN), xp, dxs);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

@@ -242,10 +242,24 @@ struct PrepArgs {
   int64_t chunk_start[kMaxMats + 1];  // first L2-prefetch chunk of matrix i
   int n_mats;
   const float *x;
+  const uint8_t *xq;  // x's Q8_0 blocks instead of x, or null
   int nb;         // K / 32
   uint32_t *rec;  // groups * kXRecWords words
   int quant_ctas;
 };
+
+// Word j (4 codes) of x's Q8_0 block b, its scale as fp32 bits and, over the 8
+// lanes of the block, its code sum: what the quantizers make of fp32 x.
+__device__ __forceinline__ void read_q8_block(const uint8_t *xq, int b, int j, uint32_t &word, uint32_t &scale, uint32_t &sum) {
+  const unsigned short *block = reinterpret_cast<const unsigned short *>(xq + int64_t(b) * Fmt<kTypeQ8_0>::kBytes);
+  word = uint32_t(__ldcg(block + 1 + 2 * j)) | uint32_t(__ldcg(block + 2 + 2 * j)) << 16;
+  scale = __float_as_uint(half_bits_to_float(__ldcg(block)));
+  int s = dp4a_ss(word, 0x01010101u, 0);
+  s += __shfl_xor_sync(kFull, s, 1);
+  s += __shfl_xor_sync(kFull, s, 2);
+  s += __shfl_xor_sync(kFull, s, 4);
+  sum = uint32_t(s);
+}
 
 __global__ void __launch_bounds__(kPrepThreads) k_gemv_prep(const PrepArgs p) {
   if (threadIdx.x == 0) {
@@ -253,8 +267,11 @@ __global__ void __launch_bounds__(kPrepThreads) k_gemv_prep(const PrepArgs p) {
     // then an L2 hit. A prefetch reads nothing into the SM, and L2 is where
     // the previous kernel's stores to x land, so it cannot expose stale data.
     if (int(blockIdx.x) < p.quant_ctas) {
-      const int b0 = int(blockIdx.x) * kPrepBlocksPerCta;
-      prefetch_l2(p.x + int64_t(b0) * kQK, uint32_t(min(kPrepBlocksPerCta, p.nb - b0)) * kQK * 4u);
+      const int b0 = int(blockIdx.x) * kPrepBlocksPerCta, nb = min(kPrepBlocksPerCta, p.nb - b0);  // multiples of 8
+      if (p.xq)
+        prefetch_l2(p.xq + int64_t(b0) * Fmt<kTypeQ8_0>::kBytes, uint32_t(nb) * Fmt<kTypeQ8_0>::kBytes);
+      else
+        prefetch_l2(p.x + int64_t(b0) * kQK, uint32_t(nb) * kQK * 4u);
     }
     for (int64_t c = blockIdx.x; c < p.chunk_start[p.n_mats]; c += gridDim.x) {
       int m = 0;
@@ -268,6 +285,20 @@ __global__ void __launch_bounds__(kPrepThreads) k_gemv_prep(const PrepArgs p) {
   // records of its own x: touch neither before it has completed
   pdl_wait();
   if (int(blockIdx.x) >= p.quant_ctas) return;  // whole CTA: the shuffles below stay converged
+  if (p.xq) {
+    const int b = int(blockIdx.x) * kPrepBlocksPerCta + int(threadIdx.x >> 3), j = int(threadIdx.x & 7);
+    uint32_t word, scale, sum;
+    read_q8_block(p.xq, min(b, p.nb - 1), j, word, scale, sum);
+    if (b < p.nb) {
+      uint32_t *r = p.rec + (b >> 3) * kXRecWords;
+      r[8 * (b & 7) + j] = word;
+      if (j == 0) {
+        r[64 + (b & 7)] = scale;
+        r[72 + (b & 7)] = sum;
+      }
+    }
+    return;
+  }
   quantize_x_records(p.x + int64_t(blockIdx.x) * kPrepBlocksPerCta * kQK,
                      min(kPrepBlocksPerCta, p.nb - int(blockIdx.x) * kPrepBlocksPerCta),
                      p.rec + blockIdx.x * (kPrepBlocksPerCta / 8) * kXRecWords, threadIdx.x, kPrepThreads, 0);
@@ -293,13 +324,25 @@ __device__ __forceinline__ void quantize_x_generic(const float *__restrict__ x, 
 // x's records for k_gemv_generic / k_gemv_staged, 8 lanes per block (the
 // same codes, scales and sums as quantize_x_generic: one block rule), 32
 // blocks per CTA.
-__global__ void __launch_bounds__(256) k_gemv_generic_prep(const float *__restrict__ x, uint32_t *__restrict__ xg,
-                                                           int nb) {
+__global__ void __launch_bounds__(256) k_gemv_generic_prep(const float *__restrict__ x, const uint8_t *__restrict__ xq,
+                                                           uint32_t *__restrict__ xg, int nb) {
   // k_gemv_staged, launched as a programmatic dependent, may start streaming
   // its rows now (it reads the records only after this launch completed)
   pdl_launch_dependents();
   const int b = int(blockIdx.x) * 32 + int(threadIdx.x >> 3), j = int(threadIdx.x & 7);
   if (int(blockIdx.x) * 32 >= nb) return;  // whole CTA: the shuffles below stay converged
+  if (xq) {
+    uint32_t word, scale, sum;
+    read_q8_block(xq, min(b, nb - 1), j, word, scale, sum);
+    if (b < nb) {
+      xg[8 * b + j] = word;
+      if (j == 0) {
+        xg[8 * nb + b] = scale;
+        xg[9 * nb + b] = sum;
+      }
+    }
+    return;
+  }
   const float4 v = b < nb ? __ldg(reinterpret_cast<const float4 *>(x + int64_t(b) * kQK) + j)
                           : make_float4(0.f, 0.f, 0.f, 0.f);
   uint16_t sc;
@@ -578,7 +621,7 @@ int next_pow2(int v) {
 
 template <int TYPE>
 cudaError_t launch_typed(int n, const uint8_t *const *W, float *const *y, const int64_t *M, const float *x,
-                         int64_t K, uint32_t *rec_ws, cudaStream_t stream) {
+                         int64_t K, uint32_t *rec_ws, cudaStream_t stream, const uint8_t *xq) {
   cudaError_t err;
   const DeviceInfo *di = device_info(&err);
   if (!di) return err;
@@ -699,6 +742,7 @@ cudaError_t launch_typed(int n, const uint8_t *const *W, float *const *y, const 
         }
         for (int i = a.n_mats; i < kMaxMats; ++i) p.chunk_start[i + 1] = p.chunk_start[i];
         p.x = x;
+        p.xq = xq;
         p.nb = nb;
         p.rec = rec_ws;
         p.quant_ctas = (nb + kPrepBlocksPerCta - 1) / kPrepBlocksPerCta;
@@ -730,7 +774,7 @@ cudaError_t launch_typed(int n, const uint8_t *const *W, float *const *y, const 
   if (e != cudaSuccess) return e;
   const uint32_t *xg = nullptr;
   if (rec_ws) {
-    k_gemv_generic_prep<<<unsigned((nb + 31) / 32), 256, 0, stream>>>(x, rec_ws, nb);
+    k_gemv_generic_prep<<<unsigned((nb + 31) / 32), 256, 0, stream>>>(x, xq, rec_ws, nb);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     xg = rec_ws;
   }
@@ -780,14 +824,14 @@ cudaError_t launch_typed(int n, const uint8_t *const *W, float *const *y, const 
 }  // namespace
 
 cudaError_t launch_gemv(int type, int n, const uint8_t *const *W, float *const *y, const int64_t *M,
-                        const float *x, int64_t K, uint32_t *rec_ws, cudaStream_t stream) {
-  if (type == kTypeQ4_K) return launch_typed<kTypeQ4_K>(n, W, y, M, x, K, rec_ws, stream);
-  if (type == kTypeQ6_K) return launch_typed<kTypeQ6_K>(n, W, y, M, x, K, rec_ws, stream);
-  if (type == kTypeQ4_1) return launch_typed<kTypeQ4_1>(n, W, y, M, x, K, rec_ws, stream);
-  if (type == kTypeQ5_0) return launch_typed<kTypeQ5_0>(n, W, y, M, x, K, rec_ws, stream);
-  if (type == kTypeQ5_1) return launch_typed<kTypeQ5_1>(n, W, y, M, x, K, rec_ws, stream);
-  if (type == kTypeQ4_0) return launch_typed<kTypeQ4_0>(n, W, y, M, x, K, rec_ws, stream);
-  return launch_typed<kTypeQ8_0>(n, W, y, M, x, K, rec_ws, stream);
+                        const float *x, int64_t K, uint32_t *rec_ws, cudaStream_t stream, const uint8_t *xq) {
+  if (type == kTypeQ4_K) return launch_typed<kTypeQ4_K>(n, W, y, M, x, K, rec_ws, stream, xq);
+  if (type == kTypeQ6_K) return launch_typed<kTypeQ6_K>(n, W, y, M, x, K, rec_ws, stream, xq);
+  if (type == kTypeQ4_1) return launch_typed<kTypeQ4_1>(n, W, y, M, x, K, rec_ws, stream, xq);
+  if (type == kTypeQ5_0) return launch_typed<kTypeQ5_0>(n, W, y, M, x, K, rec_ws, stream, xq);
+  if (type == kTypeQ5_1) return launch_typed<kTypeQ5_1>(n, W, y, M, x, K, rec_ws, stream, xq);
+  if (type == kTypeQ4_0) return launch_typed<kTypeQ4_0>(n, W, y, M, x, K, rec_ws, stream, xq);
+  return launch_typed<kTypeQ8_0>(n, W, y, M, x, K, rec_ws, stream, xq);
 }
 
 size_t gemv_workspace_bytes(int64_t K) {

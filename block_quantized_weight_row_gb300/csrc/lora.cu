@@ -1,0 +1,645 @@
+// lora.cu — low-rank adapters of many requests beside a shared projection
+// (include/bq.h: bq_lora):  out_t = y_t + s_a B_a (A_a x_t),  a = adapter[t].
+//
+// Bound by memory: 2 r (K + M) products per token against a row of x, y and out
+// each (r is 8 to 128), and in a decode step the adapters' own 2 r (K + M) bytes.
+// Tokens of one adapter are brought together in tiles of 16 or 64 tokens, so that
+// an adapter is read once per tile and the products run on tensor instructions:
+//   1. k_lora_group (from kLeaders tokens on): tokens sorted by adapter, and the
+//      list of tiles. Below that every CTA finds its tile itself: the tokens of
+//      the adapter of token j, if j is the first of sixteen of them.
+//   2. k_lora_shrink: H[t] = s_a A_a x_t, K cut over the warps and the CTAs of a
+//      cluster, whose sums meet in shared memory in a fixed order.
+//   3. k_lora_expand: out_t = y_t + B_a H[t].
+// A tile's rows do not depend on one another, so neither the order inside an
+// adapter nor the other tokens change a result.
+//
+// Fragments come straight from global memory, 16 bytes per lane: a product's sum
+// over k may be taken in any order, so lane t of a quad gives its instruction the
+// 8 consecutive k 8t .. 8t + 7 of 32 in place of the pairs of its layout, of both
+// operands alike. For the second product the columns are permuted too, so that a
+// lane's results over four n-tiles are 8 consecutive columns of out.
+//
+// Terms. A 16-bit row meets adapters of its own type: products are exact. An fp32
+// row beside bf16 adapters is cut into three bf16 terms (its 24 bits, exact),
+// beside fp16 ones into two tf32 terms (22 bits; fp16 is exact in tf32). H is kept
+// in fp32 and enters the second product in bf16 terms, three for fp32 rows of out
+// and two (16 bits) for bf16 ones, or in two fp16 terms (22 bits) after scaling
+// each row by a power of two to at most 1.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "bq_device.cuh"
+#include "bq_internal.h"
+#include "layer.h"
+#include "paged.cuh"
+
+namespace bq {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kLeaders = 256;  // up to this many tokens, CTAs find their tiles themselves
+constexpr int kGroupThreads = 1024;
+constexpr int kMaxBins = 4096 + 1;  // adapters, and the tokens without one
+constexpr int kShrinkThreads = 128, kExpandThreads = 256;
+
+struct Tile {
+  int adapter, first, count, unused;  // first: in the sorted tokens
+};
+
+// Workspace: H, then (grouped) the sorted tokens, the tiles and their number.
+struct Work {
+  float *H;         // [token][rank]
+  int32_t *sorted;  // null: tiles by leaders
+  Tile *tiles;
+  int32_t *n_tiles;
+};
+
+__device__ __forceinline__ int adapter_of(const LoraArgs &a, int t) {
+  const int id = __ldg(a.adapter + t);
+  return uint32_t(id) < uint32_t(a.n_adapters) ? id : -1;
+}
+
+// ----------------------------------------------------------------- group --
+
+template <int TM>
+__global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, const Work w) {
+  __shared__ int count[kMaxBins], tile0[kMaxBins + 1];
+  __shared__ int sums[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bins = a.n_adapters + 1;
+  pdl_launch_dependents();
+  for (int b = tid; b < bins; b += kGroupThreads) count[b] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int t0 = 0; t0 < a.n_tokens; t0 += kGroupThreads) {  // whole warps: the votes need them
+    const int t = t0 + tid;
+    const bool live = t < a.n_tokens;
+    const int id = live ? __ldg(a.adapter + t) : -2;
+    const int bin = uint32_t(id) < uint32_t(a.n_adapters) ? id + 1 : 0;
+    bad |= live && bin == 0 && id != -1;
+    const unsigned same = __match_any_sync(kFull, live ? bin : -1);
+    if (live && lane == __ffs(same) - 1) atomicAdd(&count[bin], __popc(same));
+  }
+  if (bad) atomicOr(a.err, kErrIndex);
+  __syncthreads();
+  // exclusive sums over the bins of tokens and of tiles, a run of bins per thread
+  const int run = (bins + kGroupThreads - 1) / kGroupThreads, b0 = min(tid * run, bins), b1 = min(b0 + run, bins);
+  int n = 0, m = 0;
+  for (int b = b0; b < b1; ++b) n += count[b], m += (count[b] + TM - 1) / TM;
+  int ni = n, mi = m;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(kFull, ni, d), y = __shfl_up_sync(kFull, mi, d);
+    if (lane >= d) ni += x, mi += y;
+  }
+  if (lane == 31) sums[0][warp] = ni, sums[1][warp] = mi;
+  __syncthreads();
+  ni -= n, mi -= m;
+  for (int k = 0; k < warp; ++k) ni += sums[0][k], mi += sums[1][k];
+  for (int b = b0; b < b1; ++b) {
+    const int c = count[b];
+    tile0[b] = mi;
+    count[b] = ni;  // from here on: where the bin's next token goes
+    ni += c, mi += (c + TM - 1) / TM;
+  }
+  if (tid == kGroupThreads - 1) tile0[bins] = mi;  // the last thread's sums end with all
+  __syncthreads();
+  const int tiles = tile0[bins];
+  if (tid == 0) *w.n_tiles = tiles;
+  for (int i = tid; i < tiles; i += kGroupThreads) {
+    int lo = 0, hi = bins;  // the last bin with tile0 <= i that has tiles
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      (tile0[mid] <= i ? lo : hi) = mid;
+    }
+    const int first = count[lo] + (i - tile0[lo]) * TM, end = lo + 1 < bins ? count[lo + 1] : a.n_tokens;
+    w.tiles[i] = Tile{lo - 1, first, min(TM, end - first), 0};
+  }
+  __syncthreads();
+  for (int t0 = 0; t0 < a.n_tokens; t0 += kGroupThreads) {
+    const int t = t0 + tid;
+    const bool live = t < a.n_tokens;
+    const int bin = live ? adapter_of(a, t) + 1 : -1;
+    const unsigned same = __match_any_sync(kFull, bin);
+    const int leader = __ffs(same) - 1;
+    int at = 0;
+    if (live && lane == leader) at = atomicAdd(&count[bin], __popc(same));
+    at = __shfl_sync(kFull, at, leader) + __popc(same & ((1u << lane) - 1));
+    if (live) w.sorted[at] = t;
+  }
+}
+
+// The tokens of tile `index` into rows[] (those beyond the count repeat the
+// first), by all threads of the CTA. False: there is no such tile.
+template <int TM>
+__device__ __forceinline__ bool find_tile(const LoraArgs &a, const Work &w, int index, int *rows, int &adapter, int &count) {
+  __shared__ int before[8], total[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (w.sorted) {
+    if (index >= *w.n_tiles) return false;
+    const Tile t = w.tiles[index];
+    adapter = t.adapter;
+    count = t.count;
+    if (tid < TM) rows[tid] = w.sorted[t.first + (tid < t.count ? tid : 0)];
+    __syncthreads();
+    return true;
+  }
+  // tokens of the adapter of token `index`, in order: with two passes of 128
+  // threads or one of 256, every warp has whole groups of 32 tokens
+  adapter = adapter_of(a, index);
+  if (tid < 8) before[tid] = 0;
+  __syncthreads();
+  for (int t = tid; t < kLeaders; t += blockDim.x) {
+    const unsigned same = __ballot_sync(kFull, t < a.n_tokens && adapter_of(a, t) == adapter);
+    if (lane == 0) before[t >> 5] = int(same);
+  }
+  __syncthreads();
+  if (warp == 0) {  // words of matches -> ranks
+    const unsigned word = lane < 8 ? unsigned(before[lane]) : 0u;
+    int rank = __popc(word);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) {
+      const int o = __shfl_up_sync(kFull, rank, d);
+      if (lane >= d) rank += o;
+    }
+    const int all = __shfl_sync(kFull, rank, 7);
+    rank -= __popc(word);  // matches before this word
+    const int mine = __shfl_sync(kFull, rank, index >> 5) +
+                     __popc(__shfl_sync(kFull, word, index >> 5) & ((1u << (index & 31)) - 1));  // the leader's rank
+    const int n = min(TM, all - mine);
+    if (mine % TM == 0) {
+      // lane i of 16 finds the token of rank mine + i
+      if (lane < TM) rows[lane] = index;
+      __syncwarp();
+      if (lane < 8) {
+        unsigned left = word;
+        for (int r = rank; left; ++r, left &= left - 1)
+          if (r >= mine && r < mine + TM) rows[r - mine] = lane * 32 + __ffs(left) - 1;
+      }
+    }
+    if (lane == 0) total[0] = mine % TM == 0 ? n : 0;
+  }
+  __syncthreads();
+  count = total[0];
+  return count > 0;
+}
+
+// -------------------------------------------------------------- products --
+
+template <int WE>
+__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (WE == kElemBF16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two fp32 values cut to bf16, packed; the rests (exact) stay. Three such steps
+// give all 24 bits of a value.
+__device__ __forceinline__ uint32_t cut_pair(float &x, float &y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  x = __fsub_rn(x, __uint_as_float(a & 0xffff0000u));
+  y = __fsub_rn(y, __uint_as_float(b & 0xffff0000u));
+  return __byte_perm(a, b, 0x7632);
+}
+
+// fp32 bits rounded to tf32 (11 significant bits)
+__device__ __forceinline__ uint32_t to_tf32(uint32_t x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(__uint_as_float(x)));
+  return r;
+}
+
+// 32 k of a row: a lane's 8 of them
+template <int XE>
+struct RowWords {
+  uint4 v[XE == kElemF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t *p) {
+    v[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+    if constexpr (XE == kElemF32) v[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+};
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// acc[nt] += x (rows g, g + 8; 32 k) times A (n-tile nt; 32 k)
+template <int XE, int WE, int NT>
+__device__ __forceinline__ void shrink_step(float (&acc)[NT][4], const RowWords<XE> &lo, const RowWords<XE> &hi, const uint4 (&bw)[NT]) {
+  if constexpr (XE != kElemF32) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      mma16<WE>(acc[nt], lo.v[0].x, hi.v[0].x, lo.v[0].y, hi.v[0].y, bw[nt].x, bw[nt].y);
+      mma16<WE>(acc[nt], lo.v[0].z, hi.v[0].z, lo.v[0].w, hi.v[0].w, bw[nt].z, bw[nt].w);
+    }
+  } else if constexpr (WE == kElemBF16) {
+    float l[8], h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) l[i] = __uint_as_float(word(lo.v[i >> 2], i & 3)), h[i] = __uint_as_float(word(hi.v[i >> 2], i & 3));
+#pragma unroll
+    for (int term = 0; term < 3; ++term) {
+      uint32_t lw[4], hw[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) lw[i] = cut_pair(l[2 * i], l[2 * i + 1]), hw[i] = cut_pair(h[2 * i], h[2 * i + 1]);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma16<WE>(acc[nt], lw[0], hw[0], lw[1], hw[1], bw[nt].x, bw[nt].y);
+        mma16<WE>(acc[nt], lw[2], hw[2], lw[3], hw[3], bw[nt].z, bw[nt].w);
+      }
+    }
+  } else {
+    uint32_t l[2][8], h[2][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = word(lo.v[i >> 2], i & 3), y = word(hi.v[i >> 2], i & 3);
+      l[0][i] = to_tf32(x), h[0][i] = to_tf32(y);
+      l[1][i] = to_tf32(__float_as_uint(__fsub_rn(__uint_as_float(x), __uint_as_float(l[0][i]))));
+      h[1][i] = to_tf32(__float_as_uint(__fsub_rn(__uint_as_float(y), __uint_as_float(h[0][i]))));
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 b = unpack_pair<kElemF16>(word(bw[nt], i));
+#pragma unroll
+        for (int term = 1; term >= 0; --term)
+          mma_tf32(acc[nt], l[term][2 * i], h[term][2 * i], l[term][2 * i + 1], h[term][2 * i + 1], __float_as_uint(b.x), __float_as_uint(b.y));
+      }
+  }
+}
+
+// NT: n-tiles of 8 ranks (rank <= 8 NT). TM = 64: a warp has 16 of the tile's
+// tokens and all of the CTA's k; TM = 16: all of them and a quarter of the k.
+template <int XE, int WE, int TM, int NT>
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const LoraArgs a, const Work w, const int splits) {
+  __shared__ __align__(16) float part[4][16][8 * NT];  // written in pairs
+  __shared__ int rows[TM];
+  constexpr int XS = Elem<XE>::kBytes;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
+  if (w.sorted) {
+    pdl_wait();
+  } else if (threadIdx.x == 0 && blockIdx.x == 0) {
+    const int id = __ldg(a.adapter + blockIdx.y);
+    if (id < -1 || id >= a.n_adapters) atomicOr(a.err, kErrIndex);
+  }
+  int ad, count;
+  if (!find_tile<TM>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
+  const int nb = a.K / 32, split = blockIdx.x;
+  const int pieces = TM == 16 ? splits * 4 : splits, piece = TM == 16 ? split * 4 + warp : split;
+  const int k0 = int(int64_t(nb) * piece / pieces), k1 = int(int64_t(nb) * (piece + 1) / pieces);
+  const int r0 = TM == 64 ? warp * 16 : 0;
+  const bool idle = r0 >= count;  // no token in this warp's rows
+  const uint8_t *lo = a.x + rows[r0 + g] * a.x_row + t * 8 * XS, *hi = a.x + rows[r0 + g + 8] * a.x_row + t * 8 * XS;
+  const uint8_t *ap = a.A + (int64_t(ad) * a.rank + g) * a.K * 2 + t * 16;
+  float acc[NT][4];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
+  if (!idle) {
+#pragma unroll 2
+    for (int k = k0; k < k1; ++k) {
+      RowWords<XE> xl, xh;
+      uint4 bw[NT];
+      xl.load(lo + int64_t(k) * 32 * XS);
+      xh.load(hi + int64_t(k) * 32 * XS);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        bw[nt] = make_uint4(0, 0, 0, 0);
+        if (nt * 8 < a.rank) bw[nt] = __ldg(reinterpret_cast<const uint4 *>(ap + (int64_t(nt) * 8 * a.K + k * 32) * 2));
+      }
+      shrink_step<XE, WE, NT>(acc, xl, xh, bw);
+    }
+  }
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    *reinterpret_cast<float2 *>(&part[warp][g][nt * 8 + 2 * t]) = make_float2(acc[nt][0], acc[nt][1]);
+    *reinterpret_cast<float2 *>(&part[warp][g + 8][nt * 8 + 2 * t]) = make_float2(acc[nt][2], acc[nt][3]);
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  // each CTA of the cluster adds up its share of the tile's sums
+  const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
+  const int n = count * a.rank;
+  for (int e = split * kShrinkThreads + threadIdx.x; e < n; e += splits * kShrinkThreads) {
+    const int row = e / a.rank, r = e - row * a.rank;
+    float sum = 0.0f;
+    for (int c = 0; c < splits; ++c) {
+      const float *p = cluster.map_shared_rank(&part[0][0][0], c);
+      if constexpr (TM == 64) {
+        sum += p[row * (8 * NT) + r];  // warp row / 16, its row row % 16
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += p[(q * 16 + row) * (8 * NT) + r];
+      }
+    }
+    w.H[int64_t(rows[row]) * a.rank + r] = sum * s;
+  }
+  cluster.sync();  // the others' sums are read from here until now
+}
+
+// ---------------------------------------------------------------- expand --
+
+template <int YE>
+__device__ __forceinline__ void load_y(const uint8_t *p, int n, bool vec, float (&v)[8]) {
+  constexpr int S = Elem<YE>::kBytes;
+  if (vec && n >= 8) {
+    if constexpr (YE == kElemF32) {
+      const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_pair<YE>(word(a, i));
+        v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (YE == kElemF32) v[i] = *reinterpret_cast<const float *>(p + i * S);
+        if constexpr (YE == kElemF16) v[i] = __half2float(*reinterpret_cast<const __half *>(p + i * S));
+        if constexpr (YE == kElemBF16) v[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + i * S));
+      }
+  }
+}
+template <int YE>
+__device__ __forceinline__ void store_y(uint8_t *p, int n, bool vec, const float (&v)[8]) {
+  constexpr int S = Elem<YE>::kBytes;
+  if (vec && n >= 8) {
+    if constexpr (YE == kElemF32) {
+      __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+      __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+    } else {
+      __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_pair<YE>(v[0], v[1]), pack_pair<YE>(v[2], v[3]), pack_pair<YE>(v[4], v[5]), pack_pair<YE>(v[6], v[7])));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) {
+        if constexpr (YE == kElemF32) *reinterpret_cast<float *>(p + i * S) = v[i];
+        if constexpr (YE == kElemF16) *reinterpret_cast<__half *>(p + i * S) = __float2half_rn(v[i]);
+        if constexpr (YE == kElemBF16) *reinterpret_cast<__nv_bfloat16 *>(p + i * S) = __float2bfloat16_rn(v[i]);
+      }
+  }
+}
+
+// KB: blocks of 32 ranks. A warp has MT row tiles of 16 tokens and 32 columns a
+// turn; the CTA's 8 warps are 2 x 4 (TM = 64, MT = 2) or 1 x 8 (TM = 16, MT = 1).
+template <int WE, int YE, int TM, int KB>
+struct Expand {
+  static constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2;
+  static constexpr int kPitch = KB == 1 ? 64 : KB * 64 + 64;  // 64 modulo 128: a quarter-warp's 16-byte reads of two rows meet no bank twice
+  static constexpr int kBytes = kTerms * TM * kPitch;
+  static_assert(KB == 1 || KB % 2 == 0, "pitch");
+};
+
+template <int WE, int YE, int TM, int KB>
+__global__ void __launch_bounds__(kExpandThreads) k_lora_expand(const LoraArgs a, const Work w, const int turns) {
+  constexpr int MT = TM == 64 ? 2 : 1, WM = TM == 64 ? 4 : 8;
+  constexpr int kTerms = Expand<WE, YE, TM, KB>::kTerms, kPitch = Expand<WE, YE, TM, KB>::kPitch;
+  constexpr int YS = Elem<YE>::kBytes;
+  extern __shared__ __align__(16) uint8_t terms[];  // [term][row], rows of kPitch bytes
+  __shared__ float unscale[TM];
+  __shared__ int rows[TM];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  if (w.sorted) pdl_wait();
+  int ad, count;
+  if (!find_tile<TM>(a, w, blockIdx.y, rows, ad, count)) return;
+  if (ad < 0 && a.y == a.out) return;
+  if (!w.sorted) pdl_wait();
+  if (ad >= 0) {
+    for (int r = warp; r < TM; r += kExpandThreads / 32) {
+      float h[KB], m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        const int c = lane + 32 * i;
+        h[i] = r < count && c < a.rank ? __ldcg(w.H + int64_t(rows[r]) * a.rank + c) : 0.0f;
+        m = fmaxf(m, fabsf(h[i]));
+      }
+      float up = 1.0f;
+      if constexpr (WE == kElemF16) {
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+        // 2^-e of the largest value (in [2^e, 2^(e+1))), kept within normal numbers
+        const int e = min(max(int(__float_as_uint(m) >> 23), 2), 252);
+        up = __uint_as_float(uint32_t(254 - e) << 23);
+        if (lane == 0) unscale[r] = __uint_as_float(uint32_t(e) << 23);
+      }
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        float x = h[i] * up;
+#pragma unroll
+        for (int k = 0; k < kTerms; ++k) {
+          uint16_t *to = reinterpret_cast<uint16_t *>(terms + (k * TM + r) * kPitch + (lane + 32 * i) * 2);
+          if constexpr (WE == kElemF16) {
+            const __half f = __float2half_rn(x);
+            *to = __half_as_ushort(f);
+            x -= __half2float(f);
+          } else {
+            const __nv_bfloat16 f = __float2bfloat16_rn(x);
+            *to = __bfloat16_as_ushort(f);
+            x -= __bfloat162float(f);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+  const int wr = warp / WM, wm = warp % WM, r0 = wr * 16 * MT;
+  if (r0 >= count) return;
+  for (int turn = 0; turn < turns; ++turn) {
+    const int m0 = (int(blockIdx.x) * turns + turn) * (WM * 32) + wm * 32;
+    if (m0 >= a.M) break;
+    const int c0 = m0 + 8 * t, n = a.M - c0;  // this lane's 8 columns, as many as there are
+    float y[MT][2][8];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 16 * i + 8 * h + g;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[i][h][k] = 0.0f;
+        if (a.y && r < count && n > 0) load_y<YE>(a.y + rows[r] * a.y_row + int64_t(c0) * YS, n, a.y_vec, y[i][h]);
+      }
+    if (ad >= 0) {
+      float acc[MT][4][4];
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        uint4 bw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {  // column g of n-tile j
+          const int m = m0 + 8 * (g >> 1) + 2 * j + (g & 1);
+          bw[j] = make_uint4(0, 0, 0, 0);
+          if (m < a.M && kb * 32 + 8 * t < a.rank)
+            bw[j] = __ldg(reinterpret_cast<const uint4 *>(a.B + ((int64_t(ad) * a.M + m) * a.rank + kb * 32 + 8 * t) * 2));
+        }
+#pragma unroll
+        for (int k = kTerms - 1; k >= 0; --k)
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const uint4 lo = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g) * kPitch + kb * 64 + 16 * t);
+            const uint4 hi = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g + 8) * kPitch + kb * 64 + 16 * t);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              mma16<WE>(acc[i][j], lo.x, hi.x, lo.y, hi.y, bw[j].x, bw[j].y);
+              mma16<WE>(acc[i][j], lo.z, hi.z, lo.w, hi.w, bw[j].z, bw[j].w);
+            }
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float s = WE == kElemF16 ? unscale[r0 + 16 * i + 8 * h + g] : 1.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float d = acc[i][k >> 1][2 * h + (k & 1)];
+            y[i][h][k] = WE == kElemF16 ? __fmaf_rn(d, s, y[i][h][k]) : __fadd_rn(d, y[i][h][k]);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int r = r0 + 16 * i + 8 * h + g;
+        if (r < count && n > 0) store_y<YE>(a.out + rows[r] * a.out_row + int64_t(c0) * YS, n, a.y_vec, y[i][h]);
+      }
+  }
+}
+
+// ------------------------------------------------------------------ host --
+
+struct Plan {
+  bool grouped;
+  int tm, tiles, splits;  // tiles: at most as many
+  size_t bytes;
+  size_t sorted_off, tiles_off, n_off;
+};
+
+Plan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
+  Plan p{};
+  const int64_t groups = std::min(n + 1, T);
+  p.grouped = T > kLeaders;
+  // a tile of 64 pays where an adapter fills it, by the mean
+  p.tm = p.grouped && T >= 32 * groups ? 64 : 16;
+  p.tiles = int(p.grouped ? T / p.tm + groups : T);
+  const int64_t busy = p.grouped ? T / p.tm + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2;  // about as many have work
+  const int64_t pieces = K / 32 / (p.tm == 16 ? 16 : 8);  // 4 or 8 blocks of 32 k per warp at least
+  p.splits = 1;
+  while (p.splits < 8 && busy * p.splits < 304 && 2 * p.splits <= pieces) p.splits *= 2;
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  p.bytes = up(size_t(T) * size_t(rank) * 4);
+  if (p.grouped) {
+    p.sorted_off = p.bytes;
+    p.tiles_off = p.sorted_off + up(size_t(T) * 4);
+    p.n_off = p.tiles_off + up(size_t(p.tiles) * sizeof(Tile));
+    p.bytes = p.n_off + 256;
+  }
+  return p;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_ex(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t stream, A... args) {
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  attr[n].id = cudaLaunchAttributeClusterDimension;
+  attr[n].val.clusterDim.x = unsigned(cluster);
+  attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+  ++n;
+  if (dependent) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+template <int XE, int WE, int TM>
+cudaError_t shrink(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
+  const dim3 grid(unsigned(p.splits), unsigned(p.tiles));
+  if (a.rank <= 16) return launch_ex(k_lora_shrink<XE, WE, TM, 2>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+  if (a.rank <= 32) return launch_ex(k_lora_shrink<XE, WE, TM, 4>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+  if (a.rank <= 64) return launch_ex(k_lora_shrink<XE, WE, TM, 8>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+  return launch_ex(k_lora_shrink<XE, WE, TM, 16>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+}
+
+template <int WE, int YE, int TM>
+cudaError_t expand(const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
+  const int cols = TM == 64 ? 128 : 256;
+  const int64_t groups = (a.M + cols - 1) / cols;
+  int turns = 1;  // of a CTA: several where enough CTAs remain
+  while (turns < 8 && groups * p.tiles / (2 * turns) >= int64_t(sms) * 8) turns *= 2;
+  const dim3 grid(unsigned((groups + turns - 1) / turns), unsigned(p.tiles));
+  if (a.rank <= 32) return launch_ex(k_lora_expand<WE, YE, TM, 1>, grid, kExpandThreads, Expand<WE, YE, TM, 1>::kBytes, 1, true, s, a, w, turns);
+  if (a.rank <= 64) return launch_ex(k_lora_expand<WE, YE, TM, 2>, grid, kExpandThreads, Expand<WE, YE, TM, 2>::kBytes, 1, true, s, a, w, turns);
+  return launch_ex(k_lora_expand<WE, YE, TM, 4>, grid, kExpandThreads, Expand<WE, YE, TM, 4>::kBytes, 1, true, s, a, w, turns);
+}
+
+template <int WE, int TM>
+cudaError_t run(int x_elem, int y_elem, const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
+  if (p.grouped) {
+    const cudaError_t e = launch_ex(k_lora_group<TM>, dim3(1), kGroupThreads, 0, 1, false, s, a, w);
+    if (e != cudaSuccess) return e;
+  }
+  const cudaError_t e = x_elem == kElemF32 ? shrink<kElemF32, WE, TM>(a, w, p, s) : shrink<WE, WE, TM>(a, w, p, s);
+  if (e != cudaSuccess) return e;
+  return y_elem == kElemF32 ? expand<WE, kElemF32, TM>(a, w, p, sms, s) : expand<WE, WE, TM>(a, w, p, sms, s);
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(int64_t n_tokens, int64_t n_adapters, int64_t rank, int64_t K, int64_t) {
+  return plan_of(n_tokens, n_adapters, rank, K).bytes;
+}
+
+cudaError_t launch_lora(int x_elem, int w_elem, int y_elem, LoraArgs a, void *ws, cudaStream_t stream) {
+  cudaError_t err;
+  const DeviceInfo *di = device_info(&err);
+  if (!di) return err;
+  a.err = di->err_word;
+  const Plan p = plan_of(a.n_tokens, a.n_adapters, a.rank, a.K);
+  uint8_t *base = static_cast<uint8_t *>(ws);
+  Work w{reinterpret_cast<float *>(base), nullptr, nullptr, nullptr};
+  if (p.grouped) {
+    w.sorted = reinterpret_cast<int32_t *>(base + p.sorted_off);
+    w.tiles = reinterpret_cast<Tile *>(base + p.tiles_off);
+    w.n_tiles = reinterpret_cast<int32_t *>(base + p.n_off);
+  }
+  const int sms = di->sm_count;
+  if (w_elem == kElemBF16)
+    return p.tm == 64 ? run<kElemBF16, 64>(x_elem, y_elem, a, w, p, sms, stream) : run<kElemBF16, 16>(x_elem, y_elem, a, w, p, sms, stream);
+  return p.tm == 64 ? run<kElemF16, 64>(x_elem, y_elem, a, w, p, sms, stream) : run<kElemF16, 16>(x_elem, y_elem, a, w, p, sms, stream);
+}
+
+}  // namespace bq

@@ -7,63 +7,10 @@
 // The functions return the outputs, or the library's status as an int, which
 // the Python wrapper turns into its exception. Wrong tensors raise TypeError
 // or ValueError. (The C ABI itself stays free of torch types: include/bq.h.)
-#include <Python.h>
-
-#include <ATen/ATen.h>
-#include <c10/cuda/CUDAGuard.h>
-#include <c10/cuda/CUDAStream.h>
-#include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/python_variable.h>
-
-#include <algorithm>
-#include <climits>
-#include <cstdarg>
-
-#include "bq.h"
+#include "binding_common.h"
+#include "layer_binding.h"
 
 namespace {
-
-// What the caller got wrong, raised as a Python exception.
-struct Wrong {
-  PyObject *type;
-};
-
-[[noreturn]] void wrong(PyObject *type, const char *fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  PyErr_FormatV(type, fmt, ap);
-  va_end(ap);
-  throw Wrong{type};
-}
-
-const at::Tensor &cuda_tensor(PyObject *o, const char *name) {
-  if (!THPVariable_Check(o)) wrong(PyExc_TypeError, "%s must be a CUDA tensor", name);
-  const at::Tensor &t = THPVariable_Unpack(o);
-  if (!t.is_cuda() || t.layout() != at::kStrided) wrong(PyExc_TypeError, "%s must be a CUDA tensor", name);
-  return t;
-}
-
-int64_t to_int(PyObject *o, const char *name) {
-  const int64_t v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) wrong(PyExc_TypeError, "%s must be an int", name);
-  return v;
-}
-
-// A type, basis or other code that the library takes as an int.
-int to_code(PyObject *o, const char *name) {
-  const int64_t v = to_int(o, name);
-  if (v < INT_MIN || v > INT_MAX) wrong(PyExc_ValueError, "%s must fit 32 bits", name);
-  return int(v);
-}
-
-int elem_of(at::ScalarType t) {
-  switch (t) {
-    case at::kFloat: return BQ_ELEM_F32;
-    case at::kHalf: return BQ_ELEM_F16;
-    case at::kBFloat16: return BQ_ELEM_BF16;
-    default: return -1;
-  }
-}
 
 int block_bytes(int type) { return type == BQ_TYPE_Q4_0 ? 18 : type == BQ_TYPE_Q8_0 ? 34 : 0; }
 
@@ -126,11 +73,6 @@ const float *bias_of(PyObject *o, const Cache &c) {
 
 // None as the bias's basis: the cache's
 int basis_of(PyObject *o, const Cache &c) { return o == Py_None ? c.c.k_basis : to_code(o, "bias_basis"); }
-
-void use_stream() { bq_set_stream(c10::cuda::getCurrentCUDAStream().stream()); }
-
-PyObject *none() { Py_RETURN_NONE; }
-PyObject *status(int r) { return PyLong_FromLong(r); }
 
 // cache, k, v, slots, bias, bias_basis
 PyObject *kv_write(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -220,24 +162,12 @@ PyObject *attn(PyObject *, PyObject *const *args, Py_ssize_t n) {
       if (out.size(0) != n_q) wrong(PyExc_ValueError, "out must have q's shape");
     }
     float *lse = args[10] == Py_None ? nullptr : exact(args[10], "lse", c, at::kFloat, {n_q, H}).data_ptr<float>();
-    // a workspace of this call's own, from the current stream's pool: calls on
-    // other streams and captured launches never share it; the one that the
-    // thread had set for other calls is set again after it
-    const size_t need = bq_paged_attn_workspace_size(&c.c, elem, B, n_q, max_q, max_kv, H, causal, window);
-    const at::Tensor ws = at::empty({int64_t(std::max<size_t>(need, 256))}, q.options().dtype(at::kByte));
+    CallWorkspace ws(bq_paged_attn_workspace_size(&c.c, elem, B, n_q, max_q, max_kv, H, causal, window), c.device);
     use_stream();
-    size_t before_bytes;
-    void *const before = bq_get_workspace(&before_bytes);
-    bq_set_workspace(ws.data_ptr(), size_t(ws.numel()));
     const int r = bq_paged_attn(&c.c, elem, q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(), out.stride(0), out.stride(1), lse,
                                 start.data_ptr<int>(), lens.data_ptr<int>(), table.data_ptr<int>(), pages, B, n_q, max_q, max_kv, H,
                                 float(scale), causal, window);
-    if (r) {  // the message of the call stays the last one
-      const std::string message = bq_last_error();
-      bq_set_workspace(before, before_bytes);
-      return Py_BuildValue("(is)", r, message.c_str());
-    }
-    bq_set_workspace(before, before_bytes);
+    if (r) return ws.failed(r);
     return THPVariable_Wrap(out);
   } catch (const Wrong &) {
     return nullptr;
@@ -249,6 +179,7 @@ PyMethodDef kMethods[] = {
     {"kv_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_write)), METH_FASTCALL, nullptr},
     {"kv_read", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_read)), METH_FASTCALL, nullptr},
     {"attn", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attn)), METH_FASTCALL, nullptr},
+    BQ_LAYER_METHODS,
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_paged", "Paged KV-cache calls of libbq.so on torch tensors.", -1, kMethods,

@@ -101,7 +101,7 @@ extern "C" {
 #define BQ_ERR_TIMEOUT (-6)     /* a bounded in-kernel wait ran out (see bq_device_status) */
 #define BQ_ERR_WORKSPACE (-7)   /* workspace missing or smaller than bq_workspace_size() */
 #define BQ_ERR_BASIS (-8)       /* a mean-centering bias calibrated in another basis than the K cache */
-#define BQ_ERR_INDEX (-9)       /* a slot, page or length of a paged cache out of range (see bq_device_status) */
+#define BQ_ERR_INDEX (-9)       /* a slot, page or length of a paged cache, an adapter or an axis out of range (see bq_device_status) */
 
 /* Largest K taken by bq_gemv (the quantized activation lives in shared memory). */
 #define BQ_GEMV_MAX_K 65536
@@ -404,6 +404,143 @@ int64_t bq_paged_attn_many_rows(const bq_paged_cache *cache, int elem, int64_t n
  * slot outside the pool. */
 int bq_paged_slot_check(const bq_paged_cache *cache, int64_t slot, int64_t *page, int64_t *place);
 
+/* ---- around the projections and the paged cache of a served layer ----
+ * What a step computes between those calls. The pages describe none of it (a
+ * sequence's positions and the norm belong to the model they take as given), so
+ * these definitions are this library's own. All lengths and indices are read on
+ * the device, so captured launches follow them. */
+
+/* The next tokens of a batch of sequences in a paged cache: page tables, slots
+ * and positions from lengths, on the device. Sequence b has kv_len[b] cached
+ * tokens, in pages page_table[b * max_pages ..] (its first ceil(kv_len[b] /
+ * page_size) entries), and n_new[b] tokens to come (0: it waits). With
+ *   owned_b = ceil(kv_len / page_size), need_b = ceil((kv_len + n_new) /
+ *     page_size) - owned_b, and base_b, start_b the sums of need and n_new over
+ *     the sequences before b,
+ * the call sets
+ *   page_table[b][owned_b + i] = free_pages[base_b + i]  for i < need_b (the
+ *     other entries stay as they are),
+ *   slots[start_b + i], positions[start_b + i] = slot and place (kv_len[b] + i)
+ *     of the sequence's new token i, and -1, 0 from the last token to n_slots,
+ *   q_start[b + 1] = start_b + n_new[b], q_start[0] = 0, kv_len_out[b] =
+ *     kv_len[b] + n_new[b]: what bq_paged_kv_write and bq_paged_attn take,
+ *   taken[0] = pages taken from the front of free_pages, taken[1] = pages that
+ *     all sequences needed.
+ * A sequence that cannot grow gets nothing: its tokens' slots are -1,
+ * kv_len_out is kv_len, and bq_device_status reports it (BQ_ERR_INDEX). Such are
+ * those with a negative length, more tokens than max_pages * page_size or 2^31 -
+ * 1, tokens beyond n_slots, or pages beyond n_free; as pages are given out in
+ * order, all later sequences that need one get none either (taken[1] > n_free).
+ * q_start counts every token (saturating at 2^31 - 1). A page outside 0 ..
+ * n_pages - 1 in free_pages, or where the last page of a sequence is looked up,
+ * gives slots of -1 and is reported alike.
+ * kv_len, n_new (n_seqs), free_pages (n_free), page_table (n_seqs x max_pages),
+ * q_start (n_seqs + 1), kv_len_out (n_seqs), positions (n_slots, or NULL) and
+ * taken (2) are int32, slots (n_slots) int64, all on the DEVICE. One launch, no
+ * workspace.
+ * Limits: page_size a multiple of 16 up to 2^20; n_pages * page_size, n_slots
+ * and n_free below 2^31; n_seqs up to 2^20. Errors: BQ_ERR_SHAPE,
+ * BQ_ERR_ALIGN (4 bytes, slots 8), BQ_ERR_INVALID_ARG (null pointers, negative
+ * sizes, an output overlapping another argument). */
+int bq_paged_extend(int64_t page_size, int64_t n_pages, const int32_t *kv_len, const int32_t *n_new, int64_t n_seqs,
+                    const int32_t *free_pages, int64_t n_free, int32_t *page_table, int64_t max_pages, int32_t *q_start,
+                    int32_t *kv_len_out, int64_t *slots, int32_t *positions, int64_t n_slots, int32_t *taken);
+
+#define BQ_RMS_NORM_MAX_COLS 65536
+
+/* Root-mean-square norm of rows, with the residual's addition before it and an
+ * output in 8 bits after it:
+ *   h = x + residual, rounded to `elem` (x itself where residual is NULL);
+ *   y[c] = fp32(fp32(h[c] * f) * weight[c]), f = fp32(1 / sqrt(sum_c h[c]^2 / n_cols + eps));
+ *   sum = h (`elem`; NULL: not wanted; NULL too without a residual), out = y
+ *   rounded to `elem` (NULL: not wanted), q8 = y in Q8_0 blocks (NULL: not
+ *   wanted), n_cols / 32 per row, what bq_gemv_q8 and bq_gemm_q8 take.
+ * f is rounded once from a sum that is exact to about 2^-44, so that codes and
+ * scales are those of the definition but for a row in some 2^19 whose f lies
+ * that near to a border.
+ * x, residual, sum, out: n_rows rows of n_cols, row strides in elements (up to
+ * 2^40), rows 16-byte aligned; weight: n_cols fp32 (16-byte aligned); q8:
+ * contiguous, 16-byte aligned. sum may be x or residual themselves (the same
+ * pointer and stride), in place; other overlaps are refused. Rows are taken to be
+ * finite, |h| below 2^60, and y as by every quantizer here.
+ * Limits: n_cols a multiple of 32 up to BQ_RMS_NORM_MAX_COLS; n_rows below 2^31.
+ * Errors: BQ_ERR_UNSUPPORTED (element type), BQ_ERR_SHAPE, BQ_ERR_ALIGN,
+ * BQ_ERR_INVALID_ARG (null pointers, no output, eps not above 0 or not finite,
+ * negative sizes, overlaps, rows of an output overlapping each other). */
+int bq_add_rms_norm(int elem, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
+                    const float *weight, double eps, void *sum, int64_t sum_stride, void *out, int64_t out_stride,
+                    void *q8, int64_t n_rows, int64_t n_cols);
+
+/* bq_gemv and bq_gemm on activations that are in Q8_0 blocks already (a row's
+ * K / 32 blocks in a row; X_blocks N rows of them; 16-byte aligned): bit for bit
+ * what those calls give for the rows that were quantized. bq_gemv_q8 takes all
+ * weight types of bq_gemv and needs the workspace of bq_gemv_workspace_size;
+ * bq_gemm_q8 that of bq_workspace_size. Errors as there. */
+int bq_gemv_q8(int type, const void *W_blocks, const void *x_blocks, float *y, int64_t M, int64_t K);
+int bq_gemm_q8(int type, const void *W_blocks, const void *X_blocks, float *Y, int64_t M, int64_t N, int64_t K);
+
+/* Largest number of axes of bq_rotary. */
+#define BQ_ROTARY_MAX_AXES 16
+
+/* Rotary positions on several axes (time, height, width; one axis for text), q
+ * and k in one launch. Pair i of a head's first `rot` channels is turned by the
+ * angle positions[axis[i]][t] * inv_freq[i]:
+ *   a' = a cos - b sin, b' = a sin + b cos, (a, b) = channels (i, i + rot / 2),
+ *   or (2 i, 2 i + 1) if interleaved;
+ * the other channels are copied. inverse: by the opposite angle (back to where a
+ * row came from, and the gradient's turn). Angles are reduced in 64-bit fractions
+ * of a turn, so that far positions are as exact as near ones (2^-32 of a turn and
+ * |position| 2^-53); sine, cosine and products are fp32, and the result is rounded
+ * once to `elem_out`.
+ * q, k: [token][head][head_dim] of `elem`, q_out, k_out: of `elem_out`, the same
+ * type or, from fp32, any; token and head strides in elements, rows 16-byte
+ * aligned. An output may be its input itself (pointer, strides and type), in
+ * place; other overlaps are refused. k may be NULL with n_k_heads 0.
+ * positions: n_axes x n_tokens int32 (any sign), position_stride elements between
+ * axes; inv_freq: rot / 2 doubles, in radians per position; axis: rot / 2 int32,
+ * or NULL for axis 0 everywhere; all on the DEVICE. An axis outside 0 .. n_axes -
+ * 1 counts as 0 and is reported by bq_device_status (BQ_ERR_INDEX).
+ * Limits: head_dim a multiple of 32 up to 65536, rot even up to head_dim and
+ * 16384, n_axes 1 .. BQ_ROTARY_MAX_AXES, n_tokens below 2^31, up to 65536 heads.
+ * Errors: BQ_ERR_UNSUPPORTED (element types), BQ_ERR_SHAPE, BQ_ERR_ALIGN,
+ * BQ_ERR_INVALID_ARG. */
+int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t n_q_heads, const void *k,
+              int64_t k_token_stride, int64_t k_head_stride, int64_t n_k_heads, int elem_out, void *q_out,
+              int64_t q_out_token_stride, int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride,
+              int64_t k_out_head_stride, const int32_t *positions, int64_t position_stride, int64_t n_axes,
+              const double *inv_freq, const int32_t *axis, int64_t rot, int64_t head_dim, int64_t n_tokens,
+              int interleaved, int inverse);
+
+#define BQ_LORA_MAX_RANK 128
+#define BQ_LORA_MAX_ADAPTERS 4096
+
+/* Low-rank adapters of many requests beside a shared projection: token t of the
+ * batch has adapter a = adapter[t] (-1: none), and
+ *   out[t] = y[t] + scale[a] * B[a] (A[a] x[t]),   out[t] = y[t] without one
+ * (y NULL: nothing is added to). A: n_adapters x rank x K, B: n_adapters x M x
+ * rank, of `w_elem` (BQ_ELEM_F16 or BQ_ELEM_BF16), contiguous, 16-byte aligned;
+ * an adapter of a smaller rank is filled up with zeros. scale: n_adapters fp32,
+ * or NULL for 1. x: n_tokens rows of K of `x_elem`, y, out: of M of `y_elem`; each
+ * of these types is BQ_ELEM_F32 or w_elem. Row strides in elements; rows of x
+ * 16-byte aligned, y and out aligned to their element. out may be y itself (pointer
+ * and stride); other overlaps are refused. adapter: n_tokens int32 on the DEVICE, in
+ * any order; one outside -1 .. n_adapters - 1 counts as -1 and is reported by
+ * bq_device_status (BQ_ERR_INDEX).
+ * Accuracy: sums in fp32; fp32 rows enter the products in terms of 22 bits or
+ * more, 16-bit ones exactly; A x is kept in fp32 and enters the second product in
+ * terms of 22 bits (fp32 out) or 16 (16-bit out). A token's result does not depend
+ * on the other tokens of the batch but for the order of sums, which follows
+ * n_tokens, n_adapters and K; the same call gives the same bits.
+ * Needs a workspace of bq_lora_workspace_size(...) bytes (bq_set_workspace).
+ * Limits: rank a multiple of 8 up to BQ_LORA_MAX_RANK, K a multiple of 32, K and M
+ * below 2^24, n_tokens up to 2^20, n_adapters up to BQ_LORA_MAX_ADAPTERS. Errors:
+ * BQ_ERR_UNSUPPORTED (types), BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_INVALID_ARG,
+ * BQ_ERR_WORKSPACE. */
+int bq_lora(int x_elem, const void *x, int64_t x_stride, int w_elem, const void *A, const void *B, const float *scale,
+            int64_t n_adapters, int64_t rank, const int32_t *adapter, int y_elem, const void *y, int64_t y_stride,
+            void *out, int64_t out_stride, int64_t n_tokens, int64_t M, int64_t K);
+size_t bq_lora_workspace_size(int64_t n_tokens, int64_t n_adapters, int64_t rank, int64_t K, int64_t M);
+
 /* Test export: out[m][b] = int32 dot of W block (m, b) (type Q4_0 or Q8_0)
  * with the Q8_0 block b of xq, computed by the same device code as bq_gemv's
  * inner loop. out: M x K/32 int32. */
@@ -482,7 +619,8 @@ int bq_block_values(int type);
 
 /* Synchronize the calling thread's stream, then report and clear one kind of
  * error from the device error word: BQ_ERR_TIMEOUT if a bounded wait ran out,
- * else BQ_ERR_INDEX if a slot, page or length of a paged cache was out of range,
+ * else BQ_ERR_INDEX if a slot, page or length of a paged cache (or an adapter of
+ * bq_lora, an axis of bq_rotary) was out of range,
  * else BQ_OK (where both happened, two calls report them). BQ_ERR_CUDA if the
  * synchronization itself failed. */
 int bq_device_status(void);
