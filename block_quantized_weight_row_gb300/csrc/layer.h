@@ -16,7 +16,10 @@ struct ExtendArgs {
   uint32_t page_size, n_pages, n_free, n_slots;
   uint32_t max_tokens;  // a sequence's longest length: the table's, and below 2^31
   int n_seqs;
-  bool wide;  // slots and positions allow stores of two (set by the launcher)
+  // set by the launcher:
+  bool wide;            // slots and positions allow stores of two
+  int page_shift;       // log2(page_size), or -1
+  uint64_t page_magic;  // ceil(2^64 / (page_size / 16))
   unsigned *err;
 };
 cudaError_t launch_paged_extend(ExtendArgs a, cudaStream_t stream);

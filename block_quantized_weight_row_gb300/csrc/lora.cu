@@ -279,13 +279,58 @@ __device__ __forceinline__ void shrink_step(float (&acc)[NT][4], const RowWords<
   }
 }
 
-// NT: n-tiles of 8 ranks (rank <= 8 NT). TM = 64: a warp has 16 of the tile's
-// tokens and all of the CTA's k; TM = 16: all of them and a quarter of the k.
-template <int XE, int WE, int TM, int NT>
-__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const LoraArgs a, const Work w, const int splits) {
-  __shared__ __align__(16) float part[4][16][8 * NT];  // written in pairs
-  __shared__ int rows[TM];
+// A cluster's sums of a tile: each of its CTAs adds up its share, over the CTAs
+// and, for tiles of 16, their four warps, in order. part: [4][16][8 NT] of every
+// CTA; a tile of 64 has its rows there in order.
+template <int TM, int NT>
+__device__ __forceinline__ void sum_tile(const LoraArgs &a, const Work &w, float *part, const int *rows, int ad, int count, int split, int splits) {
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
+  const int n = count * a.rank;
+  for (int e = split * kShrinkThreads + threadIdx.x; e < n; e += splits * kShrinkThreads) {
+    const int row = e / a.rank, r = e - row * a.rank;
+    float sum = 0.0f;
+    for (int c = 0; c < splits; ++c) {
+      const float *p = cluster.map_shared_rank(part, c);
+      if constexpr (TM == 64) {
+        sum += p[row * (8 * NT) + r];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum += p[(q * 16 + row) * (8 * NT) + r];
+      }
+    }
+    w.H[int64_t(rows[row]) * a.rank + r] = sum * s;
+  }
+  cluster.sync();  // the others' sums are read from here until now
+}
+
+// total += acc, acc = 0: the tensor instructions' adder truncates, so chains are kept short
+template <int NT>
+__device__ __forceinline__ void take(float (&total)[NT][4], float (&acc)[NT][4]) {
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) total[nt][i] += acc[nt][i], acc[nt][i] = 0.0f;
+}
+template <int NT>
+__device__ __forceinline__ void put(float *part, const float (&v)[NT][4], int g, int t) {  // a warp's 16 rows, in pairs
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    *reinterpret_cast<float2 *>(part + g * (8 * NT) + nt * 8 + 2 * t) = make_float2(v[nt][0], v[nt][1]);
+    *reinterpret_cast<float2 *>(part + (g + 8) * (8 * NT) + nt * 8 + 2 * t) = make_float2(v[nt][2], v[nt][3]);
+  }
+}
+
+// Tiles of 16 tokens; NT: n-tiles of 8 ranks (rank <= 8 NT). Each warp has all of
+// the tile's tokens and a quarter of the CTA's k, and loads its operands itself:
+// in a decode step a warp has four blocks of 32 k, all in flight at once.
+template <int XE, int WE, int NT>
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs a, const Work w, const int splits) {
+  __shared__ __align__(16) float part[4][16][8 * NT];
+  __shared__ int rows[16];
   constexpr int XS = Elem<XE>::kBytes;
+  constexpr int kAhead = NT <= 4 ? 4 : NT == 8 ? 2 : 1;  // blocks in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   if (w.sorted) {
@@ -295,59 +340,146 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink(const LoraArgs a
     if (id < -1 || id >= a.n_adapters) atomicOr(a.err, kErrIndex);
   }
   int ad, count;
-  if (!find_tile<TM>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
-  const int nb = a.K / 32, split = blockIdx.x;
-  const int pieces = TM == 16 ? splits * 4 : splits, piece = TM == 16 ? split * 4 + warp : split;
+  if (!find_tile<16>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
+  const int nb = a.K / 32, split = blockIdx.x, pieces = splits * 4, piece = split * 4 + warp;
   const int k0 = int(int64_t(nb) * piece / pieces), k1 = int(int64_t(nb) * (piece + 1) / pieces);
-  const int r0 = TM == 64 ? warp * 16 : 0;
-  const bool idle = r0 >= count;  // no token in this warp's rows
-  const uint8_t *lo = a.x + rows[r0 + g] * a.x_row + t * 8 * XS, *hi = a.x + rows[r0 + g + 8] * a.x_row + t * 8 * XS;
+  const uint8_t *lo = a.x + rows[g] * a.x_row + t * 8 * XS, *hi = a.x + rows[g + 8] * a.x_row + t * 8 * XS;
   const uint8_t *ap = a.A + (int64_t(ad) * a.rank + g) * a.K * 2 + t * 16;
-  float acc[NT][4];
+  const bool high = count > 8;
+  float acc[NT][4] = {}, total[NT][4] = {};
+  for (int k = k0; k < k1; k += kAhead) {
+    RowWords<XE> xl[kAhead], xh[kAhead];
+    uint4 bw[kAhead][NT];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int u = 0; u < kAhead; ++u)
+      if (k + u < k1) {
+        xl[u].load(lo + int64_t(k + u) * 32 * XS);
+        xh[u] = xl[u];
+        if (high) xh[u].load(hi + int64_t(k + u) * 32 * XS);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[nt][i] = 0.0f;
-  if (!idle) {
-#pragma unroll 2
-    for (int k = k0; k < k1; ++k) {
-      RowWords<XE> xl, xh;
-      uint4 bw[NT];
-      xl.load(lo + int64_t(k) * 32 * XS);
-      xh.load(hi + int64_t(k) * 32 * XS);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        bw[nt] = make_uint4(0, 0, 0, 0);
-        if (nt * 8 < a.rank) bw[nt] = __ldg(reinterpret_cast<const uint4 *>(ap + (int64_t(nt) * 8 * a.K + k * 32) * 2));
+        for (int nt = 0; nt < NT; ++nt) {
+          bw[u][nt] = make_uint4(0, 0, 0, 0);
+          if (nt * 8 < a.rank) bw[u][nt] = __ldg(reinterpret_cast<const uint4 *>(ap + (int64_t(nt) * 8 * a.K + (k + u) * 32) * 2));
+        }
       }
-      shrink_step<XE, WE, NT>(acc, xl, xh, bw);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (k + u < k1) shrink_step<XE, WE, NT>(acc, xl[u], xh[u], bw[u]);
+    take(total, acc);
+  }
+  put<NT>(&part[warp][0][0], total, g, t);
+  sum_tile<16, NT>(a, w, &part[0][0][0], rows, ad, count, split, splits);
+}
+
+// Tiles of 64 tokens: each of the four warps has 16 of them and all of the CTA's
+// k. Rows of x and of the adapter come through a ring of stages of 64 k by
+// asynchronous copies (straight loads left a warp waiting for memory in every
+// block of 32 k: 60 us for 2048 tokens of 4096 at rank 64).
+// A stage: two blocks of 32 k, each a row of 64 bytes per token and rank (fp32
+// rows: 128 bytes, the even 16-byte pieces in one half, which half alternates
+// from row to row), so that a quarter-warp's reads of two rows meet no bank twice.
+template <int XE, int NT>
+struct Ring {
+  static constexpr int kStages = 4;
+  static constexpr int kXRow = 32 * Elem<XE>::kBytes, kXBlock = 64 * kXRow, kABlock = 8 * NT * 64;
+  static constexpr int kStage = 2 * (kXBlock + kABlock);
+  static constexpr int kBytes = kStages * kStage > 64 * 8 * NT * 4 ? kStages * kStage : 64 * 8 * NT * 4;  // or the sums, afterwards
+};
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+
+template <int XE, int WE, int NT>
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs a, const Work w, const int splits) {
+  using R = Ring<XE, NT>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ int rows[64];
+  constexpr int XS = Elem<XE>::kBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  pdl_launch_dependents();
+  pdl_wait();
+  int ad, count;
+  if (!find_tile<64>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
+  const int nb = a.K / 32, split = blockIdx.x;
+  const int k0 = int(int64_t(nb) * split / splits), k1 = int(int64_t(nb) * (split + 1) / splits);
+  const int stages = (k1 - k0 + 1) / 2;
+  // a thread copies one 16-byte piece of every kStep-th row; rows without a
+  // token (or a rank) are left out: what they hold reaches only their own sums
+  constexpr int kPieces = 2 * R::kXRow / 16, kStep = kShrinkThreads / kPieces, kRows = 64 / kStep;
+  const int xp = tid % kPieces, xr = tid / kPieces, xb = xp / (kPieces / 2), xc = xp % (kPieces / 2);
+  const uint8_t *src[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) src[i] = a.x + rows[xr + i * kStep] * a.x_row + (int64_t(k0) * 32) * XS + xp * 16;
+  const int ap = tid % 8, ar = tid / 8;  // 8 pieces of 64 k, 16 ranks at a time
+  const uint8_t *asrc = a.A + (int64_t(ad) * a.rank + ar) * a.K * 2 + int64_t(k0) * 64 + ap * 16;
+  auto fill = [&](int s) {
+    uint8_t *x = ring + (s % R::kStages) * R::kStage, *ad_rows = x + 2 * R::kXBlock;
+    if (k0 + 2 * s + xb < k1) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = xr + i * kStep;
+        const int at = XE == kElemF32 ? (xc >> 1) + 4 * ((xc & 1) ^ (r & 1)) : xc;
+        if (r < count) copy16(x + xb * R::kXBlock + r * R::kXRow + at * 16, src[i] + int64_t(s) * 64 * XS);
+      }
+    }
+    if (k0 + 2 * s + ap / 4 < k1) {
+#pragma unroll
+      for (int i = 0; i < (NT + 1) / 2; ++i) {
+        const int r = ar + 16 * i;
+        if (r < a.rank) copy16(ad_rows + (ap / 4) * R::kABlock + r * 64 + (ap % 4) * 16, asrc + (int64_t(i) * 16 * a.K + s * 64) * 2);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int s = 0; s < R::kStages - 1; ++s) {
+    if (s < stages)
+      fill(s);
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  const int r0 = warp * 16;
+  const bool idle = r0 >= count;  // no token in this warp's rows
+  float acc[NT][4] = {}, total[NT][4] = {};
+  for (int s = 0; s < stages; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::kStages - 2) : "memory");
+    __syncthreads();  // the stage is there, and the one before it is used up
+    if (s + R::kStages - 1 < stages)
+      fill(s + R::kStages - 1);
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    if (!idle) {
+      const uint8_t *x = ring + (s % R::kStages) * R::kStage, *ad_rows = x + 2 * R::kXBlock;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (k0 + 2 * s + b >= k1) break;
+        RowWords<XE> xl, xh;
+        uint4 bw[NT];
+        const uint8_t *pl = x + b * R::kXBlock + (r0 + g) * R::kXRow, *ph = pl + 8 * R::kXRow;
+        if constexpr (XE == kElemF32) {
+          const int first = (g & 1) * 64 + t * 16;  // rows g and g + 8 are both even or both odd
+          xl.v[0] = *reinterpret_cast<const uint4 *>(pl + first);
+          xl.v[1] = *reinterpret_cast<const uint4 *>(pl + (first ^ 64));
+          xh.v[0] = *reinterpret_cast<const uint4 *>(ph + first);
+          xh.v[1] = *reinterpret_cast<const uint4 *>(ph + (first ^ 64));
+        } else {
+          xl.v[0] = *reinterpret_cast<const uint4 *>(pl + t * 16);
+          xh.v[0] = *reinterpret_cast<const uint4 *>(ph + t * 16);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) bw[nt] = *reinterpret_cast<const uint4 *>(ad_rows + b * R::kABlock + (nt * 8 + g) * 64 + t * 16);
+        shrink_step<XE, WE, NT>(acc, xl, xh, bw);
+      }
+      if (s & 1) take(total, acc);
     }
   }
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    *reinterpret_cast<float2 *>(&part[warp][g][nt * 8 + 2 * t]) = make_float2(acc[nt][0], acc[nt][1]);
-    *reinterpret_cast<float2 *>(&part[warp][g + 8][nt * 8 + 2 * t]) = make_float2(acc[nt][2], acc[nt][3]);
-  }
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  // each CTA of the cluster adds up its share of the tile's sums
-  const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
-  const int n = count * a.rank;
-  for (int e = split * kShrinkThreads + threadIdx.x; e < n; e += splits * kShrinkThreads) {
-    const int row = e / a.rank, r = e - row * a.rank;
-    float sum = 0.0f;
-    for (int c = 0; c < splits; ++c) {
-      const float *p = cluster.map_shared_rank(&part[0][0][0], c);
-      if constexpr (TM == 64) {
-        sum += p[row * (8 * NT) + r];  // warp row / 16, its row row % 16
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum += p[(q * 16 + row) * (8 * NT) + r];
-      }
-    }
-    w.H[int64_t(rows[row]) * a.rank + r] = sum * s;
-  }
-  cluster.sync();  // the others' sums are read from here until now
+  take(total, acc);
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // the ring becomes the sums' place
+  float *part = reinterpret_cast<float *>(ring);
+  put<NT>(part + r0 * (8 * NT), total, g, t);
+  sum_tile<64, NT>(a, w, part, rows, ad, count, split, splits);
 }
 
 // ---------------------------------------------------------------- expand --
@@ -409,7 +541,7 @@ struct Expand {
 };
 
 template <int WE, int YE, int TM, int KB>
-__global__ void __launch_bounds__(kExpandThreads) k_lora_expand(const LoraArgs a, const Work w, const int turns) {
+__global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArgs a, const Work w, const int turns) {
   constexpr int MT = TM == 64 ? 2 : 1, WM = TM == 64 ? 4 : 8;
   constexpr int kTerms = Expand<WE, YE, TM, KB>::kTerms, kPitch = Expand<WE, YE, TM, KB>::kPitch;
   constexpr int YS = Elem<YE>::kBytes;
@@ -585,13 +717,20 @@ cudaError_t launch_ex(void (*fn)(P...), dim3 grid, int threads, int smem, int cl
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+template <int XE, int WE, int TM, int NT>
+cudaError_t shrink_nt(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
+  const dim3 grid(unsigned(p.splits), unsigned(p.tiles));
+  if constexpr (TM == 64)
+    return launch_ex(k_lora_shrink64<XE, WE, NT>, grid, kShrinkThreads, Ring<XE, NT>::kBytes, p.splits, true, s, a, w, p.splits);
+  else
+    return launch_ex(k_lora_shrink16<XE, WE, NT>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+}
 template <int XE, int WE, int TM>
 cudaError_t shrink(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
-  const dim3 grid(unsigned(p.splits), unsigned(p.tiles));
-  if (a.rank <= 16) return launch_ex(k_lora_shrink<XE, WE, TM, 2>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
-  if (a.rank <= 32) return launch_ex(k_lora_shrink<XE, WE, TM, 4>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
-  if (a.rank <= 64) return launch_ex(k_lora_shrink<XE, WE, TM, 8>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
-  return launch_ex(k_lora_shrink<XE, WE, TM, 16>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+  if (a.rank <= 16) return shrink_nt<XE, WE, TM, 2>(a, w, p, s);
+  if (a.rank <= 32) return shrink_nt<XE, WE, TM, 4>(a, w, p, s);
+  if (a.rank <= 64) return shrink_nt<XE, WE, TM, 8>(a, w, p, s);
+  return shrink_nt<XE, WE, TM, 16>(a, w, p, s);
 }
 
 template <int WE, int YE, int TM>

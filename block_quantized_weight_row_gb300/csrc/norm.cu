@@ -13,6 +13,11 @@
 // exact sum with a probability around 2^-19 per row. (Doubles would give the
 // same, at 1/64 of the rate: 4096 of them per row take longer than the row's
 // memory time.)
+//
+// Bound by HBM and, with 16-bit rows, by instruction issue: a row stays in
+// registers from its load to its last output, values go through in pairs (packed
+// fp32 instructions), and the 34-byte blocks are put together in shared memory,
+// from where they leave in 16-byte stores.
 #include <algorithm>
 
 #include "bq_device.cuh"
@@ -54,131 +59,204 @@ __device__ __forceinline__ float factor(Two s, const NormArgs &a) {
   return __fmaf_rn(r, 0.5f * __fsub_rn(__fsub_rn(1.0f, p), pl), r);
 }
 
-// 8 values of a row as fp32
+// Two such sums at once
+struct Two2 {
+  uint64_t h, l;
+};
+__device__ __forceinline__ uint64_t two(float x) { return pack2(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float(uint32_t(v)); }
+__device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
+__device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) { return ffma2(two(-1.0f), b, a); }
+
+// 8 values of a row as pairs
 template <int ELEM>
-__device__ __forceinline__ void load8(const uint8_t *p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const uint8_t *p, uint64_t (&v)[4]) {
   if constexpr (ELEM == kElemF32) {
     const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    v[0] = pack2(__float_as_uint(a.x), __float_as_uint(a.y)), v[1] = pack2(__float_as_uint(a.z), __float_as_uint(a.w));
+    v[2] = pack2(__float_as_uint(b.x), __float_as_uint(b.y)), v[3] = pack2(__float_as_uint(b.z), __float_as_uint(b.w));
   } else {
     const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = unpack_pair<ELEM>(w[i]);
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      v[i] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
     }
   }
 }
 template <int ELEM>
-__device__ __forceinline__ void store8(uint8_t *p, const float (&v)[8]) {
+__device__ __forceinline__ void store8(uint8_t *p, const uint64_t (&v)[4]) {
   if constexpr (ELEM == kElemF32) {
-    *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *(reinterpret_cast<float4 *>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+    *reinterpret_cast<float4 *>(p) = make_float4(lo(v[0]), hi(v[0]), lo(v[1]), hi(v[1]));
+    *(reinterpret_cast<float4 *>(p) + 1) = make_float4(lo(v[2]), hi(v[2]), lo(v[3]), hi(v[3]));
   } else {
-    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_pair<ELEM>(v[0], v[1]), pack_pair<ELEM>(v[2], v[3]),
-                                               pack_pair<ELEM>(v[4], v[5]), pack_pair<ELEM>(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_pair<ELEM>(lo(v[0]), hi(v[0])), pack_pair<ELEM>(lo(v[1]), hi(v[1])),
+                                               pack_pair<ELEM>(lo(v[2]), hi(v[2])), pack_pair<ELEM>(lo(v[3]), hi(v[3])));
   }
 }
-// rounded to the rows' type
-template <int ELEM>
-__device__ __forceinline__ void round8(float (&v)[8]) {
-  if constexpr (ELEM != kElemF32) {
+
+// 8 codes as two words of bytes: the rule of quantize_block_lane, exact per value
+__device__ __forceinline__ void codes8(const uint64_t (&v)[4], float ds, float inv, uint32_t &w0, uint32_t &w1) {
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  uint32_t t[8];
+  float far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t r = fmul2(v[i], two(inv)), q = fadd2(r, two(kMagic)), e = fsub2(r, fadd2(q, two(-kMagic)));
+    t[2 * i] = uint32_t(q);
+    t[2 * i + 1] = uint32_t(q >> 32);
+    far = fmaxf(far, fmaxf(fabsf(lo(e)), fabsf(hi(e))));
+  }
+  if (far > 0.4999f || (ds > 0.0f && ds < 6.103515625e-05f)) {  // rare: near a tie, or a subnormal scale
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_pair<ELEM>(pack_pair<ELEM>(v[2 * i], v[2 * i + 1]));
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+      t[2 * i] = uint32_t(code_of<kTypeQ8_0>(lo(v[i]), ds, inv));
+      t[2 * i + 1] = uint32_t(code_of<kTypeQ8_0>(hi(v[i]), ds, inv));
     }
   }
+  w0 = pack_bytes(t[0], t[1], t[2], t[3]);
+  w1 = pack_bytes(t[4], t[5], t[6], t[7]);
 }
 
 // A row by blockDim.x threads, blockDim.y rows per CTA (more than one only
 // where a warp has a row); a thread has U units of 8 values, 4 lanes a block.
 template <int ELEM, int U>
-__global__ void __launch_bounds__(1024) k_add_rms_norm(const NormArgs a) {
+__global__ void __launch_bounds__(U == 4 ? 128 : 1024, 1) k_add_rms_norm(const NormArgs a) {
   __shared__ Two part[32];
+  extern __shared__ __align__(16) uint8_t staged[];  // the rows' blocks, each row as far past 16 bytes as in q8
   constexpr int ES = Elem<ELEM>::kBytes;
-  const int n_units = a.n_cols / 8, step = blockDim.x;
+  const int n_units = a.n_cols / 8, step = blockDim.x, lane = threadIdx.x & 31;
   const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
   if (row >= a.n_rows) return;  // whole warps; with several warps per row there is one row per CTA
-  float v[U][8];
+  uint64_t v[U][4];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int unit = threadIdx.x + u * step;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
+    for (int i = 0; i < 4; ++i) v[u][i] = 0;
     if (unit < n_units) load8<ELEM>(a.x + row * a.x_row + int64_t(unit) * 8 * ES, v[u]);
   }
   if (a.res) {
-    float r[U][8];
+    constexpr int kAhead = U < 4 ? U : 4;  // units whose residual is in flight
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int unit = threadIdx.x + u * step;
-      if (unit < n_units) load8<ELEM>(a.res + row * a.res_row + int64_t(unit) * 8 * ES, r[u]);
-    }
+    for (int u0 = 0; u0 < U; u0 += kAhead) {
+      uint64_t r[kAhead][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int unit = threadIdx.x + u * step;
-      if (unit < n_units) {
+      for (int k = 0; k < kAhead; ++k) {
+        const int unit = threadIdx.x + (u0 + k) * step;
+        if (unit < n_units) load8<ELEM>(a.res + row * a.res_row + int64_t(unit) * 8 * ES, r[k]);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] = __fadd_rn(v[u][i], r[u][i]);
-        round8<ELEM>(v[u]);
-        if (a.sum) store8<ELEM>(a.sum + row * a.sum_row + int64_t(unit) * 8 * ES, v[u]);
+      for (int k = 0; k < kAhead; ++k) {
+        const int unit = threadIdx.x + (u0 + k) * step;
+        uint64_t(&w)[4] = v[u0 + k];
+        if (unit < n_units) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = fadd2(w[i], r[k][i]);
+            if constexpr (ELEM != kElemF32) {
+              const float2 f = unpack_pair<ELEM>(pack_pair<ELEM>(lo(w[i]), hi(w[i])));
+              w[i] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+            }
+          }
+          if (a.sum) store8<ELEM>(a.sum + row * a.sum_row + int64_t(unit) * 8 * ES, w);
+        }
       }
     }
   }
-  Two s{0.0f, 0.0f};
+  Two2 s2{0, 0};
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = __fmul_rn(v[u][i], v[u][i]);
-      const Two t = two_sum(s.h, p);
+    for (int i = 0; i < 4; ++i) {
+      const uint64_t p = fmul2(v[u][i], v[u][i]);
+      const uint64_t sum = fadd2(s2.h, p), t = fsub2(sum, s2.h);
+      uint64_t e = fadd2(fsub2(s2.h, fsub2(sum, t)), fsub2(p, t));
       // a 16-bit type's square has no error (22 bits at most)
-      s = Two{t.h, __fadd_rn(s.l, ELEM == kElemF32 ? __fadd_rn(t.l, __fmaf_rn(v[u][i], v[u][i], -p)) : t.l)};
+      if constexpr (ELEM == kElemF32) e = fadd2(e, ffma2(v[u][i], v[u][i], fsub2(0, p)));
+      s2 = Two2{sum, fadd2(s2.l, e)};
     }
-  s = add(s, Two{0.0f, 0.0f});
+  Two s = add(Two{lo(s2.h), lo(s2.l)}, Two{hi(s2.h), hi(s2.l)});
 #pragma unroll
   for (int d = 16; d; d >>= 1) s = add(s, Two{__shfl_xor_sync(kFull, s.h, d), __shfl_xor_sync(kFull, s.l, d)});
   if (step > 32) {
     const int warp = threadIdx.x >> 5, warps = step >> 5;
-    if ((threadIdx.x & 31) == 0) part[warp] = s;
+    if (lane == 0) part[warp] = s;
     __syncthreads();
-    s = part[0];
-    for (int w = 1; w < warps; ++w) s = add(s, part[w]);
+    s = lane < warps ? part[lane] : Two{0.0f, 0.0f};
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s = add(s, Two{__shfl_xor_sync(kFull, s.h, d), __shfl_xor_sync(kFull, s.l, d)});
   }
   const float f = factor(s, a);
+  const int row_bytes = a.n_cols / kQK * Fmt<kTypeQ8_0>::kBytes;
+  uint8_t *const q8 = a.q8 + row * row_bytes;
+  const bool words = row_bytes % 4 == 0;  // an even number of blocks: rows of whole words
+  const int shift = words ? int(reinterpret_cast<uintptr_t>(q8) & 15) : 0;
+  uint8_t *const stage = staged + threadIdx.y * ((row_bytes + 32) / 16 * 16) + shift;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     const int unit = threadIdx.x + u * step;
-    const bool live = unit < n_units;  // the same for the 4 lanes of a block
+    const bool live = unit < n_units;  // the same for the 4 lanes of a block, and with words for those of two
     float m = 0.0f;
     if (live) {
       const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * unit), w1 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * unit + 1);
-      const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+      const uint64_t w[4] = {pack2(__float_as_uint(w0.x), __float_as_uint(w0.y)), pack2(__float_as_uint(w0.z), __float_as_uint(w0.w)),
+                             pack2(__float_as_uint(w1.x), __float_as_uint(w1.y)), pack2(__float_as_uint(w1.z), __float_as_uint(w1.w))};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[u][i] = __fmul_rn(__fmul_rn(v[u][i], f), w[i]);
-        m = fmaxf(m, fabsf(v[u][i]));
+      for (int i = 0; i < 4; ++i) {
+        v[u][i] = fmul2(fmul2(v[u][i], two(f)), w[i]);
+        m = fmaxf(m, fmaxf(fabsf(lo(v[u][i])), fabsf(hi(v[u][i]))));
       }
       if (a.out) store8<ELEM>(a.out + row * a.out_row + int64_t(unit) * 8 * ES, v[u]);
     }
     if (a.q8) {
       m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
       m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-      if (live) {
-        uint16_t bits;
-        float ds;
-        block_scale<kTypeQ8_0>(m, bits, ds);
-        const float inv = ds > 0.0f ? rcp_approx(ds) : 0.0f;
-        uint32_t c[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) c[i] = uint32_t(code_of<kTypeQ8_0>(v[u][i], ds, inv));
-        uint16_t *block = reinterpret_cast<uint16_t *>(a.q8 + (row * (a.n_cols / kQK) + unit / 4) * Fmt<kTypeQ8_0>::kBytes);
+      uint16_t bits;
+      float ds;
+      block_scale<kTypeQ8_0>(m, bits, ds);
+      uint32_t w0, w1;
+      codes8(v[u], ds, ds > 0.0f ? rcp_approx(ds) : 0.0f, w0, w1);
+      if (words) {
+        // two blocks are 17 words: those of the first lie two bytes off its codes
+        const uint32_t before = __shfl_up_sync(kFull, w1 >> 16, 1);
+        const int j = unit & 7;
+        if (live) {
+          uint32_t *pair = reinterpret_cast<uint32_t *>(stage + unit / 8 * 68);
+          if (j < 4) {
+            pair[2 * j] = (j == 0 ? bits : before) | w0 << 16;
+            pair[2 * j + 1] = __funnelshift_r(w0, w1, 16);
+          } else {
+            if (j == 4) pair[8] = before | uint32_t(bits) << 16;
+            pair[2 * j + 1] = w0;
+            pair[2 * j + 2] = w1;
+          }
+        }
+      } else if (live) {
+        uint16_t *block = reinterpret_cast<uint16_t *>(q8 + unit / 4 * Fmt<kTypeQ8_0>::kBytes);
         const int j = unit & 3;
         if (j == 0) block[0] = bits;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) block[1 + 4 * j + i] = uint16_t((c[2 * i] & 255) | (c[2 * i + 1] << 8));
+        block[1 + 4 * j] = uint16_t(w0);
+        block[2 + 4 * j] = uint16_t(w0 >> 16);
+        block[3 + 4 * j] = uint16_t(w1);
+        block[4 + 4 * j] = uint16_t(w1 >> 16);
+      }
+    }
+  }
+  if (a.q8 && words) {
+    if (step > 32)
+      __syncthreads();
+    else
+      __syncwarp();
+    const uint8_t *from = stage - shift;
+    uint8_t *to = q8 - shift;
+    for (int i = threadIdx.x * 16; i < shift + row_bytes; i += step * 16) {
+      if (i >= shift && i + 16 <= shift + row_bytes) {
+        *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
+      } else {
+        for (int k = i; k < i + 16; k += 4)
+          if (k >= shift && k < shift + row_bytes) *reinterpret_cast<uint32_t *>(to + k) = *reinterpret_cast<const uint32_t *>(from + k);
       }
     }
   }
@@ -186,26 +264,35 @@ __global__ void __launch_bounds__(1024) k_add_rms_norm(const NormArgs a) {
 
 template <int ELEM, int U>
 cudaError_t launch(const NormArgs &a, int threads, int rows, cudaStream_t stream) {
-  k_add_rms_norm<ELEM, U><<<unsigned((a.n_rows + rows - 1) / rows), dim3(threads, rows), 0, stream>>>(a);
+  const int row_bytes = a.n_cols / kQK * Fmt<kTypeQ8_0>::kBytes;
+  const int smem = a.q8 && row_bytes % 4 == 0 ? rows * ((row_bytes + 32) / 16 * 16) : 0;
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_add_rms_norm<ELEM, U>), smem);
+  if (e != cudaSuccess) return e;
+  k_add_rms_norm<ELEM, U><<<unsigned((a.n_rows + rows - 1) / rows), dim3(threads, rows), smem, stream>>>(a);
   return cudaGetLastError();
 }
 
 template <int ELEM>
-cudaError_t launch_elem(const NormArgs &a, cudaStream_t stream) {
+cudaError_t launch_elem(const NormArgs &a, int sms, cudaStream_t stream) {
   const int units = a.n_cols / 8;
+  auto threads = [&](int u) { return (units + 32 * u - 1) / (32 * u) * 32; };  // whole warps, u units each
   if (units <= 32) return launch<ELEM, 1>(a, 32, 4, stream);
+  // few rows: a row's latency counts, so one unit per thread
+  if (a.n_rows <= 2 * sms && threads(1) <= 1024) return launch<ELEM, 1>(a, threads(1), 1, stream);
   if (units <= 128) return launch<ELEM, 4>(a, 32, 4, stream);
-  const int t4 = (units + 127) / 128 * 32;  // threads for 4 units each, whole warps
-  if (t4 <= 1024) return launch<ELEM, 4>(a, t4, 1, stream);
+  if (threads(2) <= 1024) return launch<ELEM, 2>(a, threads(2), 1, stream);
   return launch<ELEM, 8>(a, 1024, 1, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_add_rms_norm(int elem, const NormArgs &a, cudaStream_t stream) {
-  if (elem == kElemF32) return launch_elem<kElemF32>(a, stream);
-  if (elem == kElemF16) return launch_elem<kElemF16>(a, stream);
-  return launch_elem<kElemBF16>(a, stream);
+  cudaError_t err;
+  const DeviceInfo *di = device_info(&err);
+  if (!di) return err;
+  if (elem == kElemF32) return launch_elem<kElemF32>(a, di->sm_count, stream);
+  if (elem == kElemF16) return launch_elem<kElemF16>(a, di->sm_count, stream);
+  return launch_elem<kElemBF16>(a, di->sm_count, stream);
 }
 
 }  // namespace bq
