@@ -18,7 +18,7 @@
 // over k may be taken in any order, so lane t of a quad gives its instruction the
 // 8 consecutive k 8t .. 8t + 7 of 32 in place of the pairs of its layout, of both
 // operands alike. For the second product the columns are permuted too, so that a
-// lane's results over four n-tiles are 8 consecutive columns of out.
+// lane's results over four n-tiles are whole 16-byte pieces of out.
 //
 // Terms. A 16-bit row meets adapters of its own type: products are exact. An fp32
 // row beside bf16 adapters is cut into three bf16 terms (its 24 bits, exact),
@@ -73,16 +73,28 @@ __global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, 
   pdl_launch_dependents();
   for (int b = tid; b < bins; b += kGroupThreads) count[b] = 0;
   __syncthreads();
+  // the loads of kIds rounds are in flight together; whole warps, as the votes need them
+  constexpr int kIds = 4;
+  auto each = [&](auto f) {
+#pragma unroll 1
+    for (int t0 = tid; t0 - tid < a.n_tokens; t0 += kIds * kGroupThreads) {
+      int id[kIds];
+#pragma unroll
+      for (int i = 0; i < kIds; ++i) id[i] = t0 + i * kGroupThreads < a.n_tokens ? __ldg(a.adapter + t0 + i * kGroupThreads) : -1;
+#pragma unroll
+      for (int i = 0; i < kIds; ++i) {
+        const int t = t0 + i * kGroupThreads;
+        const int bin = t >= a.n_tokens ? -1 : uint32_t(id[i]) < uint32_t(a.n_adapters) ? id[i] + 1 : 0;
+        // tokens in runs: one atomic for a warp; else one per token, whose collisions are few
+        f(t, id[i], bin, __all_sync(kFull, bin == __shfl_sync(kFull, bin, 0)));
+      }
+    }
+  };
   bool bad = false;
-  for (int t0 = 0; t0 < a.n_tokens; t0 += kGroupThreads) {  // whole warps: the votes need them
-    const int t = t0 + tid;
-    const bool live = t < a.n_tokens;
-    const int id = live ? __ldg(a.adapter + t) : -2;
-    const int bin = uint32_t(id) < uint32_t(a.n_adapters) ? id + 1 : 0;
-    bad |= live && bin == 0 && id != -1;
-    const unsigned same = __match_any_sync(kFull, live ? bin : -1);
-    if (live && lane == __ffs(same) - 1) atomicAdd(&count[bin], __popc(same));
-  }
+  each([&](int, int id, int bin, bool all) {
+    bad |= bin == 0 && id != -1;
+    if (bin >= 0 && (lane == 0 || !all)) atomicAdd(&count[bin], all ? 32 : 1);
+  });
   if (bad) atomicOr(a.err, kErrIndex);
   __syncthreads();
   // exclusive sums over the bins of tokens and of tiles, a run of bins per thread
@@ -119,17 +131,12 @@ __global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, 
     w.tiles[i] = Tile{lo - 1, first, min(TM, end - first), 0};
   }
   __syncthreads();
-  for (int t0 = 0; t0 < a.n_tokens; t0 += kGroupThreads) {
-    const int t = t0 + tid;
-    const bool live = t < a.n_tokens;
-    const int bin = live ? adapter_of(a, t) + 1 : -1;
-    const unsigned same = __match_any_sync(kFull, bin);
-    const int leader = __ffs(same) - 1;
+  each([&](int t, int, int bin, bool all) {
     int at = 0;
-    if (live && lane == leader) at = atomicAdd(&count[bin], __popc(same));
-    at = __shfl_sync(kFull, at, leader) + __popc(same & ((1u << lane) - 1));
-    if (live) w.sorted[at] = t;
-  }
+    if (bin >= 0 && (lane == 0 || !all)) at = atomicAdd(&count[bin], all ? 32 : 1);
+    if (all) at = __shfl_sync(kFull, at, 0) + lane;
+    if (bin >= 0) w.sorted[at] = t;
+  });
 }
 
 // The tokens of tile `index` into rows[] (those beyond the count repeat the
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
 // from row to row), so that a quarter-warp's reads of two rows meet no bank twice.
 template <int XE, int NT>
 struct Ring {
-  static constexpr int kStages = 4;
+  static constexpr int kStages = 3;
   static constexpr int kXRow = 32 * Elem<XE>::kBytes, kXBlock = 64 * kXRow, kABlock = 8 * NT * 64;
   static constexpr int kStage = 2 * (kXBlock + kABlock);
   static constexpr int kBytes = kStages * kStage > 64 * 8 * NT * 4 ? kStages * kStage : 64 * 8 * NT * 4;  // or the sums, afterwards
@@ -484,68 +491,86 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
 
 // ---------------------------------------------------------------- expand --
 
+// A lane's 8 columns of a turn's 32 are pieces of 16 bytes, a row's four lanes
+// side by side in one access, so that it covers whole sectors: 8 columns from 8 t
+// (16-bit rows), or 4 from 4 t and 4 from 16 + 4 t (fp32).
 template <int YE>
-__device__ __forceinline__ void load_y(const uint8_t *p, int n, bool vec, float (&v)[8]) {
-  constexpr int S = Elem<YE>::kBytes;
-  if (vec && n >= 8) {
+struct Piece {
+  static constexpr int kCount = Elem<YE>::kBytes / 2, kCols = 8 / kCount;
+  static __device__ __forceinline__ int column(int k, int t) { return 16 * k + kCols * t; }
+  // column c of n-tile j (a lane has 2 t and 2 t + 1 of each): the lane's column 2 j + c % 2
+  static __device__ __forceinline__ int tile_column(int j, int c) {
+    const int i = 2 * j + (c & 1);
+    return column(i / kCols, c >> 1) + i % kCols;
+  }
+};
+
+// one piece: from 16 bytes, or its first n columns one by one
+template <int YE>
+__device__ __forceinline__ void read_y(const uint8_t *p, float *v) {
+  const uint4 a = *reinterpret_cast<const uint4 *>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     if constexpr (YE == kElemF32) {
-      const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      v[i] = __uint_as_float(word(a, i));
     } else {
-      const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack_pair<YE>(word(a, i));
-        v[2 * i] = f.x, v[2 * i + 1] = f.y;
-      }
+      const float2 f = unpack_pair<YE>(word(a, i));
+      v[2 * i] = f.x, v[2 * i + 1] = f.y;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) {
-        if constexpr (YE == kElemF32) v[i] = *reinterpret_cast<const float *>(p + i * S);
-        if constexpr (YE == kElemF16) v[i] = __half2float(*reinterpret_cast<const __half *>(p + i * S));
-        if constexpr (YE == kElemBF16) v[i] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(p + i * S));
-      }
   }
 }
 template <int YE>
-__device__ __forceinline__ void store_y(uint8_t *p, int n, bool vec, const float (&v)[8]) {
-  constexpr int S = Elem<YE>::kBytes;
-  if (vec && n >= 8) {
-    if constexpr (YE == kElemF32) {
-      __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
-      __stcs(reinterpret_cast<float4 *>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-    } else {
-      __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_pair<YE>(v[0], v[1]), pack_pair<YE>(v[2], v[3]), pack_pair<YE>(v[4], v[5]), pack_pair<YE>(v[6], v[7])));
+__device__ __forceinline__ void load_y(const uint8_t *p, int n, float *v) {
+#pragma unroll
+  for (int i = 0; i < Piece<YE>::kCols; ++i)
+    if (i < n) {
+      if constexpr (YE == kElemF32) v[i] = reinterpret_cast<const float *>(p)[i];
+      if constexpr (YE == kElemF16) v[i] = __half2float(reinterpret_cast<const __half *>(p)[i]);
+      if constexpr (YE == kElemBF16) v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
     }
+}
+template <int YE>
+__device__ __forceinline__ void store_y(uint8_t *p, int n, bool vec, const float *v) {
+  if (vec && n >= Piece<YE>::kCols) {
+    if constexpr (YE == kElemF32)
+      __stcs(reinterpret_cast<float4 *>(p), make_float4(v[0], v[1], v[2], v[3]));
+    else
+      __stcs(reinterpret_cast<uint4 *>(p), make_uint4(pack_pair<YE>(v[0], v[1]), pack_pair<YE>(v[2], v[3]), pack_pair<YE>(v[4], v[5]), pack_pair<YE>(v[6], v[7])));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < Piece<YE>::kCols; ++i)
       if (i < n) {
-        if constexpr (YE == kElemF32) *reinterpret_cast<float *>(p + i * S) = v[i];
-        if constexpr (YE == kElemF16) *reinterpret_cast<__half *>(p + i * S) = __float2half_rn(v[i]);
-        if constexpr (YE == kElemBF16) *reinterpret_cast<__nv_bfloat16 *>(p + i * S) = __float2bfloat16_rn(v[i]);
+        if constexpr (YE == kElemF32) reinterpret_cast<float *>(p)[i] = v[i];
+        if constexpr (YE == kElemF16) reinterpret_cast<__half *>(p)[i] = __float2half_rn(v[i]);
+        if constexpr (YE == kElemBF16) reinterpret_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v[i]);
       }
   }
 }
 
-// KB: blocks of 32 ranks. A warp has MT row tiles of 16 tokens and 32 columns a
-// turn; the CTA's 8 warps are 2 x 4 (TM = 64, MT = 2) or 1 x 8 (TM = 16, MT = 1).
 template <int WE, int YE, int TM, int KB>
 struct Expand {
   static constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2;
   static constexpr int kPitch = KB == 1 ? 64 : KB * 64 + 64;  // 64 modulo 128: a quarter-warp's 16-byte reads of two rows meet no bank twice
-  static constexpr int kBytes = kTerms * TM * kPitch;
+  static constexpr int kRowTiles = TM == 64 ? 2 : 1;          // of a warp
+  static constexpr int kPieces = kRowTiles * 2 * Elem<YE>::kBytes / 2;  // 16-byte pieces of y per lane and turn
+  static constexpr int kTermBytes = kTerms * TM * kPitch, kYBytes = kPieces * 512;
+  static constexpr int kBytes = kTermBytes + (kExpandThreads / 32) * 2 * kYBytes;
   static_assert(KB == 1 || KB % 2 == 0, "pitch");
 };
 
+// KB: blocks of 32 ranks. A warp has MT row tiles of 16 tokens and 32 columns a
+// turn; the CTA's 8 warps are 2 x 4 (TM = 64, MT = 2) or 1 x 8 (TM = 16, MT = 1).
+// A lane's pieces of y come a turn ahead, by asynchronous copies into places of
+// its own (nobody else waits for them); the first turn's, and its part of B, are
+// asked for before the launch before this one has ended.
 template <int WE, int YE, int TM, int KB>
 __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArgs a, const Work w, const int turns) {
-  constexpr int MT = TM == 64 ? 2 : 1, WM = TM == 64 ? 4 : 8;
-  constexpr int kTerms = Expand<WE, YE, TM, KB>::kTerms, kPitch = Expand<WE, YE, TM, KB>::kPitch;
-  constexpr int YS = Elem<YE>::kBytes;
-  extern __shared__ __align__(16) uint8_t terms[];  // [term][row], rows of kPitch bytes
+  using E = Expand<WE, YE, TM, KB>;
+  constexpr int MT = E::kRowTiles, WM = TM == 64 ? 4 : 8, kTerms = E::kTerms, kPitch = E::kPitch;
+  using Pc = Piece<YE>;
+  constexpr int YS = Elem<YE>::kBytes, kPer = Pc::kCount;
+  constexpr int kAhead = KB < 2 ? KB : 2;              // blocks of B in flight
+  extern __shared__ __align__(16) uint8_t terms[];     // [term][row], rows of kPitch bytes; then y
   __shared__ float unscale[TM];
   __shared__ int rows[TM];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
@@ -553,6 +578,42 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
   int ad, count;
   if (!find_tile<TM>(a, w, blockIdx.y, rows, ad, count)) return;
   if (ad < 0 && a.y == a.out) return;
+  const int wr = warp / WM, wm = warp % WM, r0 = wr * 16 * MT;
+  uint8_t *const mine = terms + E::kTermBytes + warp * 2 * E::kYBytes + lane * 16;
+  const int first = int(blockIdx.x) * turns * (WM * 32) + wm * 32;  // column of the first turn
+  auto row_of = [&](int i, int h) { return r0 + 16 * i + 8 * h + g; };
+  // y's pieces of a turn; rows of another alignment and the last columns are loaded when they are needed
+  auto ask = [&](int turn) {
+    const int m0 = first + turn * (WM * 32);
+    if (a.y && a.y_vec && turn < turns) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (row_of(i, h) < count) {
+            const uint8_t *p = a.y + rows[row_of(i, h)] * a.y_row;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+              const int c = m0 + Pc::column(k, t);
+              if (c + Pc::kCols <= a.M) copy16(mine + (turn & 1) * E::kYBytes + ((i * 2 + h) * kPer + k) * 512, p + int64_t(c) * YS);
+            }
+          }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto load_b = [&](uint4 (&bw)[4], int m0, int kb) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {  // column g of n-tile j
+      const int m = m0 + Pc::tile_column(j, g);
+      bw[j] = make_uint4(0, 0, 0, 0);
+      if (ad >= 0 && m < a.M && kb * 32 + 8 * t < a.rank)
+        bw[j] = __ldg(reinterpret_cast<const uint4 *>(a.B + ((int64_t(ad) * a.M + m) * a.rank + kb * 32 + 8 * t) * 2));
+    }
+  };
+  ask(0);
+  uint4 bw[kAhead][4];
+#pragma unroll
+  for (int kb = 0; kb < kAhead; ++kb) load_b(bw[kb], first, kb);
   if (!w.sorted) pdl_wait();
   if (ad >= 0) {
     for (int r = warp; r < TM; r += kExpandThreads / 32) {
@@ -592,73 +653,63 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
     }
     __syncthreads();
   }
-  const int wr = warp / WM, wm = warp % WM, r0 = wr * 16 * MT;
-  if (r0 >= count) return;
-  for (int turn = 0; turn < turns; ++turn) {
-    const int m0 = (int(blockIdx.x) * turns + turn) * (WM * 32) + wm * 32;
-    if (m0 >= a.M) break;
-    const int c0 = m0 + 8 * t, n = a.M - c0;  // this lane's 8 columns, as many as there are
-    float y[MT][2][8];
+  if (r0 < count) {
+    for (int turn = 0; turn < turns; ++turn) {
+      const int m0 = first + turn * (WM * 32);
+      if (m0 >= a.M) break;
+      ask(turn + 1);
+      float acc[MT][4][4] = {};
+      if (ad >= 0) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int kb = 0; kb < KB; ++kb) {
+          uint4(&b)[4] = bw[kb % kAhead];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = r0 + 16 * i + 8 * h + g;
+          for (int k = kTerms - 1; k >= 0; --k)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) y[i][h][k] = 0.0f;
-        if (a.y && r < count && n > 0) load_y<YE>(a.y + rows[r] * a.y_row + int64_t(c0) * YS, n, a.y_vec, y[i][h]);
-      }
-    if (ad >= 0) {
-      float acc[MT][4][4];
+            for (int i = 0; i < MT; ++i) {
+              const uint4 lo = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g) * kPitch + kb * 64 + 16 * t);
+              const uint4 hi = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g + 8) * kPitch + kb * 64 + 16 * t);
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.0f;
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        uint4 bw[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {  // column g of n-tile j
-          const int m = m0 + 8 * (g >> 1) + 2 * j + (g & 1);
-          bw[j] = make_uint4(0, 0, 0, 0);
-          if (m < a.M && kb * 32 + 8 * t < a.rank)
-            bw[j] = __ldg(reinterpret_cast<const uint4 *>(a.B + ((int64_t(ad) * a.M + m) * a.rank + kb * 32 + 8 * t) * 2));
-        }
-#pragma unroll
-        for (int k = kTerms - 1; k >= 0; --k)
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const uint4 lo = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g) * kPitch + kb * 64 + 16 * t);
-            const uint4 hi = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g + 8) * kPitch + kb * 64 + 16 * t);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              mma16<WE>(acc[i][j], lo.x, hi.x, lo.y, hi.y, bw[j].x, bw[j].y);
-              mma16<WE>(acc[i][j], lo.z, hi.z, lo.w, hi.w, bw[j].z, bw[j].w);
+              for (int j = 0; j < 4; ++j) {
+                mma16<WE>(acc[i][j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+                mma16<WE>(acc[i][j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
+              }
             }
-          }
+          // the block after next, or the next turn's
+          if (kb + kAhead < KB)
+            load_b(b, m0, kb + kAhead);
+          else if (turn + 1 < turns)
+            load_b(b, m0 + WM * 32, kb + kAhead - KB);
+        }
       }
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float s = WE == kElemF16 ? unscale[r0 + 16 * i + 8 * h + g] : 1.0f;
+          const int r = row_of(i, h);
+          if (r >= count) continue;
+          const float s = WE == kElemF16 && ad >= 0 ? unscale[r] : 1.0f;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float d = acc[i][k >> 1][2 * h + (k & 1)];
-            y[i][h][k] = WE == kElemF16 ? __fmaf_rn(d, s, y[i][h][k]) : __fadd_rn(d, y[i][h][k]);
+          for (int k = 0; k < kPer; ++k) {
+            const int c = m0 + Pc::column(k, t), n = a.M - c;  // columns there are
+            float y[Pc::kCols] = {};
+            if (a.y && a.y_vec && n >= Pc::kCols)
+              read_y<YE>(mine + (turn & 1) * E::kYBytes + ((i * 2 + h) * kPer + k) * 512, y);
+            else if (a.y)
+              load_y<YE>(a.y + rows[r] * a.y_row + int64_t(c) * YS, n, y);
+#pragma unroll
+            for (int q = 0; q < Pc::kCols; ++q) {
+              const int e = k * Pc::kCols + q;
+              const float d = acc[i][e >> 1][2 * h + (e & 1)];
+              y[q] = WE == kElemF16 ? __fmaf_rn(d, s, y[q]) : __fadd_rn(d, y[q]);
+            }
+            store_y<YE>(a.out + rows[r] * a.out_row + int64_t(c) * YS, n, a.y_vec, y);
           }
         }
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = r0 + 16 * i + 8 * h + g;
-        if (r < count && n > 0) store_y<YE>(a.out + rows[r] * a.out_row + int64_t(c0) * YS, n, a.y_vec, y[i][h]);
-      }
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host --
