@@ -458,7 +458,9 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode() {
   static std::once_flag once;
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   std::call_once(once, [] {
@@ -471,8 +473,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
-
-}  // namespace
 
 bool gemm_tc_supported(int64_t M, int64_t N, int64_t K) {
   return K > 0 && K % 256 == 0 && K / kQK <= (int64_t(1) << 24) && (M + kTM - 1) / kTM <= 65535 &&
@@ -504,7 +504,7 @@ cudaError_t launch_gemm_tc(const uint8_t *W, const float *X, float *Y, int64_t M
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
   if (!encode) return cudaErrorNotSupported;
   CUtensorMap map;
   const cuuint64_t dims[2] = {cuuint64_t(nb) * 17, cuuint64_t(M)};  // 16-bit units per row, rows

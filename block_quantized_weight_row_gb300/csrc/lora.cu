@@ -34,6 +34,7 @@
 #include "bq_internal.h"
 #include "layer.h"
 #include "paged.cuh"
+#include "tcgen05.cuh"
 
 namespace bq {
 namespace {
@@ -491,6 +492,16 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
 
 // ---------------------------------------------------------------- expand --
 
+// The power of two that brings a row of H below 2, kept within normal numbers; m:
+// the lane's largest |value|. Its inverse goes to unscale[r].
+__device__ __forceinline__ float scale_row(float m, float *unscale, int r, int lane) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+  const int e = min(max(int(__float_as_uint(m) >> 23), 2), 252);
+  if (lane == 0) unscale[r] = __uint_as_float(uint32_t(e) << 23);
+  return __uint_as_float(uint32_t(254 - e) << 23);
+}
+
 // A lane's 8 columns of a turn's 32 are pieces of 16 bytes, a row's four lanes
 // side by side in one access, so that it covers whole sectors: 8 columns from 8 t
 // (16-bit rows), or 4 from 4 t and 4 from 16 + 4 t (fp32).
@@ -547,26 +558,25 @@ __device__ __forceinline__ void store_y(uint8_t *p, int n, bool vec, const float
   }
 }
 
-template <int WE, int YE, int TM, int KB>
+template <int WE, int YE, int KB>
 struct Expand {
   static constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2;
   static constexpr int kPitch = KB == 1 ? 64 : KB * 64 + 64;  // 64 modulo 128: a quarter-warp's 16-byte reads of two rows meet no bank twice
-  static constexpr int kRowTiles = TM == 64 ? 2 : 1;          // of a warp
-  static constexpr int kPieces = kRowTiles * 2 * Elem<YE>::kBytes / 2;  // 16-byte pieces of y per lane and turn
-  static constexpr int kTermBytes = kTerms * TM * kPitch, kYBytes = kPieces * 512;
+  static constexpr int kPieces = 2 * Elem<YE>::kBytes / 2;  // 16-byte pieces of y per lane and turn
+  static constexpr int kTermBytes = kTerms * 16 * kPitch, kYBytes = kPieces * 512;
   static constexpr int kBytes = kTermBytes + (kExpandThreads / 32) * 2 * kYBytes;
   static_assert(KB == 1 || KB % 2 == 0, "pitch");
 };
 
-// KB: blocks of 32 ranks. A warp has MT row tiles of 16 tokens and 32 columns a
-// turn; the CTA's 8 warps are 2 x 4 (TM = 64, MT = 2) or 1 x 8 (TM = 16, MT = 1).
-// A lane's pieces of y come a turn ahead, by asynchronous copies into places of
-// its own (nobody else waits for them); the first turn's, and its part of B, are
-// asked for before the launch before this one has ended.
-template <int WE, int YE, int TM, int KB>
+// Tiles of 16 tokens; KB: blocks of 32 ranks. A warp has the tile's tokens and 32
+// columns a turn, the CTA's 8 warps 256. A lane's pieces of y come a turn ahead,
+// by asynchronous copies into places of its own (nobody else waits for them); the
+// first turn's, and its part of B, are asked for before the launch before this one
+// has ended.
+template <int WE, int YE, int KB>
 __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArgs a, const Work w, const int turns) {
-  using E = Expand<WE, YE, TM, KB>;
-  constexpr int MT = E::kRowTiles, WM = TM == 64 ? 4 : 8, kTerms = E::kTerms, kPitch = E::kPitch;
+  using E = Expand<WE, YE, KB>;
+  constexpr int TM = 16, kStep = 256, kTerms = E::kTerms, kPitch = E::kPitch;
   using Pc = Piece<YE>;
   constexpr int YS = Elem<YE>::kBytes, kPer = Pc::kCount;
   constexpr int kAhead = KB < 2 ? KB : 2;              // blocks of B in flight
@@ -578,26 +588,22 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
   int ad, count;
   if (!find_tile<TM>(a, w, blockIdx.y, rows, ad, count)) return;
   if (ad < 0 && a.y == a.out) return;
-  const int wr = warp / WM, wm = warp % WM, r0 = wr * 16 * MT;
   uint8_t *const mine = terms + E::kTermBytes + warp * 2 * E::kYBytes + lane * 16;
-  const int first = int(blockIdx.x) * turns * (WM * 32) + wm * 32;  // column of the first turn
-  auto row_of = [&](int i, int h) { return r0 + 16 * i + 8 * h + g; };
+  const int first = int(blockIdx.x) * turns * kStep + warp * 32;  // column of the first turn
   // y's pieces of a turn; rows of another alignment and the last columns are loaded when they are needed
   auto ask = [&](int turn) {
-    const int m0 = first + turn * (WM * 32);
+    const int m0 = first + turn * kStep;
     if (a.y && a.y_vec && turn < turns) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int h = 0; h < 2; ++h)
+        if (8 * h + g < count) {
+          const uint8_t *p = a.y + rows[8 * h + g] * a.y_row;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (row_of(i, h) < count) {
-            const uint8_t *p = a.y + rows[row_of(i, h)] * a.y_row;
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-              const int c = m0 + Pc::column(k, t);
-              if (c + Pc::kCols <= a.M) copy16(mine + (turn & 1) * E::kYBytes + ((i * 2 + h) * kPer + k) * 512, p + int64_t(c) * YS);
-            }
+          for (int k = 0; k < kPer; ++k) {
+            const int c = m0 + Pc::column(k, t);
+            if (c + Pc::kCols <= a.M) copy16(mine + (turn & 1) * E::kYBytes + (h * kPer + k) * 512, p + int64_t(c) * YS);
           }
+        }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -625,14 +631,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
         m = fmaxf(m, fabsf(h[i]));
       }
       float up = 1.0f;
-      if constexpr (WE == kElemF16) {
-#pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-        // 2^-e of the largest value (in [2^e, 2^(e+1))), kept within normal numbers
-        const int e = min(max(int(__float_as_uint(m) >> 23), 2), 252);
-        up = __uint_as_float(uint32_t(254 - e) << 23);
-        if (lane == 0) unscale[r] = __uint_as_float(uint32_t(e) << 23);
-      }
+      if constexpr (WE == kElemF16) up = scale_row(m, unscale, r, lane);
 #pragma unroll
       for (int i = 0; i < KB; ++i) {
         float x = h[i] * up;
@@ -653,63 +652,332 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
     }
     __syncthreads();
   }
-  if (r0 < count) {
-    for (int turn = 0; turn < turns; ++turn) {
-      const int m0 = first + turn * (WM * 32);
-      if (m0 >= a.M) break;
-      ask(turn + 1);
-      float acc[MT][4][4] = {};
-      if (ad >= 0) {
+  for (int turn = 0; turn < turns; ++turn) {
+    const int m0 = first + turn * kStep;
+    if (m0 >= a.M) break;
+    ask(turn + 1);
+    float acc[4][4] = {};
+    if (ad >= 0) {
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          uint4(&b)[4] = bw[kb % kAhead];
+      for (int kb = 0; kb < KB; ++kb) {
+        uint4(&b)[4] = bw[kb % kAhead];
 #pragma unroll
-          for (int k = kTerms - 1; k >= 0; --k)
+        for (int k = kTerms - 1; k >= 0; --k) {
+          const uint4 lo = *reinterpret_cast<const uint4 *>(terms + (k * TM + g) * kPitch + kb * 64 + 16 * t);
+          const uint4 hi = *reinterpret_cast<const uint4 *>(terms + (k * TM + g + 8) * kPitch + kb * 64 + 16 * t);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              const uint4 lo = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g) * kPitch + kb * 64 + 16 * t);
-              const uint4 hi = *reinterpret_cast<const uint4 *>(terms + (k * TM + r0 + 16 * i + g + 8) * kPitch + kb * 64 + 16 * t);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                mma16<WE>(acc[i][j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
-                mma16<WE>(acc[i][j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
-              }
-            }
-          // the block after next, or the next turn's
-          if (kb + kAhead < KB)
-            load_b(b, m0, kb + kAhead);
-          else if (turn + 1 < turns)
-            load_b(b, m0 + WM * 32, kb + kAhead - KB);
-        }
-      }
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int r = row_of(i, h);
-          if (r >= count) continue;
-          const float s = WE == kElemF16 && ad >= 0 ? unscale[r] : 1.0f;
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            const int c = m0 + Pc::column(k, t), n = a.M - c;  // columns there are
-            float y[Pc::kCols] = {};
-            if (a.y && a.y_vec && n >= Pc::kCols)
-              read_y<YE>(mine + (turn & 1) * E::kYBytes + ((i * 2 + h) * kPer + k) * 512, y);
-            else if (a.y)
-              load_y<YE>(a.y + rows[r] * a.y_row + int64_t(c) * YS, n, y);
-#pragma unroll
-            for (int q = 0; q < Pc::kCols; ++q) {
-              const int e = k * Pc::kCols + q;
-              const float d = acc[i][e >> 1][2 * h + (e & 1)];
-              y[q] = WE == kElemF16 ? __fmaf_rn(d, s, y[q]) : __fadd_rn(d, y[q]);
-            }
-            store_y<YE>(a.out + rows[r] * a.out_row + int64_t(c) * YS, n, a.y_vec, y);
+          for (int j = 0; j < 4; ++j) {
+            mma16<WE>(acc[j], lo.x, hi.x, lo.y, hi.y, b[j].x, b[j].y);
+            mma16<WE>(acc[j], lo.z, hi.z, lo.w, hi.w, b[j].z, b[j].w);
           }
         }
+        // the block after next, or the next turn's
+        if (kb + kAhead < KB)
+          load_b(b, m0, kb + kAhead);
+        else if (turn + 1 < turns)
+          load_b(b, m0 + kStep, kb + kAhead - KB);
+      }
+    }
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = 8 * h + g;
+      if (r >= count) continue;
+      const float s = WE == kElemF16 && ad >= 0 ? unscale[r] : 1.0f;
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int c = m0 + Pc::column(k, t), n = a.M - c;  // columns there are
+        float y[Pc::kCols] = {};
+        if (a.y && a.y_vec && n >= Pc::kCols)
+          read_y<YE>(mine + (turn & 1) * E::kYBytes + (h * kPer + k) * 512, y);
+        else if (a.y)
+          load_y<YE>(a.y + rows[r] * a.y_row + int64_t(c) * YS, n, y);
+#pragma unroll
+        for (int q = 0; q < Pc::kCols; ++q) {
+          const int e = k * Pc::kCols + q;
+          const float d = acc[e >> 1][2 * h + (e & 1)];
+          if (ad >= 0) y[q] = WE == kElemF16 ? __fmaf_rn(d, s, y[q]) : __fadd_rn(d, y[q]);
+        }
+        store_y<YE>(a.out + rows[r] * a.out_row + int64_t(c) * YS, n, a.y_vec, y);
+      }
     }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// ------------------------------------- expand on the tensor-memory kernel --
+
+// Tiles of 64 tokens, 128 columns of out a turn: D[column][token] = B (128 x rank,
+// straight from the adapter by TMA) times H's terms (64 tokens, operand made once
+// per CTA) on tcgen05, accumulated over the terms in tensor memory. With columns
+// as the accumulator's lanes, a warp's access to y and out is 32 neighbouring
+// columns of one token: whole sectors at any alignment of the rows, and a 32 x 32
+// piece costs 32 loads, 32 stores and one tensor-memory load. (The warp-level
+// instructions above move the same piece with 350 instructions and 224 wavefronts
+// of shared memory and L1, which bound them: 160 us for 8192 tokens of 11008
+// columns at rank 64.)
+// Warps 0-7: lanes 32 (w mod 4) .., tokens 32 (w / 4) .., in two steps of 16
+// tokens, the next step's y in flight; warp 8: TMA; warp 9: MMA. All waits bounded.
+constexpr int kTcThreads = 320, kTcCols = 128, kTcTokens = 64, kTcTmem = 2 * kTcTokens;
+constexpr int kTcBTile = kTcCols * 128, kTcHTile = kTcTokens * 128;  // 64 ranks: rows of 128 bytes
+
+struct ExpandTc {
+  int blocks, stages, terms;  // blocks of 64 ranks
+  __host__ __device__ int h_off() const { return stages * blocks * kTcBTile; }
+  __host__ __device__ int bar_off() const { return h_off() + terms * blocks * kTcHTile; }
+  __host__ __device__ int bytes() const { return bar_off() + 128 + 1024; }  // + room to align the base
+};
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+// 16 consecutive columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int YE>
+__device__ __forceinline__ float load_one(const uint8_t *p) {
+  if constexpr (YE == kElemF32) return __ldcs(reinterpret_cast<const float *>(p));
+  if constexpr (YE == kElemF16) return __half2float(__ldcs(reinterpret_cast<const __half *>(p)));
+  if constexpr (YE == kElemBF16) return __bfloat162float(__ldcs(reinterpret_cast<const __nv_bfloat16 *>(p)));
+}
+template <int YE>
+__device__ __forceinline__ void store_one(uint8_t *p, float v) {
+  if constexpr (YE == kElemF32) __stcs(reinterpret_cast<float *>(p), v);
+  if constexpr (YE == kElemF16) __stcs(reinterpret_cast<__half *>(p), __float2half_rn(v));
+  if constexpr (YE == kElemBF16) __stcs(reinterpret_cast<__nv_bfloat16 *>(p), __float2bfloat16_rn(v));
+}
+
+// The work of a grid is one run of turns, tile after tile, cut into equal pieces,
+// one per CTA: a tile's preparation (its tokens, H's operand: 3 us) is then paid
+// once or twice per CTA, and all CTAs end together.
+template <int WE, int YE>
+__global__ void __launch_bounds__(kTcThreads, 2)
+    k_lora_expand_tc(const __grid_constant__ CUtensorMap bmap, const LoraArgs a, const Work w, const ExpandTc e, const uint32_t spin) {
+  extern __shared__ uint8_t raw[];
+  __shared__ float unscale[kTcTokens];
+  __shared__ int rows[kTcTokens];
+  __shared__ __align__(16) int64_t y_off[kTcTokens], out_off[kTcTokens];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int aborted;
+  constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2, YS = Elem<YE>::kBytes;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint8_t *sm = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
+  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + e.bar_off());
+  uint64_t *b_full = bar, *b_empty = bar + 3, *d_full = bar + 6, *d_empty = bar + 8, *done = bar + 10;
+  volatile int *abort_flag = &aborted;
+  if (tid == 0) {
+    for (int i = 0; i < e.stages; ++i) {
+      mbar_init(&b_full[i], 1);
+      mbar_init(&b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_empty[i], 8);
+    }
+    mbar_init(done, 1);
+    aborted = 0;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTcTmem) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_wait();
+
+  const int groups = (a.M + kTcCols - 1) / kTcCols;
+  const int64_t units = int64_t(*w.n_tiles) * groups;
+  const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
+  int done_turns = 0;  // with products, over all tiles: the barriers' phases
+  int armed = 0;       // turns whose copies were asked for
+  for (int64_t u = units * blockIdx.x / gridDim.x; u < u1;) {
+    const int tile = int(u / groups), g0 = int(u - int64_t(tile) * groups), n_turns = int(min(u1 - u, int64_t(groups - g0)));
+    u += n_turns;
+    __syncthreads();  // the tile before this one is done with rows, offsets and H
+    if (*abort_flag) break;
+    int ad, count;
+    if (!find_tile<kTcTokens>(a, w, tile, rows, ad, count)) break;
+    if (ad < 0 && a.y == a.out) continue;
+    if (tid < kTcTokens) {
+      y_off[tid] = rows[tid] * a.y_row;
+      out_off[tid] = rows[tid] * a.out_row;
+    }
+    // H's terms as the second operand: token rows of 64 ranks, 128-byte swizzled; a lane has two ranks
+    if (ad >= 0) {
+      for (int r = warp; r < kTcTokens; r += kTcThreads / 32) {
+        float h[2][2], m = 0.0f;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int c = 64 * b + 2 * lane + i;
+            h[b][i] = r < count && c < a.rank ? __ldcg(w.H + int64_t(rows[r]) * a.rank + c) : 0.0f;
+            m = fmaxf(m, fabsf(h[b][i]));
+          }
+        float up = 1.0f;
+        if constexpr (WE == kElemF16) up = scale_row(m, unscale, r, lane);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (b >= e.blocks) break;
+          float x = h[b][0] * up, y = h[b][1] * up;
+#pragma unroll
+          for (int k = 0; k < kTerms; ++k) {
+            const uint32_t v = pack_pair<WE>(x, y);
+            const float2 f = unpack_pair<WE>(v);
+            x -= f.x, y -= f.y;
+            *reinterpret_cast<uint32_t *>(sm + e.h_off() + (k * e.blocks + b) * kTcHTile + sw128_off(r, lane >> 2) + (lane & 3) * 4) = v;
+          }
+        }
+      }
+      fence_async_smem();
+    }
+    __syncthreads();
+
+    const int i0 = done_turns;  // turn i of the tile is turn i0 + i of the barriers
+    if (ad >= 0) done_turns += n_turns;
+    if (warp == 8) {
+      if (lane == 0 && ad >= 0) {
+        for (int i = i0; i < i0 + n_turns; ++i) {
+          const int st = i % e.stages;
+          if (!tc_wait(&b_empty[st], ((i / e.stages) & 1) ^ 1, spin, abort_flag, a.err)) break;
+          mbar_arrive_expect_tx(&b_full[st], uint32_t(e.blocks * kTcBTile));
+          for (int b = 0; b < e.blocks; ++b)
+            tma_load_3d(sm + (st * e.blocks + b) * kTcBTile, &bmap, b * 64, (g0 + i - i0) * kTcCols, ad, &b_full[st]);
+          armed = i + 1;
+        }
+      }
+    } else if (warp == 9) {
+      if (lane == 0 && ad >= 0) {
+        // kind::f16: fp32 accumulators, both operands of the adapters' type, K-major
+        constexpr uint32_t kType = WE == kElemBF16 ? (1u << 7) | (1u << 10) : 0u;
+        constexpr uint32_t kIdesc = (1u << 4) | kType | (uint32_t(kTcTokens >> 3) << 17) | (uint32_t(kTcCols >> 4) << 24);
+        const uint32_t b0 = smem_u32(sm), h0 = smem_u32(sm + e.h_off());
+        for (int i = i0; i < i0 + n_turns; ++i) {
+          const int st = i % e.stages, buf = i & 1;
+          if (!tc_wait(&b_full[st], (i / e.stages) & 1, spin, abort_flag, a.err)) break;
+          if (!tc_wait(&d_empty[buf], ((i >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
+          tc_fence_after();
+          const uint32_t d = tmem + uint32_t(buf * kTcTokens);
+          uint32_t more = 0;
+          for (int b = 0; b < e.blocks; ++b) {
+            const uint64_t b_desc = sw128_desc(b0 + (st * e.blocks + b) * kTcBTile);
+            for (int k = kTerms - 1; k >= 0; --k) {
+              const uint64_t h_desc = sw128_desc(h0 + (k * e.blocks + b) * kTcHTile);
+              for (int q = 0; q < 4 && b * 64 + q * 16 < a.rank; ++q) {
+                tc_mma(d, b_desc + uint64_t(2 * q), h_desc + uint64_t(2 * q), kIdesc, more);
+                more = 1;
+              }
+            }
+          }
+          tc_commit(&b_empty[st]);
+          tc_commit(&d_full[buf]);
+        }
+      }
+    } else {
+      const int lg = warp & 3, t0 = (warp >> 2) * 32;
+      const uint32_t lane_addr = tmem + (uint32_t(lg * 32) << 16);
+      const bool whole = count == kTcTokens;
+      // steps of 16 tokens: 2 per turn; the next one's y is asked for before this one's sums are
+      float y[2][16];
+      auto ask = [&](int step, float (&v)[16]) {
+        const int m = (g0 + (step >> 1)) * kTcCols + lg * 32 + lane, from = t0 + (step & 1) * 16;
+        const bool live = a.y && m < a.M && step < 2 * n_turns;
+        const uint8_t *p = a.y + int64_t(m) * YS;
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const longlong2 o = *reinterpret_cast<const longlong2 *>(&y_off[from + j]);
+            v[j] = live ? load_one<YE>(p + o.x) : 0.0f;
+            v[j + 1] = live ? load_one<YE>(p + o.y) : 0.0f;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = live && from + j < count ? load_one<YE>(p + y_off[from + j]) : 0.0f;
+        }
+      };
+      bool ok = true;
+      auto give = [&](int step, const float (&v)[16]) {
+        const int turn = i0 + (step >> 1), m = (g0 + (step >> 1)) * kTcCols + lg * 32 + lane, from = t0 + (step & 1) * 16;
+        float o[16];
+        if (ad >= 0) {
+          if ((step & 1) == 0) {
+            ok = tc_wait_warp(&d_full[turn & 1], (turn >> 1) & 1, spin, abort_flag, a.err);
+            if (!ok) return;
+            tc_fence_after();
+          }
+          uint32_t d[16];
+          tmem_ld16(lane_addr + uint32_t((turn & 1) * kTcTokens + from), d);
+          if (step & 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[turn & 1]);
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float x = __uint_as_float(d[j]);
+            o[j] = WE == kElemF16 ? __fmaf_rn(x, unscale[from + j], v[j]) : __fadd_rn(x, v[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] = v[j];
+        }
+        if (m >= a.M) return;
+        uint8_t *p = a.out + int64_t(m) * YS;
+        if (whole) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const longlong2 q = *reinterpret_cast<const longlong2 *>(&out_off[from + j]);
+            store_one<YE>(p + q.x, o[j]);
+            store_one<YE>(p + q.y, o[j + 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (from + j < count) store_one<YE>(p + out_off[from + j], o[j]);
+        }
+      };
+      ask(0, y[0]);
+      for (int step = 0; step < 2 * n_turns && ok; step += 2) {
+        ask(step + 1, y[1]);
+        give(step, y[0]);
+        if (!ok) break;
+        ask(step + 2, y[0]);
+        give(step + 1, y[1]);
+      }
+      tc_fence_before();
+    }
+  }
+  // copies and products in flight end by themselves: none is left behind
+  if (warp == 8 && lane == 0) {
+    for (int i = 0; i < e.stages && i < armed; ++i) {
+      const int last = armed - 1 - ((armed - 1 - i) % e.stages);
+      tc_drain(&b_full[i], (last / e.stages) & 1);
+    }
+  }
+  if (warp == 9 && lane == 0) {
+    tc_commit(done);
+    tc_drain(done, 0);
+  }
+  __syncthreads();
+  if (warp == 9) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcTmem) : "memory");
+  }
 }
 
 // ------------------------------------------------------------------ host --
@@ -784,16 +1052,39 @@ cudaError_t shrink(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t
   return shrink_nt<XE, WE, TM, 16>(a, w, p, s);
 }
 
-template <int WE, int YE, int TM>
-cudaError_t expand(const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
-  const int cols = TM == 64 ? 128 : 256;
-  const int64_t groups = (a.M + cols - 1) / cols;
+template <int WE, int YE>
+cudaError_t expand16(const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
+  const int64_t groups = (a.M + 255) / 256;
   int turns = 1;  // of a CTA: several where enough CTAs remain
   while (turns < 8 && groups * p.tiles / (2 * turns) >= int64_t(sms) * 8) turns *= 2;
   const dim3 grid(unsigned((groups + turns - 1) / turns), unsigned(p.tiles));
-  if (a.rank <= 32) return launch_ex(k_lora_expand<WE, YE, TM, 1>, grid, kExpandThreads, Expand<WE, YE, TM, 1>::kBytes, 1, true, s, a, w, turns);
-  if (a.rank <= 64) return launch_ex(k_lora_expand<WE, YE, TM, 2>, grid, kExpandThreads, Expand<WE, YE, TM, 2>::kBytes, 1, true, s, a, w, turns);
-  return launch_ex(k_lora_expand<WE, YE, TM, 4>, grid, kExpandThreads, Expand<WE, YE, TM, 4>::kBytes, 1, true, s, a, w, turns);
+  if (a.rank <= 32) return launch_ex(k_lora_expand<WE, YE, 1>, grid, kExpandThreads, Expand<WE, YE, 1>::kBytes, 1, true, s, a, w, turns);
+  if (a.rank <= 64) return launch_ex(k_lora_expand<WE, YE, 2>, grid, kExpandThreads, Expand<WE, YE, 2>::kBytes, 1, true, s, a, w, turns);
+  return launch_ex(k_lora_expand<WE, YE, 4>, grid, kExpandThreads, Expand<WE, YE, 4>::kBytes, 1, true, s, a, w, turns);
+}
+
+template <int WE, int YE>
+cudaError_t expand64(const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
+  if (!encode) return cudaErrorNotSupported;
+  CUtensorMap map{};
+  if (a.n_adapters > 0) {  // [adapter][column][rank]; ranks and columns beyond the adapter's read as zeros
+    const cuuint64_t dims[3] = {cuuint64_t(a.rank), cuuint64_t(a.M), cuuint64_t(a.n_adapters)};
+    const cuuint64_t strides[2] = {cuuint64_t(a.rank) * 2, cuuint64_t(a.rank) * 2 * cuuint64_t(a.M)};
+    const cuuint32_t box[3] = {64, kTcCols, 1}, step[3] = {1, 1, 1};
+    if (encode(&map, WE == kElemBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint8_t *>(a.B), dims, strides,
+               box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  }
+  ExpandTc e;
+  e.blocks = (a.rank + 63) / 64;
+  e.stages = e.blocks == 1 ? 3 : 2;
+  e.terms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2;
+  const int64_t units = int64_t(p.tiles) * ((a.M + kTcCols - 1) / kTcCols);
+  const int per_sm = e.bytes() <= 110 * 1024 ? 2 : 1;  // resident
+  const dim3 grid(unsigned(std::min<int64_t>(units, int64_t(sms) * per_sm)));
+  return launch_ex(k_lora_expand_tc<WE, YE>, grid, kTcThreads, e.bytes(), 1, true, s, map, a, w, e, spin_limit());
 }
 
 template <int WE, int TM>
@@ -804,7 +1095,10 @@ cudaError_t run(int x_elem, int y_elem, const LoraArgs &a, const Work &w, const 
   }
   const cudaError_t e = x_elem == kElemF32 ? shrink<kElemF32, WE, TM>(a, w, p, s) : shrink<WE, WE, TM>(a, w, p, s);
   if (e != cudaSuccess) return e;
-  return y_elem == kElemF32 ? expand<WE, kElemF32, TM>(a, w, p, sms, s) : expand<WE, WE, TM>(a, w, p, sms, s);
+  if constexpr (TM == 64)
+    return y_elem == kElemF32 ? expand64<WE, kElemF32>(a, w, p, sms, s) : expand64<WE, WE>(a, w, p, sms, s);
+  else
+    return y_elem == kElemF32 ? expand16<WE, kElemF32>(a, w, p, sms, s) : expand16<WE, WE>(a, w, p, sms, s);
 }
 
 }  // namespace

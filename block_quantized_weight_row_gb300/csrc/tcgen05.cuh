@@ -1,11 +1,17 @@
 // tcgen05.cuh — helpers around the fifth-generation tensor cores that the
-// GEMM and the many-row attention share: operand layout and descriptors, MMA
+// GEMM, the many-row attention and the adapters share: operand layout and descriptors, MMA
 // issue, tensor-memory loads and stores, bounded waits.
 #pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "bq_device.cuh"
 
 namespace bq {
+
+// The driver's cuTensorMapEncodeTiled, looked up once (gemm_tc.cu); null where it has none.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode();
 
 constexpr uint32_t kDrainPolls = 1u << 22;
 
