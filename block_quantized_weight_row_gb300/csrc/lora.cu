@@ -405,7 +405,6 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
   __shared__ int rows[64];
   constexpr int XS = Elem<XE>::kBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  pdl_launch_dependents();
   pdl_wait();
   int ad, count;
   if (!find_tile<64>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
@@ -797,7 +796,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  pdl_wait();
 
   const int groups = (a.M + kTcCols - 1) / kTcCols;
   const int64_t units = int64_t(*w.n_tiles) * groups;
@@ -1084,7 +1082,9 @@ cudaError_t expand64(const LoraArgs &a, const Work &w, const Plan &p, int sms, c
   const int64_t units = int64_t(p.tiles) * ((a.M + kTcCols - 1) / kTcCols);
   const int per_sm = e.bytes() <= 110 * 1024 ? 2 : 1;  // resident
   const dim3 grid(unsigned(std::min<int64_t>(units, int64_t(sms) * per_sm)));
-  return launch_ex(k_lora_expand_tc<WE, YE>, grid, kTcThreads, e.bytes(), 1, true, s, map, a, w, e, spin_limit());
+  // not a dependent launch: CTAs that come while the first product's are still there
+  // find less shared memory to share an SM, and the grid runs in two parts (200 us for 161)
+  return launch_ex(k_lora_expand_tc<WE, YE>, grid, kTcThreads, e.bytes(), 1, false, s, map, a, w, e, spin_limit());
 }
 
 template <int WE, int TM>
