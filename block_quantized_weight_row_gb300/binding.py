@@ -193,11 +193,10 @@ def dequantize_rows(t: int, blocks: torch.Tensor, cols: int, out: torch.Tensor |
     _cuda(blocks, "blocks")
     nbr = (cols // max(block_values(t), 1)) * block_bytes(t)
     R = blocks.numel() // nbr if nbr else 0
-    if out is None:
-        out = torch.empty((R, cols), dtype=torch.float32, device=blocks.device)
-    L = _prep(blocks.device)
-    _check(L.bq_dequantize_rows(t, _ptr(blocks), _ptr(out), R, cols), "bq_dequantize_rows")
-    return out
+    r = (_ext or _paged()).dequantize_rows(t, blocks, R, cols, out)
+    if type(r) is tuple:
+        _raise(r, "bq_dequantize_rows")
+    return r
 
 
 def gemv(t: int, w_blocks: torch.Tensor, x: torch.Tensor, M: int, K: int,

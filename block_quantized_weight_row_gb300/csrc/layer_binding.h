@@ -67,6 +67,15 @@ PyObject *tuple_of(std::initializer_list<const at::Tensor *> tensors) {
   return r;
 }
 
+// n elements of `type` from int32 element `from` of an allocation, as a tensor of
+// its own (a view made through the dispatcher takes a microsecond, this a tenth).
+at::Tensor part(const at::Tensor &all, at::ScalarType type, int64_t from, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), at::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  t.unsafeGetTensorImpl()->set_storage_offset(from * 4 / int64_t(at::elementSize(type)));
+  return t;
+}
+
 // page_size, n_pages, kv_len, n_new, page_table, free_pages, n_slots
 PyObject *paged_extend(PyObject *, PyObject *const *args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -80,13 +89,11 @@ PyObject *paged_extend(PyObject *, PyObject *const *args, Py_ssize_t n) {
                      &free = plain(args[5], "free_pages", d, at::kInt, {-1});
     if (n_slots < 0) wrong(PyExc_ValueError, "n_slots is negative");
     const c10::cuda::CUDAGuard guard(d);
-    // one allocation for the four int32 outputs, each 16-byte aligned
-    const auto i32 = at::TensorOptions().dtype(at::kInt).device(d);
-    const int64_t a1 = (B + 4) / 4 * 4, a2 = a1 + (B + 3) / 4 * 4, a3 = a2 + (n_slots + 3) / 4 * 4;
-    const at::Tensor all = at::empty({a3 + 2}, i32);
-    const at::Tensor q_start = all.narrow(0, 0, B + 1), kv_out = all.narrow(0, a1, B), positions = all.narrow(0, a2, n_slots),
-                     taken = all.narrow(0, a3, 2);
-    const at::Tensor slots = at::empty({n_slots}, i32.dtype(at::kLong));
+    // one allocation for the five outputs, each 16-byte aligned
+    const int64_t a1 = 2 * ((n_slots + 1) / 2 * 2), a2 = a1 + (B + 4) / 4 * 4, a3 = a2 + (B + 3) / 4 * 4, a4 = a3 + (n_slots + 3) / 4 * 4;
+    const at::Tensor all = at::empty({a4 + 4}, kv.options());
+    const at::Tensor slots = part(all, at::kLong, 0, n_slots), q_start = part(all, at::kInt, a1, B + 1), kv_out = part(all, at::kInt, a2, B),
+                     positions = part(all, at::kInt, a3, n_slots), taken = part(all, at::kInt, a4, 2);
     use_stream();
     const int r = bq_paged_extend(page, pages, kv.data_ptr<int>(), fresh.data_ptr<int>(), B, free.data_ptr<int>(), free.size(0),
                                   table.data_ptr<int>(), table.size(1), q_start.data_ptr<int>(), kv_out.data_ptr<int>(),
@@ -235,7 +242,27 @@ PyObject *lora(PyObject *, PyObject *const *args, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// type, blocks, rows, cols, out
+PyObject *dequantize_rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  try {
+    if (n != 5) wrong(PyExc_TypeError, "dequantize_rows: wrong number of arguments");
+    const int type = to_code(args[0], "t");
+    const at::Tensor &blocks = cuda_tensor(args[1], "blocks");
+    const int64_t rows = to_int(args[2], "rows"), cols = to_int(args[3], "cols");
+    const c10::cuda::CUDAGuard guard(blocks.device());
+    const at::Tensor out = args[4] == Py_None ? at::empty({rows, cols}, blocks.options().dtype(at::kFloat)) : cuda_tensor(args[4], "out");
+    use_stream();
+    const int r = bq_dequantize_rows(type, blocks.data_ptr(), static_cast<float *>(out.data_ptr()), rows, cols);
+    if (r) return failed(r);
+    return THPVariable_Wrap(out);
+  } catch (const Wrong &) {
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
 #define BQ_METHOD(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
-#define BQ_LAYER_METHODS BQ_METHOD(paged_extend), BQ_METHOD(add_rms_norm), BQ_METHOD(rotary), BQ_METHOD(lora)
+#define BQ_LAYER_METHODS BQ_METHOD(paged_extend), BQ_METHOD(add_rms_norm), BQ_METHOD(rotary), BQ_METHOD(lora), BQ_METHOD(dequantize_rows)
 
 }  // namespace

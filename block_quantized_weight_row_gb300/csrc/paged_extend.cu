@@ -91,16 +91,28 @@ __global__ void __launch_bounds__(NT, 1) k_paged_extend(const ExtendArgs a, cons
   if (tid == 0) most = 0;
 
   // ---- the sums of all chunks, then those before each ----
-  for (int c = warp; c < chunks; c += kWarps) {
-    uint32_t t = 0, p = 0;
+  constexpr int kAhead = 4;  // chunks of a warp whose lengths are in flight
+  for (int c0 = warp; c0 < chunks; c0 += kAhead * kWarps) {
+    uint32_t t[kAhead] = {}, p[kAhead] = {};
     for (int r = 0; r < rounds; ++r) {
-      const Seq s = load_seq(a, (c * rounds + r) * 32 + lane);
-      t = sat_add(t, s.n);
-      p = sat_add(p, s.need);
+      Seq s[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) s[k] = c0 + k * kWarps < chunks ? load_seq(a, ((c0 + k * kWarps) * rounds + r) * 32 + lane) : Seq{0, 0, 0, 0, true};
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        t[k] = sat_add(t[k], s[k].n);
+        p[k] = sat_add(p[k], s[k].need);
+      }
     }
-    t = sat_sum_warp(t);
-    p = sat_sum_warp(p);
-    if (lane == 0) tok[c] = t, pag[c] = p;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int c = c0 + k * kWarps;
+      if (c < chunks) {  // the warp's
+        t[k] = sat_sum_warp(t[k]);
+        p[k] = sat_sum_warp(p[k]);
+        if (lane == 0) tok[c] = t[k], pag[c] = p[k];
+      }
+    }
   }
   __syncthreads();
   uint32_t t = 0, p = 0;

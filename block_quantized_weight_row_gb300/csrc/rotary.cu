@@ -13,7 +13,9 @@
 //
 // Bound by HBM: q and k are read and written once. A CTA makes the sines and
 // cosines of a few tokens once, in shared memory, for all heads of both tensors;
-// then its threads take units of 16 bytes of output, four at a time, loads first.
+// then its threads take units of 16 bytes of output, several at a time, loads
+// first, the first of them before the sines; a CTA has as many tokens as make the
+// grid one wave.
 // A unit's partner channels are in the unit (adjacent pairs), in another one that
 // the same thread takes (halves of a multiple of the unit), or are gathered (other
 // halves: each lane loads them beside its own unit, from L1).
@@ -46,25 +48,31 @@ __device__ __forceinline__ uint64_t turns(double f) {
   return __double2ull_rz((t - floor(t)) * 18446744073709551616.0);
 }
 
-// V channels as fp32
+// V channels as they lie in memory, and as fp32
 template <int ELEM, int V>
-__device__ __forceinline__ void load(const uint8_t *p, float (&v)[V]) {
-  if constexpr (ELEM == kElemF32) {
+struct Raw {
+  static constexpr int kWords = V * Elem<ELEM>::kBytes / 16;
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const uint8_t *p) {
 #pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 f = *(reinterpret_cast<const float4 *>(p) + i);
-      v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
-    }
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < kWords; ++i) w[i] = *(reinterpret_cast<const uint4 *>(p) + i);
+  }
+  __device__ __forceinline__ void get(float (&v)[V]) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_pair<ELEM>(u[i]);
-      v[2 * i] = f.x, v[2 * i + 1] = f.y;
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (ELEM == kElemF32) {
+          v[4 * i + k] = __uint_as_float(u[k]);
+        } else {
+          const float2 f = unpack_pair<ELEM>(u[k]);
+          v[2 * k] = f.x, v[2 * k + 1] = f.y;
+        }
+      }
     }
   }
-}
+};
 template <int ELEM, int V>
 __device__ __forceinline__ void store(uint8_t *p, const float (&v)[V]) {
   if constexpr (ELEM == kElemF32)
@@ -78,24 +86,71 @@ __device__ __forceinline__ float2 turn_pair(float x, float y, float2 w) {
 }
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // of a CTA
+constexpr int kMaxTokens = 32;  // of a CTA
+constexpr int kResident = 4;     // CTAs of an SM (64 registers)
 
 // How a unit finds its partners
 enum Path { kAdjacent, kHalves, kGather, kScalar };
 
 // units: of a head (with kHalves, a unit of the first half stands for both); tokens: of a CTA
 template <int IN, int OUT, int PATH>
-__global__ void __launch_bounds__(kThreads) k_rotary(const RotaryArgs a, const int units, const int tokens) {
+__global__ void __launch_bounds__(kThreads, kResident) k_rotary(const RotaryArgs a, const int units, const int tokens) {
   constexpr int IS = Elem<IN>::kBytes, OS = Elem<OUT>::kBytes;
-  constexpr int V = PATH == kScalar ? 1 : 16 / OS;        // channels of a unit
-  constexpr int P = PATH == kAdjacent ? V / 2 : V;        // pairs of a unit
-  constexpr int NB = PATH == kGather || PATH == kScalar ? 1 : PATH == kHalves ? 2 : 4;  // units in flight
+  constexpr int V = PATH == kScalar ? 1 : 16 / OS;   // channels of a unit
+  constexpr int P = PATH == kAdjacent ? V / 2 : V;   // pairs of a unit
+  constexpr int W = PATH == kHalves ? 2 : 1;         // units that are turned together
+  constexpr bool kWide = PATH == kAdjacent || PATH == kHalves;
+  constexpr int NB = !kWide ? 1 : 4 / (W * (IS / OS));  // in flight
+  constexpr int LV = PATH == kScalar ? 16 / IS : V;  // (the scalar path keeps none)
   extern __shared__ uint64_t freq[];  // per pair, then cosine and sine per token and pair
   const int pairs = a.rot / 2;
   const int cols = (pairs + P - 1) / P;  // pair p of a token at (p % P) * cols + p / P: neighbouring units meet no bank twice
   float2 *const table = reinterpret_cast<float2 *>(freq + pairs);
   const int64_t t0 = int64_t(blockIdx.x) * tokens;
   const int nt = int(min(int64_t(tokens), a.n_tokens - t0));
+  const int heads = a.heads[0] + a.heads[1], n = nt * heads * units;
+
+  // item i: a unit of a head of a token, and where its head lies
+  struct Item {
+    const uint8_t *in;
+    uint8_t *out;
+    int unit, tok;  // unit < 0: none
+  };
+  auto item = [&](int i) {
+    Item x{nullptr, nullptr, -1, 0};
+    if (i < n) {
+      const int r = i / units;
+      x.unit = i - r * units;
+      x.tok = r / heads;
+      int h = r - x.tok * heads;
+      const bool k = h >= a.heads[0];
+      if (k) h -= a.heads[0];
+      const RotarySide &s = a.side[k];
+      x.in = s.in + (t0 + x.tok) * s.in_token + h * s.in_head;
+      x.out = s.out + (t0 + x.tok) * s.out_token + h * s.out_head;
+    }
+    return x;
+  };
+  // with kHalves: a unit of the first half and its partner, or two of the channels behind
+  auto channel = [&](int unit, int k) {
+    if constexpr (PATH == kHalves) return unit < cols ? unit * V + k * pairs : a.rot + (2 * (unit - cols) + k) * V;
+    return unit * V;
+  };
+  Item it[NB];
+  Raw<IN, LV> x[NB][W];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      it[b] = item(i0 + b * kThreads);
+      if constexpr (PATH != kScalar)
+        if (it[b].unit >= 0) {
+#pragma unroll
+          for (int k = 0; k < W; ++k) x[b][k].load(it[b].in + channel(it[b].unit, k) * IS);
+        }
+    }
+  };
+  fetch(threadIdx.x);
+
   for (int p = threadIdx.x; p < pairs; p += kThreads) freq[p] = turns(a.inv_freq[p]);
   __syncthreads();
   for (int i = threadIdx.x; i < nt * cols * P; i += kThreads) {
@@ -113,89 +168,57 @@ __global__ void __launch_bounds__(kThreads) k_rotary(const RotaryArgs a, const i
     table[tt * cols * P + (p % P) * cols + p / P] = make_float2(c, a.inverse ? -s : s);
   }
   __syncthreads();
-  const int heads = a.heads[0] + a.heads[1], n = nt * heads * units;
-  for (int i0 = threadIdx.x; i0 < n; i0 += NB * kThreads) {
-    float x[NB][PATH == kHalves ? 2 : 1][V];
-    const uint8_t *in[NB];
-    uint8_t *out[NB];
-    int unit[NB], tok[NB];
+
+  for (int i0 = threadIdx.x; i0 < n;) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int i = i0 + b * kThreads;
-      unit[b] = -1;
-      if (i < n) {
-        const int r = i / units, tt = r / heads;
-        unit[b] = i - r * units;
-        tok[b] = tt;
-        int h = r - tt * heads;
-        const bool k = h >= a.heads[0];
-        if (k) h -= a.heads[0];
-        const RotarySide &s = a.side[k];
-        in[b] = s.in + (t0 + tt) * s.in_token + h * s.in_head;
-        out[b] = s.out + (t0 + tt) * s.out_token + h * s.out_head;
-        if constexpr (PATH == kAdjacent || PATH == kGather) load<IN, V>(in[b] + unit[b] * V * IS, x[b][0]);
-        if constexpr (PATH == kHalves) {
-          // a unit of the first half with its partner, or two of the channels behind
-          const int c = unit[b] < cols ? unit[b] * V : a.rot + 2 * (unit[b] - cols) * V;
-          load<IN, V>(in[b] + c * IS, x[b][0]);
-          load<IN, V>(in[b] + (c + (unit[b] < cols ? pairs : V)) * IS, x[b][1]);
-        }
-      }
-    }
-    if constexpr (PATH == kAdjacent || PATH == kHalves) {
+      if (it[b].unit < 0) continue;
+      const int unit = it[b].unit;
+      const float2 *w = table + it[b].tok * cols * P;
+      if constexpr (kWide) {
+        float v[W][V];
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
-        if (unit[b] >= 0) {
-          const bool turned = unit[b] < cols;
-          const float2 *w = table + tok[b] * cols * P + unit[b];
-          if (turned) {
+        for (int k = 0; k < W; ++k) x[b][k].get(v[k]);
+        if (unit < cols) {
 #pragma unroll
-            for (int j = 0; j < P; ++j) {
-              float &u = PATH == kHalves ? x[b][0][j] : x[b][0][2 * j], &v = PATH == kHalves ? x[b][PATH == kHalves][j] : x[b][0][2 * j + 1];
-              const float2 f = turn_pair(u, v, w[j * cols]);
-              u = f.x, v = f.y;
-            }
-          }
-          if constexpr (PATH == kAdjacent) {
-            store<OUT, V>(out[b] + unit[b] * V * OS, x[b][0]);
-          } else {
-            const int c = turned ? unit[b] * V : a.rot + 2 * (unit[b] - cols) * V;
-            store<OUT, V>(out[b] + c * OS, x[b][0]);
-            store<OUT, V>(out[b] + (c + (turned ? pairs : V)) * OS, x[b][PATH == kHalves]);
+          for (int j = 0; j < P; ++j) {
+            float &u = PATH == kHalves ? v[0][j] : v[0][2 * j], &y = PATH == kHalves ? v[W - 1][j] : v[0][2 * j + 1];
+            const float2 f = turn_pair(u, y, w[j * cols + unit]);
+            u = f.x, y = f.y;
           }
         }
-    } else if constexpr (PATH == kGather) {
-      // a head is `units` lanes of one warp (units a power of two up to 32): all load before one stores
-      if (unit[0] >= 0) {
-        const float2 *w = table + tok[0] * cols * P;
-        float y[V];
+#pragma unroll
+        for (int k = 0; k < W; ++k) store<OUT, V>(it[b].out + channel(unit, k) * OS, v[k]);
+      } else if constexpr (PATH == kGather) {
+        // a head is `units` lanes of one warp (units a power of two up to 32): all load before one stores
+        float v[V], y[V];
+        x[b][0].get(v);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int c = unit[0] * V + j;
-          y[j] = c < a.rot ? load1<IN>(in[0] + (c < pairs ? c + pairs : c - pairs) * IS) : 0.0f;
+          const int c = unit * V + j;
+          y[j] = c < a.rot ? load1<IN>(it[b].in + (c < pairs ? c + pairs : c - pairs) * IS) : 0.0f;
         }
         __syncwarp((units == 32 ? kFull : (1u << units) - 1) << (threadIdx.x & 31 & ~(units - 1)));
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-          const int c = unit[0] * V + j, p = c < pairs ? c : c - pairs;
+          const int c = unit * V + j, p = c < pairs ? c : c - pairs;
           if (c < a.rot) {
             const float2 f = w[(p % P) * cols + p / P];
-            x[0][0][j] = c < pairs ? __fmaf_rn(x[0][0][j], f.x, -__fmul_rn(y[j], f.y)) : __fmaf_rn(y[j], f.y, __fmul_rn(x[0][0][j], f.x));
+            v[j] = c < pairs ? __fmaf_rn(v[j], f.x, -__fmul_rn(y[j], f.y)) : __fmaf_rn(y[j], f.y, __fmul_rn(v[j], f.x));
           }
         }
-        store<OUT, V>(out[0] + unit[0] * V * OS, x[0][0]);
-      }
-    } else {
-      const int p = unit[0];  // a pair, then the channels behind
-      if (p < pairs) {
-        const float2 f = turn_pair(load1<IN>(in[0] + p * IS), load1<IN>(in[0] + (p + pairs) * IS), table[tok[0] * cols + p]);
-        store1<OUT>(out[0] + p * OS, f.x);
-        store1<OUT>(out[0] + (p + pairs) * OS, f.y);
+        store<OUT, V>(it[b].out + unit * V * OS, v);
+      } else if (unit < pairs) {  // a pair, then the channels behind
+        const float2 f = turn_pair(load1<IN>(it[b].in + unit * IS), load1<IN>(it[b].in + (unit + pairs) * IS), w[unit]);
+        store1<OUT>(it[b].out + unit * OS, f.x);
+        store1<OUT>(it[b].out + (unit + pairs) * OS, f.y);
       } else {
-        const int c = p + pairs;
-        store1<OUT>(out[0] + c * OS, load1<IN>(in[0] + c * IS));
+        const int c = unit + pairs;
+        store1<OUT>(it[b].out + c * OS, load1<IN>(it[b].in + c * IS));
       }
     }
+    i0 += NB * kThreads;
+    if (i0 < n) fetch(i0);
   }
 }
 
@@ -208,11 +231,8 @@ cudaError_t launch_path(const RotaryArgs &a, int sms, cudaStream_t stream) {
                   : PATH == kHalves   ? (a.in_place ? cols : a.dim / (2 * V))
                   : PATH == kGather   ? a.dim / V
                                       : (a.in_place ? pairs : a.dim - pairs);
-  // tokens of a CTA: enough units for four of each thread, where CTAs remain for four waves
-  const int64_t work = int64_t(units) * (a.heads[0] + a.heads[1]);
-  int tokens = 1;
-  while (tokens < kMaxTokens && tokens * work < 4 * kThreads && a.n_tokens / (2 * tokens) >= int64_t(sms) * 16) tokens *= 2;
-  while (tokens > 1 && (pairs + tokens * cols * P) * 8 > 100 * 1024) tokens /= 2;
+  int tokens = int(std::min<int64_t>(kMaxTokens, (a.n_tokens + int64_t(sms) * kResident - 1) / (int64_t(sms) * kResident)));
+  while (tokens > 1 && (pairs + tokens * cols * P) * 8 > 48 * 1024) tokens /= 2;
   const int smem = (pairs + tokens * cols * P) * 8;
   const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_rotary<IN, OUT, PATH>), smem);
   if (e != cudaSuccess) return e;
