@@ -41,6 +41,11 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   const float l = __fadd_rn(s.l, __fadd_rn(a.l, b.l)), h = __fadd_rn(s.h, l);
   return Two{h, __fsub_rn(l, __fsub_rn(h, s.h))};
 }
+// without the last normalization: the low parts stay small enough for some twenty such sums
+__device__ __forceinline__ Two add_loose(Two a, Two b) {
+  const Two s = two_sum(a.h, b.h);
+  return Two{s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l))};
+}
 __device__ __forceinline__ Two mul(Two a, Two b) {
   const float p = __fmul_rn(a.h, b.h);
   const float e = __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.h, b.h, -p)));
@@ -68,23 +73,31 @@ __device__ __forceinline__ float lo(uint64_t v) { return __uint_as_float(uint32_
 __device__ __forceinline__ float hi(uint64_t v) { return __uint_as_float(uint32_t(v >> 32)); }
 __device__ __forceinline__ uint64_t fsub2(uint64_t a, uint64_t b) { return ffma2(two(-1.0f), b, a); }
 
-// 8 values of a row as pairs
+// 8 values of a row as they lie in memory, and as pairs
 template <int ELEM>
-__device__ __forceinline__ void load8(const uint8_t *p, uint64_t (&v)[4]) {
-  if constexpr (ELEM == kElemF32) {
-    const float4 a = __ldcs(reinterpret_cast<const float4 *>(p)), b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = pack2(__float_as_uint(a.x), __float_as_uint(a.y)), v[1] = pack2(__float_as_uint(a.z), __float_as_uint(a.w));
-    v[2] = pack2(__float_as_uint(b.x), __float_as_uint(b.y)), v[3] = pack2(__float_as_uint(b.z), __float_as_uint(b.w));
-  } else {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw8 {
+  uint4 w[ELEM == kElemF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const uint8_t *p) {
+    w[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
+    if constexpr (ELEM == kElemF32) w[1] = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() {
+    w[0] = make_uint4(0, 0, 0, 0);
+    if constexpr (ELEM == kElemF32) w[1] = w[0];
+  }
+  __device__ __forceinline__ void get(uint64_t (&v)[4]) const {
+    if constexpr (ELEM == kElemF32) {
+      v[0] = pack2(w[0].x, w[0].y), v[1] = pack2(w[0].z, w[0].w), v[2] = pack2(w[1].x, w[1].y), v[3] = pack2(w[1].z, w[1].w);
+    } else {
+      const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack_pair<ELEM>(w[i]);
-      v[i] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack_pair<ELEM>(u[i]);
+        v[i] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
+      }
     }
   }
-}
+};
 template <int ELEM>
 __device__ __forceinline__ void store8(uint8_t *p, const uint64_t (&v)[4]) {
   if constexpr (ELEM == kElemF32) {
@@ -119,156 +132,173 @@ __device__ __forceinline__ void codes8(const uint64_t (&v)[4], float ds, float i
   w1 = pack_bytes(t[4], t[5], t[6], t[7]);
 }
 
-// A row by blockDim.x threads, blockDim.y rows per CTA (more than one only
-// where a warp has a row); a thread has U units of 8 values, 4 lanes a block.
-template <int ELEM, int U>
-__global__ void __launch_bounds__(U == 4 ? 128 : 1024, 1) k_add_rms_norm(const NormArgs a) {
-  __shared__ Two part[32];
+// Rows by blockDim.x threads each, blockDim.y of them at a time in a CTA (more than
+// one only where a warp has a row), the next ones' loads in flight while these are
+// worked on; a thread has U units of 8 values, 4 lanes a block.
+template <int ELEM, int U, int MAX>
+__global__ void __launch_bounds__(MAX, MAX == 256 ? 3 : MAX == 128 ? 6 : 1) k_add_rms_norm(const NormArgs a) {
+  __shared__ Two part[2][32];
   extern __shared__ __align__(16) uint8_t staged[];  // the rows' blocks, each row as far past 16 bytes as in q8
   constexpr int ES = Elem<ELEM>::kBytes;
   const int n_units = a.n_cols / 8, step = blockDim.x, lane = threadIdx.x & 31;
-  const int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (row >= a.n_rows) return;  // whole warps; with several warps per row there is one row per CTA
-  uint64_t v[U][4];
+  const int row_bytes = a.n_cols / kQK * Fmt<kTypeQ8_0>::kBytes;
+  const bool words = row_bytes % 4 == 0;  // an even number of blocks: rows of whole words
+  const int64_t stride = int64_t(gridDim.x) * blockDim.y;
+  Raw8<ELEM> x[U], r[U];
+  auto fetch = [&](int64_t row) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int unit = threadIdx.x + u * step;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[u][i] = 0;
-    if (unit < n_units) load8<ELEM>(a.x + row * a.x_row + int64_t(unit) * 8 * ES, v[u]);
-  }
-  if (a.res) {
-    constexpr int kAhead = U < 4 ? U : 4;  // units whose residual is in flight
-#pragma unroll
-    for (int u0 = 0; u0 < U; u0 += kAhead) {
-      uint64_t r[kAhead][4];
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int unit = threadIdx.x + (u0 + k) * step;
-        if (unit < n_units) load8<ELEM>(a.res + row * a.res_row + int64_t(unit) * 8 * ES, r[k]);
+    for (int u = 0; u < U; ++u) {
+      const int unit = threadIdx.x + u * step;
+      if (unit < n_units) {
+        x[u].load(a.x + row * a.x_row + int64_t(unit) * 8 * ES);
+        if (a.res) r[u].load(a.res + row * a.res_row + int64_t(unit) * 8 * ES);
       }
+    }
+  };
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const int unit = threadIdx.x + (u0 + k) * step;
-        uint64_t(&w)[4] = v[u0 + k];
-        if (unit < n_units) {
+  for (int u = 0; u < U; ++u) x[u].zero(), r[u].zero();
+  int64_t row = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+  if (row < a.n_rows) fetch(row);
+  // rows end for whole warps; with several warps per row there is one row per CTA
+  for (int turn = 0; row < a.n_rows; row += stride, turn ^= 1) {
+    uint64_t v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int unit = threadIdx.x + u * step;
+      x[u].get(v[u]);
+      if (a.res && unit < n_units) {
+        uint64_t w[4];
+        r[u].get(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[u][i] = fadd2(v[u][i], w[i]);
+        uint8_t *to = a.sum + row * a.sum_row + int64_t(unit) * 8 * ES;
+        if constexpr (ELEM == kElemF32) {
+          if (a.sum) store8<ELEM>(to, v[u]);
+        } else {
+          uint32_t h[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            w[i] = fadd2(w[i], r[k][i]);
-            if constexpr (ELEM != kElemF32) {
-              const float2 f = unpack_pair<ELEM>(pack_pair<ELEM>(lo(w[i]), hi(w[i])));
-              w[i] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
-            }
+            h[i] = pack_pair<ELEM>(lo(v[u][i]), hi(v[u][i]));
+            const float2 f = unpack_pair<ELEM>(h[i]);
+            v[u][i] = pack2(__float_as_uint(f.x), __float_as_uint(f.y));
           }
-          if (a.sum) store8<ELEM>(a.sum + row * a.sum_row + int64_t(unit) * 8 * ES, w);
+          if (a.sum) *reinterpret_cast<uint4 *>(to) = make_uint4(h[0], h[1], h[2], h[3]);
         }
       }
     }
-  }
-  Two2 s2{0, 0};
+    if (row + stride < a.n_rows) fetch(row + stride);
+    Two2 s2{0, 0};
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint64_t p = fmul2(v[u][i], v[u][i]);
-      const uint64_t sum = fadd2(s2.h, p), t = fsub2(sum, s2.h);
-      uint64_t e = fadd2(fsub2(s2.h, fsub2(sum, t)), fsub2(p, t));
-      // a 16-bit type's square has no error (22 bits at most)
-      if constexpr (ELEM == kElemF32) e = fadd2(e, ffma2(v[u][i], v[u][i], fsub2(0, p)));
-      s2 = Two2{sum, fadd2(s2.l, e)};
-    }
-  Two s = add(Two{lo(s2.h), lo(s2.l)}, Two{hi(s2.h), hi(s2.l)});
-#pragma unroll
-  for (int d = 16; d; d >>= 1) s = add(s, Two{__shfl_xor_sync(kFull, s.h, d), __shfl_xor_sync(kFull, s.l, d)});
-  if (step > 32) {
-    const int warp = threadIdx.x >> 5, warps = step >> 5;
-    if (lane == 0) part[warp] = s;
-    __syncthreads();
-    s = lane < warps ? part[lane] : Two{0.0f, 0.0f};
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s = add(s, Two{__shfl_xor_sync(kFull, s.h, d), __shfl_xor_sync(kFull, s.l, d)});
-  }
-  const float f = factor(s, a);
-  const int row_bytes = a.n_cols / kQK * Fmt<kTypeQ8_0>::kBytes;
-  uint8_t *const q8 = a.q8 + row * row_bytes;
-  const bool words = row_bytes % 4 == 0;  // an even number of blocks: rows of whole words
-  const int shift = words ? int(reinterpret_cast<uintptr_t>(q8) & 15) : 0;
-  uint8_t *const stage = staged + threadIdx.y * ((row_bytes + 32) / 16 * 16) + shift;
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int unit = threadIdx.x + u * step;
-    const bool live = unit < n_units;  // the same for the 4 lanes of a block, and with words for those of two
-    float m = 0.0f;
-    if (live) {
-      const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * unit), w1 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * unit + 1);
-      const uint64_t w[4] = {pack2(__float_as_uint(w0.x), __float_as_uint(w0.y)), pack2(__float_as_uint(w0.z), __float_as_uint(w0.w)),
-                             pack2(__float_as_uint(w1.x), __float_as_uint(w1.y)), pack2(__float_as_uint(w1.z), __float_as_uint(w1.w))};
+    for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        v[u][i] = fmul2(fmul2(v[u][i], two(f)), w[i]);
-        m = fmaxf(m, fmaxf(fabsf(lo(v[u][i])), fabsf(hi(v[u][i]))));
+        const uint64_t p = fmul2(v[u][i], v[u][i]);
+        const uint64_t sum = fadd2(s2.h, p), t = fsub2(sum, s2.h);
+        uint64_t e = fadd2(fsub2(s2.h, fsub2(sum, t)), fsub2(p, t));
+        // a 16-bit type's square has no error (22 bits at most)
+        if constexpr (ELEM == kElemF32) e = fadd2(e, ffma2(v[u][i], v[u][i], fsub2(0, p)));
+        s2 = Two2{sum, fadd2(s2.l, e)};
       }
-      if (a.out) store8<ELEM>(a.out + row * a.out_row + int64_t(unit) * 8 * ES, v[u]);
-    }
-    if (a.q8) {
-      m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-      m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-      uint16_t bits;
-      float ds;
-      block_scale<kTypeQ8_0>(m, bits, ds);
-      uint32_t w0, w1;
-      codes8(v[u], ds, ds > 0.0f ? rcp_approx(ds) : 0.0f, w0, w1);
-      if (words) {
-        // two blocks are 17 words: those of the first lie two bytes off its codes
-        const uint32_t before = __shfl_up_sync(kFull, w1 >> 16, 1);
-        const int j = unit & 7;
-        if (live) {
-          uint32_t *pair = reinterpret_cast<uint32_t *>(stage + unit / 8 * 68);
-          if (j < 4) {
-            pair[2 * j] = (j == 0 ? bits : before) | w0 << 16;
-            pair[2 * j + 1] = __funnelshift_r(w0, w1, 16);
-          } else {
-            if (j == 4) pair[8] = before | uint32_t(bits) << 16;
-            pair[2 * j + 1] = w0;
-            pair[2 * j + 2] = w1;
-          }
-        }
-      } else if (live) {
-        uint16_t *block = reinterpret_cast<uint16_t *>(q8 + unit / 4 * Fmt<kTypeQ8_0>::kBytes);
-        const int j = unit & 3;
-        if (j == 0) block[0] = bits;
-        block[1 + 4 * j] = uint16_t(w0);
-        block[2 + 4 * j] = uint16_t(w0 >> 16);
-        block[3 + 4 * j] = uint16_t(w1);
-        block[4 + 4 * j] = uint16_t(w1 >> 16);
-      }
-    }
-  }
-  if (a.q8 && words) {
-    if (step > 32)
+    Two s = add_loose(Two{lo(s2.h), lo(s2.l)}, Two{hi(s2.h), hi(s2.l)});
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s = add_loose(s, Two{__shfl_xor_sync(kFull, s.h, d), __shfl_xor_sync(kFull, s.l, d)});
+    if (step > 32) {
+      const int warp = threadIdx.x >> 5, warps = step >> 5;
+      if (lane == 0) part[turn][warp] = s;
       __syncthreads();
-    else
-      __syncwarp();
-    const uint8_t *from = stage - shift;
-    uint8_t *to = q8 - shift;
-    for (int i = threadIdx.x * 16; i < shift + row_bytes; i += step * 16) {
-      if (i >= shift && i + 16 <= shift + row_bytes) {
-        *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
-      } else {
-        for (int k = i; k < i + 16; k += 4)
-          if (k >= shift && k < shift + row_bytes) *reinterpret_cast<uint32_t *>(to + k) = *reinterpret_cast<const uint32_t *>(from + k);
+      s = lane < warps ? part[turn][lane] : Two{0.0f, 0.0f};
+      for (int d = warps <= 4 ? 2 : warps <= 8 ? 4 : 16; d; d >>= 1) s = add_loose(s, Two{__shfl_xor_sync(kFull, s.h, d), __shfl_xor_sync(kFull, s.l, d)});
+      if (warps <= 8) s = Two{__shfl_sync(kFull, s.h, 0), __shfl_sync(kFull, s.l, 0)};
+    } else {
+      __syncwarp();  // the row before this one has left the staging place
+    }
+    const float f = factor(add(s, Two{0.0f, 0.0f}), a);
+    uint8_t *const q8 = a.q8 + row * row_bytes;
+    const int shift = words ? int(reinterpret_cast<uintptr_t>(q8) & 15) : 0;
+    uint8_t *const stage = staged + threadIdx.y * ((row_bytes + 32) / 16 * 16) + shift;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int unit = threadIdx.x + u * step;
+      const bool live = unit < n_units;  // the same for the 4 lanes of a block, and with words for those of two
+      float m = 0.0f;
+      if (live) {
+        const float4 w0 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * unit), w1 = __ldg(reinterpret_cast<const float4 *>(a.weight) + 2 * unit + 1);
+        const uint64_t w[4] = {pack2(__float_as_uint(w0.x), __float_as_uint(w0.y)), pack2(__float_as_uint(w0.z), __float_as_uint(w0.w)),
+                               pack2(__float_as_uint(w1.x), __float_as_uint(w1.y)), pack2(__float_as_uint(w1.z), __float_as_uint(w1.w))};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[u][i] = fmul2(fmul2(v[u][i], two(f)), w[i]);
+          m = fmaxf(m, fmaxf(fabsf(lo(v[u][i])), fabsf(hi(v[u][i]))));
+        }
+        if (a.out) store8<ELEM>(a.out + row * a.out_row + int64_t(unit) * 8 * ES, v[u]);
+      }
+      if (a.q8) {
+        m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+        uint16_t bits;
+        float ds;
+        block_scale<kTypeQ8_0>(m, bits, ds);
+        uint32_t w0, w1;
+        codes8(v[u], ds, ds > 0.0f ? rcp_approx(ds) : 0.0f, w0, w1);
+        if (words) {
+          // two blocks are 17 words: those of the first lie two bytes off its codes
+          const uint32_t before = __shfl_up_sync(kFull, w1 >> 16, 1);
+          const int j = unit & 7;
+          if (live) {
+            uint32_t *pair = reinterpret_cast<uint32_t *>(stage + unit / 8 * 68);
+            if (j < 4) {
+              pair[2 * j] = (j == 0 ? bits : before) | w0 << 16;
+              pair[2 * j + 1] = __funnelshift_r(w0, w1, 16);
+            } else {
+              if (j == 4) pair[8] = before | uint32_t(bits) << 16;
+              pair[2 * j + 1] = w0;
+              pair[2 * j + 2] = w1;
+            }
+          }
+        } else if (live) {
+          uint16_t *block = reinterpret_cast<uint16_t *>(q8 + unit / 4 * Fmt<kTypeQ8_0>::kBytes);
+          const int j = unit & 3;
+          if (j == 0) block[0] = bits;
+          block[1 + 4 * j] = uint16_t(w0);
+          block[2 + 4 * j] = uint16_t(w0 >> 16);
+          block[3 + 4 * j] = uint16_t(w1);
+          block[4 + 4 * j] = uint16_t(w1 >> 16);
+        }
+      }
+    }
+    if (a.q8 && words) {
+      if (step > 32)
+        __syncthreads();
+      else
+        __syncwarp();
+      const uint8_t *from = stage - shift;
+      uint8_t *to = q8 - shift;
+      for (int i = threadIdx.x * 16; i < shift + row_bytes; i += step * 16) {
+        if (i >= shift && i + 16 <= shift + row_bytes) {
+          *reinterpret_cast<uint4 *>(to + i) = *reinterpret_cast<const uint4 *>(from + i);
+        } else {
+          for (int k = i; k < i + 16; k += 4)
+            if (k >= shift && k < shift + row_bytes) *reinterpret_cast<uint32_t *>(to + k) = *reinterpret_cast<const uint32_t *>(from + k);
+        }
       }
     }
   }
 }
 
-template <int ELEM, int U>
-cudaError_t launch(const NormArgs &a, int threads, int rows, cudaStream_t stream) {
+template <int ELEM, int U, int MAX>
+cudaError_t launch(const NormArgs &a, int threads, int rows, int sms, cudaStream_t stream) {
   const int row_bytes = a.n_cols / kQK * Fmt<kTypeQ8_0>::kBytes;
   const int smem = a.q8 && row_bytes % 4 == 0 ? rows * ((row_bytes + 32) / 16 * 16) : 0;
-  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_add_rms_norm<ELEM, U>), smem);
+  const void *fn = reinterpret_cast<const void *>(k_add_rms_norm<ELEM, U, MAX>);
+  cudaError_t e = ensure_smem(fn, smem);
   if (e != cudaSuccess) return e;
-  k_add_rms_norm<ELEM, U><<<unsigned((a.n_rows + rows - 1) / rows), dim3(threads, rows), smem, stream>>>(a);
+  int64_t grid = (a.n_rows + rows - 1) / rows;
+  if (grid > sms) {  // as many CTAs as are resident, each with rows to come
+    int per_sm = 0;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, fn, threads * rows, smem)) != cudaSuccess) return e;
+    grid = std::min(grid, int64_t(sms) * std::max(per_sm, 1));
+  }
+  k_add_rms_norm<ELEM, U, MAX><<<unsigned(grid), dim3(threads, rows), smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -276,12 +306,13 @@ template <int ELEM>
 cudaError_t launch_elem(const NormArgs &a, int sms, cudaStream_t stream) {
   const int units = a.n_cols / 8;
   auto threads = [&](int u) { return (units + 32 * u - 1) / (32 * u) * 32; };  // whole warps, u units each
-  if (units <= 32) return launch<ELEM, 1>(a, 32, 4, stream);
+  if (units <= 32) return launch<ELEM, 1, 128>(a, 32, 4, sms, stream);
   // few rows: a row's latency counts, so one unit per thread
-  if (a.n_rows <= 2 * sms && threads(1) <= 1024) return launch<ELEM, 1>(a, threads(1), 1, stream);
-  if (units <= 128) return launch<ELEM, 4>(a, 32, 4, stream);
-  if (threads(2) <= 1024) return launch<ELEM, 2>(a, threads(2), 1, stream);
-  return launch<ELEM, 8>(a, 1024, 1, stream);
+  if (a.n_rows <= 2 * sms && threads(1) <= 1024) return launch<ELEM, 1, 1024>(a, threads(1), 1, sms, stream);
+  if (units <= 64) return launch<ELEM, 2, 128>(a, 32, 4, sms, stream);
+  if (threads(2) <= 256) return launch<ELEM, 2, 256>(a, threads(2), 1, sms, stream);
+  if (threads(2) <= 1024) return launch<ELEM, 2, 1024>(a, threads(2), 1, sms, stream);
+  return launch<ELEM, 8, 1024>(a, 1024, 1, sms, stream);
 }
 
 }  // namespace
