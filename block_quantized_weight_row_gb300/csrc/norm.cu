@@ -109,6 +109,16 @@ __device__ __forceinline__ void store8(uint8_t *p, const uint64_t (&v)[4]) {
   }
 }
 
+// m / 127 rounded once, for the magnitudes whose quotient is not far below
+// binary16's range (the others round to a scale of zero either way): a quotient
+// within one step, its exact remainder, and the correction by the correctly rounded
+// reciprocal, which gives the rounded quotient (Markstein 1990, theorem 7; the
+// divisor's significand is not all ones).
+__device__ __forceinline__ float div127(float m) {
+  const float y = 1.0f / 127.0f, q = __fmul_rn(m, y);
+  return __fmaf_rn(__fmaf_rn(-127.0f, q, m), y, q);
+}
+
 // 8 codes as two words of bytes: the rule of quantize_block_lane, exact per value
 __device__ __forceinline__ void codes8(const uint64_t (&v)[4], float ds, float inv, uint32_t &w0, uint32_t &w1) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
@@ -136,7 +146,7 @@ __device__ __forceinline__ void codes8(const uint64_t (&v)[4], float ds, float i
 // one only where a warp has a row), the next ones' loads in flight while these are
 // worked on; a thread has U units of 8 values, 4 lanes a block.
 template <int ELEM, int U, int MAX>
-__global__ void __launch_bounds__(MAX, MAX == 256 ? 3 : MAX == 128 ? 6 : 1) k_add_rms_norm(const NormArgs a) {
+__global__ void __launch_bounds__(MAX, U == 4 ? 512 / MAX : MAX == 256 ? 3 : MAX == 128 ? 6 : 1) k_add_rms_norm(const NormArgs a) {
   __shared__ Two part[2][32];
   extern __shared__ __align__(16) uint8_t staged[];  // the rows' blocks, each row as far past 16 bytes as in q8
   constexpr int ES = Elem<ELEM>::kBytes;
@@ -235,9 +245,8 @@ __global__ void __launch_bounds__(MAX, MAX == 256 ? 3 : MAX == 128 ? 6 : 1) k_ad
       if (a.q8) {
         m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
         m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-        uint16_t bits;
-        float ds;
-        block_scale<kTypeQ8_0>(m, bits, ds);
+        const uint16_t bits = __half_as_ushort(__float2half_rn(div127(m)));
+        const float ds = half_bits_to_float(bits);
         uint32_t w0, w1;
         codes8(v[u], ds, ds > 0.0f ? rcp_approx(ds) : 0.0f, w0, w1);
         if (words) {
@@ -246,14 +255,11 @@ __global__ void __launch_bounds__(MAX, MAX == 256 ? 3 : MAX == 128 ? 6 : 1) k_ad
           const int j = unit & 7;
           if (live) {
             uint32_t *pair = reinterpret_cast<uint32_t *>(stage + unit / 8 * 68);
-            if (j < 4) {
-              pair[2 * j] = (j == 0 ? bits : before) | w0 << 16;
-              pair[2 * j + 1] = __funnelshift_r(w0, w1, 16);
-            } else {
-              if (j == 4) pair[8] = before | uint32_t(bits) << 16;
-              pair[2 * j + 1] = w0;
-              pair[2 * j + 2] = w1;
-            }
+            const bool first = j < 4;
+            const int at = 2 * j + !first;
+            pair[at] = first ? (j == 0 ? bits : before) | w0 << 16 : w0;
+            pair[at + 1] = first ? __funnelshift_r(w0, w1, 16) : w1;
+            if (j == 4) pair[8] = before | uint32_t(bits) << 16;
           }
         } else if (live) {
           uint16_t *block = reinterpret_cast<uint16_t *>(q8 + unit / 4 * Fmt<kTypeQ8_0>::kBytes);
@@ -310,8 +316,13 @@ cudaError_t launch_elem(const NormArgs &a, int sms, cudaStream_t stream) {
   // few rows: a row's latency counts, so one unit per thread
   if (a.n_rows <= 2 * sms && threads(1) <= 1024) return launch<ELEM, 1, 1024>(a, threads(1), 1, sms, stream);
   if (units <= 64) return launch<ELEM, 2, 128>(a, 32, 4, sms, stream);
-  if (threads(2) <= 256) return launch<ELEM, 2, 256>(a, threads(2), 1, sms, stream);
-  if (threads(2) <= 1024) return launch<ELEM, 2, 1024>(a, threads(2), 1, sms, stream);
+  if (units <= 128) return launch<ELEM, 4, 128>(a, 32, 4, sms, stream);
+  // four units where three warps or more have a row: the sums over its threads are
+  // a quarter of the instructions then, half with two (112 us for 115 at 16384 x 4096)
+  if (units <= 256) return launch<ELEM, 2, 256>(a, threads(2), 1, sms, stream);
+  if (units <= 512) return launch<ELEM, 4, 128>(a, threads(4), 1, sms, stream);
+  if (units <= 1024) return launch<ELEM, 4, 256>(a, threads(4), 1, sms, stream);
+  if (units <= 2048) return launch<ELEM, 2, 1024>(a, threads(2), 1, sms, stream);
   return launch<ELEM, 8, 1024>(a, 1024, 1, sms, stream);
 }
 

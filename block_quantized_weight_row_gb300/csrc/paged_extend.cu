@@ -24,7 +24,6 @@
 namespace bq {
 namespace {
 
-constexpr int kPerThread = 2;     // tokens of a thread: one 16-byte store of slots
 constexpr int kMaxChunks = 1024;  // chunks of 32 sequences, or of several times 32 beyond 32768 sequences
 constexpr uint32_t kCap = 0x7fffffffu;
 
@@ -74,12 +73,12 @@ struct Record {
   int seq, base;       // base: place in the free list of page column 0, if that were new; INT_MIN: the sequence gets nothing
 };
 
-// NT threads; chunks of 32 * rounds sequences
-template <int NT>
+// NT threads with kPerThread tokens of a tile each; chunks of 32 * rounds sequences
+template <int NT, int kPerThread>
 __global__ void __launch_bounds__(NT, 1) k_paged_extend(const ExtendArgs a, const int chunks, const int rounds) {
   constexpr int kWarps = NT / 32, kTile = NT * kPerThread, kEach = kMaxChunks / NT;
-  __shared__ Record rec[kTile];
-  __shared__ short head[kTile];  // the token itself where a sequence begins in the tile, else -1
+  extern __shared__ __align__(16) Record rec[];           // of the sequence that begins at a token of the tile
+  __shared__ __align__(8) short head[kTile];  // the token itself where a sequence begins in the tile, else -1
   __shared__ uint32_t tok[kMaxChunks + 1], pag[kMaxChunks + 1];  // sums of a chunk, then before it
   __shared__ uint32_t sums[2][kWarps];
   __shared__ int warp_head[kWarps];
@@ -207,10 +206,10 @@ __global__ void __launch_bounds__(NT, 1) k_paged_extend(const ExtendArgs a, cons
 
     // ---- the latest sequence that began at or before each token ----
     const int at = tid * kPerThread;
-    int h[kPerThread], m = -1;
+    int h[kPerThread];
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) h[i] = m = max(m, int(head[at + i]));
-    int run = m;
+    for (int i = 0; i < kPerThread; ++i) h[i] = i ? max(int(head[at + i]), h[i ? i - 1 : 0]) : head[at];
+    int run = h[kPerThread - 1];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(kFull, run, d);
@@ -220,15 +219,15 @@ __global__ void __launch_bounds__(NT, 1) k_paged_extend(const ExtendArgs a, cons
     int before = __shfl_up_sync(kFull, run, 1);
     if (lane == 0) before = -1;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) before = max(before, warp_head[w]);
+    before = max(before, __reduce_max_sync(kFull, lane < warp ? warp_head[lane] : -1));
 
-    longlong2 slot;
+    long long slot[kPerThread];
     int pos[kPerThread];
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
       const uint32_t t = lo + at + i;
       const int k = max(h[i], before);
-      int64_t sl = -1;
+      slot[i] = -1;
       pos[i] = 0;
       if (t < n_slots && t < all_tokens && k >= 0) {
         const Record r = rec[k];
@@ -241,42 +240,44 @@ __global__ void __launch_bounds__(NT, 1) k_paged_extend(const ExtendArgs a, cons
           const int page = fresh ? __ldg(a.free_pages + (r.base + int(col))) : *entry;
           if (uint32_t(page) < a.n_pages) {
             if (fresh && place == 0) *entry = page;
-            sl = int64_t(page) * P + place;
+            slot[i] = int64_t(page) * P + place;
           } else {
             bad = kErrIndex;
           }
         }
       }
-      (i == 0 ? slot.x : slot.y) = sl;
     }
     const uint32_t t = lo + at;
-    if (t + 1 < n_slots && a.wide) {
-      *reinterpret_cast<longlong2 *>(a.slots + t) = slot;
-      if (a.positions) *reinterpret_cast<int2 *>(a.positions + t) = make_int2(pos[0], pos[1]);
+    if (t + kPerThread <= n_slots && a.wide) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; i += 2) {
+        *reinterpret_cast<longlong2 *>(a.slots + t + i) = make_longlong2(slot[i], slot[i + 1]);
+        if (a.positions) *reinterpret_cast<int2 *>(a.positions + t + i) = make_int2(pos[i], pos[i + 1]);
+      }
     } else {
-      if (t < n_slots) {
-        a.slots[t] = slot.x;
-        if (a.positions) a.positions[t] = pos[0];
-      }
-      if (t + 1 < n_slots) {
-        a.slots[t + 1] = slot.y;
-        if (a.positions) a.positions[t + 1] = pos[1];
-      }
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i)
+        if (t + i < n_slots) {
+          a.slots[t + i] = slot[i];
+          if (a.positions) a.positions[t + i] = pos[i];
+        }
     }
     __syncthreads();  // the next tile writes rec, head and met
   }
   if (bad) atomicOr(a.err, bad);
 }
 
-template <int NT>
+template <int NT, int PT>
 cudaError_t launch(const ExtendArgs &a, int sms, cudaStream_t stream) {
   const int rounds = std::max(1, (a.n_seqs + 32 * kMaxChunks - 1) / (32 * kMaxChunks));
   const int chunks = (a.n_seqs + 32 * rounds - 1) / (32 * rounds);
-  constexpr int kTile = NT * kPerThread;
+  constexpr int kTile = NT * PT, kSmem = kTile * int(sizeof(Record));
   const int64_t tiles = (int64_t(a.n_slots) + kTile - 1) / kTile, shares = (chunks + NT / 32 - 1) / (NT / 32);
   // one CTA per SM at most: each sums up all sequences
   const int64_t grid = std::min<int64_t>(std::max<int64_t>(std::max(tiles, shares), 1), sms);
-  k_paged_extend<NT><<<unsigned(grid), NT, 0, stream>>>(a, chunks, rounds);
+  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(k_paged_extend<NT, PT>), kSmem);
+  if (e != cudaSuccess) return e;
+  k_paged_extend<NT, PT><<<unsigned(grid), NT, kSmem, stream>>>(a, chunks, rounds);
   return cudaGetLastError();
 }
 
@@ -293,7 +294,10 @@ cudaError_t launch_paged_extend(ExtendArgs a, cudaStream_t stream) {
     if (a.page_size == 1u << k) a.page_shift = k;
   a.page_magic = ~uint64_t(0) / (a.page_size / 16) + 1;
   // a decode step of a few hundred sequences: fewer threads meet at a barrier sooner
-  return a.n_seqs <= 512 && a.n_slots <= 2048 ? launch<256>(a, di->sm_count, stream) : launch<1024>(a, di->sm_count, stream);
+  if (a.n_seqs <= 512 && a.n_slots <= 2048) return launch<256, 2>(a, di->sm_count, stream);
+  // small tiles as long as every SM has one at most; then fewer turns count (936000 tokens: 15.3 us for 18.4)
+  if (int64_t(a.n_slots) <= int64_t(di->sm_count) * 2048) return launch<1024, 2>(a, di->sm_count, stream);
+  return launch<1024, 4>(a, di->sm_count, stream);
 }
 
 }  // namespace bq
