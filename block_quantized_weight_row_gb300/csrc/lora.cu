@@ -721,8 +721,9 @@ constexpr int kTcThreads = 320, kTcCols = 128, kTcTokens = 64, kTcTmem = 2 * kTc
 constexpr int kTcBTile = kTcCols * 128, kTcHTile = kTcTokens * 128;  // 64 ranks: rows of 128 bytes
 
 struct ExpandTc {
-  int blocks, stages, terms;  // blocks of 64 ranks
-  __host__ __device__ int h_off() const { return stages * blocks * kTcBTile; }
+  static constexpr int kStages = 3;  // of B: a block of 64 ranks each
+  int blocks, terms;                 // blocks of 64 ranks
+  __host__ __device__ int h_off() const { return kStages * kTcBTile; }
   __host__ __device__ int bar_off() const { return h_off() + terms * blocks * kTcHTile; }
   __host__ __device__ int bytes() const { return bar_off() + 128 + 1024; }  // + room to align the base
 };
@@ -744,17 +745,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
-template <int YE>
-__device__ __forceinline__ float load_one(const uint8_t *p) {
-  if constexpr (YE == kElemF32) return __ldcs(reinterpret_cast<const float *>(p));
-  if constexpr (YE == kElemF16) return __half2float(__ldcs(reinterpret_cast<const __half *>(p)));
-  if constexpr (YE == kElemBF16) return __bfloat162float(__ldcs(reinterpret_cast<const __nv_bfloat16 *>(p)));
+// Loads and stores under a predicate, without a branch (which would have each
+// load waited for where its branch ends); the bits as they lie in memory.
+__device__ __forceinline__ void load_if(bool live, const uint8_t *p, uint32_t &v) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.cs.b32 %0, [%1];\n}\n" : "=&r"(v) : "l"(p), "r"(int(live)));
 }
-template <int YE>
-__device__ __forceinline__ void store_one(uint8_t *p, float v) {
-  if constexpr (YE == kElemF32) __stcs(reinterpret_cast<float *>(p), v);
-  if constexpr (YE == kElemF16) __stcs(reinterpret_cast<__half *>(p), __float2half_rn(v));
-  if constexpr (YE == kElemBF16) __stcs(reinterpret_cast<__nv_bfloat16 *>(p), __float2bfloat16_rn(v));
+__device__ __forceinline__ void load_half_if(bool live, const uint8_t *p, uint32_t &v) {
+  asm volatile("{\n .reg .pred q;\n .reg .b16 h;\n setp.ne.b32 q, %2, 0;\n mov.b16 h, 0;\n @q ld.global.cs.b16 h, [%1];\n cvt.u32.u16 %0, h;\n}\n"
+               : "=r"(v) : "l"(p), "r"(int(live)));
+}
+__device__ __forceinline__ void store_if(bool live, uint8_t *p, uint32_t v) {
+  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q st.global.cs.b32 [%0], %1;\n}\n" ::"l"(p), "r"(v), "r"(int(live)) : "memory");
+}
+__device__ __forceinline__ void store_half_if(bool live, uint8_t *p, uint32_t v) {
+  asm volatile("{\n .reg .pred q;\n .reg .b16 h;\n setp.ne.b32 q, %2, 0;\n cvt.u16.u32 h, %1;\n @q st.global.cs.b16 [%0], h;\n}\n" ::"l"(p), "r"(v), "r"(int(live)) : "memory");
 }
 
 // The work of a grid is one run of turns, tile after tile, cut into equal pieces,
@@ -769,14 +773,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   __shared__ __align__(16) int64_t y_off[kTcTokens], out_off[kTcTokens];
   __shared__ uint32_t tmem_slot;
   __shared__ int aborted;
-  constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2, YS = Elem<YE>::kBytes;
+  constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2, YS = Elem<YE>::kBytes, S = ExpandTc::kStages;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint8_t *sm = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
   uint64_t *bar = reinterpret_cast<uint64_t *>(sm + e.bar_off());
   uint64_t *b_full = bar, *b_empty = bar + 3, *d_full = bar + 6, *d_empty = bar + 8, *done = bar + 10;
   volatile int *abort_flag = &aborted;
   if (tid == 0) {
-    for (int i = 0; i < e.stages; ++i) {
+    for (int i = 0; i < S; ++i) {
       mbar_init(&b_full[i], 1);
       mbar_init(&b_empty[i], 1);
     }
@@ -801,7 +805,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   const int64_t units = int64_t(*w.n_tiles) * groups;
   const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
   int done_turns = 0;  // with products, over all tiles: the barriers' phases
-  int armed = 0;       // turns whose copies were asked for
+  int armed = 0;       // blocks of B that were asked for
   for (int64_t u = units * blockIdx.x / gridDim.x; u < u1;) {
     const int tile = int(u / groups), g0 = int(u - int64_t(tile) * groups), n_turns = int(min(u1 - u, int64_t(groups - g0)));
     u += n_turns;
@@ -849,13 +853,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     if (ad >= 0) done_turns += n_turns;
     if (warp == 8) {
       if (lane == 0 && ad >= 0) {
-        for (int i = i0; i < i0 + n_turns; ++i) {
-          const int st = i % e.stages;
-          if (!tc_wait(&b_empty[st], ((i / e.stages) & 1) ^ 1, spin, abort_flag, a.err)) break;
-          mbar_arrive_expect_tx(&b_full[st], uint32_t(e.blocks * kTcBTile));
-          for (int b = 0; b < e.blocks; ++b)
-            tma_load_3d(sm + (st * e.blocks + b) * kTcBTile, &bmap, b * 64, (g0 + i - i0) * kTcCols, ad, &b_full[st]);
-          armed = i + 1;
+        for (int q = i0 * e.blocks; q < (i0 + n_turns) * e.blocks; ++q) {  // block q of all turns
+          const int st = q % S, turn = q / e.blocks - i0, b = q % e.blocks;
+          if (!tc_wait(&b_empty[st], ((q / S) & 1) ^ 1, spin, abort_flag, a.err)) break;
+          mbar_arrive_expect_tx(&b_full[st], uint32_t(kTcBTile));
+          tma_load_3d(sm + st * kTcBTile, &bmap, b * 64, (g0 + turn) * kTcCols, ad, &b_full[st]);
+          armed = q + 1;
         }
       }
     } else if (warp == 9) {
@@ -865,87 +868,108 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         constexpr uint32_t kIdesc = (1u << 4) | kType | (uint32_t(kTcTokens >> 3) << 17) | (uint32_t(kTcCols >> 4) << 24);
         const uint32_t b0 = smem_u32(sm), h0 = smem_u32(sm + e.h_off());
         for (int i = i0; i < i0 + n_turns; ++i) {
-          const int st = i % e.stages, buf = i & 1;
-          if (!tc_wait(&b_full[st], (i / e.stages) & 1, spin, abort_flag, a.err)) break;
-          if (!tc_wait(&d_empty[buf], ((i >> 1) & 1) ^ 1, spin, abort_flag, a.err)) break;
-          tc_fence_after();
+          const int buf = i & 1;
+          bool there = tc_wait(&d_empty[buf], ((i >> 1) & 1) ^ 1, spin, abort_flag, a.err);
           const uint32_t d = tmem + uint32_t(buf * kTcTokens);
           uint32_t more = 0;
-          for (int b = 0; b < e.blocks; ++b) {
-            const uint64_t b_desc = sw128_desc(b0 + (st * e.blocks + b) * kTcBTile);
+          for (int b = 0; b < e.blocks && there; ++b) {
+            const int q = i * e.blocks + b, st = q % S;
+            there = tc_wait(&b_full[st], (q / S) & 1, spin, abort_flag, a.err);
+            if (!there) break;
+            tc_fence_after();
+            const uint64_t b_desc = sw128_desc(b0 + st * kTcBTile);
             for (int k = kTerms - 1; k >= 0; --k) {
               const uint64_t h_desc = sw128_desc(h0 + (k * e.blocks + b) * kTcHTile);
-              for (int q = 0; q < 4 && b * 64 + q * 16 < a.rank; ++q) {
-                tc_mma(d, b_desc + uint64_t(2 * q), h_desc + uint64_t(2 * q), kIdesc, more);
+              for (int n = 0; n < 4 && b * 64 + n * 16 < a.rank; ++n) {
+                tc_mma(d, b_desc + uint64_t(2 * n), h_desc + uint64_t(2 * n), kIdesc, more);
                 more = 1;
               }
             }
+            tc_commit(&b_empty[st]);
           }
-          tc_commit(&b_empty[st]);
+          if (!there) break;
           tc_commit(&d_full[buf]);
         }
       }
     } else {
       const int lg = warp & 3, t0 = (warp >> 2) * 32;
       const uint32_t lane_addr = tmem + (uint32_t(lg * 32) << 16);
-      const bool whole = count == kTcTokens;
-      // steps of 16 tokens: 2 per turn; the next one's y is asked for before this one's sums are
-      float y[2][16];
-      auto ask = [&](int step, float (&v)[16]) {
-        const int m = (g0 + (step >> 1)) * kTcCols + lg * 32 + lane, from = t0 + (step & 1) * 16;
-        const bool live = a.y && m < a.M && step < 2 * n_turns;
-        const uint8_t *p = a.y + int64_t(m) * YS;
-        if (whole) {
+      const int odd = lane & 1;
+      // 16-bit rows, where their boundaries allow it: two columns of one token per access (220 us -> 125 for
+      // 8192 tokens of 11008 columns; fp32 rows, whose 32 columns are a line of 128 bytes, lose by it, 161 -> 184)
+      const bool pairs = YS == 2 && a.y_vec && a.M % 2 == 0;
+      // steps of 16 tokens: 2 per turn; the next one's y is asked for before this one's sums are.
+      // The bits of y. With pairs: of the lane's and its neighbour's column of one token, the first of
+      // two in the even lane, the second in the odd one (16-bit rows: one word); else of the lane's column
+      uint32_t y[2][16];
+      auto column = [&](int step) { return (g0 + (step >> 1)) * kTcCols + lg * 32 + lane; };
+      auto ask = [&](int step, uint32_t (&v)[16]) {
+        const int m = column(step), from = t0 + (step & 1) * 16, end = a.y && step < 2 * n_turns && m < a.M ? count : 0;
+        if (pairs) {
+          const uint8_t *p = a.y + int64_t(m - odd) * YS;
 #pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const longlong2 o = *reinterpret_cast<const longlong2 *>(&y_off[from + j]);
-            v[j] = live ? load_one<YE>(p + o.x) : 0.0f;
-            v[j + 1] = live ? load_one<YE>(p + o.y) : 0.0f;
+          for (int j = 0; j < 8; ++j) {
+            const int r = from + 2 * j + odd;
+            load_if(r < end, p + y_off[r], v[j]);
           }
         } else {
+          const uint8_t *p = a.y + int64_t(m) * YS;
 #pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] = live && from + j < count ? load_one<YE>(p + y_off[from + j]) : 0.0f;
+          for (int j = 0; j < 16; ++j) {
+            const int64_t o = y_off[from + j];
+            if constexpr (YS == 4)
+              load_if(from + j < end, p + o, v[j]);
+            else
+              load_half_if(from + j < end, p + o, v[j]);
+          }
         }
       };
       bool ok = true;
-      auto give = [&](int step, const float (&v)[16]) {
-        const int turn = i0 + (step >> 1), m = (g0 + (step >> 1)) * kTcCols + lg * 32 + lane, from = t0 + (step & 1) * 16;
-        float o[16];
+      auto give = [&](int step, const uint32_t (&v)[16]) {
+        const int turn = i0 + (step >> 1), m = column(step), from = t0 + (step & 1) * 16, end = m < a.M ? count : 0;
+        uint32_t d[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) d[j] = 0;
         if (ad >= 0) {
           if ((step & 1) == 0) {
             ok = tc_wait_warp(&d_full[turn & 1], (turn >> 1) & 1, spin, abort_flag, a.err);
             if (!ok) return;
             tc_fence_after();
           }
-          uint32_t d[16];
           tmem_ld16(lane_addr + uint32_t((turn & 1) * kTcTokens + from), d);
           if (step & 1) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_empty[turn & 1]);
           }
+        }
+        // the token's row of y plus its products; without an adapter y as it is
+        auto sum = [&](uint32_t x, float with, int r) {
+          return ad < 0 ? with : WE == kElemF16 ? __fmaf_rn(__uint_as_float(x), unscale[r], with) : __fadd_rn(__uint_as_float(x), with);
+        };
+        if (pairs) {
+          uint8_t *p = a.out + int64_t(m - odd) * YS;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t other = __shfl_xor_sync(kFull, odd ? d[2 * j] : d[2 * j + 1], 1);
+            const int r = from + 2 * j + odd;
+            const uint32_t x0 = odd ? other : d[2 * j], x1 = odd ? d[2 * j + 1] : other;
+            if constexpr (YS == 2) {
+              const float2 with = unpack_pair<YE>(v[j]);
+              store_if(r < end, p + out_off[r], pack_pair<YE>(sum(x0, with.x, r), sum(x1, with.y, r)));
+            }
+          }
+        } else {
+          uint8_t *p = a.out + int64_t(m) * YS;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float x = __uint_as_float(d[j]);
-            o[j] = WE == kElemF16 ? __fmaf_rn(x, unscale[from + j], v[j]) : __fadd_rn(x, v[j]);
+            const int r = from + j;
+            const int64_t o = out_off[r];
+            if constexpr (YS == 4)
+              store_if(r < end, p + o, __float_as_uint(sum(d[j], __uint_as_float(v[j]), r)));
+            else
+              store_half_if(r < end, p + o, pack_pair<YE>(sum(d[j], unpack_pair<YE>(v[j]).x, r), 0.0f));
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] = v[j];
-        }
-        if (m >= a.M) return;
-        uint8_t *p = a.out + int64_t(m) * YS;
-        if (whole) {
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const longlong2 q = *reinterpret_cast<const longlong2 *>(&out_off[from + j]);
-            store_one<YE>(p + q.x, o[j]);
-            store_one<YE>(p + q.y, o[j + 1]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (from + j < count) store_one<YE>(p + out_off[from + j], o[j]);
         }
       };
       ask(0, y[0]);
@@ -961,9 +985,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
   }
   // copies and products in flight end by themselves: none is left behind
   if (warp == 8 && lane == 0) {
-    for (int i = 0; i < e.stages && i < armed; ++i) {
-      const int last = armed - 1 - ((armed - 1 - i) % e.stages);
-      tc_drain(&b_full[i], (last / e.stages) & 1);
+    for (int i = 0; i < S && i < armed; ++i) {
+      const int last = armed - 1 - ((armed - 1 - i) % S);
+      tc_drain(&b_full[i], (last / S) & 1);
     }
   }
   if (warp == 9 && lane == 0) {
@@ -991,8 +1015,10 @@ Plan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
   Plan p{};
   const int64_t groups = std::min(n + 1, T);
   p.grouped = T > kLeaders;
-  // a tile of 64 pays where an adapter fills it, by the mean
-  p.tm = p.grouped && T >= 32 * groups ? 64 : 16;
+  // a tile of 64 pays where an adapter fills it, by the mean, and there is work
+  // enough for its preparation (4096 x 4096: 1024 tokens at rank 32 27 us with tiles
+  // of 16, 30 with 64; 2048 tokens at rank 16 27 and 32, at rank 32 51 and 44)
+  p.tm = T > 512 && T * rank > 32768 && T >= 32 * groups ? 64 : 16;
   p.tiles = int(p.grouped ? T / p.tm + groups : T);
   const int64_t busy = p.grouped ? T / p.tm + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2;  // about as many have work
   const int64_t pieces = K / 32 / (p.tm == 16 ? 16 : 8);  // 4 or 8 blocks of 32 k per warp at least
@@ -1077,7 +1103,6 @@ cudaError_t expand64(const LoraArgs &a, const Work &w, const Plan &p, int sms, c
   }
   ExpandTc e;
   e.blocks = (a.rank + 63) / 64;
-  e.stages = e.blocks == 1 ? 3 : 2;
   e.terms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2;
   const int64_t units = int64_t(p.tiles) * ((a.M + kTcCols - 1) / kTcCols);
   const int per_sm = e.bytes() <= 110 * 1024 ? 2 : 1;  // resident
