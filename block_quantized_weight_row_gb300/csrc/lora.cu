@@ -291,13 +291,13 @@ __device__ __forceinline__ void shrink_step(float (&acc)[NT][4], const RowWords<
 // and, for tiles of 16, their four warps, in order. part: [4][16][8 NT] of every
 // CTA; a tile of 64 has its rows there in order.
 template <int TM, int NT>
-__device__ __forceinline__ void sum_tile(const LoraArgs &a, const Work &w, float *part, const int *rows, int ad, int count, int split, int splits) {
+__device__ __forceinline__ void sum_tile(const LoraArgs &a, const Work &w, float *part, const int *rows, int ad, int count, int first, int split, int splits) {
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
   const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
-  const int n = count * a.rank;
+  const int ranks = min(8 * NT, a.rank - first), n = count * ranks;
   for (int e = split * kShrinkThreads + threadIdx.x; e < n; e += splits * kShrinkThreads) {
-    const int row = e / a.rank, r = e - row * a.rank;
+    const int row = e / ranks, r = e - row * ranks;
     float sum = 0.0f;
     for (int c = 0; c < splits; ++c) {
       const float *p = cluster.map_shared_rank(part, c);
@@ -308,7 +308,7 @@ __device__ __forceinline__ void sum_tile(const LoraArgs &a, const Work &w, float
         for (int q = 0; q < 4; ++q) sum += p[(q * 16 + row) * (8 * NT) + r];
       }
     }
-    w.H[int64_t(rows[row]) * a.rank + r] = sum * s;
+    w.H[int64_t(rows[row]) * a.rank + first + r] = sum * s;
   }
   cluster.sync();  // the others' sums are read from here until now
 }
@@ -330,15 +330,16 @@ __device__ __forceinline__ void put(float *part, const float (&v)[NT][4], int g,
   }
 }
 
-// Tiles of 16 tokens; NT: n-tiles of 8 ranks (rank <= 8 NT). Each warp has all of
-// the tile's tokens and a quarter of the CTA's k, and loads its operands itself:
-// in a decode step a warp has four blocks of 32 k, all in flight at once.
+// Tiles of 16 tokens, up to 32 ranks of the adapter (NT n-tiles of 8; other
+// clusters have its others, so that ranks, too, are spread over the SMs). Each warp
+// has all of the tile's tokens and a quarter of the CTA's k, and loads its operands
+// itself: in a decode step a warp has up to four blocks of 32 k, all in flight at once.
 template <int XE, int WE, int NT>
 __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs a, const Work w, const int splits) {
   __shared__ __align__(16) float part[4][16][8 * NT];
   __shared__ int rows[16];
   constexpr int XS = Elem<XE>::kBytes;
-  constexpr int kAhead = NT <= 4 ? 4 : NT == 8 ? 2 : 1;  // blocks in flight
+  constexpr int kAhead = 4;  // blocks in flight
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   pdl_launch_dependents();
   if (w.sorted) {
@@ -349,10 +350,10 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
   }
   int ad, count;
   if (!find_tile<16>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
-  const int nb = a.K / 32, split = blockIdx.x, pieces = splits * 4, piece = split * 4 + warp;
+  const int nb = a.K / 32, split = blockIdx.x % splits, first = int(blockIdx.x) / splits * 8 * NT, pieces = splits * 4, piece = split * 4 + warp;
   const int k0 = int(int64_t(nb) * piece / pieces), k1 = int(int64_t(nb) * (piece + 1) / pieces);
   const uint8_t *lo = a.x + rows[g] * a.x_row + t * 8 * XS, *hi = a.x + rows[g + 8] * a.x_row + t * 8 * XS;
-  const uint8_t *ap = a.A + (int64_t(ad) * a.rank + g) * a.K * 2 + t * 16;
+  const uint8_t *ap = a.A + (int64_t(ad) * a.rank + first + g) * a.K * 2 + t * 16;
   const bool high = count > 8;
   float acc[NT][4] = {}, total[NT][4] = {};
   for (int k = k0; k < k1; k += kAhead) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           bw[u][nt] = make_uint4(0, 0, 0, 0);
-          if (nt * 8 < a.rank) bw[u][nt] = __ldg(reinterpret_cast<const uint4 *>(ap + (int64_t(nt) * 8 * a.K + (k + u) * 32) * 2));
+          if (first + nt * 8 < a.rank) bw[u][nt] = __ldg(reinterpret_cast<const uint4 *>(ap + (int64_t(nt) * 8 * a.K + (k + u) * 32) * 2));
         }
       }
 #pragma unroll
@@ -376,11 +377,11 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
     take(total, acc);
   }
   put<NT>(&part[warp][0][0], total, g, t);
-  sum_tile<16, NT>(a, w, &part[0][0][0], rows, ad, count, split, splits);
+  sum_tile<16, NT>(a, w, &part[0][0][0], rows, ad, count, first, split, splits);
 }
 
-// Tiles of 64 tokens: each of the four warps has 16 of them and all of the CTA's
-// k. Rows of x and of the adapter come through a ring of stages of 64 k by
+// Tiles of 64 tokens, up to 64 ranks: each of the four warps has 16 of the tokens
+// and all of the CTA's k. Rows of x and of the adapter come through a ring of stages of 64 k by
 // asynchronous copies (straight loads left a warp waiting for memory in every
 // block of 32 k: 60 us for 2048 tokens of 4096 at rank 64).
 // A stage: two blocks of 32 k, each a row of 64 bytes per token and rank (fp32
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
   pdl_wait();
   int ad, count;
   if (!find_tile<64>(a, w, blockIdx.y, rows, ad, count) || ad < 0) return;  // all CTAs of the cluster alike
-  const int nb = a.K / 32, split = blockIdx.x;
+  const int nb = a.K / 32, split = blockIdx.x % splits, first = int(blockIdx.x) / splits * 8 * NT;
   const int k0 = int(int64_t(nb) * split / splits), k1 = int(int64_t(nb) * (split + 1) / splits);
   const int stages = (k1 - k0 + 1) / 2;
   // a thread copies one 16-byte piece of every kStep-th row; rows without a
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
 #pragma unroll
   for (int i = 0; i < kRows; ++i) src[i] = a.x + rows[xr + i * kStep] * a.x_row + (int64_t(k0) * 32) * XS + xp * 16;
   const int ap = tid % 8, ar = tid / 8;  // 8 pieces of 64 k, 16 ranks at a time
-  const uint8_t *asrc = a.A + (int64_t(ad) * a.rank + ar) * a.K * 2 + int64_t(k0) * 64 + ap * 16;
+  const uint8_t *asrc = a.A + (int64_t(ad) * a.rank + first + ar) * a.K * 2 + int64_t(k0) * 64 + ap * 16;
   auto fill = [&](int s) {
     uint8_t *x = ring + (s % R::kStages) * R::kStage, *ad_rows = x + 2 * R::kXBlock;
     if (k0 + 2 * s + xb < k1) {
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
 #pragma unroll
       for (int i = 0; i < (NT + 1) / 2; ++i) {
         const int r = ar + 16 * i;
-        if (r < a.rank) copy16(ad_rows + (ap / 4) * R::kABlock + r * 64 + (ap % 4) * 16, asrc + (int64_t(i) * 16 * a.K + s * 64) * 2);
+        if (r < 8 * NT && first + r < a.rank) copy16(ad_rows + (ap / 4) * R::kABlock + r * 64 + (ap % 4) * 16, asrc + (int64_t(i) * 16 * a.K + s * 64) * 2);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
   __syncthreads();  // the ring becomes the sums' place
   float *part = reinterpret_cast<float *>(ring);
   put<NT>(part + r0 * (8 * NT), total, g, t);
-  sum_tile<64, NT>(a, w, part, rows, ad, count, split, splits);
+  sum_tile<64, NT>(a, w, part, rows, ad, count, first, split, splits);
 }
 
 // ---------------------------------------------------------------- expand --
@@ -1020,8 +1021,12 @@ Plan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
   // of 16, 30 with 64; 2048 tokens at rank 16 27 and 32, at rank 32 51 and 44)
   p.tm = T > 512 && T * rank > 32768 && T >= 32 * groups ? 64 : 16;
   p.tiles = int(p.grouped ? T / p.tm + groups : T);
-  const int64_t busy = p.grouped ? T / p.tm + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2;  // about as many have work
-  const int64_t pieces = K / 32 / (p.tm == 16 ? 16 : 8);  // 4 or 8 blocks of 32 k per warp at least
+  // clusters that have work, about; each split in up to 8 CTAs while SMs are left,
+  // down to four blocks of 32 k per warp (tiles of 64: 8 per CTA), or one where
+  // clusters are few
+  const int64_t chunk = p.tm == 16 ? (rank <= 16 ? 16 : 32) : 64;
+  const int64_t busy = (p.grouped ? T / p.tm + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2) * ((rank + chunk - 1) / chunk);
+  const int64_t pieces = K / 32 / (p.tm == 64 ? 8 : busy < 32 ? 4 : 16);
   p.splits = 1;
   while (p.splits < 8 && busy * p.splits < 304 && 2 * p.splits <= pieces) p.splits *= 2;
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -1062,7 +1067,7 @@ cudaError_t launch_ex(void (*fn)(P...), dim3 grid, int threads, int smem, int cl
 
 template <int XE, int WE, int TM, int NT>
 cudaError_t shrink_nt(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
-  const dim3 grid(unsigned(p.splits), unsigned(p.tiles));
+  const dim3 grid(unsigned(p.splits * ((a.rank + 8 * NT - 1) / (8 * NT))), unsigned(p.tiles));  // chunks of ranks side by side: they read the same x
   if constexpr (TM == 64)
     return launch_ex(k_lora_shrink64<XE, WE, NT>, grid, kShrinkThreads, Ring<XE, NT>::kBytes, p.splits, true, s, a, w, p.splits);
   else
@@ -1071,9 +1076,8 @@ cudaError_t shrink_nt(const LoraArgs &a, const Work &w, const Plan &p, cudaStrea
 template <int XE, int WE, int TM>
 cudaError_t shrink(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
   if (a.rank <= 16) return shrink_nt<XE, WE, TM, 2>(a, w, p, s);
-  if (a.rank <= 32) return shrink_nt<XE, WE, TM, 4>(a, w, p, s);
-  if (a.rank <= 64) return shrink_nt<XE, WE, TM, 8>(a, w, p, s);
-  return shrink_nt<XE, WE, TM, 16>(a, w, p, s);
+  if (TM == 16 || a.rank <= 32) return shrink_nt<XE, WE, TM, 4>(a, w, p, s);
+  if constexpr (TM == 64) return shrink_nt<XE, WE, TM, 8>(a, w, p, s);
 }
 
 template <int WE, int YE>
