@@ -138,7 +138,7 @@ int bq_add_rms_norm(int elem, const void *x, int64_t x_stride, const void *resid
   if (n_rows > 1 && ((sum && sum_stride < n_cols) || (out && out_stride < n_cols)))
     return report_error(BQ_ERR_INVALID_ARG, "%s: rows of an output overlap each other", who);
   const Range rw{weight, uint64_t(n_cols) * 4}, rq{q8, uint64_t(n_rows) * uint64_t(n_cols / kQK) * Fmt<kTypeQ8_0>::kBytes};
-  const bool on_x = sum == x && sum_stride == x_stride, on_r = sum == residual && sum_stride == residual_stride;
+  const bool on_x = sum == x && (n_rows == 1 || sum_stride == x_stride), on_r = sum == residual && (n_rows == 1 || sum_stride == residual_stride);
   if ((meet(rs, rx) && !on_x) || (meet(rs, rr) && !on_r) || meet(rs, rw))
     return report_error(BQ_ERR_INVALID_ARG, "%s: sum overlaps an input that it is not", who);
   for (const Range &r : {ro, rq})
@@ -182,7 +182,8 @@ int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_st
   if (rot % 2 || rot > head_dim || rot > 16384)
     return report_error(BQ_ERR_SHAPE, "%s: rot %lld is odd or above head_dim or 16384", who, (long long)rot);
   if (n_axes < 1 || n_axes > BQ_ROTARY_MAX_AXES) return report_error(BQ_ERR_SHAPE, "%s: n_axes not in 1..%d", who, BQ_ROTARY_MAX_AXES);
-  if (n_q_heads > 65536 || n_k_heads > 65536 || n_tokens > INT_MAX) return report_error(BQ_ERR_SHAPE, "%s: too many heads or tokens", who);
+  if (n_q_heads > 65536 || n_k_heads > 65536 || n_tokens > INT_MAX || (n_q_heads + n_k_heads) * head_dim > (1 << 24))
+    return report_error(BQ_ERR_SHAPE, "%s: too many heads or tokens (channels of a token: 2^24)", who);
   if (n_tokens == 0 || n_q_heads + n_k_heads == 0) return report_ok();
   struct {
     const void *in;

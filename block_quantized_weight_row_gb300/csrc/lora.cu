@@ -1042,8 +1042,10 @@ Plan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
 
 template <typename... P, typename... A>
 cudaError_t launch_ex(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t stream, A... args) {
-  const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), smem);
-  if (e != cudaSuccess) return e;
+  if (smem > 0) {
+    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[2];
   int n = 0;
   attr[n].id = cudaLaunchAttributeClusterDimension;

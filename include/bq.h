@@ -501,7 +501,8 @@ int bq_gemm_q8(int type, const void *W_blocks, const void *X_blocks, float *Y, i
  * or NULL for axis 0 everywhere; all on the DEVICE. An axis outside 0 .. n_axes -
  * 1 counts as 0 and is reported by bq_device_status (BQ_ERR_INDEX).
  * Limits: head_dim a multiple of 32 up to 65536, rot even up to head_dim and
- * 16384, n_axes 1 .. BQ_ROTARY_MAX_AXES, n_tokens below 2^31, up to 65536 heads.
+ * 16384, n_axes 1 .. BQ_ROTARY_MAX_AXES, n_tokens below 2^31, head_dim times all
+ * heads of a token up to 2^24.
  * Errors: BQ_ERR_UNSUPPORTED (element types), BQ_ERR_SHAPE, BQ_ERR_ALIGN,
  * BQ_ERR_INVALID_ARG. */
 int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t n_q_heads, const void *k,

@@ -97,7 +97,7 @@ def _rotary(bq, elem=BF16, q=at(1), qs=(256, 64), qh=4, k=at(2), ks=(128, 64), k
 
 @pytest.mark.parametrize("kw,want", [
     (dict(elem=5), UNSUPPORTED), (dict(eo=F16), UNSUPPORTED), (dict(elem=F16, eo=F32), UNSUPPORTED), (dict(dim=48), SHAPE), (dict(dim=0), SHAPE),
-    (dict(rot=63), SHAPE), (dict(rot=66), SHAPE), (dict(axes=0), SHAPE), (dict(axes=17), SHAPE), (dict(qh=-1), INVALID), (dict(qh=70000), SHAPE),
+    (dict(rot=63), SHAPE), (dict(rot=66), SHAPE), (dict(axes=0), SHAPE), (dict(axes=17), SHAPE), (dict(qh=-1), INVALID), (dict(qh=70000), SHAPE), (dict(dim=65536, rot=64, qh=254, kh=3), SHAPE),
     (dict(n=-1), INVALID), (dict(n=1 << 31), SHAPE), (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(ko=None), INVALID), (dict(pos=None), INVALID),
     (dict(freq=None), INVALID), (dict(q=at(1) + 8), ALIGN), (dict(qs=(260, 64)), ALIGN), (dict(kos=(128, 68)), ALIGN), (dict(pos=at(5) + 2), ALIGN),
     (dict(freq=at(6) + 4), ALIGN), (dict(qs=(-256, 64)), INVALID), (dict(qos=(64, 64)), INVALID), (dict(pst=-1), INVALID),
