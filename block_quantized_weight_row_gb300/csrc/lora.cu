@@ -26,47 +26,19 @@
 // in fp32 and enters the second product in bf16 terms, three for fp32 rows of out
 // and two (16 bits) for bf16 ones, or in two fp16 terms (22 bits) after scaling
 // each row by a power of two to at most 1.
-#include <cooperative_groups.h>
-
 #include <algorithm>
 
-#include "bq_device.cuh"
-#include "bq_internal.h"
-#include "layer.h"
-#include "paged.cuh"
-#include "tcgen05.cuh"
+#include "lora.cuh"
 
 namespace bq {
 namespace {
 
-namespace cg = cooperative_groups;
-
-constexpr int kLeaders = 256;  // up to this many tokens, CTAs find their tiles themselves
-constexpr int kGroupThreads = 1024;
-constexpr int kMaxBins = 4096 + 1;  // adapters, and the tokens without one
-constexpr int kShrinkThreads = 128, kExpandThreads = 256;
-
-struct Tile {
-  int adapter, first, count, unused;  // first: in the sorted tokens
-};
-
-// Workspace: H, then (grouped) the sorted tokens, the tiles and their number.
-struct Work {
-  float *H;         // [token][rank]
-  int32_t *sorted;  // null: tiles by leaders
-  Tile *tiles;
-  int32_t *n_tiles;
-};
-
-__device__ __forceinline__ int adapter_of(const LoraArgs &a, int t) {
-  const int id = __ldg(a.adapter + t);
-  return uint32_t(id) < uint32_t(a.n_adapters) ? id : -1;
-}
+constexpr int kGroupThreads = 1024, kShrinkThreads = 128, kExpandThreads = 256;
 
 // ----------------------------------------------------------------- group --
 
 template <int TM>
-__global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, const Work w) {
+__global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, const LoraWork w) {
   __shared__ int count[kMaxBins], tile0[kMaxBins + 1];
   __shared__ int sums[2][32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -129,7 +101,7 @@ __global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, 
       (tile0[mid] <= i ? lo : hi) = mid;
     }
     const int first = count[lo] + (i - tile0[lo]) * TM, end = lo + 1 < bins ? count[lo + 1] : a.n_tokens;
-    w.tiles[i] = Tile{lo - 1, first, min(TM, end - first), 0};
+    w.tiles[i] = LoraTile{lo - 1, first, min(TM, end - first), 0};
   }
   __syncthreads();
   each([&](int t, int, int bin, bool all) {
@@ -138,61 +110,6 @@ __global__ void __launch_bounds__(kGroupThreads) k_lora_group(const LoraArgs a, 
     if (all) at = __shfl_sync(kFull, at, 0) + lane;
     if (bin >= 0) w.sorted[at] = t;
   });
-}
-
-// The tokens of tile `index` into rows[] (those beyond the count repeat the
-// first), by all threads of the CTA. False: there is no such tile.
-template <int TM>
-__device__ __forceinline__ bool find_tile(const LoraArgs &a, const Work &w, int index, int *rows, int &adapter, int &count) {
-  __shared__ int before[8], total[2];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (w.sorted) {
-    if (index >= *w.n_tiles) return false;
-    const Tile t = w.tiles[index];
-    adapter = t.adapter;
-    count = t.count;
-    if (tid < TM) rows[tid] = w.sorted[t.first + (tid < t.count ? tid : 0)];
-    __syncthreads();
-    return true;
-  }
-  // tokens of the adapter of token `index`, in order: with two passes of 128
-  // threads or one of 256, every warp has whole groups of 32 tokens
-  adapter = adapter_of(a, index);
-  if (tid < 8) before[tid] = 0;
-  __syncthreads();
-  for (int t = tid; t < kLeaders; t += blockDim.x) {
-    const unsigned same = __ballot_sync(kFull, t < a.n_tokens && adapter_of(a, t) == adapter);
-    if (lane == 0) before[t >> 5] = int(same);
-  }
-  __syncthreads();
-  if (warp == 0) {  // words of matches -> ranks
-    const unsigned word = lane < 8 ? unsigned(before[lane]) : 0u;
-    int rank = __popc(word);
-#pragma unroll
-    for (int d = 1; d < 8; d <<= 1) {
-      const int o = __shfl_up_sync(kFull, rank, d);
-      if (lane >= d) rank += o;
-    }
-    const int all = __shfl_sync(kFull, rank, 7);
-    rank -= __popc(word);  // matches before this word
-    const int mine = __shfl_sync(kFull, rank, index >> 5) +
-                     __popc(__shfl_sync(kFull, word, index >> 5) & ((1u << (index & 31)) - 1));  // the leader's rank
-    const int n = min(TM, all - mine);
-    if (mine % TM == 0) {
-      // lane i of 16 finds the token of rank mine + i
-      if (lane < TM) rows[lane] = index;
-      __syncwarp();
-      if (lane < 8) {
-        unsigned left = word;
-        for (int r = rank; left; ++r, left &= left - 1)
-          if (r >= mine && r < mine + TM) rows[r - mine] = lane * 32 + __ffs(left) - 1;
-      }
-    }
-    if (lane == 0) total[0] = mine % TM == 0 ? n : 0;
-  }
-  __syncthreads();
-  count = total[0];
-  return count > 0;
 }
 
 // -------------------------------------------------------------- products --
@@ -212,15 +129,6 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1
   asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Two fp32 values cut to bf16, packed; the rests (exact) stay. Three such steps
-// give all 24 bits of a value.
-__device__ __forceinline__ uint32_t cut_pair(float &x, float &y) {
-  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
-  x = __fsub_rn(x, __uint_as_float(a & 0xffff0000u));
-  y = __fsub_rn(y, __uint_as_float(b & 0xffff0000u));
-  return __byte_perm(a, b, 0x7632);
 }
 
 // fp32 bits rounded to tf32 (11 significant bits)
@@ -287,32 +195,6 @@ __device__ __forceinline__ void shrink_step(float (&acc)[NT][4], const RowWords<
   }
 }
 
-// A cluster's sums of a tile: each of its CTAs adds up its share, over the CTAs
-// and, for tiles of 16, their four warps, in order. part: [4][16][8 NT] of every
-// CTA; a tile of 64 has its rows there in order.
-template <int TM, int NT>
-__device__ __forceinline__ void sum_tile(const LoraArgs &a, const Work &w, float *part, const int *rows, int ad, int count, int first, int split, int splits) {
-  cg::cluster_group cluster = cg::this_cluster();
-  cluster.sync();
-  const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
-  const int ranks = min(8 * NT, a.rank - first), n = count * ranks;
-  for (int e = split * kShrinkThreads + threadIdx.x; e < n; e += splits * kShrinkThreads) {
-    const int row = e / ranks, r = e - row * ranks;
-    float sum = 0.0f;
-    for (int c = 0; c < splits; ++c) {
-      const float *p = cluster.map_shared_rank(part, c);
-      if constexpr (TM == 64) {
-        sum += p[row * (8 * NT) + r];
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum += p[(q * 16 + row) * (8 * NT) + r];
-      }
-    }
-    w.H[int64_t(rows[row]) * a.rank + first + r] = sum * s;
-  }
-  cluster.sync();  // the others' sums are read from here until now
-}
-
 // total += acc, acc = 0: the tensor instructions' adder truncates, so chains are kept short
 template <int NT>
 __device__ __forceinline__ void take(float (&total)[NT][4], float (&acc)[NT][4]) {
@@ -335,7 +217,7 @@ __device__ __forceinline__ void put(float *part, const float (&v)[NT][4], int g,
 // has all of the tile's tokens and a quarter of the CTA's k, and loads its operands
 // itself: in a decode step a warp has up to four blocks of 32 k, all in flight at once.
 template <int XE, int WE, int NT>
-__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs a, const Work w, const int splits) {
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs a, const LoraWork w, const int splits) {
   __shared__ __align__(16) float part[4][16][8 * NT];
   __shared__ int rows[16];
   constexpr int XS = Elem<XE>::kBytes;
@@ -377,34 +259,30 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
     take(total, acc);
   }
   put<NT>(&part[warp][0][0], total, g, t);
-  sum_tile<16, NT>(a, w, &part[0][0][0], rows, ad, count, first, split, splits);
+  sum_tile<4>(a, w, &part[0][0][0], 8 * NT, 16 * 8 * NT, rows, ad, count, first, min(8 * NT, a.rank - first), split, splits);
 }
 
-// Tiles of 64 tokens, up to 64 ranks: each of the four warps has 16 of the tokens
-// and all of the CTA's k. Rows of x and of the adapter come through a ring of stages of 64 k by
-// asynchronous copies (straight loads left a warp waiting for memory in every
-// block of 32 k: 60 us for 2048 tokens of 4096 at rank 64).
-// A stage: two blocks of 32 k, each a row of 64 bytes per token and rank (fp32
-// rows: 128 bytes, the even 16-byte pieces in one half, which half alternates
-// from row to row), so that a quarter-warp's reads of two rows meet no bank twice.
-template <int XE, int NT>
+// Tiles of 64 fp32 tokens beside fp16 adapters (whose products the tensor-memory
+// kernel cannot take: terms of fp16 would need each row's range first), up to 64
+// ranks: each of the four warps has 16 of the tokens and all of the CTA's k. Rows of
+// x and of the adapter come through a ring of stages of 64 k by asynchronous copies.
+// A stage: two blocks of 32 k, each a row of 128 bytes per token (the even 16-byte
+// pieces in one half, which half alternates from row to row) and of 64 per rank, so
+// that a quarter-warp's reads of two rows meet no bank twice.
+template <int NT>
 struct Ring {
   static constexpr int kStages = 3;
-  static constexpr int kXRow = 32 * Elem<XE>::kBytes, kXBlock = 64 * kXRow, kABlock = 8 * NT * 64;
+  static constexpr int kXRow = 128, kXBlock = 64 * kXRow, kABlock = 8 * NT * 64;
   static constexpr int kStage = 2 * (kXBlock + kABlock);
   static constexpr int kBytes = kStages * kStage > 64 * 8 * NT * 4 ? kStages * kStage : 64 * 8 * NT * 4;  // or the sums, afterwards
 };
 
-__device__ __forceinline__ void copy16(void *to, const void *from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
-}
-
-template <int XE, int WE, int NT>
-__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs a, const Work w, const int splits) {
-  using R = Ring<XE, NT>;
+template <int NT>
+__global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs a, const LoraWork w, const int splits) {
+  using R = Ring<NT>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int rows[64];
-  constexpr int XS = Elem<XE>::kBytes;
+  constexpr int XE = kElemF32, WE = kElemF16, XS = 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   pdl_wait();
   int ad, count;
@@ -427,7 +305,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = xr + i * kStep;
-        const int at = XE == kElemF32 ? (xc >> 1) + 4 * ((xc & 1) ^ (r & 1)) : xc;
+        const int at = (xc >> 1) + 4 * ((xc & 1) ^ (r & 1));
         if (r < count) copy16(x + xb * R::kXBlock + r * R::kXRow + at * 16, src[i] + int64_t(s) * 64 * XS);
       }
     }
@@ -465,16 +343,11 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
         RowWords<XE> xl, xh;
         uint4 bw[NT];
         const uint8_t *pl = x + b * R::kXBlock + (r0 + g) * R::kXRow, *ph = pl + 8 * R::kXRow;
-        if constexpr (XE == kElemF32) {
-          const int first = (g & 1) * 64 + t * 16;  // rows g and g + 8 are both even or both odd
-          xl.v[0] = *reinterpret_cast<const uint4 *>(pl + first);
-          xl.v[1] = *reinterpret_cast<const uint4 *>(pl + (first ^ 64));
-          xh.v[0] = *reinterpret_cast<const uint4 *>(ph + first);
-          xh.v[1] = *reinterpret_cast<const uint4 *>(ph + (first ^ 64));
-        } else {
-          xl.v[0] = *reinterpret_cast<const uint4 *>(pl + t * 16);
-          xh.v[0] = *reinterpret_cast<const uint4 *>(ph + t * 16);
-        }
+        const int half = (g & 1) * 64 + t * 16;  // rows g and g + 8 are both even or both odd
+        xl.v[0] = *reinterpret_cast<const uint4 *>(pl + half);
+        xl.v[1] = *reinterpret_cast<const uint4 *>(pl + (half ^ 64));
+        xh.v[0] = *reinterpret_cast<const uint4 *>(ph + half);
+        xh.v[1] = *reinterpret_cast<const uint4 *>(ph + (half ^ 64));
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) bw[nt] = *reinterpret_cast<const uint4 *>(ad_rows + b * R::kABlock + (nt * 8 + g) * 64 + t * 16);
         shrink_step<XE, WE, NT>(acc, xl, xh, bw);
@@ -487,20 +360,10 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
   __syncthreads();  // the ring becomes the sums' place
   float *part = reinterpret_cast<float *>(ring);
   put<NT>(part + r0 * (8 * NT), total, g, t);
-  sum_tile<64, NT>(a, w, part, rows, ad, count, first, split, splits);
+  sum_tile<1>(a, w, part, 8 * NT, 0, rows, ad, count, first, min(8 * NT, a.rank - first), split, splits);
 }
 
 // ---------------------------------------------------------------- expand --
-
-// The power of two that brings a row of H below 2, kept within normal numbers; m:
-// the lane's largest |value|. Its inverse goes to unscale[r].
-__device__ __forceinline__ float scale_row(float m, float *unscale, int r, int lane) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-  const int e = min(max(int(__float_as_uint(m) >> 23), 2), 252);
-  if (lane == 0) unscale[r] = __uint_as_float(uint32_t(e) << 23);
-  return __uint_as_float(uint32_t(254 - e) << 23);
-}
 
 // A lane's 8 columns of a turn's 32 are pieces of 16 bytes, a row's four lanes
 // side by side in one access, so that it covers whole sectors: 8 columns from 8 t
@@ -574,7 +437,7 @@ struct Expand {
 // first turn's, and its part of B, are asked for before the launch before this one
 // has ended.
 template <int WE, int YE, int KB>
-__global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArgs a, const Work w, const int turns) {
+__global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArgs a, const LoraWork w, const int turns) {
   using E = Expand<WE, YE, KB>;
   constexpr int TM = 16, kStep = 256, kTerms = E::kTerms, kPitch = E::kPitch;
   using Pc = Piece<YE>;
@@ -705,315 +568,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// ------------------------------------- expand on the tensor-memory kernel --
-
-// Tiles of 64 tokens, 128 columns of out a turn: D[column][token] = B (128 x rank,
-// straight from the adapter by TMA) times H's terms (64 tokens, operand made once
-// per CTA) on tcgen05, accumulated over the terms in tensor memory. With columns
-// as the accumulator's lanes, a warp's access to y and out is 32 neighbouring
-// columns of one token: whole sectors at any alignment of the rows, and a 32 x 32
-// piece costs 32 loads, 32 stores and one tensor-memory load. (The warp-level
-// instructions above move the same piece with 350 instructions and 224 wavefronts
-// of shared memory and L1, which bound them: 160 us for 8192 tokens of 11008
-// columns at rank 64.)
-// Warps 0-7: lanes 32 (w mod 4) .., tokens 32 (w / 4) .., in two steps of 16
-// tokens, the next step's y in flight; warp 8: TMA; warp 9: MMA. All waits bounded.
-constexpr int kTcThreads = 320, kTcCols = 128, kTcTokens = 64, kTcTmem = 2 * kTcTokens;
-constexpr int kTcBTile = kTcCols * 128, kTcHTile = kTcTokens * 128;  // 64 ranks: rows of 128 bytes
-
-struct ExpandTc {
-  static constexpr int kStages = 3;  // of B: a block of 64 ranks each
-  int blocks, terms;                 // blocks of 64 ranks
-  __host__ __device__ int h_off() const { return kStages * kTcBTile; }
-  __host__ __device__ int bar_off() const { return h_off() + terms * blocks * kTcHTile; }
-  __host__ __device__ int bytes() const { return bar_off() + 128 + 1024; }  // + room to align the base
-};
-
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-// 16 consecutive columns of this warp's 32 lanes
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
-// Loads and stores under a predicate, without a branch (which would have each
-// load waited for where its branch ends); the bits as they lie in memory.
-__device__ __forceinline__ void load_if(bool live, const uint8_t *p, uint32_t &v) {
-  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.cs.b32 %0, [%1];\n}\n" : "=&r"(v) : "l"(p), "r"(int(live)));
-}
-__device__ __forceinline__ void load_half_if(bool live, const uint8_t *p, uint32_t &v) {
-  asm volatile("{\n .reg .pred q;\n .reg .b16 h;\n setp.ne.b32 q, %2, 0;\n mov.b16 h, 0;\n @q ld.global.cs.b16 h, [%1];\n cvt.u32.u16 %0, h;\n}\n"
-               : "=r"(v) : "l"(p), "r"(int(live)));
-}
-__device__ __forceinline__ void store_if(bool live, uint8_t *p, uint32_t v) {
-  asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q st.global.cs.b32 [%0], %1;\n}\n" ::"l"(p), "r"(v), "r"(int(live)) : "memory");
-}
-__device__ __forceinline__ void store_half_if(bool live, uint8_t *p, uint32_t v) {
-  asm volatile("{\n .reg .pred q;\n .reg .b16 h;\n setp.ne.b32 q, %2, 0;\n cvt.u16.u32 h, %1;\n @q st.global.cs.b16 [%0], h;\n}\n" ::"l"(p), "r"(v), "r"(int(live)) : "memory");
-}
-
-// The work of a grid is one run of turns, tile after tile, cut into equal pieces,
-// one per CTA: a tile's preparation (its tokens, H's operand: 3 us) is then paid
-// once or twice per CTA, and all CTAs end together.
-template <int WE, int YE>
-__global__ void __launch_bounds__(kTcThreads, 2)
-    k_lora_expand_tc(const __grid_constant__ CUtensorMap bmap, const LoraArgs a, const Work w, const ExpandTc e, const uint32_t spin) {
-  extern __shared__ uint8_t raw[];
-  __shared__ float unscale[kTcTokens];
-  __shared__ int rows[kTcTokens];
-  __shared__ __align__(16) int64_t y_off[kTcTokens], out_off[kTcTokens];
-  __shared__ uint32_t tmem_slot;
-  __shared__ int aborted;
-  constexpr int kTerms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2, YS = Elem<YE>::kBytes, S = ExpandTc::kStages;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint8_t *sm = raw + (((smem_u32(raw) + 1023u) & ~1023u) - smem_u32(raw));
-  uint64_t *bar = reinterpret_cast<uint64_t *>(sm + e.bar_off());
-  uint64_t *b_full = bar, *b_empty = bar + 3, *d_full = bar + 6, *d_empty = bar + 8, *done = bar + 10;
-  volatile int *abort_flag = &aborted;
-  if (tid == 0) {
-    for (int i = 0; i < S; ++i) {
-      mbar_init(&b_full[i], 1);
-      mbar_init(&b_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&d_full[i], 1);
-      mbar_init(&d_empty[i], 8);
-    }
-    mbar_init(done, 1);
-    aborted = 0;
-    fence_mbar_init();
-  }
-  if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)), "r"(kTcTmem) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-
-  const int groups = (a.M + kTcCols - 1) / kTcCols;
-  const int64_t units = int64_t(*w.n_tiles) * groups;
-  const int64_t u1 = units * (blockIdx.x + 1) / gridDim.x;
-  int done_turns = 0;  // with products, over all tiles: the barriers' phases
-  int armed = 0;       // blocks of B that were asked for
-  for (int64_t u = units * blockIdx.x / gridDim.x; u < u1;) {
-    const int tile = int(u / groups), g0 = int(u - int64_t(tile) * groups), n_turns = int(min(u1 - u, int64_t(groups - g0)));
-    u += n_turns;
-    __syncthreads();  // the tile before this one is done with rows, offsets and H
-    if (*abort_flag) break;
-    int ad, count;
-    if (!find_tile<kTcTokens>(a, w, tile, rows, ad, count)) break;
-    if (ad < 0 && a.y == a.out) continue;
-    if (tid < kTcTokens) {
-      y_off[tid] = rows[tid] * a.y_row;
-      out_off[tid] = rows[tid] * a.out_row;
-    }
-    // H's terms as the second operand: token rows of 64 ranks, 128-byte swizzled; a lane has two ranks
-    if (ad >= 0) {
-      for (int r = warp; r < kTcTokens; r += kTcThreads / 32) {
-        float h[2][2], m = 0.0f;
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int c = 64 * b + 2 * lane + i;
-            h[b][i] = r < count && c < a.rank ? __ldcg(w.H + int64_t(rows[r]) * a.rank + c) : 0.0f;
-            m = fmaxf(m, fabsf(h[b][i]));
-          }
-        float up = 1.0f;
-        if constexpr (WE == kElemF16) up = scale_row(m, unscale, r, lane);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (b >= e.blocks) break;
-          float x = h[b][0] * up, y = h[b][1] * up;
-#pragma unroll
-          for (int k = 0; k < kTerms; ++k) {
-            const uint32_t v = pack_pair<WE>(x, y);
-            const float2 f = unpack_pair<WE>(v);
-            x -= f.x, y -= f.y;
-            *reinterpret_cast<uint32_t *>(sm + e.h_off() + (k * e.blocks + b) * kTcHTile + sw128_off(r, lane >> 2) + (lane & 3) * 4) = v;
-          }
-        }
-      }
-      fence_async_smem();
-    }
-    __syncthreads();
-
-    const int i0 = done_turns;  // turn i of the tile is turn i0 + i of the barriers
-    if (ad >= 0) done_turns += n_turns;
-    if (warp == 8) {
-      if (lane == 0 && ad >= 0) {
-        for (int q = i0 * e.blocks; q < (i0 + n_turns) * e.blocks; ++q) {  // block q of all turns
-          const int st = q % S, turn = q / e.blocks - i0, b = q % e.blocks;
-          if (!tc_wait(&b_empty[st], ((q / S) & 1) ^ 1, spin, abort_flag, a.err)) break;
-          mbar_arrive_expect_tx(&b_full[st], uint32_t(kTcBTile));
-          tma_load_3d(sm + st * kTcBTile, &bmap, b * 64, (g0 + turn) * kTcCols, ad, &b_full[st]);
-          armed = q + 1;
-        }
-      }
-    } else if (warp == 9) {
-      if (lane == 0 && ad >= 0) {
-        // kind::f16: fp32 accumulators, both operands of the adapters' type, K-major
-        constexpr uint32_t kType = WE == kElemBF16 ? (1u << 7) | (1u << 10) : 0u;
-        constexpr uint32_t kIdesc = (1u << 4) | kType | (uint32_t(kTcTokens >> 3) << 17) | (uint32_t(kTcCols >> 4) << 24);
-        const uint32_t b0 = smem_u32(sm), h0 = smem_u32(sm + e.h_off());
-        for (int i = i0; i < i0 + n_turns; ++i) {
-          const int buf = i & 1;
-          bool there = tc_wait(&d_empty[buf], ((i >> 1) & 1) ^ 1, spin, abort_flag, a.err);
-          const uint32_t d = tmem + uint32_t(buf * kTcTokens);
-          uint32_t more = 0;
-          for (int b = 0; b < e.blocks && there; ++b) {
-            const int q = i * e.blocks + b, st = q % S;
-            there = tc_wait(&b_full[st], (q / S) & 1, spin, abort_flag, a.err);
-            if (!there) break;
-            tc_fence_after();
-            const uint64_t b_desc = sw128_desc(b0 + st * kTcBTile);
-            for (int k = kTerms - 1; k >= 0; --k) {
-              const uint64_t h_desc = sw128_desc(h0 + (k * e.blocks + b) * kTcHTile);
-              for (int n = 0; n < 4 && b * 64 + n * 16 < a.rank; ++n) {
-                tc_mma(d, b_desc + uint64_t(2 * n), h_desc + uint64_t(2 * n), kIdesc, more);
-                more = 1;
-              }
-            }
-            tc_commit(&b_empty[st]);
-          }
-          if (!there) break;
-          tc_commit(&d_full[buf]);
-        }
-      }
-    } else {
-      const int lg = warp & 3, t0 = (warp >> 2) * 32;
-      const uint32_t lane_addr = tmem + (uint32_t(lg * 32) << 16);
-      const int odd = lane & 1;
-      // 16-bit rows, where their boundaries allow it: two columns of one token per access (220 us -> 125 for
-      // 8192 tokens of 11008 columns; fp32 rows, whose 32 columns are a line of 128 bytes, lose by it, 161 -> 184)
-      const bool pairs = YS == 2 && a.y_vec && a.M % 2 == 0;
-      // steps of 16 tokens: 2 per turn; the next one's y is asked for before this one's sums are.
-      // The bits of y. With pairs: of the lane's and its neighbour's column of one token, the first of
-      // two in the even lane, the second in the odd one (16-bit rows: one word); else of the lane's column
-      uint32_t y[2][16];
-      auto column = [&](int step) { return (g0 + (step >> 1)) * kTcCols + lg * 32 + lane; };
-      auto ask = [&](int step, uint32_t (&v)[16]) {
-        const int m = column(step), from = t0 + (step & 1) * 16, end = a.y && step < 2 * n_turns && m < a.M ? count : 0;
-        if (pairs) {
-          const uint8_t *p = a.y + int64_t(m - odd) * YS;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int r = from + 2 * j + odd;
-            load_if(r < end, p + y_off[r], v[j]);
-          }
-        } else {
-          const uint8_t *p = a.y + int64_t(m) * YS;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int64_t o = y_off[from + j];
-            if constexpr (YS == 4)
-              load_if(from + j < end, p + o, v[j]);
-            else
-              load_half_if(from + j < end, p + o, v[j]);
-          }
-        }
-      };
-      bool ok = true;
-      auto give = [&](int step, const uint32_t (&v)[16]) {
-        const int turn = i0 + (step >> 1), m = column(step), from = t0 + (step & 1) * 16, end = m < a.M ? count : 0;
-        uint32_t d[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) d[j] = 0;
-        if (ad >= 0) {
-          if ((step & 1) == 0) {
-            ok = tc_wait_warp(&d_full[turn & 1], (turn >> 1) & 1, spin, abort_flag, a.err);
-            if (!ok) return;
-            tc_fence_after();
-          }
-          tmem_ld16(lane_addr + uint32_t((turn & 1) * kTcTokens + from), d);
-          if (step & 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[turn & 1]);
-          }
-        }
-        // the token's row of y plus its products; without an adapter y as it is
-        auto sum = [&](uint32_t x, float with, int r) {
-          return ad < 0 ? with : WE == kElemF16 ? __fmaf_rn(__uint_as_float(x), unscale[r], with) : __fadd_rn(__uint_as_float(x), with);
-        };
-        if (pairs) {
-          uint8_t *p = a.out + int64_t(m - odd) * YS;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t other = __shfl_xor_sync(kFull, odd ? d[2 * j] : d[2 * j + 1], 1);
-            const int r = from + 2 * j + odd;
-            const uint32_t x0 = odd ? other : d[2 * j], x1 = odd ? d[2 * j + 1] : other;
-            if constexpr (YS == 2) {
-              const float2 with = unpack_pair<YE>(v[j]);
-              store_if(r < end, p + out_off[r], pack_pair<YE>(sum(x0, with.x, r), sum(x1, with.y, r)));
-            }
-          }
-        } else {
-          uint8_t *p = a.out + int64_t(m) * YS;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int r = from + j;
-            const int64_t o = out_off[r];
-            if constexpr (YS == 4)
-              store_if(r < end, p + o, __float_as_uint(sum(d[j], __uint_as_float(v[j]), r)));
-            else
-              store_half_if(r < end, p + o, pack_pair<YE>(sum(d[j], unpack_pair<YE>(v[j]).x, r), 0.0f));
-          }
-        }
-      };
-      ask(0, y[0]);
-      for (int step = 0; step < 2 * n_turns && ok; step += 2) {
-        ask(step + 1, y[1]);
-        give(step, y[0]);
-        if (!ok) break;
-        ask(step + 2, y[0]);
-        give(step + 1, y[1]);
-      }
-      tc_fence_before();
-    }
-  }
-  // copies and products in flight end by themselves: none is left behind
-  if (warp == 8 && lane == 0) {
-    for (int i = 0; i < S && i < armed; ++i) {
-      const int last = armed - 1 - ((armed - 1 - i) % S);
-      tc_drain(&b_full[i], (last / S) & 1);
-    }
-  }
-  if (warp == 9 && lane == 0) {
-    tc_commit(done);
-    tc_drain(done, 0);
-  }
-  __syncthreads();
-  if (warp == 9) {
-    __syncwarp();
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcTmem) : "memory");
-  }
-}
-
 // ------------------------------------------------------------------ host --
 
-struct Plan {
-  bool grouped;
-  int tm, tiles, splits;  // tiles: at most as many
-  size_t bytes;
-  size_t sorted_off, tiles_off, n_off;
-};
-
-Plan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
-  Plan p{};
+LoraPlan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
+  LoraPlan p{};
   const int64_t groups = std::min(n + 1, T);
   p.grouped = T > kLeaders;
   // a tile of 64 pays where an adapter fills it, by the mean, and there is work
@@ -1021,69 +579,52 @@ Plan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
   // of 16, 30 with 64; 2048 tokens at rank 16 27 and 32, at rank 32 51 and 44)
   p.tm = T > 512 && T * rank > 32768 && T >= 32 * groups ? 64 : 16;
   p.tiles = int(p.grouped ? T / p.tm + groups : T);
-  // clusters that have work, about; each split in up to 8 CTAs while SMs are left,
-  // down to four blocks of 32 k per warp (tiles of 64: 8 per CTA), or one where
-  // clusters are few
-  const int64_t chunk = p.tm == 16 ? (rank <= 16 ? 16 : 32) : 64;
-  const int64_t busy = (p.grouped ? T / p.tm + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2) * ((rank + chunk - 1) / chunk);
-  const int64_t pieces = K / 32 / (p.tm == 64 ? 8 : busy < 32 ? 4 : 16);
+  // clusters that have work, about; each split in up to 8 CTAs while SMs are left:
+  // tiles of 16 down to four blocks of 32 k per warp, or one where clusters are few;
+  // tiles of 64, of which an SM has two CTAs, down to four stages of 64 k
   p.splits = 1;
-  while (p.splits < 8 && busy * p.splits < 304 && 2 * p.splits <= pieces) p.splits *= 2;
+  if (p.tm == 64) {
+    const int64_t busy = T / 64 + groups / 2, pieces = K / 256;
+    while (p.splits < 8 && busy * p.splits < 160 && 2 * p.splits <= pieces) p.splits *= 2;
+  } else {
+    const int64_t chunk = rank <= 16 ? 16 : 32;
+    const int64_t busy = (p.grouped ? T / 16 + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2) * ((rank + chunk - 1) / chunk);
+    const int64_t pieces = K / 32 / (busy < 32 ? 4 : 16);
+    while (p.splits < 8 && busy * p.splits < 304 && 2 * p.splits <= pieces) p.splits *= 2;
+  }
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   p.bytes = up(size_t(T) * size_t(rank) * 4);
   if (p.grouped) {
     p.sorted_off = p.bytes;
     p.tiles_off = p.sorted_off + up(size_t(T) * 4);
-    p.n_off = p.tiles_off + up(size_t(p.tiles) * sizeof(Tile));
+    p.n_off = p.tiles_off + up(size_t(p.tiles) * sizeof(LoraTile));
     p.bytes = p.n_off + 256;
   }
   return p;
 }
 
-template <typename... P, typename... A>
-cudaError_t launch_ex(void (*fn)(P...), dim3 grid, int threads, int smem, int cluster, bool dependent, cudaStream_t stream, A... args) {
-  if (smem > 0) {
-    const cudaError_t e = ensure_smem(reinterpret_cast<const void *>(fn), smem);
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  attr[n].id = cudaLaunchAttributeClusterDimension;
-  attr[n].val.clusterDim.x = unsigned(cluster);
-  attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
-  ++n;
-  if (dependent) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n].val.programmaticStreamSerializationAllowed = 1;
-    ++n;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
+// chunks of ranks side by side in the grid: they read the same x
+template <int XE, int WE, int NT>
+cudaError_t shrink16_nt(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
+  const dim3 grid(unsigned(p.splits * ((a.rank + 8 * NT - 1) / (8 * NT))), unsigned(p.tiles));
+  return launch_ex(k_lora_shrink16<XE, WE, NT>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
 }
-
-template <int XE, int WE, int TM, int NT>
-cudaError_t shrink_nt(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
-  const dim3 grid(unsigned(p.splits * ((a.rank + 8 * NT - 1) / (8 * NT))), unsigned(p.tiles));  // chunks of ranks side by side: they read the same x
-  if constexpr (TM == 64)
-    return launch_ex(k_lora_shrink64<XE, WE, NT>, grid, kShrinkThreads, Ring<XE, NT>::kBytes, p.splits, true, s, a, w, p.splits);
-  else
-    return launch_ex(k_lora_shrink16<XE, WE, NT>, grid, kShrinkThreads, 0, p.splits, p.grouped, s, a, w, p.splits);
+template <int XE, int WE>
+cudaError_t shrink16(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
+  return a.rank <= 16 ? shrink16_nt<XE, WE, 2>(a, w, p, s) : shrink16_nt<XE, WE, 4>(a, w, p, s);
 }
-template <int XE, int WE, int TM>
-cudaError_t shrink(const LoraArgs &a, const Work &w, const Plan &p, cudaStream_t s) {
-  if (a.rank <= 16) return shrink_nt<XE, WE, TM, 2>(a, w, p, s);
-  if (TM == 16 || a.rank <= 32) return shrink_nt<XE, WE, TM, 4>(a, w, p, s);
-  if constexpr (TM == 64) return shrink_nt<XE, WE, TM, 8>(a, w, p, s);
+template <int NT>
+cudaError_t shrink64_nt(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
+  const dim3 grid(unsigned(p.splits * ((a.rank + 8 * NT - 1) / (8 * NT))), unsigned(p.tiles));
+  return launch_ex(k_lora_shrink64<NT>, grid, kShrinkThreads, Ring<NT>::kBytes, p.splits, true, s, a, w, p.splits);
+}
+cudaError_t shrink64_f32_f16(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
+  if (a.rank <= 16) return shrink64_nt<2>(a, w, p, s);
+  return a.rank <= 32 ? shrink64_nt<4>(a, w, p, s) : shrink64_nt<8>(a, w, p, s);
 }
 
 template <int WE, int YE>
-cudaError_t expand16(const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
+cudaError_t expand16(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, int sms, cudaStream_t s) {
   const int64_t groups = (a.M + 255) / 256;
   int turns = 1;  // of a CTA: several where enough CTAs remain
   while (turns < 8 && groups * p.tiles / (2 * turns) >= int64_t(sms) * 8) turns *= 2;
@@ -1093,43 +634,24 @@ cudaError_t expand16(const LoraArgs &a, const Work &w, const Plan &p, int sms, c
   return launch_ex(k_lora_expand<WE, YE, 4>, grid, kExpandThreads, Expand<WE, YE, 4>::kBytes, 1, true, s, a, w, turns);
 }
 
-template <int WE, int YE>
-cudaError_t expand64(const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
-  if (!encode) return cudaErrorNotSupported;
-  CUtensorMap map{};
-  if (a.n_adapters > 0) {  // [adapter][column][rank]; ranks and columns beyond the adapter's read as zeros
-    const cuuint64_t dims[3] = {cuuint64_t(a.rank), cuuint64_t(a.M), cuuint64_t(a.n_adapters)};
-    const cuuint64_t strides[2] = {cuuint64_t(a.rank) * 2, cuuint64_t(a.rank) * 2 * cuuint64_t(a.M)};
-    const cuuint32_t box[3] = {64, kTcCols, 1}, step[3] = {1, 1, 1};
-    if (encode(&map, WE == kElemBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint8_t *>(a.B), dims, strides,
-               box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  }
-  ExpandTc e;
-  e.blocks = (a.rank + 63) / 64;
-  e.terms = WE == kElemF16 ? 2 : YE == kElemF32 ? 3 : 2;
-  const int64_t units = int64_t(p.tiles) * ((a.M + kTcCols - 1) / kTcCols);
-  const int per_sm = e.bytes() <= 110 * 1024 ? 2 : 1;  // resident
-  const dim3 grid(unsigned(std::min<int64_t>(units, int64_t(sms) * per_sm)));
-  // not a dependent launch: CTAs that come while the first product's are still there
-  // find less shared memory to share an SM, and the grid runs in two parts (200 us for 161)
-  return launch_ex(k_lora_expand_tc<WE, YE>, grid, kTcThreads, e.bytes(), 1, false, s, map, a, w, e, spin_limit());
-}
-
 template <int WE, int TM>
-cudaError_t run(int x_elem, int y_elem, const LoraArgs &a, const Work &w, const Plan &p, int sms, cudaStream_t s) {
+cudaError_t run(int x_elem, int y_elem, const LoraArgs &a, const LoraWork &w, const LoraPlan &p, int sms, cudaStream_t s) {
   if (p.grouped) {
     const cudaError_t e = launch_ex(k_lora_group<TM>, dim3(1), kGroupThreads, 0, 1, false, s, a, w);
     if (e != cudaSuccess) return e;
   }
-  const cudaError_t e = x_elem == kElemF32 ? shrink<kElemF32, WE, TM>(a, w, p, s) : shrink<WE, WE, TM>(a, w, p, s);
-  if (e != cudaSuccess) return e;
-  if constexpr (TM == 64)
-    return y_elem == kElemF32 ? expand64<WE, kElemF32>(a, w, p, sms, s) : expand64<WE, WE>(a, w, p, sms, s);
-  else
+  if constexpr (TM == 64) {
+    cudaError_t e;
+    if constexpr (WE == kElemF16)
+      e = x_elem == kElemF32 ? shrink64_f32_f16(a, w, p, s) : launch_lora_shrink_tc(x_elem, WE, a, w, p, s);
+    else
+      e = launch_lora_shrink_tc(x_elem, WE, a, w, p, s);
+    return e == cudaSuccess ? launch_lora_expand_tc(WE, y_elem, a, w, p, sms, s) : e;
+  } else {
+    const cudaError_t e = x_elem == kElemF32 ? shrink16<kElemF32, WE>(a, w, p, s) : shrink16<WE, WE>(a, w, p, s);
+    if (e != cudaSuccess) return e;
     return y_elem == kElemF32 ? expand16<WE, kElemF32>(a, w, p, sms, s) : expand16<WE, WE>(a, w, p, sms, s);
+  }
 }
 
 }  // namespace
@@ -1143,12 +665,12 @@ cudaError_t launch_lora(int x_elem, int w_elem, int y_elem, LoraArgs a, void *ws
   const DeviceInfo *di = device_info(&err);
   if (!di) return err;
   a.err = di->err_word;
-  const Plan p = plan_of(a.n_tokens, a.n_adapters, a.rank, a.K);
+  const LoraPlan p = plan_of(a.n_tokens, a.n_adapters, a.rank, a.K);
   uint8_t *base = static_cast<uint8_t *>(ws);
-  Work w{reinterpret_cast<float *>(base), nullptr, nullptr, nullptr};
+  LoraWork w{reinterpret_cast<float *>(base), nullptr, nullptr, nullptr};
   if (p.grouped) {
     w.sorted = reinterpret_cast<int32_t *>(base + p.sorted_off);
-    w.tiles = reinterpret_cast<Tile *>(base + p.tiles_off);
+    w.tiles = reinterpret_cast<LoraTile *>(base + p.tiles_off);
     w.n_tiles = reinterpret_cast<int32_t *>(base + p.n_off);
   }
   const int sms = di->sm_count;
