@@ -262,27 +262,30 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
   sum_tile<4>(a, w, &part[0][0][0], 8 * NT, 16 * 8 * NT, rows, ad, count, first, min(8 * NT, a.rank - first), split, splits);
 }
 
-// Tiles of 64 fp32 tokens beside fp16 adapters (whose products the tensor-memory
-// kernel cannot take: terms of fp16 would need each row's range first), up to 64
-// ranks: each of the four warps has 16 of the tokens and all of the CTA's k. Rows of
-// x and of the adapter come through a ring of stages of 64 k by asynchronous copies.
-// A stage: two blocks of 32 k, each a row of 128 bytes per token (the even 16-byte
-// pieces in one half, which half alternates from row to row) and of 64 per rank, so
-// that a quarter-warp's reads of two rows meet no bank twice.
-template <int NT>
+// Tiles of 64 tokens on warp-level instructions, up to 64 ranks: 16-bit rows of up
+// to 64 ranks (31 us for 8192 bf16 tokens of 4096 at rank 64, where the kernel of
+// lora_tc.cu takes 33; at rank 16 21) and fp32 rows beside fp16 adapters (which that
+// kernel cannot take: terms of fp16 would need each row's range first). Each of the
+// four warps has 16 of the tokens and all of the CTA's k. Rows of x and of the
+// adapter come through a ring of stages of 64 k by asynchronous copies (straight
+// loads left a warp waiting for memory in every block of 32 k: 60 us for 2048 tokens).
+// A stage: two blocks of 32 k, each a row of 64 bytes per token and rank (fp32
+// rows: 128 bytes, the even 16-byte pieces in one half, which half alternates
+// from row to row), so that a quarter-warp's reads of two rows meet no bank twice.
+template <int XE, int NT>
 struct Ring {
   static constexpr int kStages = 3;
-  static constexpr int kXRow = 128, kXBlock = 64 * kXRow, kABlock = 8 * NT * 64;
+  static constexpr int kXRow = 32 * Elem<XE>::kBytes, kXBlock = 64 * kXRow, kABlock = 8 * NT * 64;
   static constexpr int kStage = 2 * (kXBlock + kABlock);
   static constexpr int kBytes = kStages * kStage > 64 * 8 * NT * 4 ? kStages * kStage : 64 * 8 * NT * 4;  // or the sums, afterwards
 };
 
-template <int NT>
+template <int XE, int WE, int NT>
 __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs a, const LoraWork w, const int splits) {
-  using R = Ring<NT>;
+  using R = Ring<XE, NT>;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ int rows[64];
-  constexpr int XE = kElemF32, WE = kElemF16, XS = 4;
+  constexpr int XS = Elem<XE>::kBytes;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   pdl_wait();
   int ad, count;
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = xr + i * kStep;
-        const int at = (xc >> 1) + 4 * ((xc & 1) ^ (r & 1));
+        const int at = XE == kElemF32 ? (xc >> 1) + 4 * ((xc & 1) ^ (r & 1)) : xc;
         if (r < count) copy16(x + xb * R::kXBlock + r * R::kXRow + at * 16, src[i] + int64_t(s) * 64 * XS);
       }
     }
@@ -343,11 +346,16 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
         RowWords<XE> xl, xh;
         uint4 bw[NT];
         const uint8_t *pl = x + b * R::kXBlock + (r0 + g) * R::kXRow, *ph = pl + 8 * R::kXRow;
-        const int half = (g & 1) * 64 + t * 16;  // rows g and g + 8 are both even or both odd
-        xl.v[0] = *reinterpret_cast<const uint4 *>(pl + half);
-        xl.v[1] = *reinterpret_cast<const uint4 *>(pl + (half ^ 64));
-        xh.v[0] = *reinterpret_cast<const uint4 *>(ph + half);
-        xh.v[1] = *reinterpret_cast<const uint4 *>(ph + (half ^ 64));
+        if constexpr (XE == kElemF32) {
+          const int half = (g & 1) * 64 + t * 16;  // rows g and g + 8 are both even or both odd
+          xl.v[0] = *reinterpret_cast<const uint4 *>(pl + half);
+          xl.v[1] = *reinterpret_cast<const uint4 *>(pl + (half ^ 64));
+          xh.v[0] = *reinterpret_cast<const uint4 *>(ph + half);
+          xh.v[1] = *reinterpret_cast<const uint4 *>(ph + (half ^ 64));
+        } else {
+          xl.v[0] = *reinterpret_cast<const uint4 *>(pl + t * 16);
+          xh.v[0] = *reinterpret_cast<const uint4 *>(ph + t * 16);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) bw[nt] = *reinterpret_cast<const uint4 *>(ad_rows + b * R::kABlock + (nt * 8 + g) * 64 + t * 16);
         shrink_step<XE, WE, NT>(acc, xl, xh, bw);
@@ -570,6 +578,14 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
 
 // ------------------------------------------------------------------ host --
 
+// CTAs of a cluster, among which K is split: up to 8, while there are fewer than
+// `limit` of them all and each has one of `pieces` pieces of K at least
+int splits_of(int64_t clusters, int64_t limit, int64_t pieces) {
+  int n = 1;
+  while (n < 8 && clusters * n < limit && 2 * n <= pieces) n *= 2;
+  return n;
+}
+
 LoraPlan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
   LoraPlan p{};
   const int64_t groups = std::min(n + 1, T);
@@ -579,18 +595,12 @@ LoraPlan plan_of(int64_t T, int64_t n, int64_t rank, int64_t K) {
   // of 16, 30 with 64; 2048 tokens at rank 16 27 and 32, at rank 32 51 and 44)
   p.tm = T > 512 && T * rank > 32768 && T >= 32 * groups ? 64 : 16;
   p.tiles = int(p.grouped ? T / p.tm + groups : T);
-  // clusters that have work, about; each split in up to 8 CTAs while SMs are left:
-  // tiles of 16 down to four blocks of 32 k per warp, or one where clusters are few;
-  // tiles of 64, of which an SM has two CTAs, down to four stages of 64 k
-  p.splits = 1;
-  if (p.tm == 64) {
-    const int64_t busy = T / 64 + groups / 2, pieces = K / 256;
-    while (p.splits < 8 && busy * p.splits < 160 && 2 * p.splits <= pieces) p.splits *= 2;
-  } else {
-    const int64_t chunk = rank <= 16 ? 16 : 32;
-    const int64_t busy = (p.grouped ? T / 16 + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2) * ((rank + chunk - 1) / chunk);
-    const int64_t pieces = K / 32 / (busy < 32 ? 4 : 16);
-    while (p.splits < 8 && busy * p.splits < 304 && 2 * p.splits <= pieces) p.splits *= 2;
+  // about as many tiles have work; in tiles of 16 a warp has four blocks of 32 k at
+  // least, or one where clusters are few
+  p.busy = p.grouped ? T / p.tm + groups / 2 : (T + 15) / 16 + std::min(n, T) / 2;
+  if (p.tm == 16) {
+    const int64_t clusters = p.busy * (rank <= 16 ? 1 : (rank + 31) / 32);
+    p.splits = splits_of(clusters, 304, K / 32 / (clusters < 32 ? 4 : 16));
   }
   auto up = [](size_t b) { return (b + 255) / 256 * 256; };
   p.bytes = up(size_t(T) * size_t(rank) * 4);
@@ -613,14 +623,24 @@ template <int XE, int WE>
 cudaError_t shrink16(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
   return a.rank <= 16 ? shrink16_nt<XE, WE, 2>(a, w, p, s) : shrink16_nt<XE, WE, 4>(a, w, p, s);
 }
-template <int NT>
+template <int XE, int WE, int NT>
 cudaError_t shrink64_nt(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
   const dim3 grid(unsigned(p.splits * ((a.rank + 8 * NT - 1) / (8 * NT))), unsigned(p.tiles));
-  return launch_ex(k_lora_shrink64<NT>, grid, kShrinkThreads, Ring<NT>::kBytes, p.splits, true, s, a, w, p.splits);
+  return launch_ex(k_lora_shrink64<XE, WE, NT>, grid, kShrinkThreads, Ring<XE, NT>::kBytes, p.splits, true, s, a, w, p.splits);
 }
-cudaError_t shrink64_f32_f16(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
-  if (a.rank <= 16) return shrink64_nt<2>(a, w, p, s);
-  return a.rank <= 32 ? shrink64_nt<4>(a, w, p, s) : shrink64_nt<8>(a, w, p, s);
+template <int XE, int WE>
+cudaError_t shrink64(const LoraArgs &a, const LoraWork &w, LoraPlan p, cudaStream_t s) {
+  if constexpr (XE != kElemF32 || WE == kElemBF16)
+    if (XE == kElemF32 || a.rank > 64) {
+      p.splits = splits_of(p.busy, 160, a.K / 256);  // an SM has two CTAs, each four stages of 64 k at least
+      return launch_lora_shrink_tc(XE, WE, a, w, p, s);
+    }
+  p.splits = splits_of(p.busy * ((a.rank + 63) / 64), 304, a.K / 256);
+  if constexpr (XE != kElemF32 || WE != kElemBF16) {
+    if (a.rank <= 16) return shrink64_nt<XE, WE, 2>(a, w, p, s);
+    return a.rank <= 32 ? shrink64_nt<XE, WE, 4>(a, w, p, s) : shrink64_nt<XE, WE, 8>(a, w, p, s);
+  }
+  return cudaErrorInvalidValue;  // not reached
 }
 
 template <int WE, int YE>
@@ -641,11 +661,7 @@ cudaError_t run(int x_elem, int y_elem, const LoraArgs &a, const LoraWork &w, co
     if (e != cudaSuccess) return e;
   }
   if constexpr (TM == 64) {
-    cudaError_t e;
-    if constexpr (WE == kElemF16)
-      e = x_elem == kElemF32 ? shrink64_f32_f16(a, w, p, s) : launch_lora_shrink_tc(x_elem, WE, a, w, p, s);
-    else
-      e = launch_lora_shrink_tc(x_elem, WE, a, w, p, s);
+    const cudaError_t e = x_elem == kElemF32 ? shrink64<kElemF32, WE>(a, w, p, s) : shrink64<WE, WE>(a, w, p, s);
     return e == cudaSuccess ? launch_lora_expand_tc(WE, y_elem, a, w, p, sms, s) : e;
   } else {
     const cudaError_t e = x_elem == kElemF32 ? shrink16<kElemF32, WE>(a, w, p, s) : shrink16<WE, WE>(a, w, p, s);

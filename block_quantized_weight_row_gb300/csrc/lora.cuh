@@ -98,23 +98,33 @@ __device__ __forceinline__ uint32_t cut_pair(float &x, float &y) {
 
 // A cluster's sums of a tile: each of its CTAs adds up its share, over the CTAs
 // and, in each, over PARTS pieces of k (kept `apart` floats from one another), in
-// order. part: [token][rank] of every CTA, `pitch` floats per token.
+// order. part: [token][rank] of every CTA, `pitch` floats per token, 16-byte aligned.
 template <int PARTS>
 __device__ __forceinline__ void sum_tile(const LoraArgs &a, const LoraWork &w, float *part, int pitch, int apart, const int *rows, int ad, int count, int first,
                                          int ranks, int split, int splits) {
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   cluster.sync();
   const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
-  const int n = count * ranks;
+  // four ranks at a time (ranks come in eights), the loads from all CTAs in flight together
+  const int quads = ranks / 4, n = count * quads;
   for (int e = split * blockDim.x + threadIdx.x; e < n; e += splits * blockDim.x) {
-    const int row = e / ranks, r = e - row * ranks;
-    float sum = 0.0f;
-    for (int c = 0; c < splits; ++c) {
-      const float *p = cluster.map_shared_rank(part, c) + row * pitch + r;
+    const int row = e / quads, r = 4 * (e - row * quads);
+    float4 v[8][PARTS];
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) sum += p[q * apart];
-    }
-    w.H[int64_t(rows[row]) * a.rank + first + r] = sum * s;
+    for (int c = 0; c < 8; ++c)
+      if (c < splits) {
+        const float *p = cluster.map_shared_rank(part, c) + row * pitch + r;
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) v[c][q] = *reinterpret_cast<const float4 *>(p + q * apart);
+      }
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (c < splits) {
+#pragma unroll
+        for (int q = 0; q < PARTS; ++q) sum.x += v[c][q].x, sum.y += v[c][q].y, sum.z += v[c][q].z, sum.w += v[c][q].w;
+      }
+    *reinterpret_cast<float4 *>(w.H + int64_t(rows[row]) * a.rank + first + r) = make_float4(sum.x * s, sum.y * s, sum.z * s, sum.w * s);
   }
   cluster.sync();  // the others' sums are read from here until now
 }
@@ -135,7 +145,8 @@ __device__ __forceinline__ float scale_row(float m, float *unscale, int r, int l
 
 struct LoraPlan {
   bool grouped;
-  int tm, tiles, splits;  // tiles: at most as many
+  int tm, tiles, splits;  // tiles: at most as many; splits: set here for tiles of 16
+  int64_t busy;
   size_t bytes;
   size_t sorted_off, tiles_off, n_off;
 };
@@ -167,8 +178,8 @@ cudaError_t launch_ex(void (*fn)(P...), dim3 grid, int threads, int smem, int cl
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// Tiles of 64 tokens on the tensor-memory kernels (lora_tc.cu).
-bool lora_tc_shrinks(int x_elem, int w_elem);  // not fp32 rows beside fp16 adapters
+// Tiles of 64 tokens on the tensor-memory kernels (lora_tc.cu); the first product not
+// for fp32 rows beside fp16 adapters.
 cudaError_t launch_lora_shrink_tc(int x_elem, int w_elem, const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s);
 cudaError_t launch_lora_expand_tc(int w_elem, int y_elem, const LoraArgs &a, const LoraWork &w, const LoraPlan &p, int sms, cudaStream_t s);
 

@@ -53,6 +53,12 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 __device__ __forceinline__ void load_if(bool live, const uint8_t *p, uint32_t &v) {
   asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n mov.b32 %0, 0;\n @q ld.global.cs.b32 %0, [%1];\n}\n" : "=&r"(v) : "l"(p), "r"(int(live)));
 }
+__device__ __forceinline__ void load16_if(bool live, const uint8_t *p, uint4 &v) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n mov.b32 %0, 0;\n mov.b32 %1, 0;\n mov.b32 %2, 0;\n mov.b32 %3, 0;\n"
+      " @q ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n}\n"
+      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w) : "l"(p), "r"(int(live)));
+}
 __device__ __forceinline__ void load_half_if(bool live, const uint8_t *p, uint32_t &v) {
   asm volatile("{\n .reg .pred q;\n .reg .b16 h;\n setp.ne.b32 q, %2, 0;\n mov.b16 h, 0;\n @q ld.global.cs.b16 h, [%1];\n cvt.u32.u16 %0, h;\n}\n"
                : "=r"(v) : "l"(p), "r"(int(live)));
@@ -307,33 +313,39 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 
 // ------------------------------------- first product on tcgen05 --
 
-// H of a tile of 64 tokens: D[rank][token] = A (128 ranks x 64 k a stage, straight
-// from the adapter by TMA; ranks it has not read as zeros) times the tokens' rows of
-// x, in tensor memory. 16-bit rows go by asynchronous copies to where the operand's
-// swizzle wants them; fp32 rows through registers, two stages ahead, cut into three
-// bf16 terms, each an operand tile. K is cut over the CTAs of a cluster and, in a
-// CTA, over four accumulators (256 columns), so that the products' chains stay
-// short; the sums of all meet in fp32 in a fixed order.
-// (Warp-level products, fed from shared memory by their own loads, took 31 us for
-// 8192 bf16 tokens of 4096 at rank 64 and 85 us for fp32 ones.)
+// H of a tile of 64 tokens: D[rank][token] = A (up to 128 ranks x 64 k a stage,
+// straight from the adapter by TMA; ranks it has not read as zeros) times the tokens'
+// rows of x, in tensor memory. Rows go through registers, stages ahead, to where the
+// operand's swizzle wants them; fp32 rows are cut into three bf16 terms, each an
+// operand tile. K is cut over the CTAs of a cluster and, in a CTA, over four
+// accumulators (256 columns), so that the products' chains stay short; the sums of
+// all meet in fp32 in a fixed order.
+// For fp32 rows and for more than 64 ranks, where the warp-level kernel of lora.cu
+// is bound by its instructions: whole calls of 8192 tokens of 4096 to 11008 columns
+// take 189 us for 219 (fp32, rank 64) and 216 for 231 (bf16, rank 128). A stage takes
+// 0.8 us whatever the copies' form or depth.
 // Warps 0-7: rows of x, then the sums; warp 8: TMA; warp 9: MMA. All waits bounded.
 constexpr int kShThreads = 320, kShRegions = 4, kShTmem = kShRegions * kTcTokens;
-constexpr int kShATile = 128 * 128, kShXTile = kTcTokens * 128, kShPitch = 128;
+constexpr int kShXTile = kTcTokens * 128, kShPitch = 128;
 
-template <int XE>
+// ROWS: ranks of a stage, 64 or 128. With 64 the products still have 128 rows: those
+// beyond, of what lies behind the tile, reach only sums that nobody reads.
+template <int XE, int ROWS>
 struct ShrinkTc {
   static constexpr int kTerms = XE == kElemF32 ? 3 : 1;
-  static constexpr int kStages = XE == kElemF32 ? 2 : 4;
-  static constexpr int kStage = kShATile + kTerms * kShXTile;
+  static constexpr int kStages = XE == kElemF32 ? (ROWS == 64 ? 3 : 2) : (ROWS == 64 ? 6 : 4);
+  static constexpr int kAhead = XE == kElemF32 ? 2 : 5;  // stages of x in registers
+  static constexpr int kATile = ROWS * 128, kStage = kATile + kTerms * kShXTile;
   static constexpr int kBarOff = kStages * kStage;
-  static constexpr int kBytes = kBarOff + 128 + 1024;  // + room to align the base
+  static constexpr int kBytes = kBarOff + 256 + 1024;  // + room to align the base
+  static_assert(kStage >= 128 * 128, "the last stage's products stay inside");
   static_assert(kBarOff >= kTcTokens * kShPitch * 4, "the sums' place");
 };
 
-template <int XE, int WE>
+template <int XE, int WE, int ROWS>
 __global__ void __launch_bounds__(kShThreads, 2)
     k_lora_shrink_tc(const __grid_constant__ CUtensorMap amap, const LoraArgs a, const LoraWork w, const int splits, const uint32_t spin) {
-  using R = ShrinkTc<XE>;
+  using R = ShrinkTc<XE, ROWS>;
   constexpr int S = R::kStages, XS = Elem<XE>::kBytes;
   extern __shared__ uint8_t raw[];
   __shared__ int rows[kTcTokens];
@@ -378,65 +390,52 @@ __global__ void __launch_bounds__(kShThreads, 2)
     const uint32_t to[2] = {sw128_off(r, c), sw128_off(r + 32, c)};
     auto there = [&](int i) { return (s0 + i) * 64 + c * 8 < a.K; };
     bool ok = true;
-    if constexpr (XE == kElemF32) {
-      uint4 v[3][2][2];
-      auto ask = [&](int i, uint4 (&q)[2][2]) {
+    constexpr int kAhead = R::kAhead, kVec = XS / 2;  // stages in registers; 16-byte pieces of 8 k
+    uint4 v[kAhead + 1][2][kVec];
+    auto ask = [&](int i, uint4 (&q)[2][kVec]) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (i < n && live[h] && there(i)) {
-            const uint4 *p = reinterpret_cast<const uint4 *>(src[h] + int64_t(i) * 64 * XS);
-            q[h][0] = __ldg(p);
-            q[h][1] = __ldg(p + 1);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) load16_if(i < n && live[h] && there(i), src[h] + int64_t(i) * 64 * XS + 16 * k, q[h][k]);
+    };
+#pragma unroll
+    for (int k = 0; k <= kAhead; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < kVec; ++q) v[k][h][q] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ask(k, v[k]);
+    // (buffers by constant indices: moving a register that a load is on its way to waits for it)
+    for (int i0 = 0; i0 < n && ok; i0 += kAhead + 1)
+#pragma unroll
+    for (int u = 0; u <= kAhead; ++u) {
+      const int i = i0 + u;
+      if (i >= n) break;
+      ask(i + kAhead, v[(u + kAhead) % (kAhead + 1)]);
+      ok = tc_wait_warp(&empty[i % S], ((i / S) & 1) ^ 1, spin, abort_flag, a.err);
+      if (!ok) break;
+      uint8_t *x = sm + (i % S) * R::kStage + R::kATile;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if constexpr (XE == kElemF32) {
+          float f[8];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const uint4 q = v[u][h][k];
+            f[4 * k] = __uint_as_float(q.x), f[4 * k + 1] = __uint_as_float(q.y), f[4 * k + 2] = __uint_as_float(q.z), f[4 * k + 3] = __uint_as_float(q.w);
           }
-      };
-#pragma unroll
-      for (int k = 0; k < 3; ++k)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) v[k][h][0] = v[k][h][1] = make_uint4(0, 0, 0, 0);
-      ask(0, v[0]);
-      ask(1, v[1]);
-      for (int i = 0; i < n; ++i) {
-        ask(i + 2, v[2]);
-        ok = tc_wait_warp(&empty[i % S], ((i / S) & 1) ^ 1, spin, abort_flag, a.err);
-        if (!ok) break;
-        uint8_t *x = sm + (i % S) * R::kStage + kShATile;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float f[8] = {__uint_as_float(v[0][h][0].x), __uint_as_float(v[0][h][0].y), __uint_as_float(v[0][h][0].z), __uint_as_float(v[0][h][0].w),
-                        __uint_as_float(v[0][h][1].x), __uint_as_float(v[0][h][1].y), __uint_as_float(v[0][h][1].z), __uint_as_float(v[0][h][1].w)};
 #pragma unroll
           for (int k = 0; k < 3; ++k)
             *reinterpret_cast<uint4 *>(x + k * kShXTile + to[h]) =
                 make_uint4(cut_pair(f[0], f[1]), cut_pair(f[2], f[3]), cut_pair(f[4], f[5]), cut_pair(f[6], f[7]));
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&x_full[i % S]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) v[0][h][k] = v[1][h][k], v[1][h][k] = v[2][h][k];
-      }
-    } else {
-      constexpr int kLag = S - 2;  // copies of as many stages are in flight behind a stage's
-      for (int i = 0; i < n + kLag; ++i) {
-        if (i < n) {
-          ok = tc_wait_warp(&empty[i % S], ((i / S) & 1) ^ 1, spin, abort_flag, a.err);
-          if (!ok) break;
-          uint8_t *x = sm + (i % S) * R::kStage + kShATile;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (live[h] && there(i)) copy16(x + to[h], src[h] + int64_t(i) * 64 * XS);
-        }
-        asm volatile("cp.async.commit_group;" ::: "memory");  // behind the last stage: empty groups
-        if (i >= kLag) {
-          asm volatile("cp.async.wait_group %0;" ::"n"(kLag) : "memory");
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&x_full[(i - kLag) % S]);
+        } else {
+          *reinterpret_cast<uint4 *>(x + to[h]) = v[u][h][0];
         }
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&x_full[i % S]);
     }
     // the sums of the four accumulators; the ring becomes their place once all products are done
     const int lg = warp & 3, half = warp >> 2;
@@ -464,7 +463,7 @@ __global__ void __launch_bounds__(kShThreads, 2)
       int armed = 0;
       for (int i = 0; i < n; ++i) {
         if (!tc_wait(&empty[i % S], ((i / S) & 1) ^ 1, spin, abort_flag, a.err)) break;
-        mbar_arrive_expect_tx(&a_full[i % S], uint32_t(kShATile));
+        mbar_arrive_expect_tx(&a_full[i % S], uint32_t(R::kATile));
         tma_load_3d(sm + (i % S) * R::kStage, &amap, (s0 + i) * 64, 0, ad, &a_full[i % S]);
         armed = i + 1;
       }
@@ -488,7 +487,7 @@ __global__ void __launch_bounds__(kShThreads, 2)
       uint32_t more = region(i) == last;
       last = region(i);
       for (int k = R::kTerms - 1; k >= 0; --k) {
-        const uint64_t x_desc = sw128_desc(base + st * R::kStage + kShATile + k * kShXTile);
+        const uint64_t x_desc = sw128_desc(base + st * R::kStage + R::kATile + k * kShXTile);
         for (int q = 0; q < steps; ++q) {
           tc_mma(tmem + uint32_t(last * kTcTokens), a_desc + uint64_t(2 * q), x_desc + uint64_t(2 * q), kIdesc, more);
           more = 1;
@@ -509,15 +508,15 @@ __global__ void __launch_bounds__(kShThreads, 2)
 }
 
 // [adapter][row][column] of 16-bit values in boxes of 64 columns (128 bytes,
-// swizzled) x 128 rows; columns and rows beyond an adapter's read as zeros
-cudaError_t adapter_map(CUtensorMap &map, int w_elem, const uint8_t *base, int columns, int rows, int n) {
+// swizzled) x box_rows; columns and rows beyond an adapter's read as zeros
+cudaError_t adapter_map(CUtensorMap &map, int w_elem, const uint8_t *base, int columns, int rows, int n, int box_rows) {
   map = CUtensorMap{};
   if (n == 0) return cudaSuccess;  // nobody loads from it
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encode();
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {cuuint64_t(columns), cuuint64_t(rows), cuuint64_t(n)};
   const cuuint64_t strides[2] = {cuuint64_t(columns) * 2, cuuint64_t(columns) * 2 * cuuint64_t(rows)};
-  const cuuint32_t box[3] = {64, 128, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1}, step[3] = {1, 1, 1};
   return encode(&map, w_elem == kElemBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint8_t *>(base), dims,
                 strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
@@ -525,19 +524,23 @@ cudaError_t adapter_map(CUtensorMap &map, int w_elem, const uint8_t *base, int c
              : cudaErrorInvalidValue;
 }
 
+template <int XE, int WE, int ROWS>
+cudaError_t shrink64_rows(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
+  CUtensorMap map;
+  const cudaError_t e = adapter_map(map, WE, a.A, a.K, a.rank, a.n_adapters, ROWS);
+  if (e != cudaSuccess) return e;
+  return launch_ex(k_lora_shrink_tc<XE, WE, ROWS>, dim3(unsigned(p.splits), unsigned(p.tiles)), kShThreads, ShrinkTc<XE, ROWS>::kBytes, p.splits, true, s,
+                   map, a, w, p.splits, spin_limit());
+}
 template <int XE, int WE>
 cudaError_t shrink64(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
-  CUtensorMap map;
-  const cudaError_t e = adapter_map(map, WE, a.A, a.K, a.rank, a.n_adapters);
-  if (e != cudaSuccess) return e;
-  return launch_ex(k_lora_shrink_tc<XE, WE>, dim3(unsigned(p.splits), unsigned(p.tiles)), kShThreads, ShrinkTc<XE>::kBytes, p.splits, true, s, map, a, w,
-                   p.splits, spin_limit());
+  return a.rank <= 64 ? shrink64_rows<XE, WE, 64>(a, w, p, s) : shrink64_rows<XE, WE, 128>(a, w, p, s);
 }
 
 template <int WE, int YE>
 cudaError_t expand64(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, int sms, cudaStream_t s) {
   CUtensorMap map;
-  const cudaError_t st = adapter_map(map, WE, a.B, a.rank, a.M, a.n_adapters);
+  const cudaError_t st = adapter_map(map, WE, a.B, a.rank, a.M, a.n_adapters, kTcCols);
   if (st != cudaSuccess) return st;
   ExpandTc e;
   e.blocks = (a.rank + 63) / 64;
@@ -551,8 +554,6 @@ cudaError_t expand64(const LoraArgs &a, const LoraWork &w, const LoraPlan &p, in
 }
 
 }  // namespace
-
-bool lora_tc_shrinks(int x_elem, int w_elem) { return x_elem != kElemF32 || w_elem == kElemBF16; }
 
 cudaError_t launch_lora_shrink_tc(int x_elem, int w_elem, const LoraArgs &a, const LoraWork &w, const LoraPlan &p, cudaStream_t s) {
   if (w_elem == kElemF16) return shrink64<kElemF16, kElemF16>(a, w, p, s);
