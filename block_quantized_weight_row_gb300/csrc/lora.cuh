@@ -105,26 +105,41 @@ __device__ __forceinline__ void sum_tile(const LoraArgs &a, const LoraWork &w, f
   cooperative_groups::cluster_group cluster = cooperative_groups::this_cluster();
   cluster.sync();
   const float s = a.scale ? __ldg(a.scale + ad) : 1.0f;
-  // four ranks at a time (ranks come in eights), the loads from all CTAs in flight together
-  const int quads = ranks / 4, n = count * quads;
+  // the loads from all CTAs in flight together; four ranks at a time (they come in
+  // eights) where a CTA has one piece, one at a time in the small tiles of four
+  constexpr int V = PARTS == 1 ? 4 : 1;
+  const int wide = ranks / V, n = count * wide;
   for (int e = split * blockDim.x + threadIdx.x; e < n; e += splits * blockDim.x) {
-    const int row = e / quads, r = 4 * (e - row * quads);
-    float4 v[8][PARTS];
+    const int row = e / wide, r = V * (e - row * wide);
+    float v[8][PARTS][V];
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (c < splits) {
         const float *p = cluster.map_shared_rank(part, c) + row * pitch + r;
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) v[c][q] = *reinterpret_cast<const float4 *>(p + q * apart);
+        for (int q = 0; q < PARTS; ++q) {
+          if constexpr (V == 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(p + q * apart);
+            v[c][q][0] = f.x, v[c][q][1] = f.y, v[c][q][2] = f.z, v[c][q][3] = f.w;
+          } else {
+            v[c][q][0] = p[q * apart];
+          }
+        }
       }
-    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum[V] = {};
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (c < splits) {
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) sum.x += v[c][q].x, sum.y += v[c][q].y, sum.z += v[c][q].z, sum.w += v[c][q].w;
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+          for (int k = 0; k < V; ++k) sum[k] += v[c][q][k];
       }
-    *reinterpret_cast<float4 *>(w.H + int64_t(rows[row]) * a.rank + first + r) = make_float4(sum.x * s, sum.y * s, sum.z * s, sum.w * s);
+    float *to = w.H + int64_t(rows[row]) * a.rank + first + r;
+    if constexpr (V == 4)
+      *reinterpret_cast<float4 *>(to) = make_float4(sum[0] * s, sum[1] * s, sum[2] * s, sum[3] * s);
+    else
+      *to = sum[0] * s;
   }
   cluster.sync();  // the others' sums are read from here until now
 }
