@@ -621,6 +621,16 @@ def test_lora_many_tokens(bq, types, T, n, rank, K, M, ids):
 
 
 @gpu
+@pytest.mark.parametrize("types", TYPES)
+@pytest.mark.parametrize("T,n,rank,K,M,ids", [(2100, 2, 24, 32, 50, "runs"), (1100, 1, 128, 32, 257, "same"), (1300, 3, 72, 160, 66, "random"),
+                                              (900, 2, 104, 416, 130, "random"), (1500, 2, 48, 1376, 64, "runs"), (800, 1, 64, 4096, 40, "same")])
+def test_lora_large_tiles(bq, types, T, n, rank, K, M, ids):
+    """Tiles of 64 tokens: one stage of 32 k and many, ranks on both sides of 64, K split over a cluster."""
+    c = lora_case(T, n, rank, K, M, *types, ids, seed=T)
+    check_lora(run_lora(bq, *c), *c)
+
+
+@gpu
 @pytest.mark.parametrize("T", [20, 600])
 def test_lora_without_base_scale_or_adapter(bq, T):
     X, A, B, s, Y, ids = lora_case(T, 3, 16, 128, 70, F32, BF16, F32, "random")

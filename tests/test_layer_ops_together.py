@@ -130,12 +130,13 @@ def test_lora_beyond_4_gigabytes(bq, y):
 
 
 @gpu
-def test_lora_timeout_path_returns_error(bq):
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_lora_timeout_path_returns_error(bq, dtype):
     """Every bounded wait gives up at once: the call ends, the status says so, and the next call is right."""
     from block_quantized_weight_row_gb300 import binding
     g = torch.Generator(device="cuda").manual_seed(1)
     T, K, M, n, rank = 4096, 128, 700, 2, 64  # tiles of 64 tokens, on the tensor-memory kernel
-    x = torch.randn(T, K, generator=g, device="cuda").bfloat16()
+    x = torch.randn(T, K, generator=g, device="cuda").to(dtype)
     a, b = torch.randn(n, rank, K, generator=g, device="cuda").bfloat16(), torch.randn(n, M, rank, generator=g, device="cuda").bfloat16()
     ids = torch.randint(0, n, (T,), generator=g, device="cuda", dtype=torch.int32)
     first = bq.lora(x, a, b, ids)
