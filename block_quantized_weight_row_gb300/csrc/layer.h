@@ -50,7 +50,9 @@ struct RotaryArgs {
   const int32_t *axis;  // null: all 0
   int64_t n_tokens;
   int n_axes, dim, rot;
-  bool interleaved, inverse, in_place;
+  bool interleaved, inverse;
+  bool in_place;  // all outputs are their inputs: channels that no pair reaches need nothing
+  bool onto;      // some output is its input
   unsigned *err;
 };
 cudaError_t launch_rotary(int elem_in, int elem_out, RotaryArgs a, cudaStream_t stream);

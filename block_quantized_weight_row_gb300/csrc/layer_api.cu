@@ -245,6 +245,7 @@ int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_st
   a.interleaved = interleaved != 0;
   a.inverse = inverse != 0;
   a.in_place = same[0] && same[1];
+  a.onto = (n_q_heads > 0 && same[0]) || (n_k_heads > 0 && same[1]);
   if (a.in_place && rot == 0) return report_ok();
   return launch_status(launch_rotary(elem, elem_out, a, current_stream()), who);
 }

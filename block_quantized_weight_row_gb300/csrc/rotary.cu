@@ -15,10 +15,12 @@
 // cosines of a few tokens once, in shared memory, for all heads of both tensors;
 // then its threads take units of 16 bytes of output, several at a time, loads
 // first, the first of them before the sines; a CTA has as many tokens as make the
-// grid one wave.
+// grid one wave. 32768 tokens of 32 + 8 bf16 heads of 128 (671 MB): 117 us, 5.7 TB/s
+// (pair by pair, with an integer division each, 365 us); 32 tokens 3 us.
 // A unit's partner channels are in the unit (adjacent pairs), in another one that
 // the same thread takes (halves of a multiple of the unit), or are gathered (other
-// halves: each lane loads them beside its own unit, from L1).
+// halves: each lane loads them beside its own unit, from L1; onto the input itself
+// where a head fits a warp's lanes, else pair by pair).
 #include <algorithm>
 
 #include "bq_device.cuh"
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_rotary(const RotaryArgs
 #pragma unroll
         for (int k = 0; k < W; ++k) store<OUT, V>(it[b].out + channel(unit, k) * OS, v[k]);
       } else if constexpr (PATH == kGather) {
-        // a head is `units` lanes of one warp (units a power of two up to 32): all load before one stores
+        // onto the input itself a head is `units` lanes of one warp (a power of two up to 32): all load before one stores
         float v[V], y[V];
         x[b][0].get(v);
 #pragma unroll
@@ -198,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_rotary(const RotaryArgs
           const int c = unit * V + j;
           y[j] = c < a.rot ? load1<IN>(it[b].in + (c < pairs ? c + pairs : c - pairs) * IS) : 0.0f;
         }
-        __syncwarp((units == 32 ? kFull : (1u << units) - 1) << (threadIdx.x & 31 & ~(units - 1)));
+        if (a.onto) __syncwarp((units == 32 ? kFull : (1u << units) - 1) << (threadIdx.x & 31 & ~(units - 1)));
 #pragma unroll
         for (int j = 0; j < V; ++j) {
           const int c = unit * V + j, p = c < pairs ? c : c - pairs;
@@ -246,7 +248,7 @@ cudaError_t launch(const RotaryArgs &a, int sms, cudaStream_t stream) {
   const int units = a.dim / V;
   if (a.interleaved) return launch_path<IN, OUT, kAdjacent>(a, sms, stream);
   if (a.rot / 2 % V == 0) return launch_path<IN, OUT, kHalves>(a, sms, stream);
-  if (units <= 32 && (units & (units - 1)) == 0) return launch_path<IN, OUT, kGather>(a, sms, stream);
+  if (!a.onto || (units <= 32 && (units & (units - 1)) == 0)) return launch_path<IN, OUT, kGather>(a, sms, stream);
   return launch_path<IN, OUT, kScalar>(a, sms, stream);
 }
 

@@ -531,7 +531,7 @@ int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_st
  * more, 16-bit ones exactly; A x is kept in fp32 and enters the second product in
  * terms of 22 bits (fp32 out) or 16 (16-bit out). A token's result does not depend
  * on the other tokens of the batch but for the order of sums, which follows
- * n_tokens, n_adapters and K; the same call gives the same bits.
+ * n_tokens, n_adapters, rank and K; the same call gives the same bits.
  * Needs a workspace of bq_lora_workspace_size(...) bytes (bq_set_workspace).
  * Limits: rank a multiple of 8 up to BQ_LORA_MAX_RANK, K a multiple of 32, K and M
  * below 2^24, n_tokens up to 2^20, n_adapters up to BQ_LORA_MAX_ADAPTERS. Errors:

@@ -531,6 +531,28 @@ def test_rotary_in_place_strides_and_back(bq, interleaved, rot):
 
 
 @gpu
+@pytest.mark.parametrize("elem", [F32, BF16])
+@pytest.mark.parametrize("dim,rot", [(96, 74), (256, 74), (128, 10), (32, 6), (160, 154)])
+def test_rotary_of_odd_halves(bq, elem, dim, rot):
+    """Halves on no 16-byte boundary, heads of any number of units: apart, on q alone and on both, the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(dim + rot)
+    T, H, KH = 13, 3, 2
+    q, k = (torch.randn(T, n, dim, generator=g, device="cuda").to(DT[elem]) for n in (H, KH))
+    pos = torch.randint(0, 9000, (T,), generator=g, device="cuda", dtype=torch.int32)
+    freq = (10000.0 ** -(torch.arange(rot // 2).double() / (rot // 2))).cuda()
+    a, b = bq.rotary(q, k, pos, freq)
+    axis = torch.zeros(rot // 2, dtype=torch.int32)
+    check_rotary(a, q.cpu(), pos[None].cpu(), freq.cpu(), axis, False)
+    check_rotary(b, k.cpu(), pos[None].cpu(), freq.cpu(), axis, False)
+    c, d = bq.rotary(q, k, pos, freq, out_k=k.clone())
+    q2, k2 = q.clone(), k.clone()
+    _, f = bq.rotary(q2, k, pos, freq, out_q=q2)
+    assert torch.equal(c, a) and torch.equal(d, b) and torch.equal(q2, a) and torch.equal(f, b)
+    bq.rotary(q, k2, pos, freq, out_q=q, out_k=k2)
+    assert torch.equal(q, a) and torch.equal(k2, b)
+
+
+@gpu
 def test_rotary_bad_axis_and_one_axis(bq):
     assert quiet(bq) == OK
     q = torch.randn(3, 1, 64, device="cuda")
