@@ -14,8 +14,8 @@
 //   3. out_t = y_t + B_a H[t]: k_lora_expand for tiles of 16, k_lora_expand_tc on
 //      tcgen05 for tiles of 64.
 // Measured (GPU alone): 48 fp32 tokens of 16 adapters, 4096 to 4096 at rank 16, 10.1
-// us; 8192 bf16 tokens, 4096 to 11008 fp32 columns at rank 64, 164 us (8 for step 1,
-// 31, and 125 for 720 MB of y and out: 5.8 TB/s).
+// us; 8192 bf16 tokens, 4096 to 11008 fp32 columns at rank 64, 163 us (8 for step 1,
+// 28, and 128 for 720 MB of y and out: 5.6 TB/s).
 // A tile's rows do not depend on one another, so neither the order inside an
 // adapter nor the other tokens change a result.
 //
@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink16(const LoraArgs
 }
 
 // Tiles of 64 tokens on warp-level instructions, up to 64 ranks: 16-bit rows of up
-// to 64 ranks (31 us for 8192 bf16 tokens of 4096 at rank 64, where the kernel of
-// lora_tc.cu takes 33; at rank 16 21) and fp32 rows beside fp16 adapters (which that
+// to 64 ranks (28 to 31 us for 8192 bf16 tokens of 4096 at rank 64, where the kernel of
+// lora_tc.cu takes 32 to 35; at rank 16 21) and fp32 rows beside fp16 adapters (which that
 // kernel cannot take: terms of fp16 would need each row's range first). Each of the
 // four warps has 16 of the tokens and all of the CTA's k. Rows of x and of the
 // adapter come through a ring of stages of 64 k by asynchronous copies (straight

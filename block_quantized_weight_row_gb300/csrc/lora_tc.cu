@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
       const int lg = warp & 3, t0 = (warp >> 2) * 32;
       const uint32_t lane_addr = tmem + (uint32_t(lg * 32) << 16);
       const int odd = lane & 1;
-      // 16-bit rows, where their boundaries allow it: two columns of one token per access (220 us -> 125 for
-      // 8192 tokens of 11008 columns; fp32 rows, whose 32 columns are a line of 128 bytes, lose by it, 161 -> 184)
+      // 16-bit rows, where their boundaries allow it: two columns of one token per access (188 us -> 125 for
+      // 8192 tokens of 11008 columns, the predicated loads included; fp32 rows, whose 32 columns are a line of
+      // 128 bytes, lose by it: 166 -> 184)
       const bool pairs = YS == 2 && a.y_vec && a.M % 2 == 0;
       // steps of 16 tokens: 2 per turn; the next one's y is asked for before this one's sums are.
       // The bits of y. With pairs: of the lane's and its neighbour's column of one token, the first of
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // accumulators (256 columns), so that the products' chains stay short; the sums of
 // all meet in fp32 in a fixed order.
 // For fp32 rows and for more than 64 ranks, where the warp-level kernel of lora.cu
-// is bound by its instructions: whole calls of 8192 tokens of 4096 to 11008 columns
+// is slower: whole calls of 8192 tokens of 4096 to 11008 columns
 // take 189 us for 219 (fp32, rank 64) and 216 for 231 (bf16, rank 128). A stage takes
 // 0.8 us whatever the copies' form or depth.
 // Warps 0-7: rows of x, then the sums; warp 8: TMA; warp 9: MMA. All waits bounded.
