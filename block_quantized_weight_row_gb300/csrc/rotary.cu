@@ -184,6 +184,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_rotary(const RotaryArgs
         if (unit < cols) {
 #pragma unroll
           for (int j = 0; j < P; ++j) {
+            // a unit that reaches past `rot`: its other channels as they are (a turn by 0 would make inf - inf of an infinity beside)
+            if (PATH == kAdjacent && unit * P + j >= pairs) continue;
             float &u = PATH == kHalves ? v[0][j] : v[0][2 * j], &y = PATH == kHalves ? v[W - 1][j] : v[0][2 * j + 1];
             const float2 f = turn_pair(u, y, w[j * cols + unit]);
             u = f.x, y = f.y;

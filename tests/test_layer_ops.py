@@ -553,6 +553,31 @@ def test_rotary_of_odd_halves(bq, elem, dim, rot):
 
 
 @gpu
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (F16, F16), (F32, BF16)])
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("rot", [2, 6, 10, 74, 126])
+def test_rotary_leaves_the_other_channels(bq, types, interleaved, rot):
+    """Channels behind `rot` are copies, whatever stands beside them: infinities, zeros of either sign."""
+    T, H, dim = 7, 2, 128
+    g = torch.Generator().manual_seed(rot)
+    q = torch.randn(T, H, dim, generator=g)
+    odd = torch.tensor([math.inf, -1.5, -0.0, -2.0, 0.0, -math.inf, 3.0])
+    q[..., rot:] = odd[torch.randint(0, 7, (T, H, dim - rot), generator=g)]
+    q = q.to(DT[types[0]])
+    pos = torch.randint(-50, 9000, (T,), generator=g, dtype=torch.int32).cuda()
+    freq = (10000.0 ** -(torch.arange(rot // 2).double() / (rot // 2))).cuda()
+    rest = q[..., rot:].to(DT[types[1]])
+    want = rest.view(torch.int32 if types[1] == F32 else torch.int16)
+    out, _ = bq.rotary(q.cuda(), None, pos, freq, interleaved=interleaved, dtype=DT[types[1]])
+    assert torch.equal(out[..., rot:].contiguous().cpu().view(want.dtype), want)
+    assert bool(out[..., :rot].isfinite().all())
+    if types[0] == types[1]:
+        own = q.cuda()
+        bq.rotary(own, None, pos, freq, interleaved=interleaved, out_q=own)
+        assert torch.equal(own.cpu().view(want.dtype), out.cpu().view(want.dtype))
+
+
+@gpu
 def test_rotary_bad_axis_and_one_axis(bq):
     assert quiet(bq) == OK
     q = torch.randn(3, 1, 64, device="cuda")
