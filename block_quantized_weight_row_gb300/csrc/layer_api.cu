@@ -3,7 +3,6 @@
 // the arguments the kernels take.
 #include <algorithm>
 #include <climits>
-#include <cmath>
 
 #include "bq.h"
 #include "bq_device.cuh"
@@ -123,7 +122,8 @@ int bq_add_rms_norm(int elem, const void *x, int64_t x_stride, const void *resid
   if (n_cols % kQK || n_cols > BQ_RMS_NORM_MAX_COLS)
     return report_error(BQ_ERR_SHAPE, "%s: n_cols %lld is not a multiple of 32 up to %d", who, (long long)n_cols, BQ_RMS_NORM_MAX_COLS);
   if (n_rows > INT_MAX) return report_error(BQ_ERR_SHAPE, "%s: n_rows must be below 2^31", who);
-  if (!(eps > 0.0) || !std::isfinite(eps)) return report_error(BQ_ERR_INVALID_ARG, "%s: eps must be above 0 and finite", who);
+  // what keeps the factor's arithmetic (m, 1 / m and the errors of both) among fp32's normal numbers
+  if (!(eps >= 1e-30 && eps <= 1e30)) return report_error(BQ_ERR_INVALID_ARG, "%s: eps is not in 1e-30 .. 1e30", who);
   if (sum && !residual) return report_error(BQ_ERR_INVALID_ARG, "%s: a sum without a residual", who);
   if (!sum && !out && !q8) return report_error(BQ_ERR_INVALID_ARG, "%s: no output", who);
   if (n_rows == 0 || n_cols == 0) return report_ok();

@@ -462,10 +462,10 @@ int bq_paged_extend(int64_t page_size, int64_t n_pages, const int32_t *kv_len, c
  * 2^40), rows 16-byte aligned; weight: n_cols fp32 (16-byte aligned); q8:
  * contiguous, 16-byte aligned. sum may be x or residual themselves (the same
  * pointer and stride), in place; other overlaps are refused. Rows are taken to be
- * finite, |h| below 2^60, and y as by every quantizer here.
+ * finite, |h| below 2^50, and y as by every quantizer here.
  * Limits: n_cols a multiple of 32 up to BQ_RMS_NORM_MAX_COLS; n_rows below 2^31.
  * Errors: BQ_ERR_UNSUPPORTED (element type), BQ_ERR_SHAPE, BQ_ERR_ALIGN,
- * BQ_ERR_INVALID_ARG (null pointers, no output, eps not above 0 or not finite,
+ * BQ_ERR_INVALID_ARG (null pointers, no output, eps not in 1e-30 .. 1e30,
  * negative sizes, overlaps, rows of an output overlapping each other). */
 int bq_add_rms_norm(int elem, const void *x, int64_t x_stride, const void *residual, int64_t residual_stride,
                     const float *weight, double eps, void *sum, int64_t sum_stride, void *out, int64_t out_stride,

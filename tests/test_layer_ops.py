@@ -86,6 +86,13 @@ def test_norm_refusals(bq, kw, want):
     assert _norm(bq, **kw) == want
 
 
+@pytest.mark.parametrize("eps,want", [(1e-31, INVALID), (1e-40, INVALID), (1e-50, INVALID), (1.1e30, INVALID), (1e39, INVALID), (1e300, INVALID)])
+def test_norm_refuses_eps_beyond_its_arithmetic(bq, eps, want):
+    """In fp32 these are zero, subnormal or infinite, or their reciprocal is: a row of zeros would become NaN."""
+    assert _norm(bq, eps=eps) == want
+    assert _norm(bq, eps=1e-30, rows=0) == OK and _norm(bq, eps=1e30, rows=0) == OK
+
+
 def test_norm_without_rows_is_a_no_op(bq):
     assert _norm(bq, rows=0, x=None, w=None) == OK
 
@@ -388,6 +395,19 @@ def test_norm_of_odd_values(bq, elem, kind, eps):
     h, y, blocks = norm_ref(x, r, w, eps)
     got = bq.add_rms_norm(x.cuda(), w.cuda(), eps, r.cuda(), q8=True)
     assert torch.equal(got.sum.cpu(), h) and torch.equal(got.out.cpu(), y.to(x.dtype)) and torch.equal(got.q8.cpu(), blocks)
+
+
+@gpu
+@pytest.mark.parametrize("elem", [F32, BF16])
+@pytest.mark.parametrize("power,eps", [(47, 1e-6), (47, 1e30), (-60, 1e-30), (-20, 1e-30)])
+@pytest.mark.parametrize("cols", [64, 4096, 65536])
+def test_norm_at_the_ends_of_its_range(bq, elem, power, eps, cols):
+    """|h| near 2^50 and far below the smallest eps."""
+    x, _, w = norm_rows(3, cols, torch.float32, cols)
+    x = (x.clamp(-7.9, 7.9) * 2.0**power).to(DT[elem])
+    h, y, blocks = norm_ref(x, None, w, eps)
+    got = bq.add_rms_norm(x.cuda(), w.cuda(), eps, q8=True)
+    assert torch.equal(got.out.cpu(), y.to(x.dtype)) and torch.equal(got.q8.cpu(), blocks)
 
 
 @gpu
