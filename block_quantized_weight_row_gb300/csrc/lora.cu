@@ -463,7 +463,11 @@ __global__ void __launch_bounds__(kExpandThreads, 2) k_lora_expand(const LoraArg
   if (w.sorted) pdl_wait();
   int ad, count;
   if (!find_tile<TM>(a, w, blockIdx.y, rows, ad, count)) return;
-  if (ad < 0 && a.y == a.out) return;
+  if (ad < 0 && a.y == a.out) {
+    // every launch has a tile that waits for the one before it, so that it never ends before that one
+    if (!w.sorted) pdl_wait();
+    return;
+  }
   uint8_t *const mine = terms + E::kTermBytes + warp * 2 * E::kYBytes + lane * 16;
   const int first = int(blockIdx.x) * turns * kStep + warp * 32;  // column of the first turn
   // y's pieces of a turn; rows of another alignment and the last columns are loaded when they are needed

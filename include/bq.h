@@ -527,6 +527,8 @@ int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_st
  * and stride); other overlaps are refused. adapter: n_tokens int32 on the DEVICE, in
  * any order; one outside -1 .. n_adapters - 1 counts as -1 and is reported by
  * bq_device_status (BQ_ERR_INDEX).
+ * An infinite or NaN value of x gives NaN, or an infinity, in its own token's
+ * row and reaches no other.
  * Accuracy: sums in fp32; fp32 rows enter the products in terms of 22 bits or
  * more, 16-bit ones exactly; A x is kept in fp32 and enters the second product in
  * terms of 22 bits (fp32 out) or 16 (16-bit out). A token's result does not depend

@@ -755,6 +755,38 @@ def test_lora_rows_do_not_see_each_other(bq, T):
 
 
 @gpu
+@pytest.mark.parametrize("xe,we,ye,rank", [(BF16, BF16, F32, 64), (BF16, BF16, BF16, 40), (BF16, BF16, BF16, 128), (F32, BF16, F32, 48), (F32, BF16, BF16, 120),
+                                           (F32, F16, F32, 64), (F16, F16, F16, 104)])
+def test_lora_large_tiles_do_not_see_each_other(bq, xe, we, ye, rank):
+    """As above, in tiles of 64 tokens of every type."""
+    T = 1100
+    X, A, B, s, Y, ids = lora_case(T, 3, rank, 288, 130, xe, we, ye, "random")
+    first = run_lora(bq, X, A, B, s, Y, ids).cpu()
+    p = torch.randperm(T, generator=torch.Generator().manual_seed(6))
+    assert torch.equal(run_lora(bq, X[p], A, B, s, Y[p], ids[p]).cpu(), first[p])
+    X[5, 3], X[11], X[700, 100] = math.inf, math.nan, -math.inf
+    got = run_lora(bq, X, A, B, s, Y, ids).cpu()
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[5] = keep[11] = keep[700] = False
+    assert torch.equal(got[keep], first[keep])
+
+
+@gpu
+@pytest.mark.parametrize("T", [1, 40, 256, 300, 1200])
+@pytest.mark.parametrize("rank", [8, 64])
+def test_lora_without_any_adapter(bq, T, rank):
+    """Nobody has one: y as it is, in place and apart, zeros without y; the next call on the stream sees them."""
+    X, A, B, s, Y, _ = (t.cuda() for t in lora_case(T, 3, rank, 288, 130, BF16, BF16, F32, "random"))
+    ids = torch.full((T,), -1, dtype=torch.int32, device="cuda")
+    want = Y.clone()
+    for _ in range(3):
+        assert bq.lora(X, A, B, ids, Y, s, out=Y) is not None
+        X.zero_()
+    assert torch.equal(Y, want) and torch.equal(bq.lora(X, A, B, ids, Y, s), want)
+    assert not bool(bq.lora(X, A, B, ids, None, s, dtype=torch.float32).any())
+
+
+@gpu
 @pytest.mark.parametrize("T", [30, 700])
 def test_lora_captured_and_on_many_streams(bq, T):
     X, A, B, s, Y, ids = (t.cuda() for t in lora_case(T, 4, 16, 256, 70, F32, BF16, F32, "random"))
