@@ -160,10 +160,23 @@ def _cuda(t, name):
     return t
 
 
-def _q8_rows(x, rows, K):
-    """Activations given as Q8_0 blocks: the bytes of whole rows."""
-    if x.dtype == torch.uint8 and x.numel() != rows * (K // QK) * 34:
-        raise ValueError(f"activations of {rows} x {K} values in Q8_0 are {rows * (K // QK) * 34} bytes, not {x.numel()}")
+def _f32(t, name, n=0):
+    """A contiguous fp32 tensor of n values at least: the library takes a bare pointer."""
+    if _cuda(t, name).dtype != torch.float32:
+        raise TypeError(f"{name} must be float32, not {t.dtype}")
+    if t.numel() < n:
+        raise ValueError(f"{name} must have {n} values, not {t.numel()}")
+    return t
+
+
+def _rows(x, name, rows, K):
+    """Activations: fp32 values, or whole rows as Q8_0 blocks (the bytes)."""
+    if x.dtype != torch.uint8:
+        return _f32(x, name, rows * K)
+    n = rows * (K // QK) * 34
+    if _cuda(x, name).numel() != n:
+        raise ValueError(f"{name}: {rows} x {K} values in Q8_0 are {n} bytes, not {x.numel()}")
+    return x
 
 
 def block_bytes(t: int) -> int:
@@ -204,10 +217,11 @@ def gemv(t: int, w_blocks: torch.Tensor, x: torch.Tensor, M: int, K: int,
     """y[M] = W (M x K, blocks of type t) . x[K] (fp32, quantized to Q8_0 in-kernel;
     or uint8: its Q8_0 blocks, as add_rms_norm and quantize_rows give them)."""
     _cuda(w_blocks, "w_blocks")
-    _cuda(x, "x")
-    _q8_rows(x, 1, K)
+    _rows(x, "x", 1, K)
     if out is None:
         out = torch.empty(M, dtype=torch.float32, device=x.device)
+    else:
+        _f32(out, "out", M)
     L = _prep(x.device)
     _workspace(x.device, int(L.bq_gemv_workspace_size(t, K)))
     if x.dtype == torch.uint8:
@@ -230,9 +244,12 @@ def gemv_multi(t: int, w_list, x: torch.Tensor, M_list, K: int, outs=None):
     """y_i = W_i . x for matrices sharing one input x, in one launch."""
     for w in w_list:
         _cuda(w, "w_blocks")
-    _cuda(x, "x")
+    _f32(x, "x", K)
     if outs is None:
         outs = [torch.empty(m, dtype=torch.float32, device=x.device) for m in M_list]
+    else:
+        for y, m in zip(outs, M_list):
+            _f32(y, "outs", m)
     n, W, Y, M = gemv_multi_args(w_list, outs, M_list)
     L = _prep(x.device)
     _workspace(x.device, int(L.bq_gemv_workspace_size(t, K)))
@@ -270,9 +287,12 @@ def gemv_sequence(t: int, groups):
     for w_list, x, M_list, K, outs in groups:
         for w in w_list:
             _cuda(w, "w_blocks")
-        _cuda(x, "x")
+        _f32(x, "x", K)
         if outs is None:
             outs = [torch.empty(m, dtype=torch.float32, device=x.device) for m in M_list]
+        else:
+            for y, m in zip(outs, M_list):
+                _f32(y, "outs", m)
         full.append((w_list, x, M_list, K, outs))
     if full:
         gemv_sequence_call(t, gemv_sequence_args(full), full[0][1].device)
@@ -285,7 +305,7 @@ def attn_decode(k_type: int, v_type: int, q: torch.Tensor, K_cache: torch.Tensor
     """o (n_heads, head_dim) = attention of q (n_heads, head_dim) over the
     quantized caches (n_tokens, n_kv_heads, head_dim/32 blocks as bytes);
     k_basis: the basis the K cache was written in."""
-    _cuda(q, "q")
+    _f32(q, "q")
     _cuda(K_cache, "K_cache")
     _cuda(V_cache, "V_cache")
     H, D = q.shape
@@ -304,10 +324,11 @@ def gemm(t: int, w_blocks: torch.Tensor, X: torch.Tensor, M: int, N: int, K: int
     """Y (N x M) = X (N x K fp32, quantized to Q8_0; or uint8: its Q8_0 blocks) . W^T
     (W: M x K blocks)."""
     _cuda(w_blocks, "w_blocks")
-    _cuda(X, "X")
-    _q8_rows(X, N, K)
+    _rows(X, "X", N, K)
     if out is None:
         out = torch.empty((N, M), dtype=torch.float32, device=X.device)
+    else:
+        _f32(out, "out", N * M)
     L = _prep(X.device)
     _workspace(X.device, int(L.bq_workspace_size(t, M, N, K)))
     if X.dtype == torch.uint8:
@@ -323,9 +344,9 @@ def kv_quantize(t: int, rows: torch.Tensor, bias: torch.Tensor | None,
     """rows: (n_tokens, n_kv_heads, head_dim) fp32; bias: (n_kv_heads, head_dim) or None.
     basis: the cache's basis; bias_basis: the basis the bias was calibrated in
     (default: the cache's)."""
-    _cuda(rows, "rows")
+    _f32(rows, "rows")
     if bias is not None:
-        _cuda(bias, "bias")
+        _f32(bias, "bias")
     T, H, D = rows.shape
     if out is None:
         out = torch.empty((T, H, (D // QK) * max(block_bytes(t), 1)), dtype=torch.uint8, device=rows.device)
@@ -341,10 +362,10 @@ def kv_write(k_type: int, k_rows: torch.Tensor, bias: torch.Tensor | None, v_typ
     """One layer's K and V cache write in one launch (bq_kv_write): k_rows and
     v_rows (n_tokens, n_kv_heads, head_dim) fp32; bias (n_kv_heads, head_dim)
     or None; basis: the K cache's basis. Returns (K blocks, V blocks)."""
-    _cuda(k_rows, "k_rows")
-    _cuda(v_rows, "v_rows")
+    _f32(k_rows, "k_rows")
+    _f32(v_rows, "v_rows")
     if bias is not None:
-        _cuda(bias, "bias")
+        _f32(bias, "bias")
     T, H, D = k_rows.shape
     if tuple(v_rows.shape) != (T, H, D):
         raise ValueError("k_rows and v_rows must have the same shape")
@@ -361,7 +382,7 @@ def kv_write(k_type: int, k_rows: torch.Tensor, bias: torch.Tensor | None, v_typ
 def kv_bias(rows: torch.Tensor, basis: int = BASIS_PLAIN, out: torch.Tensor | None = None) -> torch.Tensor:
     """Mean-centering bias (n_kv_heads, head_dim) fp32 of calibration rows
     (n_tokens, n_kv_heads, head_dim), measured in `basis`."""
-    _cuda(rows, "rows")
+    _f32(rows, "rows")
     T, H, D = rows.shape
     if out is None:
         out = torch.empty((H, D), dtype=torch.float32, device=rows.device)

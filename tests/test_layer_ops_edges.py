@@ -1,0 +1,75 @@
+"""What the calls around a served layer, and those that their outputs go into, do at
+their edges: wrong element types and sizes, workspaces, kernels of large batches."""
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+Q4, Q8 = 2, 8
+gpu = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def bq():
+    import os
+    from block_quantized_weight_row_gb300 import binding
+    if not os.path.exists(binding.library_path()):
+        import __graft_entry__
+        __graft_entry__.build()
+    import block_quantized_weight_row_gb300 as bq
+    bq.lib()
+    return bq
+
+
+# ------------------------------------------------------- types and sizes --
+
+
+def refused(call, tensors, error):
+    """`call` with tensors of the device that have no memory: (shape, type) or None each."""
+    with FakeTensorMode():
+        t = [None if s is None else torch.empty(s[0], dtype=s[1], device="cuda") for s in tensors]
+        with pytest.raises(error):
+            call(*t)
+
+
+U8, BF16, F16, F32 = torch.uint8, torch.bfloat16, torch.float16, torch.float32
+W4, W8 = ((5 * 2 * 18,), U8), ((5 * 2 * 34,), U8)  # 5 rows of 64
+
+
+@pytest.mark.parametrize("x,out,error", [
+    ((64, BF16), None, TypeError), ((64, F16), None, TypeError), ((64, torch.float64), None, TypeError), ((64, torch.int8), None, TypeError),
+    ((63, F32), None, ValueError), ((2 * 34 - 1, U8), None, ValueError), ((2 * 34 + 1, U8), None, ValueError),
+    ((64, F32), (5, BF16), TypeError), ((64, F32), (4, F32), ValueError), ((2 * 34, U8), (4, F32), ValueError)])
+def test_gemv_refuses_other_types_and_sizes(bq, x, out, error):
+    refused(lambda w, x, y: bq.gemv(Q4, w, x, 5, 64, out=y), [W4, x and ((x[0],), x[1]), out and ((out[0],), out[1])], error)
+
+
+@pytest.mark.parametrize("x,out,error", [
+    ((3, 64, BF16), None, TypeError), ((3, 64, F16), None, TypeError), ((2, 64, F32), None, ValueError), ((3, 67, U8), None, ValueError),
+    ((3, 64, F32), (3, 5, BF16), TypeError), ((3, 64, F32), (2, 5, F32), ValueError), ((3, 68, U8), (2, 5, F32), ValueError)])
+def test_gemm_refuses_other_types_and_sizes(bq, x, out, error):
+    refused(lambda w, x, y: bq.gemm(Q8, w, x, 5, 3, 64, out=y), [W8, (x[:-1], x[-1]), out and (out[:-1], out[-1])], error)
+
+
+@pytest.mark.parametrize("x,error", [((64, BF16), TypeError), ((68, U8), TypeError), ((63, F32), ValueError)])
+def test_gemv_batches_refuse_other_types_and_sizes(bq, x, error):
+    refused(lambda w, x: bq.gemv_multi(Q4, [w], x, [5], 64), [W4, ((x[0],), x[1])], error)
+    refused(lambda w, x: bq.gemv_sequence(Q4, [([w], x, [5], 64, None)]), [W4, ((x[0],), x[1])], error)
+
+
+@pytest.mark.parametrize("outs,error", [([((5,), BF16)], TypeError), ([((4,), F32)], ValueError)])
+def test_gemv_batches_refuse_other_outputs(bq, outs, error):
+    refused(lambda w, x, *y: bq.gemv_multi(Q4, [w], x, [5], 64, outs=list(y)), [W4, ((64,), F32), *outs], error)
+    refused(lambda w, x, *y: bq.gemv_sequence(Q4, [([w], x, [5], 64, list(y))]), [W4, ((64,), F32), *outs], error)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_rows_of_another_type_are_refused(bq, dtype):
+    """What rotary gives in the rows' type, taken on by the calls of an unpaged cache."""
+    rows, f32 = ((7, 2, 64), dtype), ((7, 2, 64), F32)
+    refused(lambda q, k, v: bq.attn_decode(Q4, Q8, q, k, v, 2, 0.1), [((4, 64), dtype), ((7, 2, 36), U8), ((7, 2, 68), U8)], TypeError)
+    refused(lambda r: bq.kv_quantize(Q8, r, None), [rows], TypeError)
+    refused(lambda r, b: bq.kv_quantize(Q8, r, b), [f32, ((2, 64), dtype)], TypeError)
+    refused(lambda k, v: bq.kv_write(Q4, k, None, Q8, v), [rows, f32], TypeError)
+    refused(lambda k, v: bq.kv_write(Q4, k, None, Q8, v), [f32, rows], TypeError)
+    refused(lambda k, b, v: bq.kv_write(Q4, k, b, Q8, v), [f32, ((2, 64), dtype), f32], TypeError)
+    refused(bq.kv_bias, [rows], TypeError)
