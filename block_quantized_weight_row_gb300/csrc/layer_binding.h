@@ -249,9 +249,19 @@ PyObject *dequantize_rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 5) wrong(PyExc_TypeError, "dequantize_rows: wrong number of arguments");
     const int type = to_code(args[0], "t");
     const at::Tensor &blocks = cuda_tensor(args[1], "blocks");
+    const at::Device d = blocks.device();
+    if (blocks.scalar_type() != at::kByte) wrong(PyExc_TypeError, "blocks must be Byte");
     const int64_t rows = to_int(args[2], "rows"), cols = to_int(args[3], "cols");
-    const c10::cuda::CUDAGuard guard(blocks.device());
-    const at::Tensor out = args[4] == Py_None ? at::empty({rows, cols}, blocks.options().dtype(at::kFloat)) : cuda_tensor(args[4], "out");
+    at::Tensor out;
+    if (args[4] != Py_None) {
+      out = cuda_tensor(args[4], "out");
+      if (out.scalar_type() != at::kFloat) wrong(PyExc_TypeError, "out must be Float");
+      if (!out.is_contiguous()) wrong(PyExc_ValueError, "out must be contiguous");
+      on(out, d, "out");
+      if (out.numel() < rows * cols) wrong(PyExc_ValueError, "out must have rows * cols values");
+    }
+    const c10::cuda::CUDAGuard guard(d);
+    if (!out.defined()) out = at::empty({rows, cols}, blocks.options().dtype(at::kFloat));
     use_stream();
     const int r = bq_dequantize_rows(type, blocks.data_ptr(), static_cast<float *>(out.data_ptr()), rows, cols);
     if (r) return failed(r);

@@ -73,3 +73,21 @@ def test_rows_of_another_type_are_refused(bq, dtype):
     refused(lambda k, v: bq.kv_write(Q4, k, None, Q8, v), [f32, rows], TypeError)
     refused(lambda k, b, v: bq.kv_write(Q4, k, b, Q8, v), [f32, ((2, 64), dtype), f32], TypeError)
     refused(bq.kv_bias, [rows], TypeError)
+
+
+@pytest.mark.parametrize("blocks,out,error", [
+    (((3, 68), F32), None, TypeError), (((3, 68), torch.int16), None, TypeError), (((3, 68), U8), ((3, 64), BF16), TypeError),
+    (((3, 68), U8), ((3, 64), torch.float64), TypeError), (((3, 68), U8), ((2, 64), F32), ValueError), (((3, 68), U8), ((3, 63), F32), ValueError)])
+def test_dequantize_refuses_other_types_and_sizes(bq, blocks, out, error):
+    refused(lambda b, y: bq.dequantize_rows(Q8, b, 64, out=y), [blocks, out], error)
+
+
+def test_dequantize_refuses_strided_outputs_and_those_of_the_host(bq):
+    with FakeTensorMode():
+        blocks = torch.empty(3, 68, dtype=U8, device="cuda")
+        with pytest.raises(ValueError):
+            bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 128, device="cuda")[:, :64])
+        with pytest.raises(TypeError):
+            bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64))
+        with pytest.raises(ValueError):
+            bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64, device="cuda:1"))
