@@ -206,10 +206,27 @@ def dequantize_rows(t: int, blocks: torch.Tensor, cols: int, out: torch.Tensor |
     _cuda(blocks, "blocks")
     nbr = (cols // max(block_values(t), 1)) * block_bytes(t)
     R = blocks.numel() // nbr if nbr else 0
-    r = (_ext or _paged()).dequantize_rows(t, blocks, R, cols, out)
+    try:
+        ext = _ext or _paged()
+    except ImportError:  # the library alone serves this call too, with more host time
+        return _dequantize_rows(t, blocks, R, cols, out)
+    r = ext.dequantize_rows(t, blocks, R, cols, out)
     if type(r) is tuple:
         _raise(r, "bq_dequantize_rows")
     return r
+
+
+def _dequantize_rows(t, blocks, R, cols, out):
+    if blocks.dtype != torch.uint8:
+        raise TypeError(f"blocks must be uint8, not {blocks.dtype}")
+    if out is None:
+        out = torch.empty((R, cols), dtype=torch.float32, device=blocks.device)
+    elif _f32(out, "out", R * cols).device != blocks.device:
+        raise ValueError("out is on another device than blocks")
+    with torch.cuda.device(blocks.device):
+        L = _prep(blocks.device)
+        _check(L.bq_dequantize_rows(t, _ptr(blocks), _ptr(out), R, cols), "bq_dequantize_rows")
+    return out
 
 
 def gemv(t: int, w_blocks: torch.Tensor, x: torch.Tensor, M: int, K: int,

@@ -91,3 +91,36 @@ def test_dequantize_refuses_strided_outputs_and_those_of_the_host(bq):
             bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64))
         with pytest.raises(ValueError):
             bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64, device="cuda:1"))
+
+
+@pytest.fixture
+def library_alone(bq, monkeypatch):
+    """libbq.so without the extension beside it, as a build without g++ or torch's headers leaves them."""
+    import sys
+    from block_quantized_weight_row_gb300 import binding
+    monkeypatch.setattr(binding, "_ext", None)
+    monkeypatch.delattr(bq, "_paged", raising=False)
+    monkeypatch.setitem(sys.modules, bq.__name__ + "._paged", None)
+    with pytest.raises(ImportError):
+        binding._paged()
+    return bq
+
+
+@pytest.mark.parametrize("blocks,out,error", [
+    (((3, 68), F32), None, TypeError), (((3, 68), U8), ((3, 64), BF16), TypeError), (((3, 68), U8), ((2, 64), F32), ValueError)])
+def test_dequantize_refuses_the_same_without_the_extension(library_alone, blocks, out, error):
+    refused(lambda b, y: library_alone.dequantize_rows(Q8, b, 64, out=y), [blocks, out], error)
+
+
+@gpu
+def test_dequantize_needs_no_extension(bq, library_alone):
+    g = torch.Generator(device="cuda").manual_seed(1)
+    blocks = bq.quantize_rows(Q8, torch.randn(5, 96, generator=g, device="cuda"))
+    got = bq.dequantize_rows(Q8, blocks, 96)
+    scales = blocks.view(5, 3, 34)[..., :2].contiguous().view(torch.float16).float()
+    want = (blocks.view(5, 3, 34)[..., 2:].contiguous().view(torch.int8).float() * scales).view(5, 96)  # 11 + 7 bits: exact
+    assert torch.equal(got, want)
+    out = torch.zeros(5, 96, device="cuda")
+    assert bq.dequantize_rows(Q8, blocks, 96, out=out) is out and torch.equal(out, want)
+    with pytest.raises(bq.BQError):
+        bq.dequantize_rows(Q8, blocks, 48)
