@@ -9,6 +9,7 @@ libbq.so is missing or fails to load, every call raises.
 import ctypes
 import dataclasses
 import os
+import threading
 from typing import NamedTuple
 
 import torch
@@ -49,7 +50,16 @@ def library_path() -> str:
 
 
 _lib = None
-_ws = {}  # device index -> torch.uint8 workspace tensor
+
+
+class _Workspaces(threading.local):
+    def __init__(self):
+        self.stream = None  # of the thread's latest call
+        self.eager = {}     # (device, stream) -> uint8 tensor
+        self.given = None   # what the library has
+
+
+_ws = _Workspaces()
 
 
 def lib():
@@ -131,8 +141,9 @@ def _ptr(t):
 def _prep(device):
     """Point the library at torch's current stream on `device`."""
     L = lib()
-    s = torch.cuda.current_stream(device)
-    _check(L.bq_set_stream(ctypes.c_void_p(s.cuda_stream)), "bq_set_stream")
+    s = torch.cuda.current_stream(device).cuda_stream
+    _check(L.bq_set_stream(s), "bq_set_stream")
+    _ws.stream = s
     return L
 
 
@@ -142,13 +153,20 @@ def clear_workspace() -> None:
 
 
 def _workspace(device, nbytes: int):
-    """Grow (never shrink) a torch-owned workspace and hand it to the library."""
-    idx = torch.device(device).index or 0
-    ws = _ws.get(idx)
+    """Hand the library a torch-owned workspace that nothing else uses meanwhile: a
+    thread has one for each stream, which follows its calls there and grows; while a
+    graph is captured each call has its own, in the graph's pool, since replays run
+    beside later calls of any stream and outlive a growing buffer. (One from the
+    allocator for every call costs 5 us of host time.)"""
+    capturing = torch.cuda.is_current_stream_capturing()
+    key = device, _ws.stream
+    ws = None if capturing else _ws.eager.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws[idx] = ws
-    _check(lib().bq_set_workspace(_ptr(ws), ws.numel()), "bq_set_workspace")
+        if not capturing:
+            _ws.eager[key] = ws
+    _check(lib().bq_set_workspace(ws.data_ptr(), ws.numel()), "bq_set_workspace")
+    _ws.given = ws  # lives as long as the library has its address
     return ws
 
 

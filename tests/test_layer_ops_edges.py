@@ -124,3 +124,102 @@ def test_dequantize_needs_no_extension(bq, library_alone):
     assert bq.dequantize_rows(Q8, blocks, 96, out=out) is out and torch.equal(out, want)
     with pytest.raises(bq.BQError):
         bq.dequantize_rows(Q8, blocks, 48)
+
+
+# ------------------------------------------------------------ workspaces --
+
+
+def test_workspaces_are_not_shared(bq, monkeypatch):
+    """Streams, threads and captured calls have their own; a captured one is given to nobody else."""
+    import threading
+    from block_quantized_weight_row_gb300 import binding
+    given, now = [], {"stream": 1, "capturing": False}
+
+    class Library:
+        def bq_set_workspace(self, p, n):
+            given.append((p, n))
+            return 0
+
+        def bq_set_stream(self, s):
+            return 0
+
+    monkeypatch.setattr(binding, "lib", Library)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now["capturing"])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: type("Stream", (), {"cuda_stream": now["stream"]}))
+    made = []
+
+    def empty(n, dtype, device):  # of the host, whatever the device, and never freed
+        made.append(torch.zeros(n, dtype=dtype))
+        return made[-1]
+
+    monkeypatch.setattr(binding.torch, "empty", empty)
+
+    def of(n, stream=1, capturing=False):
+        now.update(stream=stream, capturing=capturing)
+        device = torch.device("cuda:5")
+        binding._prep(device)
+        ws = binding._workspace(device, n)
+        assert given[-1] == (ws.data_ptr(), ws.numel()) and ws.numel() >= n
+        return ws.data_ptr()
+
+    first = of(1000)
+    assert of(2000) == first and of(0) == first  # a stream's calls follow one another
+    second = of(1000, stream=2)
+    captured = [of(1000, capturing=True), of(1000, capturing=True), of(5 << 20, capturing=True)]
+    assert of(1000) == first and of(1000, stream=2) == second
+    larger = of(5 << 20)
+    assert of(5 << 20, stream=2) != second and of(1000) == larger
+    elsewhere = []
+    other = threading.Thread(target=lambda: elsewhere.append(of(1000)))
+    other.start()
+    other.join()
+    assert len({first, second, larger, *captured, *elsewhere}) == 7
+
+
+@gpu
+def test_captured_projections_keep_their_workspace(bq):
+    """Graphs of calls with a workspace, replayed after larger calls and other tensors had their turn, and two at once."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    M, N, K = 96, 40, 1024
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+
+    w8, w4 = bq.quantize_rows(Q8, normal(M, K)), bq.quantize_rows(Q4, normal(M, K))
+    x = [normal(N, K) for _ in range(3)]
+    xq = [bq.quantize_rows(Q8, t) for t in x]
+    kq, vq = bq.quantize_rows(Q4, normal(300 * 2, 64)).view(300, 2, -1), bq.quantize_rows(Q8, normal(300 * 2, 64)).view(300, 2, -1)
+
+    def step(rows, q8):
+        return (bq.gemm(Q8, w8, q8, M, N, K), bq.gemv(Q4, w4, q8[0], M, K), bq.gemm(Q8, w8, rows, M, N, K), bq.gemv(Q4, w4, rows[0], M, K),
+                bq.gemv_multi(Q4, [w4, w4], rows[1], [M, M], K)[1], bq.gemv_sequence(Q4, [([w4], rows[2], [M], K, None)])[0][0],
+                bq.attn_decode(Q4, Q8, rows[0, :256].view(4, 64), kq, vq, 2, 0.125))
+
+    want = [[t.clone() for t in step(x[i], xq[i])] for i in range(3)]
+    cases = []
+    for i in range(2):
+        own = x[i].clone(), xq[i].clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = step(*own)
+        cases.append((own, graph, outs))
+    big = normal(2048, 4096)
+    bq.gemm(Q8, bq.quantize_rows(Q8, normal(128, 4096)), big, 128, 2048, 4096)  # a much larger workspace
+    others = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(64)]
+    for (own, graph, outs), rows, q8, right in zip(cases, x[1:], xq[1:], want[1:]):
+        own[0].copy_(rows)
+        own[1].copy_(q8)
+        graph.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, right))
+    assert all(bool((t == 7).all()) for t in others)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(50):
+        for st, (_, graph, _) in zip(streams, cases):
+            with torch.cuda.stream(st):
+                graph.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = step(x[0], xq[0])
+    torch.cuda.synchronize()
+    for got, right in ((cases[0][2], want[1]), (cases[1][2], want[2]), (eager, want[0])):
+        assert all(torch.equal(a, b) for a, b in zip(got, right))
