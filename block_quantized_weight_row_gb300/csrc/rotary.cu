@@ -5,9 +5,11 @@
 //
 // The angle is kept as a 64-bit fraction of a turn: with F_i = f_i / 2 pi mod 1
 // as a multiple of 2^-64, pos * F_i modulo 2^64 (one integer product) is the
-// turn's fraction, off by at most |pos| 2^-54 of a turn from the double F_i was
-// made of, for any position. Its upper half, signed, is an angle in [-1/2, 1/2)
-// turns, exact to 2^-33, for sincospif, which needs no range reduction: a far
+// turn's fraction, off by at most |pos| (2^-52 |f_i| / 2 pi + 2^-54) of a turn from the
+// double F_i was made of, for any position. Its upper half, signed, is an angle in
+// [-1/2, 1/2) turns, exact to 2^-33: its upper 24 bits, which fp32 holds, go to
+// sincospif, which needs no range reduction, and the lower 8 turn the result on by
+// their small angle (as one float the angle was off by up to 2^-26 of a turn). A far
 // position costs and errs no more than a near one (fp32 angles lose all digits
 // from positions around 2^24 on).
 //
@@ -165,7 +167,11 @@ __global__ void __launch_bounds__(kThreads, kResident) k_rotary(const RotaryArgs
         ax = 0;
       }
       const uint64_t turn = uint64_t(int64_t(__ldg(a.pos + ax * a.pos_axis + t0 + tt))) * freq[p];
-      sincospif(float(int32_t((turn + 0x80000000u) >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31: halves of a turn
+      const int32_t angle = int32_t((turn + 0x80000000u) >> 32), low = angle & 255;
+      sincospif(float(angle - low) * 4.656612873077393e-10f, &s, &c);  // 2^-31: halves of a turn
+      const float d = float(low) * 1.4629180792671596e-9f, s0 = s;     // pi 2^-31; up to 3.8e-7, so that 1 - cos d, 7e-14, is nothing
+      s = __fmaf_rn(d, c, s);
+      c = __fmaf_rn(-d, s0, c);
     }
     table[tt * cols * P + (p % P) * cols + p / P] = make_float2(c, a.inverse ? -s : s);
   }

@@ -489,8 +489,9 @@ int bq_gemm_q8(int type, const void *W_blocks, const void *X_blocks, float *Y, i
  *   or (2 i, 2 i + 1) if interleaved;
  * the other channels are copied. inverse: by the opposite angle (back to where a
  * row came from, and the gradient's turn). Angles are reduced in 64-bit fractions
- * of a turn, so that far positions are as exact as near ones (2^-32 of a turn and
- * |position| 2^-53); sine, cosine and products are fp32, and the result is rounded
+ * of a turn, so that far positions are as exact as near ones: off by 2^-32 of a turn
+ * and |position| (2^-52 F + 2^-54), where F = |inv_freq| / 2 pi, in turns; sine,
+ * cosine and products are fp32, and the result is rounded
  * once to `elem_out`.
  * q, k: [token][head][head_dim] of `elem`, q_out, k_out: of `elem_out`, the same
  * type or, from fp32, any; token and head strides in elements, rows 16-byte

@@ -223,3 +223,41 @@ def test_captured_projections_keep_their_workspace(bq):
     torch.cuda.synchronize()
     for got, right in ((cases[0][2], want[1]), (cases[1][2], want[2]), (eager, want[0])):
         assert all(torch.equal(a, b) for a, b in zip(got, right))
+
+
+# ---------------------------------------------------------------- rotary --
+
+
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("inverse", [False, True])
+def test_rotary_angles_to_the_32nd_bit_of_a_turn(bq, interleaved, inverse):
+    """Angles of 32 bits, at half a turn above all, where the sine is small and shows what the angle lost: the turn of (1, 0) is cosine
+    and sine. Off by the angle's 2^-32 of a turn, 2 ulp of sincospif and the rounding of what its argument's last bits add."""
+    import math
+    import random
+    rng = random.Random(3)
+    near = [0, 1 << 30, 1 << 31, 3 << 30, 1 << 29]
+    units = [c + s * d for c in near for s in (1, -1) for d in (1, 77, 128, 255, 4097, rng.randrange(1 << 20), rng.randrange(1 << 26))]
+    units += [rng.getrandbits(32) for _ in range(128 - len(units))]  # of 2^-32 turns per position
+    n, where = len(units), [1, -1, 3, -5, 0]
+    # in -1/2 .. 1/2 turns, so that the double holds them to 2^-54
+    signed = [(u + 2**31) % 2**32 - 2**31 for u in units]
+    freq = torch.tensor(signed, dtype=torch.float64) * 2**-32 * (2 * math.pi)
+    q = torch.zeros(len(where), 1, 2 * n)
+    first, second = (slice(0, None, 2), slice(1, None, 2)) if interleaved else (slice(0, n), slice(n, None))
+    q[..., first] = 1
+    got, _ = bq.rotary(q.cuda(), None, torch.tensor(where, dtype=torch.int32).cuda(), freq.cuda(), interleaved=interleaved, inverse=inverse)
+    got = got.cpu().double()[:, 0]
+    turned = torch.tensor([[(p * s + 2**31) % 2**32 - 2**31 for s in signed] for p in where], dtype=torch.float64)
+    quarter = (turned / 2**30).round()  # whole quarters are exact; the rest is small enough for the library's sine
+    rest = (turned - quarter * 2**30) * (2 * math.pi * 2**-32)
+    c, s = rest.cos(), rest.sin()
+    k = (quarter % 4).long()
+    cos, sin = (torch.stack(v).gather(0, k[None])[0] for v in ((c, -s, -c, s), (s, c, -s, -c)))
+    if inverse:
+        sin = -sin
+    for value, right in ((got[:, first], cos), (got[:, second], sin)):
+        tol = 1.01 * 2 * math.pi * 2**-32 + 2.5 * 2**-23 * right.abs()
+        beyond = float(((value - right).abs() - tol).max())
+        assert beyond <= 0, beyond
