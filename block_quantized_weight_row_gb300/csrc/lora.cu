@@ -30,7 +30,7 @@
 // beside fp16 ones into two tf32 terms (22 bits; fp16 is exact in tf32). H is kept
 // in fp32 and enters the second product in bf16 terms, three for fp32 rows of out
 // and two (16 bits) for bf16 ones, or in two fp16 terms (22 bits) after scaling
-// each row by a power of two to at most 1.
+// each row by a power of two to at most 2^15.
 #include <algorithm>
 
 #include "lora.cuh"

@@ -148,14 +148,16 @@ __device__ __forceinline__ void copy16(void *to, const void *from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// The power of two that brings a row of H below 2, kept within normal numbers; m:
-// the lane's largest |value|. Its inverse goes to unscale[r].
+// The power of two that brings a row of H to 2^14 .. 2^15, near the upper end of
+// binary16, so that values down to 2^-17 of the largest keep the 22 bits of two terms
+// (at 1 .. 2 those below 2^-3 of it lost some, and 2^-25 of it in all), within normal
+// numbers; m: the lane's largest |value|. Its inverse goes to unscale[r].
 __device__ __forceinline__ float scale_row(float m, float *unscale, int r, int lane) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-  const int e = min(max(int(__float_as_uint(m) >> 23), 2), 252);
-  if (lane == 0) unscale[r] = __uint_as_float(uint32_t(e) << 23);
-  return __uint_as_float(uint32_t(254 - e) << 23);
+  const int e = min(max(int(__float_as_uint(m) >> 23), 16), 254);
+  if (lane == 0) unscale[r] = __uint_as_float(uint32_t(e - 14) << 23);
+  return __uint_as_float(uint32_t(268 - e) << 23);
 }
 
 struct LoraPlan {

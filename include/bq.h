@@ -532,7 +532,8 @@ int bq_rotary(int elem, const void *q, int64_t q_token_stride, int64_t q_head_st
  * row and reaches no other.
  * Accuracy: sums in fp32; fp32 rows enter the products in terms of 22 bits or
  * more, 16-bit ones exactly; A x is kept in fp32 and enters the second product in
- * terms of 22 bits (fp32 out) or 16 (16-bit out). A token's result does not depend
+ * terms of 22 bits (fp32 out, or fp16 adapters: there to 2^-40 of the token's largest
+ * value of it) or 16 (bf16 out). A token's result does not depend
  * on the other tokens of the batch but for the order of sums, which follows
  * n_tokens, n_adapters, rank and K; the same call gives the same bits.
  * Needs a workspace of bq_lora_workspace_size(...) bytes (bq_set_workspace).

@@ -261,3 +261,33 @@ def test_rotary_angles_to_the_32nd_bit_of_a_turn(bq, interleaved, inverse):
         tol = 1.01 * 2 * math.pi * 2**-32 + 2.5 * 2**-23 * right.abs()
         beyond = float(((value - right).abs() - tol).max())
         assert beyond <= 0, beyond
+
+
+# -------------------------------------------------------------- adapters --
+
+
+@gpu
+@pytest.mark.parametrize("x,y", [(F32, F32), (F16, F32), (F32, F16)])
+@pytest.mark.parametrize("T,rank", [(20, 16), (300, 64), (1100, 64), (1100, 128)])
+def test_lora_small_ranks_beside_dominant_ones(bq, x, y, T, rank):
+    """fp16 adapters whose ranks differ by 2^15 in A x and as much, the other way, in B: all matter alike. Chains of matrix instructions
+    add 4 u of the magnitudes each, A x enters the second product in 22 bits, or 2^-40 of its row's largest; outputs are rounded."""
+    g = torch.Generator().manual_seed(T + rank)
+    n, K, M, u = 2, 64, 70, 2.0**-24
+    power = torch.pow(2.0, 6 - torch.arange(rank) * 15 // (rank - 1))
+    X = torch.randn(T, K, generator=g).to(x)
+    A = (torch.randn(n, rank, K, generator=g) / 8 * power[:, None]).half()
+    B = (torch.randn(n, M, rank, generator=g) / power).half()
+    Y = torch.randn(T, M, generator=g).to(y)
+    ids = torch.randint(0, n, (T,), generator=g).int()
+    got = bq.lora(X.cuda(), A.cuda(), B.cuda(), ids.cuda(), Y.cuda()).cpu().double()
+    a, b = A.double()[ids.long()], B.double()[ids.long()]
+    h = torch.einsum("trk,tk->tr", a, X.double())
+    hm = torch.einsum("trk,tk->tr", a.abs(), X.double().abs())
+    right = Y.double() + torch.einsum("tmr,tr->tm", b, h)
+    terms = 4 if x == F32 else 1
+    eh = hm * ((4 * 2 * terms * K // 32 + 37) * u + (2**-22 if x == F32 else 0)) + 2**-22 * h.abs() + 2**-40 * h.abs().amax(-1, keepdim=True)
+    tol = torch.einsum("tmr,tr->tm", b.abs(), eh + 4 * 2 * 2 * -(-rank // 32) * u * h.abs())
+    tol += 2 * u * right.abs() + torch.finfo(y).eps / 2 * right.abs()
+    beyond = float(((got - right).abs() - tol).max())
+    assert beyond <= 0, beyond
