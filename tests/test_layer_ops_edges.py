@@ -291,3 +291,27 @@ def test_lora_small_ranks_beside_dominant_ones(bq, x, y, T, rank):
     tol += 2 * u * right.abs() + torch.finfo(y).eps / 2 * right.abs()
     beyond = float(((got - right).abs() - tol).max())
     assert beyond <= 0, beyond
+
+
+@gpu
+@pytest.mark.parametrize("w", [BF16, F16])
+@pytest.mark.parametrize("rank,seed", [(16, 1), (16, 2), (64, 3)])
+def test_lora_of_fp32_rows_is_as_exact_as_fp32_sums(bq, w, rank, seed):
+    """A decode batch, against the same formula in 64 bits: no further off, in the output's norm, than fp32 products and sums are."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    T, n, K, M = 48, 16, 4096, 1024
+    X = torch.randn(T, K, generator=g, device="cuda")
+    A = (torch.randn(n, rank, K, generator=g, device="cuda") / 64).to(w)
+    B = (torch.randn(n, M, rank, generator=g, device="cuda") * 0.2).to(w)
+    Y = torch.randn(T, M, generator=g, device="cuda")
+    ids = torch.randint(0, n, (T,), generator=g, device="cuda", dtype=torch.int32)
+
+    def formula(t):
+        h = (X.to(t) @ A.to(t).flatten(0, 1).T).view(T, n, rank)
+        h = torch.where(ids[:, None, None] == torch.arange(n, device="cuda")[:, None], h, torch.zeros((), dtype=t, device="cuda"))
+        return Y.to(t) + h.flatten(1) @ B.to(t).permute(0, 2, 1).flatten(0, 1)
+
+    right = formula(torch.float64)
+    off = float((bq.lora(X, A, B, ids, Y).double() - right).norm())
+    plain = float((formula(F32).double() - right).norm())
+    assert off <= plain, (off, plain)
