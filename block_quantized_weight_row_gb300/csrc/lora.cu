@@ -372,7 +372,8 @@ __global__ void __launch_bounds__(kShrinkThreads) k_lora_shrink64(const LoraArgs
         for (int nt = 0; nt < NT; ++nt) bw[nt] = *reinterpret_cast<const uint4 *>(ad_rows + b * R::kABlock + (nt * 8 + g) * 64 + t * 16);
         shrink_step<XE, WE, NT>(acc, xl, xh, bw);
       }
-      if (s & 1) take(total, acc);
+      // after 16 instructions of fp32 rows (32: 600 of 4096 at rank 64 off by 4.7e-7 of the output's norm for 2.8e-7), 8 in 16 bits
+      if (XE == kElemF32 || (s & 1)) take(total, acc);
     }
   }
   take(total, acc);

@@ -319,8 +319,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // rows of x, in tensor memory. Rows go through registers, stages ahead, to where the
 // operand's swizzle wants them; fp32 rows are cut into three bf16 terms, each an
 // operand tile. K is cut over the CTAs of a cluster and, in a CTA, over four
-// accumulators (256 columns), so that the products' chains stay short; the sums of
-// all meet in fp32 in a fixed order.
+// accumulators (256 columns), so that the products' chains stay short: four parts of
+// k, or for fp32 rows two, each with the largest term apart from the others, whose
+// instructions would cut its sum too (4096 rows of 8192 at rank 128: 1.1e-6 of the
+// output's norm for 1.6e-6 with four parts); the sums of all meet in fp32 in a
+// fixed order.
 // For fp32 rows and for more than 64 ranks, where the warp-level kernel of lora.cu
 // is slower: whole calls of 8192 tokens of 4096 to 11008 columns
 // take 189 us for 219 (fp32, rank 64) and 216 for 231 (bf16, rank 128). A stage takes
@@ -380,7 +383,8 @@ __global__ void __launch_bounds__(kShThreads, 2)
   const uint32_t tmem = tmem_slot;
   const int split = blockIdx.x, all = (a.K + 63) / 64;
   const int s0 = int(int64_t(all) * split / splits), n = int(int64_t(all) * (split + 1) / splits) - s0;  // stages of 64 k
-  auto region = [&](int i) { return i * kShRegions / n; };
+  constexpr int kParts = R::kTerms > 1 ? kShRegions / 2 : kShRegions;  // of k
+  auto region = [&](int i) { return i * kParts / n; };
   float *part = reinterpret_cast<float *>(sm);
 
   if (warp < 8) {
@@ -446,8 +450,8 @@ __global__ void __launch_bounds__(kShThreads, 2)
     if (tc_wait_warp(done, 0, spin, abort_flag, a.err)) {
       tc_fence_after();
       for (int q = 0; q < kShRegions; ++q) {
-        const int first = (q * n + kShRegions - 1) / kShRegions;  // the region's first stage, if it has one
-        if (first >= n || region(first) != q) continue;
+        const int r = q * kParts / kShRegions, first = (r * n + kParts - 1) / kParts;  // the region's first stage, if it has one
+        if (first >= n || region(first) != r) continue;
         uint32_t d[32];
         tmem_ld32(tmem + (uint32_t(lg * 32) << 16) + uint32_t(q * kTcTokens + half * 32), d);
 #pragma unroll
@@ -485,12 +489,14 @@ __global__ void __launch_bounds__(kShThreads, 2)
       tc_fence_after();
       const uint64_t a_desc = sw128_desc(base + st * R::kStage);
       const int steps = min(4, (a.K - (s0 + i) * 64) / 16);  // of 16 k
-      uint32_t more = region(i) == last;
+      const bool begun = region(i) == last;
       last = region(i);
       for (int k = R::kTerms - 1; k >= 0; --k) {
         const uint64_t x_desc = sw128_desc(base + st * R::kStage + R::kATile + k * kShXTile);
+        const uint32_t d = tmem + uint32_t((R::kTerms > 1 ? 2 * last + (k > 0) : last) * kTcTokens);
+        uint32_t more = begun || (k > 0 && k < R::kTerms - 1);
         for (int q = 0; q < steps; ++q) {
-          tc_mma(tmem + uint32_t(last * kTcTokens), a_desc + uint64_t(2 * q), x_desc + uint64_t(2 * q), kIdesc, more);
+          tc_mma(d, a_desc + uint64_t(2 * q), x_desc + uint64_t(2 * q), kIdesc, more);
           more = 1;
         }
       }

@@ -298,10 +298,20 @@ def test_lora_small_ranks_beside_dominant_ones(bq, x, y, T, rank):
 @pytest.mark.parametrize("rank,seed", [(16, 1), (16, 2), (64, 3)])
 def test_lora_of_fp32_rows_is_as_exact_as_fp32_sums(bq, w, rank, seed):
     """A decode batch, against the same formula in 64 bits: no further off, in the output's norm, than fp32 products and sums are."""
+    as_exact(bq, w, 48, 16, rank, 4096, 1024, seed)
+
+
+@gpu
+@pytest.mark.parametrize("w,rank,K", [(F16, 64, 1024), (BF16, 128, 8192)])
+def test_lora_prompts_of_fp32_rows_are_as_exact_as_fp32_sums(bq, w, rank, K):
+    """The same in tiles of 64 tokens: long chains of instructions."""
+    as_exact(bq, w, 4096, 4, rank, K, 2048, 1)
+
+
+def as_exact(bq, w, T, n, rank, K, M, seed):
     g = torch.Generator(device="cuda").manual_seed(seed)
-    T, n, K, M = 48, 16, 4096, 1024
     X = torch.randn(T, K, generator=g, device="cuda")
-    A = (torch.randn(n, rank, K, generator=g, device="cuda") / 64).to(w)
+    A = (torch.randn(n, rank, K, generator=g, device="cuda") / K**0.5).to(w)
     B = (torch.randn(n, M, rank, generator=g, device="cuda") * 0.2).to(w)
     Y = torch.randn(T, M, generator=g, device="cuda")
     ids = torch.randint(0, n, (T,), generator=g, device="cuda", dtype=torch.int32)
