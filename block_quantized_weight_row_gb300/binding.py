@@ -522,7 +522,8 @@ def _raise(r, what):
 
 
 class PagedStep(NamedTuple):
-    """What paged_extend makes of a batch's lengths (all on the device)."""
+    """What paged_extend makes of a batch's lengths (all on the device). The tensors lie
+    in one allocation, which each of them keeps alive: copy what outlives the step."""
     q_start: torch.Tensor    # int32 (sequences + 1): rows of each sequence in the batch
     kv_len: torch.Tensor     # int32 (sequences): tokens cached once the step's rows are written
     slots: torch.Tensor      # int64 (n_slots): where each row goes, -1 behind the last
@@ -535,8 +536,8 @@ def paged_extend(page_size: int, n_pages: int, kv_len: torch.Tensor, n_new: torc
     """The next tokens of a batch of sequences in paged caches of n_pages pages
     (bq_paged_extend): kv_len and n_new (sequences) int32, the cached and the coming
     tokens; page_table (sequences, max_pages) int32, to which new pages are added in
-    place, from the front of free_pages (int32); n_slots: room for the batch's
-    tokens. A sequence that cannot grow gets slots of -1 and keeps its kv_len, which
+    place, from the front of free_pages (int32), which the caller moves on by taken[0]
+    before the next call; n_slots: room for the batch's tokens. A sequence that cannot grow gets slots of -1 and keeps its kv_len, which
     device_status reports; taken[1] > taken[0] tells so too where pages ran out."""
     r = (_ext or _paged()).paged_extend(page_size, n_pages, kv_len, n_new, page_table, free_pages, n_slots)
     if type(r[0]) is int:

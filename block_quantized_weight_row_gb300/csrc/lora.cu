@@ -13,9 +13,9 @@
 //      warp-level instructions, k_lora_shrink_tc on tcgen05 (lora_tc.cu).
 //   3. out_t = y_t + B_a H[t]: k_lora_expand for tiles of 16, k_lora_expand_tc on
 //      tcgen05 for tiles of 64.
-// Measured (GPU alone): 48 fp32 tokens of 16 adapters, 4096 to 4096 at rank 16, 10.1
-// us; 8192 bf16 tokens, 4096 to 11008 fp32 columns at rank 64, 163 to 165 us (8 for step 1,
-// 28, and 128 for 720 MB of y and out: 5.6 TB/s).
+// Measured (GPU alone): 48 fp32 tokens of 16 adapters, 4096 to 4096 at rank 16, 10.2
+// to 10.6 us; 8192 bf16 tokens, 4096 to 11008 fp32 columns at rank 64, 163.5 us (8 for step
+// 1, 29, and 128 for 720 MB of y and out: 5.6 TB/s).
 // A tile's rows do not depend on one another, so neither the order inside an
 // adapter nor the other tokens change a result.
 //

@@ -326,8 +326,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 // fixed order.
 // For fp32 rows and for more than 64 ranks, where the warp-level kernel of lora.cu
 // is slower: whole calls of 8192 tokens of 4096 to 11008 columns
-// take 189 us for 219 (fp32, rank 64) and 216 for 231 (bf16, rank 128). A stage takes
-// 0.8 us whatever the copies' form or depth.
+// take 189 us for 219 (fp32, rank 64) and 216 for 231 (bf16, rank 128). Of the two CTAs
+// of an SM each takes a stage in 1.6 us of fp32 rows (2.6 TB/s of x) and 1.2 us of 16-bit
+// ones at rank 128, whatever the copies' form or depth.
 // Warps 0-7: rows of x, then the sums; warp 8: TMA; warp 9: MMA. All waits bounded.
 constexpr int kShThreads = 320, kShRegions = 4, kShTmem = kShRegions * kTcTokens;
 constexpr int kShXTile = kTcTokens * 128, kShPitch = 128;

@@ -2,7 +2,8 @@
 requests' own adapters, rotary positions, the paged cache, and the norms between.
 
 Every step is the same calls, whether a request brings a chunk of its prompt or one
-token, and all lengths stay on the device:
+token, and all lengths stay on the device; the host reads one number, the pages
+taken, to move the front of the free list on:
 
     paged_extend    page tables, slots and positions of the step's tokens
     add_rms_norm    the residual stream's sum and norm, in fp32 for the adapters and

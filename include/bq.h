@@ -425,7 +425,8 @@ int bq_paged_slot_check(const bq_paged_cache *cache, int64_t slot, int64_t *page
  *   q_start[b + 1] = start_b + n_new[b], q_start[0] = 0, kv_len_out[b] =
  *     kv_len[b] + n_new[b]: what bq_paged_kv_write and bq_paged_attn take,
  *   taken[0] = pages taken from the front of free_pages, taken[1] = pages that
- *     all sequences needed.
+ *     all sequences needed. The list stays as it is: the caller moves its front on
+ *     by taken[0] before the next call.
  * A sequence that cannot grow gets nothing: its tokens' slots are -1,
  * kv_len_out is kv_len, and bq_device_status reports it (BQ_ERR_INDEX). Such are
  * those with a negative length, more tokens than max_pages * page_size or 2^31 -
