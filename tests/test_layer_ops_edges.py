@@ -89,8 +89,9 @@ def test_dequantize_refuses_strided_outputs_and_those_of_the_host(bq):
             bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 128, device="cuda")[:, :64])
         with pytest.raises(TypeError):
             bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64))
-        with pytest.raises(ValueError):
-            bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64, device="cuda:1"))
+        if torch.cuda.device_count() != 1:  # with one device there is no name for another
+            with pytest.raises(ValueError):
+                bq.dequantize_rows(Q8, blocks, 64, out=torch.empty(3, 64, device="cuda:1"))
 
 
 @pytest.fixture
